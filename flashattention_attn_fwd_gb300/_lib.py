@@ -45,7 +45,14 @@ EXPORTS = (
     "fl_diffattn_bwd_workspace_size",
     "fl_last_error_detail",
     "fl_attn_schedule",
+    "fl_kv_append",
+    "fl_attn_paged_decode_fwd",
+    "fl_attn_paged_decode_workspace_size",
+    "fl_kv_cache_size",
+    "fl_kv_append_desc_size",
 )
+
+KV_FORMATS = {"bf16": 0, "e2m1": 1}
 
 
 class AttnDesc(ctypes.Structure):
@@ -63,7 +70,36 @@ class AttnDesc(ctypes.Structure):
         ("stream", ctypes.c_void_p),
         ("debug_flags", ctypes.c_uint32), ("debug_arg", ctypes.c_int32),
         ("wait_limit_ms", ctypes.c_uint32),
-        ("reserved", ctypes.c_int32 * 7),
+        ("sink", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 6),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+        ("format", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32),
+        ("reserved", ctypes.c_int32 * 5),
+    ]
+
+
+class KvAppendDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p),
+        ("rope_positions", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("rope_interleaved", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+        ("q_strides", ctypes.c_int64 * 2), ("k_strides", ctypes.c_int64 * 2), ("v_strides", ctypes.c_int64 * 2),
+        ("q_out_strides", ctypes.c_int64 * 2), ("k_out_strides", ctypes.c_int64 * 2),
+        ("v_out_strides", ctypes.c_int64 * 2),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -124,10 +160,24 @@ def lib() -> ctypes.CDLL:
         L.fl_status_string.restype = ctypes.c_char_p
         L.fl_abi_version.argtypes = []
         L.fl_abi_version.restype = i32
+        L.fl_kv_append.argtypes = [vp, vp, ctypes.POINTER(KvCache), ctypes.POINTER(KvAppendDesc)]
+        L.fl_kv_append.restype = i32
+        L.fl_attn_paged_decode_fwd.argtypes = [vp, ctypes.POINTER(KvCache), vp, vp, ctypes.c_int64, vp, vp, vp,
+                                               ctypes.c_size_t, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_paged_decode_fwd.restype = i32
+        L.fl_attn_paged_decode_workspace_size.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(KvCache)]
+        L.fl_attn_paged_decode_workspace_size.restype = ctypes.c_size_t
+        L.fl_kv_cache_size.argtypes = []
+        L.fl_kv_cache_size.restype = i32
+        L.fl_kv_append_desc_size.argtypes = []
+        L.fl_kv_append_desc_size.restype = i32
         L.fl_attn_desc_size.argtypes = []
         L.fl_attn_desc_size.restype = i32
         if L.fl_attn_desc_size() != ctypes.sizeof(AttnDesc):
             raise RuntimeError("fl_attn_desc layout mismatch between flattn.h and the binding")
+        if L.fl_kv_cache_size() != ctypes.sizeof(KvCache) or \
+                L.fl_kv_append_desc_size() != ctypes.sizeof(KvAppendDesc):
+            raise RuntimeError("paged cache layout mismatch between flattn.h and the binding")
         _lib = L
     return _lib
 

@@ -179,6 +179,9 @@ int box_width(int c) { return c >= 64 ? 64 : c; }
 
 uint64_t wait_ns(uint32_t ms) { return ms ? static_cast<uint64_t>(ms) * 1000ull * 1000ull : kDefaultWaitNs; }
 
+// Sinks are keys that a sliding window leaves behind; no other mask has them.
+bool sink_ok(const fl_attn_desc& d) { return d.sink == 0 || (d.sink > 0 && d.mask_kind == FL_MASK_SLIDING_WINDOW); }
+
 bool head_dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 // Softcap on the FMA pipe: cap*log2(e)*tanh(s*scale/cap) = s * Q(s^2) while
@@ -275,6 +278,8 @@ fl_status attn_fwd_check(const void* q, const void* k, const void* v, void* out,
   if (d.mask_kind < FL_MASK_NONE || d.mask_kind > FL_MASK_DOCUMENT) return FL_ERR_INVALID_ARG;
   if (d.mask_kind != FL_MASK_NONE && d.Lq != d.Lk) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_SLIDING_WINDOW && d.window < 1) return FL_ERR_INVALID_ARG;
+  if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
+  if (d.sink) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_PREFIX_LM && d.prefix_len < 0) return FL_ERR_INVALID_ARG;
   if (d.mask_kind == FL_MASK_DOCUMENT && (!d.doc_offsets || d.num_docs < 1 || d.num_docs > d.Lq))
     return FL_ERR_INVALID_ARG;
@@ -328,6 +333,17 @@ fl_status attn_fwd_launch(const void* q, const void* k, const void* v, void* out
   return launched("attention kernel launch",
                   launch_attn(d.d, d.dv, d.score_mod, maps, p, grid, static_cast<cudaStream_t>(d.stream)));
 }
+
+fl_status device_info(int* sm_count, uint32_t** status) {
+  DeviceState* ds = nullptr;
+  const fl_status st = device_state(&ds);
+  if (st != FL_OK) return st;
+  *sm_count = ds->sm_count;
+  *status = ds->status;
+  return FL_OK;
+}
+
+fl_status launch_result(const char* where, cudaError_t e) { return launched(where, e); }
 
 }  // namespace fl
 
@@ -438,6 +454,7 @@ fl_status decode_check(const void* q, const void* k, const void* v, void* out, f
   if ((d.Hq / d.Hkv) * d.Lq > fl::kDecodeMaxRows) return FL_ERR_UNSUPPORTED;
   if (!std::isfinite(d.scale)) return FL_ERR_INVALID_ARG;
   if (d.mask_kind != FL_MASK_NONE && d.mask_kind != FL_MASK_CAUSAL) return FL_ERR_UNSUPPORTED;
+  if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
   if (d.score_mod < FL_SCORE_NONE || d.score_mod > FL_SCORE_SOFTCAP) return FL_ERR_INVALID_ARG;
   if (d.score_mod == FL_SCORE_ALIBI && !d.alibi_slopes) return FL_ERR_INVALID_ARG;
   if (d.score_mod == FL_SCORE_SOFTCAP && !(d.softcap > 0.f && std::isfinite(d.softcap))) return FL_ERR_INVALID_ARG;
@@ -479,6 +496,8 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   if (d.mask_kind < FL_MASK_NONE || d.mask_kind > FL_MASK_DOCUMENT) return FL_ERR_INVALID_ARG;
   if (d.mask_kind != FL_MASK_NONE && d.Lq != d.Lk) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_SLIDING_WINDOW && d.window < 1) return FL_ERR_INVALID_ARG;
+  if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
+  if (d.sink) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_PREFIX_LM && d.prefix_len < 0) return FL_ERR_INVALID_ARG;
   if (d.mask_kind == FL_MASK_DOCUMENT && (!d.doc_offsets || d.num_docs < 1 || d.num_docs > d.Lq))
     return FL_ERR_INVALID_ARG;
@@ -567,6 +586,7 @@ fl_status fl_diffattn_bwd(const void* q1, const void* k1, const void* q2, const 
   if (!std::isfinite(lambda) || !std::isfinite(d.scale)) return FL_ERR_INVALID_ARG;
   if (d.d != 64 || d.dv != 128) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind != FL_MASK_NONE && d.mask_kind != FL_MASK_CAUSAL) return FL_ERR_UNSUPPORTED;
+  if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
   if (d.score_mod != FL_SCORE_NONE) return FL_ERR_UNSUPPORTED;
   for (int i = 0; i < 4; ++i)
     if (d.q_strides[i] || d.k_strides[i] || d.v_strides[i] || d.o_strides[i]) return FL_ERR_UNSUPPORTED;
@@ -649,6 +669,7 @@ fl_status fl_diffattn_fwd(const void* q1, const void* k1, const void* q2, const 
   if (!std::isfinite(lambda) || !std::isfinite(d.scale)) return FL_ERR_INVALID_ARG;
   if (d.d != 64 || d.dv != 128) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind != FL_MASK_NONE && d.mask_kind != FL_MASK_CAUSAL) return FL_ERR_UNSUPPORTED;
+  if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
   if (d.score_mod != FL_SCORE_NONE) return FL_ERR_UNSUPPORTED;
   for (int i = 0; i < 4; ++i)
     if (d.q_strides[i] || d.k_strides[i] || d.v_strides[i] || d.o_strides[i]) return FL_ERR_UNSUPPORTED;

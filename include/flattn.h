@@ -56,13 +56,14 @@ typedef enum {
   FL_ERR_ALIGNMENT = 3,     /* pointer or stride not 16-byte aligned           */
   FL_ERR_CUDA = 4,          /* a CUDA runtime / driver call failed             */
   FL_ERR_TIMEOUT = 5,       /* a device-side pipeline wait hit its time limit  */
-  FL_ERR_DEVICE_BOUNDS = 6  /* reserved: a device-side bounds check tripped    */
+  FL_ERR_DEVICE_BOUNDS = 6  /* a kernel met a page or position out of range    */
 } fl_status;
 
 typedef enum {
   FL_MASK_NONE = 0,           /* every key visible                              */
   FL_MASK_CAUSAL = 1,         /* key j visible to query i iff j <= i            */
-  FL_MASK_SLIDING_WINDOW = 2, /* iff i - window < j <= i (window keys, self incl.) */
+  FL_MASK_SLIDING_WINDOW = 2, /* iff i - window < j <= i (window keys, self incl.)
+                                 or j < sink and j <= i (fl_attn_desc.sink)    */
   FL_MASK_PREFIX_LM = 3,      /* iff j <= i or j < prefix_len                   */
   FL_MASK_DOCUMENT = 4        /* iff doc(i) == doc(j) [and j <= i if doc_causal] */
 } fl_mask_kind;
@@ -112,7 +113,9 @@ typedef struct fl_attn_desc {
   uint32_t debug_flags;     /* FL_DEBUG_*; 0 in normal use                     */
   int32_t debug_arg;
   uint32_t wait_limit_ms;   /* device wait limit; 0 = default (2000 ms)        */
-  int32_t reserved[7];
+  int32_t sink;             /* SLIDING_WINDOW: the first `sink` keys stay
+                               visible to every later query; 0: none           */
+  int32_t reserved[6];
 } fl_attn_desc;
 
 /* Fill *desc with zeros and the defaults (mask NONE, score NONE, scale 1/sqrt(d)). */
@@ -226,6 +229,130 @@ FL_API fl_status fl_attn_decode_fwd(const void* q, const void* k_cache, const vo
 /* Workspace bytes fl_attn_decode_fwd needs for `desc` on the current device
    (0 when the key axis is not split, or on an invalid descriptor). */
 FL_API size_t fl_attn_decode_workspace_size(const fl_attn_desc* desc);
+
+/*
+ * Paged key/value cache.  The cache's tokens live in fixed-size pages of one
+ * pool; a block table gives, for every sequence, the page that holds its
+ * positions [i * page_size, (i + 1) * page_size).  Pages are head-major, so
+ * one (page, head) is one contiguous run:
+ *   FL_KV_BF16   k, v : bf16 [num_pages, Hkv, page_size, d]
+ *   FL_KV_E2M1   k, v : 4-bit codes [num_pages, Hkv, page_size, d / 2] bytes,
+ *                  channel 2c in the low and 2c + 1 in the high nibble; a code
+ *                  is sign, two exponent bits, one mantissa bit (magnitudes
+ *                  0, 0.5, 1, 1.5, 2, 3, 4, 6)
+ *                k_scales : e4m3 [num_pages, Hkv, page_size, d / 16]
+ *                v_scales : e4m3 [num_pages, Hkv, d / 16, page_size]
+ *                A stored value is code * block scale * k_scale (v_scale),
+ *                one e4m3 block scale per 16 channels of one token.
+ * page_size is a power of two from 16 to 256, d is 64 or 128.  v_scales is
+ * block-major so that one load brings the scales of consecutive tokens.
+ */
+typedef enum { FL_KV_BF16 = 0, FL_KV_E2M1 = 1 } fl_kv_format;
+
+typedef struct fl_kv_cache {
+  void* k;
+  void* v;
+  void* k_scales;           /* E2M1, else NULL                                 */
+  void* v_scales;           /* E2M1, else NULL                                 */
+  float k_scale, v_scale;   /* E2M1: per-tensor scales, normal fp32 > 0; BF16: 1 */
+  int32_t format;           /* fl_kv_format                                    */
+  int32_t num_pages, page_size, Hkv, d;
+  int32_t reserved[5];      /* zero                                            */
+} fl_kv_cache;
+
+/*
+ * Tokens to append.  The T new tokens of B sequences are packed: sequence b
+ * owns rows [seq_offsets[b], seq_offsets[b + 1]).  kv_len[b] counts b's tokens
+ * with the new ones, so row seq_offsets[b] + i takes position
+ * kv_len[b] - n_b + i, n_b = seq_offsets[b + 1] - seq_offsets[b] (the same
+ * kv_len that fl_attn_paged_decode_fwd then reads).
+ * Row strides are in elements, (token, head), multiples of 8; channels are
+ * contiguous.
+ */
+typedef struct fl_kv_append_desc {
+  int32_t T, B;
+  int32_t Hq;                   /* heads of q; 0 without q                      */
+  int32_t max_pages;            /* columns of block_table                      */
+  const int32_t* seq_offsets;   /* device int32 [B + 1], non-decreasing from 0;
+                                   NULL: T == B, one token per sequence        */
+  const int32_t* kv_len;        /* device int32 [B]                            */
+  const int32_t* block_table;   /* device int32 [B, max_pages]                 */
+  int64_t table_stride;         /* elements between rows of block_table        */
+  const float* rope_cos;        /* device fp32 [rope_positions, rope_dim / 2]  */
+  const float* rope_sin;        /* the same; both NULL: no rotation            */
+  int32_t rope_positions, rope_dim;
+  int32_t rope_interleaved;     /* 0: channel c pairs with c + rope_dim / 2;
+                                   1: channel 2c with 2c + 1                   */
+  int32_t reserved0;
+  const void* q;                /* bf16 [T, Hq, d] or NULL                     */
+  void* q_out;                  /* bf16 [T, Hq, d]: rotated q                  */
+  void* k_out;                  /* bf16 [T, Hkv, d] or NULL: what the cache now */
+  void* v_out;                  /* holds for the new tokens (both or neither)  */
+  int64_t q_strides[2], k_strides[2], v_strides[2];
+  int64_t q_out_strides[2], k_out_strides[2], v_out_strides[2];
+  void* stream;
+} fl_kv_append_desc;
+
+/*
+ * Rotate the new tokens' queries and keys by their positions (rotary position
+ * embedding) and append keys and values to the paged cache, in one pass.
+ *   k, v : bf16 [T, Hkv, d] (Hkv, d: the cache's)
+ * The first rope_dim channels (a multiple of 16, at most d) are rotated in
+ * fp32, each product and sum rounded once:
+ *   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * for each pair (x1, x2), cos and sin from row `position` of the tables; the
+ * rest passes through.  A bf16 cache takes y rounded once.  An e2m1 cache
+ * takes, per 16 channels of u = y * (1 / k_scale): block scale s = e4m3(max|u|
+ * * (1/6)), codes e2m1(u / s), all rounded to nearest even and saturating; a
+ * block whose scale rounds to 0 is stored as zeros.  Values are stored the
+ * same way without rotation.  k_out and v_out receive the stored values (for
+ * the new tokens' own attention); q_out may be q, k_out k and v_out v (same
+ * strides) to work in place.
+ * Left as they are: rows from seq_offsets[B] on, and rows whose position is
+ * negative (kv_len[b] < n_b: a sequence that takes no part).  A row whose
+ * position has no rotation, no block_table column or a page outside the pool
+ * is left too, and the call reports FL_ERR_DEVICE_BOUNDS through
+ * fl_sync_status.  Every (sequence, position) must map to its own page slot:
+ * pages that the call writes must not be shared between sequences.
+ */
+FL_API fl_status fl_kv_append(const void* k, const void* v, const fl_kv_cache* cache,
+                              const fl_kv_append_desc* desc);
+
+/*
+ * Decode-phase attention over a paged cache (bf16 or 4-bit): as
+ * fl_attn_decode_fwd, with the keys and values of sequence b found through
+ * row b of block_table.  Query row i of sequence b sits at position
+ * p = kv_len[b] - Lq + i.  Key j is visible when j < kv_len[b] and, by mask,
+ *   NONE            always
+ *   CAUSAL          j <= p
+ *   SLIDING_WINDOW  j <= p and (p - window < j or j < sink)
+ * Pages that hold no visible key are not read and may be missing from the
+ * table (any value).
+ *   q, out      : bf16 [B, Hq, Lq, d], desc->q_strides / o_strides (zero:
+ *                 contiguous)
+ *   lse         : fp32 [B, Hq, Lq] contiguous, or NULL
+ *   kv_len      : device int32 [B], clamped to [0, max_pages * page_size]
+ *   block_table : device int32 [B, max_pages], rows table_stride apart
+ *   workspace   : caller-owned device buffer of at least
+ *                 fl_attn_paged_decode_workspace_size() bytes, 16-byte aligned;
+ *                 calls that may overlap need one each
+ * desc: B, Hq, Hkv, Lq, d == dv (the cache's Hkv and d), Lk = max_pages *
+ * page_size, (Hq / Hkv) * Lq <= 64, any score_mod, k_strides and v_strides
+ * zero.  A visible key whose page is outside the pool is left out and the
+ * call reports FL_ERR_DEVICE_BOUNDS through fl_sync_status.  Rows that see no
+ * key get out = 0 and lse = -inf.  Results do not depend on where pages lie.
+ */
+FL_API fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, const int32_t* kv_len,
+                                          const int32_t* block_table, int64_t table_stride, void* out, float* lse,
+                                          void* workspace, size_t workspace_bytes, const fl_attn_desc* desc);
+
+/* Workspace bytes fl_attn_paged_decode_fwd needs for `desc` and `cache` on the
+   current device (0 on an invalid descriptor or without a device). */
+FL_API size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv_cache* cache);
+
+/* sizeof(fl_kv_cache) and sizeof(fl_kv_append_desc) as compiled (binding check). */
+FL_API int32_t fl_kv_cache_size(void);
+FL_API int32_t fl_kv_append_desc_size(void);
 
 /*
  * Backward pass of fl_attn_fwd (the Flashlight wiki summary lists the

@@ -14,5 +14,7 @@ from .attention import *  # noqa: F401,F403
 from .attention import __all__ as _att_all
 from .backward import attention_backward, diff_attention_backward  # noqa: F401
 from .online import online_attention  # noqa: F401
+from .paged import dequantise, paged_attention, quantise, rotate  # noqa: F401
 
-__all__ = list(_att_all) + ["online_attention", "attention_backward", "diff_attention_backward"]
+__all__ = list(_att_all) + ["online_attention", "attention_backward", "diff_attention_backward", "rotate", "quantise",
+                             "dequantise", "paged_attention"]

@@ -100,7 +100,7 @@ def doc_ids(offsets, L: int) -> np.ndarray:
 
 def visibility(mask: str, Lq: int, Lk: int, *, window: int | None = None,
                prefix: int | None = None, offsets=None,
-               doc_causal: bool = False) -> np.ndarray:
+               doc_causal: bool = False, sink: int = 0) -> np.ndarray:
     """Boolean [Lq, Lk]: True where key j is visible to query i."""
     i = np.arange(Lq)[:, None]
     j = np.arange(Lk)[None, :]
@@ -109,7 +109,7 @@ def visibility(mask: str, Lq: int, Lk: int, *, window: int | None = None,
     if mask == "causal":
         return j <= i
     if mask == "window":
-        return (j <= i) & (j > i - int(window))
+        return (j <= i) & ((j > i - int(window)) | (j < int(sink)))
     if mask == "prefix_lm":
         return (j <= i) | (j < int(prefix))
     if mask == "document":
@@ -160,7 +160,7 @@ def attention(q, k, v, *, scale: float | None = None, mask: str = "none",
               window: int | None = None, prefix: int | None = None,
               doc_offsets=None, doc_causal: bool = False,
               score_mod: str = "none", slopes=None, softcap: float | None = None,
-              return_probs: bool = False):
+              sink: int = 0, return_probs: bool = False):
     """softmax(score_mod(scale Q K^T) masked) V for q [B,Hq,Lq,d],
     k [B,Hkv,Lk,d], v [B,Hkv,Lk,dv].  Returns (out [B,Hq,Lq,dv],
     lse [B,Hq,Lq]) in float64, and P [B,Hq,Lq,Lk] when return_probs."""
@@ -179,7 +179,7 @@ def attention(q, k, v, *, scale: float | None = None, mask: str = "none",
     probs = np.zeros((B, Hq, Lq, Lk)) if return_probs else None
     vis_common = None
     if mask != "document":
-        vis_common = visibility(mask, Lq, Lk, window=window, prefix=prefix)
+        vis_common = visibility(mask, Lq, Lk, window=window, prefix=prefix, sink=sink)
     for b in range(B):
         vis = vis_common if vis_common is not None else visibility(
             "document", Lq, Lk, offsets=offs[b], doc_causal=doc_causal)

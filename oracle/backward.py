@@ -31,7 +31,7 @@ __all__ = ["attention_backward", "diff_attention_backward"]
 def attention_backward(q, k, v, dout, *, scale: float | None = None, mask: str = "none",
                        window: int | None = None, prefix: int | None = None,
                        doc_offsets=None, doc_causal: bool = False,
-                       score_mod: str = "none", slopes=None, softcap: float | None = None):
+                       score_mod: str = "none", slopes=None, softcap: float | None = None, sink: int = 0):
     """(dq, dk, dv) of L = sum(dout * attention(q, k, v, ...)) in float64;
     shapes as ``oracle.attention``'s inputs."""
     q, k, v, dout = _f64(q), _f64(k), _f64(v), _f64(dout)
@@ -46,7 +46,7 @@ def attention_backward(q, k, v, dout, *, scale: float | None = None, mask: str =
     dv = np.zeros_like(v)
     for b in range(B):
         vis = visibility(mask, Lq, Lk, window=window, prefix=prefix,
-                         offsets=None if offs is None else offs[b], doc_causal=doc_causal)
+                         offsets=None if offs is None else offs[b], doc_causal=doc_causal, sink=sink)
         for h in range(Hq):
             g = h // grp
             s = scale * (q[b, h] @ k[b, g].T)
