@@ -38,7 +38,7 @@ def _strides4(t: torch.Tensor):
 
 
 def _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, *, mask="none", window=None, prefix=None, doc_offsets=None,
-                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None):
+                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None, sink=None):
     desc = _lib.new_desc()
     desc.B, desc.Hq, desc.Hkv, desc.Lq, desc.Lk, desc.d, desc.dv = B, Hq, Hkv, Lq, Lk, d, dv
     desc.scale = 0.0 if scale is None else float(scale)
@@ -47,6 +47,7 @@ def _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, *, mask="none", window=None, prefix
     desc.mask_kind = MASKS[mask]
     desc.doc_causal = 1 if doc_causal else 0
     desc.window = 0 if window is None else int(window)
+    desc.sink = 0 if sink is None else int(sink)
     desc.prefix_len = 0 if prefix is None else int(prefix)
     if score_mod not in SCORE_MODS:
         raise ValueError(f"unknown score_mod {score_mod!r}")
@@ -64,7 +65,8 @@ def _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, *, mask="none", window=None, prefix
     return desc
 
 
-def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, prefix: int | None = None,
+def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, sink: int | None = None,
+             prefix: int | None = None,
              doc_offsets: torch.Tensor | None = None, doc_causal: bool = False,
              score_mod: str = "none", alibi_slopes: torch.Tensor | None = None,
              softcap: float | None = None, scale: float | None = None,
@@ -72,7 +74,9 @@ def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, prefix: 
              return_lse: bool = True, stream=None, debug_flags: int = 0, debug_arg: int = -1,
              wait_limit_ms: int = 0):
     """fl_attn_fwd: q [B,Hq,Lq,d], k/v [B,Hkv,Lk,d] bf16 CUDA tensors (head dim
-    contiguous).  Returns (out [B,Hq,Lq,d] bf16, lse [B,Hq,Lq] fp32 or None)."""
+    contiguous).  With mask "window", the first ``sink`` keys stay visible to
+    every later query.  Returns (out [B,Hq,Lq,d] bf16, lse [B,Hq,Lq] fp32 or
+    None)."""
     for name, t in (("q", q), ("k", k), ("v", v)):
         _need(t, name, 4)
         if t.stride(-1) != 1:
@@ -91,7 +95,7 @@ def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, prefix: 
             raise ValueError("lse must be contiguous")
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
-                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale)
+                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink)
     desc.q_strides, desc.k_strides = _strides4(q), _strides4(k)
     desc.v_strides, desc.o_strides = _strides4(v), _strides4(out)
     desc.stream = _stream_ptr(stream)
@@ -270,7 +274,7 @@ def attn_decode_fwd(q, k_cache, v_cache, kv_len=None, *, causal: bool = False, s
 
 
 def attn_bwd(q, k, v, out, dout, lse, *, mask: str = "none", window: int | None = None,
-             prefix: int | None = None, doc_offsets: torch.Tensor | None = None, doc_causal: bool = False,
+             sink: int | None = None, prefix: int | None = None, doc_offsets: torch.Tensor | None = None, doc_causal: bool = False,
              score_mod: str = "none", alibi_slopes: torch.Tensor | None = None, softcap: float | None = None,
              scale: float | None = None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """fl_attn_bwd: gradients (dq, dk, dv) of attn_fwd given its out, lse and
@@ -287,7 +291,7 @@ def attn_bwd(q, k, v, out, dout, lse, *, mask: str = "none", window: int | None 
     dv = torch.empty_like(v) if dv is None else dv
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, v.shape[-1], mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
-                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale)
+                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink)
     desc.stream = _stream_ptr(stream)
     need = int(_lib.lib().fl_attn_bwd_workspace_size(ctypes.byref(desc)))
     if workspace is None:

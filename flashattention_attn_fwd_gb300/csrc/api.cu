@@ -146,10 +146,11 @@ bool encode_pair_bias(CUtensorMap* m, const float* pb, int64_t B, int64_t H, int
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, pb, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// fp32 row-major matrix [rows, cols]: boxes of one 128-column row segment.
-bool encode_rows_f32(CUtensorMap* m, const float* base, int64_t rows, int64_t cols) {
+// fp32 row-major matrix [rows, cols], rows `stride` apart: boxes of one
+// 128-column row segment (zeros past the last column).
+bool encode_rows_f32(CUtensorMap* m, const float* base, int64_t rows, int64_t cols, int64_t stride) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
-  const uint64_t str[1] = {static_cast<uint64_t>(cols * 4)};
+  const uint64_t str[1] = {static_cast<uint64_t>(stride * 4)};
   const uint32_t box[2] = {128u, 1u};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
@@ -219,6 +220,7 @@ fl_status fill_attn_params(const fl_attn_desc& d, const Strides& so, uint32_t* s
   p->scale_log2 = scale * static_cast<float>(kLog2e);
   p->mask_kind = d.mask_kind; p->doc_causal = d.doc_causal ? 1 : 0;
   p->window = d.window; p->prefix = d.prefix_len;
+  p->sink = d.sink;
   p->doc_offsets = d.doc_offsets; p->num_docs = d.num_docs;
   p->slopes = d.alibi_slopes; p->softcap = d.softcap;
   if (d.score_mod == FL_SCORE_SOFTCAP) softcap_coefficients(*p, scale, d.softcap);
@@ -245,10 +247,11 @@ fl_status fill_attn_params(const fl_attn_desc& d, const Strides& so, uint32_t* s
 // the full waves while W - R CTAs idle.  When R <= W / 2 each of those R
 // units becomes two key-split units (one per query tile, each walking its
 // key range in two halves on the two slots): the last wave then takes half
-// as long.  FL_DEBUG_KEY_SPLIT splits every unit.
+// as long.  FL_DEBUG_KEY_SPLIT splits every unit.  Not with sinks, whose key
+// range is not one run of tiles.
 void plan_key_split(const fl_attn_desc& d, int sm_count, KParams* p) {
   p->ks_count = 0;
-  if (!fl::key_split_ok(d.d, d.dv)) return;
+  if (!fl::key_split_ok(d.d, d.dv) || d.sink) return;
   const int units = p->num_units;
   if (d.debug_flags & FL_DEBUG_KEY_SPLIT) {
     if (units > 0x3fffffff) return;
@@ -279,7 +282,6 @@ fl_status attn_fwd_check(const void* q, const void* k, const void* v, void* out,
   if (d.mask_kind != FL_MASK_NONE && d.Lq != d.Lk) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_SLIDING_WINDOW && d.window < 1) return FL_ERR_INVALID_ARG;
   if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
-  if (d.sink) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_PREFIX_LM && d.prefix_len < 0) return FL_ERR_INVALID_ARG;
   if (d.mask_kind == FL_MASK_DOCUMENT && (!d.doc_offsets || d.num_docs < 1 || d.num_docs > d.Lq))
     return FL_ERR_INVALID_ARG;
@@ -415,9 +417,9 @@ fl_status fl_attn_schedule(const fl_attn_desc* desc, const int32_t* doc_offsets_
   const bool per_slot = d.dv <= 64;  // one MMA thread per slot: per-slot key ranges
   int64_t own = 0, all = 0;
   for (int u = 0; u < p.num_units; ++u) {
-    const fl::Unit U = fl::decode_unit<fl::KIND_ATTN>(p, u, per_slot);
+    const fl::Unit U = fl::decode_unit<fl::KIND_ATTN>(p, u, per_slot, fl::sink_skip_ok(d.d, d.dv));
     for (int s = 0; s < 2; ++s) {
-      const int64_t n = U.hi[s] - U.lo[s] + 1;
+      const int64_t n = fl::slot_len(U, s);
       all += n;
       // a key-split unit's second slot computes the lower half of the rows' keys
       if (U.ks || (U.valid[s] && U.row0[s] < p.Lq &&
@@ -476,8 +478,15 @@ size_t decode_workspace(const fl_attn_desc& d, int sm_count, int* n_split, int* 
 
 size_t fl_attn_bwd_workspace_size(const fl_attn_desc* desc) {
   if (!desc || desc->B < 1 || desc->Hq < 1 || desc->Lq < 1 || desc->d < 1) return 0;
-  const size_t rows = static_cast<size_t>(desc->B) * desc->Hq * desc->Lq;
-  return rows * (static_cast<size_t>(desc->d) + 2) * sizeof(float);
+  const size_t heads = static_cast<size_t>(desc->B) * desc->Hq;
+  const size_t lq_pad = (static_cast<size_t>(desc->Lq) + 3) / 4 * 4;
+  size_t n = heads * (static_cast<size_t>(desc->Lq) * desc->d + 2 * lq_pad);
+  if (desc->sink > 0 && desc->Hkv > 0 && desc->Lk > 0 && desc->window > 0 && desc->dv > 0) {
+    const fl::SinkSplit s = fl::sink_split(desc->B, desc->Hkv, desc->Lq, desc->Lk, desc->window, desc->sink);
+    n = (n + 3) / 4 * 4 + static_cast<size_t>(desc->B) * desc->Hkv * s.tiles * (s.chunks ? 1 + s.chunks : 0) * 128 *
+                              (static_cast<size_t>(desc->d) + desc->dv);
+  }
+  return n * sizeof(float);
 }
 
 namespace {
@@ -497,7 +506,6 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   if (d.mask_kind != FL_MASK_NONE && d.Lq != d.Lk) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_SLIDING_WINDOW && d.window < 1) return FL_ERR_INVALID_ARG;
   if (!sink_ok(d)) return FL_ERR_INVALID_ARG;
-  if (d.sink) return FL_ERR_UNSUPPORTED;
   if (d.mask_kind == FL_MASK_PREFIX_LM && d.prefix_len < 0) return FL_ERR_INVALID_ARG;
   if (d.mask_kind == FL_MASK_DOCUMENT && (!d.doc_offsets || d.num_docs < 1 || d.num_docs > d.Lq))
     return FL_ERR_INVALID_ARG;
@@ -510,7 +518,7 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return FL_ERR_ALIGNMENT;
   if (!aligned4(lse) || (d.mask_kind == FL_MASK_DOCUMENT && !aligned4(d.doc_offsets))) return FL_ERR_ALIGNMENT;
-  if (d.Lq % 4 != 0) return FL_ERR_UNSUPPORTED;  // 16-byte rows of the per-query vectors (TMA)
+  if (d.Lq % 4 != 0 && !d.sink) return FL_ERR_UNSUPPORTED;  // see fl_attn_bwd: padded vectors come with sinks
   const size_t need = fl_attn_bwd_workspace_size(desc);
   if (!workspace || workspace_bytes < need) return FL_ERR_INVALID_ARG;
 
@@ -521,8 +529,16 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   p.out = out; p.dout = dout; p.lse = lse; p.dq = dq; p.dk = dk; p.dv = dv;
   p.rows = static_cast<int64_t>(d.B) * d.Hq * d.Lq;
   p.dq_acc = static_cast<float*>(workspace);
+  p.Lq_pad = (d.Lq + 3) / 4 * 4;  // 16-byte rows of the per-query vectors (TMA)
+  const int64_t vec = static_cast<int64_t>(d.B) * d.Hq * p.Lq_pad;
   p.dvec = p.dq_acc + p.rows * d.d;
-  p.l2 = p.dvec + p.rows;
+  p.l2 = p.dvec + vec;
+  if (d.sink) {
+    const fl::SinkSplit ss = fl::sink_split(d.B, d.Hkv, d.Lq, d.Lk, d.window, d.sink);
+    p.sink = d.sink;
+    p.sink_tiles = ss.tiles; p.far_chunks = ss.chunks; p.far_len = ss.len;
+    p.part = p.dq_acc + (p.rows * d.d + 2 * vec + 3) / 4 * 4;
+  }
   p.slopes = d.alibi_slopes; p.doc_offsets = d.doc_offsets;
   p.status = ds->status;
   p.timeout_ns = wait_ns(d.wait_limit_ms);
@@ -535,7 +551,8 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   p.dv_accumulate = dv_accumulate ? 1 : 0;
   p.mask_kind = d.mask_kind; p.doc_causal = d.doc_causal ? 1 : 0;
   p.window = d.window; p.prefix = d.prefix_len; p.num_docs = d.num_docs;
-  if (static_cast<int64_t>(d.B) * d.Hkv * p.n_ktiles > 0x7fffffff) return FL_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d.B) * d.Hkv * (p.n_ktiles + static_cast<int64_t>(p.far_chunks) * p.sink_tiles) > 0x7fffffff)
+    return FL_ERR_UNSUPPORTED;
   CUtensorMap maps[7];
   const int bw = box_width(d.d), bwv = box_width(d.dv);
   const int64_t sl = d.d, slv = d.dv;
@@ -553,8 +570,8 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
                    static_cast<int64_t>(d.Hkv) * d.Lk * d.dv, bwv) ||
       !encode_bhlc(&maps[3], dout, d.dv, d.Lq, d.Hq, d.B, slv, static_cast<int64_t>(d.Lq) * d.dv,
                    static_cast<int64_t>(d.Hq) * d.Lq * d.dv, bwv) ||
-      !encode_rows_f32(&maps[4], p.l2, static_cast<int64_t>(d.B) * d.Hq, d.Lq) ||
-      !encode_rows_f32(&maps[5], p.dvec, static_cast<int64_t>(d.B) * d.Hq, d.Lq) ||
+      !encode_rows_f32(&maps[4], p.l2, static_cast<int64_t>(d.B) * d.Hq, d.Lq, p.Lq_pad) ||
+      !encode_rows_f32(&maps[5], p.dvec, static_cast<int64_t>(d.B) * d.Hq, d.Lq, p.Lq_pad) ||
       !encode(&maps[6], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dq_acc, qa_dims, qa_str, qa_box,
               CU_TENSOR_MAP_SWIZZLE_128B))
     return cuda_fail("cuTensorMapEncodeTiled", cudaSuccess);
@@ -770,7 +787,7 @@ fl_status fl_evoformer_gated_attn_fwd(const void* q, const void* k, const void* 
   maps[7] = maps[0];
   if (pair_bias && !encode_pair_bias(&maps[6], pair_bias, B, H, N_res))
     return cuda_fail("cuTensorMapEncodeTiled (pair bias)", cudaSuccess);
-  if (mask_bias && !encode_rows_f32(&maps[7], mask_bias, Bf, N_res))
+  if (mask_bias && !encode_rows_f32(&maps[7], mask_bias, Bf, N_res, N_res))
     return cuda_fail("cuTensorMapEncodeTiled (mask bias)", cudaSuccess);
   const int grid = static_cast<int>(units < ds->sm_count ? units : ds->sm_count);
   return launched("Evoformer kernel launch", fl::launch_evo_row(maps, p, grid, static_cast<cudaStream_t>(stream)));
@@ -827,7 +844,7 @@ fl_status fl_evoformer_col_gated_attn_fwd(const void* q, const void* k, const vo
   maps[4] = maps[1];
   maps[6] = maps[0];
   maps[7] = maps[0];
-  if (mask_bias && !encode_rows_f32(&maps[7], mask_bias, static_cast<int64_t>(B) * N_res, N_seq))
+  if (mask_bias && !encode_rows_f32(&maps[7], mask_bias, static_cast<int64_t>(B) * N_res, N_seq, N_seq))
     return cuda_fail("cuTensorMapEncodeTiled (mask bias)", cudaSuccess);
   const int grid = static_cast<int>(units < ds->sm_count ? units : ds->sm_count);
   return launched("Evoformer kernel launch", fl::launch_evo_col(d, maps, p, grid, static_cast<cudaStream_t>(stream)));

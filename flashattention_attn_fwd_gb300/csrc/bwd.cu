@@ -122,14 +122,17 @@ struct BwdLayout {
 
 // Queries that see key k form one interval [qlo, qhi] for every mask kind
 // (the mirror of row_bounds: the visible-key intervals of the rows are
-// non-decreasing in the row).
+// non-decreasing in the row; a sink is seen by every later query).
 __device__ __forceinline__ void col_bounds(const BwdParams& p, int b, int k, int& qlo, int& qhi) {
   qlo = 0;
   qhi = p.Lq - 1;
   switch (p.mask_kind) {
     case MASK_NONE: break;
     case MASK_CAUSAL: qlo = k; break;
-    case MASK_WINDOW: qlo = k; qhi = k + p.window - 1; break;
+    case MASK_WINDOW:
+      qlo = k;
+      if (k >= p.sink) qhi = p.window < p.Lq ? k + p.window - 1 : p.Lq - 1;
+      break;
     case MASK_PREFIX: qlo = k < p.prefix ? 0 : k; break;
     default: {
       const int32_t* off = p.doc_offsets + static_cast<int64_t>(b) * (p.num_docs + 1);
@@ -194,8 +197,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // this CTA: (batch b, key/value head hkv, key tile jt), key tiles in the
   // outer order so that the first tiles of every head (the longest walks
   // under causal and prefix masks) start first and the short ones end the grid
-  const int jt = blockIdx.x / (p.B * p.Hkv);
-  const int bh = blockIdx.x % (p.B * p.Hkv);
+  // (the far runs of the sink tiles come before them: each is as long as a
+  // window tile's walk)
+  const int n_far = p.far_chunks * p.sink_tiles * p.B * p.Hkv;
+  const bool far = static_cast<int>(blockIdx.x) < n_far;
+  const int unit = far ? blockIdx.x % (p.sink_tiles * p.B * p.Hkv) : blockIdx.x - n_far;
+  const int chunk = far ? blockIdx.x / (p.sink_tiles * p.B * p.Hkv) : -1;
+  const int jt = unit / (p.B * p.Hkv);
+  const int bh = unit % (p.B * p.Hkv);
   const int hkv = bh % p.Hkv, b = bh / p.Hkv;
   const int j0 = jt * 128;
   const int group = p.Hq / p.Hkv;
@@ -203,8 +212,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int qlo0, qhi0, qlo1, qhi1;
   col_bounds(p, b, j0, qlo0, qhi0);
   col_bounds(p, b, min(j0 + 127, p.Lk - 1), qlo1, qhi1);
-  const int it_lo = qlo0 / 128;
-  const int it_hi = qhi1 >= qlo0 ? qhi1 / 128 : it_lo - 1;
+  // with sinks an early key of the tile may reach further than its last one
+  qhi1 = max(qhi0, qhi1);
+  int it_lo = qlo0 / 128;
+  int it_hi = qhi1 >= qlo0 ? qhi1 / 128 : it_lo - 1;
+  const bool part = jt < p.sink_tiles && p.far_chunks > 0;  // this walk leaves partial dV, dK
+  if (part) {
+    const int f0 = far_begin(jt, p.window) + max(chunk, 0) * p.far_len;
+    if (far) {
+      it_lo = f0;
+      it_hi = min(it_hi, f0 + p.far_len - 1);
+    } else {
+      it_hi = min(it_hi, f0 - 1);
+    }
+  }
   const int nq = it_hi - it_lo + 1;
   const int n_tiles = nq > 0 ? nq * group : 0;
 
@@ -628,7 +649,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int64_t row = (static_cast<int64_t>(b) * p.Hkv + hkv) * p.Lk + kg;
       // NC columns of TMEM from col, times f, as bf16 into base's row (plus
       // what is there with acc)
-      auto write_row = [&](auto nc, uint32_t col, void* base, float f, bool acc) {
+      float* prow = part ? p.part + (((static_cast<int64_t>(bh) * p.sink_tiles + jt) * (1 + p.far_chunks) + chunk + 1) * 128 + r) * (D + DV)
+                         : nullptr;
+      auto write_row = [&](auto nc, uint32_t col, void* base, float f, bool acc, int pcol) {
         constexpr int NC = decltype(nc)::value;
         constexpr int EC = NC < 64 ? NC : 64;  // columns per TMEM read-out
         uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + row * NC);
@@ -640,7 +663,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ptx::tmem_ld_wait();
 #pragma unroll
           for (int c = 0; c < EC; c += 32) ptx::reg_fence32f(&a[c]);
-          if (kg < p.Lk) {
+          if (prow) {
+#pragma unroll
+            for (int c = 0; c < EC; c += 4)
+              *reinterpret_cast<float4*>(prow + pcol + c0 + c) =
+                  z ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
+          } else if (kg < p.Lk) {
 #pragma unroll
             for (int c = 0; c < EC; c += 8) {
               float o[8];
@@ -662,8 +690,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
       };
-      if (hf) write_row(std::integral_constant<int, D>{}, kColDK, p.dk, n_tiles > 0 ? p.scale : 1.0f, false);
-      else write_row(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, p.dv_accumulate != 0);
+      if (hf) write_row(std::integral_constant<int, D>{}, kColDK, p.dk, n_tiles > 0 ? p.scale : 1.0f, false, DV);
+      else write_row(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, p.dv_accumulate != 0, 0);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -786,9 +814,10 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < ZPL / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (sub == 0) {
-    p.dvec[row] = s * p.dout_scale;
+    const int64_t vrow = p.Lq_pad == p.Lq ? row : row / p.Lq * p.Lq_pad + row % p.Lq;
+    p.dvec[vrow] = s * p.dout_scale;
     const float l = p.lse[row];
-    p.l2[row] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+    p.l2[vrow] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
   }
 }
 
@@ -803,6 +832,29 @@ __global__ void __launch_bounds__(256) attn_bwd_post_kernel(const __grid_constan
   *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.dq) + e) =
       make_uint4(ptx::pack_bf16x2(a.x * f, a.y * f), ptx::pack_bf16x2(a.z * f, a.w * f),
                  ptx::pack_bf16x2(c.x * f, c.y * f), ptx::pack_bf16x2(c.z * f, c.w * f));
+}
+
+// dV and dK of the sink tiles' keys: the partial sums of their walks, in
+// order, rounded to bf16; four channels per thread.
+template <int D, int DV>
+__global__ void __launch_bounds__(256) attn_bwd_sink_kernel(const __grid_constant__ BwdParams p) {
+  constexpr int W4 = (D + DV) / 4;
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int c = static_cast<int>(e % W4) * 4;
+  const int64_t krow = e / W4;                 // (batch * head, key of the sink tiles)
+  const int keys = p.sink_tiles * 128;
+  const int64_t bh = krow / keys;
+  const int k = static_cast<int>(krow % keys);
+  if (bh >= static_cast<int64_t>(p.B) * p.Hkv || k >= p.Lk) return;
+  const float* src = p.part + ((bh * p.sink_tiles + k / 128) * (1 + p.far_chunks) * 128 + k % 128) * (D + DV) + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i <= p.far_chunks; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * 128 * (D + DV));
+    a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+  }
+  __nv_bfloat16* dst = c < DV ? static_cast<__nv_bfloat16*>(p.dv) + (bh * p.Lk + k) * DV + c
+                              : static_cast<__nv_bfloat16*>(p.dk) + (bh * p.Lk + k) * D + c - DV;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(a.z, a.w));
 }
 
 template <int D, int DV, int SCORE>
@@ -821,11 +873,16 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
   attn_bwd_pre_kernel<D, DV><<<rgrid, 256, 0, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kern<<<p.B * p.Hkv * p.n_ktiles, kBwdThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], p);
+  const int walks = p.B * p.Hkv * (p.n_ktiles + p.far_chunks * p.sink_tiles);
+  kern<<<walks, kBwdThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int pgrid = static_cast<int>((p.rows * D / 8 + 255) / 256);
   attn_bwd_post_kernel<D><<<pgrid, 256, 0, s>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.far_chunks == 0) return e;
+  const int64_t quads = static_cast<int64_t>(p.B) * p.Hkv * p.sink_tiles * 128 * ((D + DV) / 4);
+  attn_bwd_sink_kernel<D, DV><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -210,6 +210,9 @@ struct Unit {
   int lo[2], hi[2];  // key tiles each slot walks (inclusive, walked from hi down)
   int kv_lo, kv_hi;  // union of the slots' ranges: the tiles the load warp fetches
   int pb_b, pb_h;    // Evoformer: pair-bias tile coordinates
+  int nsink;         // window with sinks: tiles [0, nsink) follow the window's in
+                     // the ring (walked from nsink - 1 down)
+  int sk[2];         // those each slot walks: nsink, or 0 for a slot without rows
   int ks;            // key-split unit: both slots hold the same query rows,
                      // slot 0 the upper and slot 1 the lower half of the key
                      // range; their tiles alternate in the ring
@@ -226,7 +229,9 @@ __host__ __device__ __forceinline__ int32_t load_offset(const int32_t* x) {
 #endif
 }
 
-// Visible keys of query row i form one interval [lo, hi] for every mask kind.
+// Visible keys of query row i form one interval [lo, hi] for every mask kind
+// (with sinks, the window's; the row's sinks left of it, [0, min(sink, lo)),
+// are walked as tiles of their own).
 __host__ __device__ __forceinline__ void row_bounds(const KParams& p, int b, int i, int& lo, int& hi) {
   switch (p.mask_kind) {
     case MASK_NONE: lo = 0; hi = p.Lk - 1; break;
@@ -266,19 +271,33 @@ __device__ __forceinline__ Sched make_sched(const KParams& p) {
   return s;
 }
 
+// Tiles a unit fetches, and tiles slot s walks of them.
+__host__ __device__ __forceinline__ int ring_len(const Unit& U) { return U.kv_hi - U.kv_lo + 1 + U.nsink; }
+__host__ __device__ __forceinline__ int slot_len(const Unit& U, int s) { return U.hi[s] - U.lo[s] + 1 + U.sk[s]; }
 // Ring position of slot s's first own tile within a unit, and the distance
-// between its consecutive own tiles.
+// between its consecutive own tiles (past its window's last tile the slot also
+// skips the window tiles that only the other slot walks).
 __host__ __device__ __forceinline__ int ring_first(const Unit& U, int s) { return U.ks ? s : U.kv_hi - U.hi[s]; }
 __host__ __device__ __forceinline__ int ring_stride(const Unit& U) { return U.ks ? 2 : 1; }
 // Key tile the load warp fetches at ring position i of a unit.
 __host__ __device__ __forceinline__ int ring_tile(const Unit& U, int i) {
-  return U.ks ? U.hi[i & 1] - (i >> 1) : U.kv_hi - i;
+  if (U.ks) return U.hi[i & 1] - (i >> 1);
+  const int n = U.kv_hi - U.kv_lo + 1;
+  return i < n ? U.kv_hi - i : U.nsink - 1 - (i - n);
+}
+// Does slot s walk the tile at ring position i?
+__host__ __device__ __forceinline__ bool ring_used(const Unit& U, int i, int s) {
+  if (U.ks) return s == (i & 1);
+  if (i > U.kv_hi - U.kv_lo) return U.sk[s] > 0;
+  const int t = U.kv_hi - i;
+  return t >= U.lo[s] && t <= U.hi[s];
 }
 
 template <int KIND>
-__host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bool per_slot) {
+__host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bool per_slot, bool skip_ok) {
   Unit U;
   U.ks = 0;
+  U.nsink = U.sk[0] = U.sk[1] = 0;
   U.pb_b = 0;
   U.pb_h = 0;
   U.mbrow[0] = U.mbrow[1] = 0;
@@ -369,7 +388,7 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
       U.valid[s] = 1;
     }
   }
-  int lo_min = 0x7fffffff, hi_max = -1;
+  int lo_min = 0x7fffffff, hi_max = -1, sink_end = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     U.lo[s] = 0;
@@ -379,6 +398,7 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
     int lo, hi, lo2, hi2;
     row_bounds(p, U.b[s], U.row0[s], lo, hi);
     row_bounds(p, U.b[s], r1, lo2, hi2);
+    if (KIND == KIND_ATTN) sink_end = max(sink_end, min(p.sink, lo2));  // of the last row, whose window starts last
     lo = min(lo, lo2);
     hi = max(hi, hi2);
     if (hi < lo) { lo = 0; hi = 0; }  // keep >= 1 tile
@@ -390,15 +410,22 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
   if (hi_max < 0) { lo_min = 0; hi_max = 0; }
   U.kv_lo = lo_min;
   U.kv_hi = hi_max;
+  if (KIND == KIND_ATTN) U.nsink = (sink_end + kBlockN - 1) / kBlockN;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     // a slot with no rows of its own runs one tile (its results are dropped);
-    // without per-slot ranges both slots walk the union
+    // without per-slot ranges both slots walk the union.  A slot whose window
+    // starts a tile after the union's skips that tile on the way to the
+    // sinks, with the tile after the skipped one in flight: three ring stages
     if (!per_slot) {
       U.lo[s] = lo_min;
       U.hi[s] = hi_max;
+      U.sk[s] = U.nsink;
     } else if (U.hi[s] < U.lo[s]) {
       U.lo[s] = U.hi[s] = hi_max;
+    } else {
+      U.sk[s] = U.nsink;
+      if (U.nsink > 0 && !skip_ok) U.lo[s] = lo_min;
     }
   }
   return U;
@@ -411,11 +438,11 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
 // single key tile (or a padding tile) is not split: it runs as a unit whose
 // second slot is a dropped copy of the first.
 template <int KIND>
-__host__ __device__ __forceinline__ Unit decode_unit(const KParams& p, int u, bool per_slot) {
+__host__ __device__ __forceinline__ Unit decode_unit(const KParams& p, int u, bool per_slot, bool skip_ok) {
   const int ks_first = p.num_units - p.ks_count;
-  if (KIND != KIND_ATTN || !per_slot || u < ks_first) return decode_base<KIND>(p, u, per_slot);
+  if (KIND != KIND_ATTN || !per_slot || u < ks_first) return decode_base<KIND>(p, u, per_slot, skip_ok);
   const int j = u - ks_first;
-  Unit U = decode_base<KIND>(p, ks_first + (j >> 1), per_slot);
+  Unit U = decode_base<KIND>(p, ks_first + (j >> 1), per_slot, skip_ok);
   const bool s1 = (j & 1) != 0;
   // selects rather than a runtime index: U stays in registers
   const bool real = (s1 ? U.valid[1] : U.valid[0]) && (s1 ? U.row0[1] : U.row0[0]) < p.Lq &&
@@ -542,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kColO = kSepP ? 384u : 256u;
   // per-slot key ranges need one MMA thread per slot
   constexpr bool kPerSlot = kSepP;
+  static_assert(KIND != KIND_ATTN || !sink_skip_ok(D, DV) || S >= 3, "a skipped tile between two of a slot needs three ring stages");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -657,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < S; ++st) pb_tag[st] = -1;
       constexpr uint32_t kStageTx = L::NK * L::K_BYTES + L::NV * L::V_BYTES;
       for (int u = sch.first; u < sch.end; u += sch.step, ++uc) {
-        unit_at(uc) = decode_unit<KIND>(p, u, kPerSlot);
+        unit_at(uc) = decode_unit<KIND>(p, u, kPerSlot, sink_skip_ok(D, DV));
         const Unit& U = unit_at(uc);  // fields are read back from shared memory
         const uint32_t qb = uc % L::QBUF, qph = (uc / L::QBUF) & 1u;
         bool ok = true;
@@ -691,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           q_iss[qi] = static_cast<int>(qph);
         }
         if (!ok) break;
-        const int n_ring = U.kv_hi - U.kv_lo + 1;
+        const int n_ring = ring_len(U);
         for (int i = 0; i < n_ring; ++i, ++it) {
           const int t = ring_tile(U, i);
           const int st = static_cast<int>(it % S);
@@ -743,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // release the stage on behalf of a slot that does not use this tile
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (U.ks ? s != (i & 1) : (t < U.lo[s] || t > U.hi[s])) ptx::mbar_arrive(&kv_empty[st]);
+            if (!ring_used(U, i, s)) ptx::mbar_arrive(&kv_empty[st]);
           kv_count = it + 1;
         }
         if (!ok) break;
@@ -836,8 +864,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (ok && u < sch.end) {
         if (!wait_q(uc, s)) { ok = false; break; }
         const Unit& Us = unit_at(uc);
-        const int n = Us.kv_hi - Us.kv_lo + 1;
-        const int ns = Us.hi[s] - Us.lo[s] + 1;
+        const int n = ring_len(Us);
+        const int ns = slot_len(Us, s);
+        const int nw = ns - Us.sk[s];                      // window tiles, then sinks
+        const uint32_t gap = static_cast<uint32_t>(Us.lo[s] - Us.kv_lo);
         const uint32_t idx0 = first_idx(Us, it);
         if (!s_issued && !first_s(uc, idx0)) { ok = false; break; }
         s_issued = false;
@@ -845,8 +875,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int un = u + sch.step;
         const uint32_t stride = static_cast<uint32_t>(ring_stride(Us));
         for (int k = 0; k < ns && ok; ++k) {
-          const uint32_t idx = idx0 + k * stride;
-          const uint32_t idn = idx + stride;
+          const uint32_t idx = idx0 + k * stride + (k >= nw ? gap : 0u);
+          const uint32_t idn = idx + stride + (k + 1 == nw ? gap : 0u);
           const int st = static_cast<int>(idx % S);
           FL_TR(s, idx, 0);
           if (k + 1 < ns) {
@@ -904,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int u = sch.first;
       if (u < sch.end) ok = first_s(0u, 0u);
       while (u < sch.end && ok) {
-        const int n = unit_at(uc).kv_hi - unit_at(uc).kv_lo + 1;
+        const int n = ring_len(unit_at(uc));
         const uint32_t qb = uc % L::QBUF;
         for (int t = 0; t < n && ok; ++t) {
           const uint32_t itc = it + t;
@@ -1283,9 +1313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // this slot's fields of the unit, read straight from shared memory
       const Unit& Us = unit_at(uc);
       const int u_hi = Us.hi[s], u_b = Us.b[s], u_hq = Us.hq[s], u_row0 = Us.row0[s];
-      const int ns = u_hi - Us.lo[s] + 1;
+      const int ns = slot_len(Us, s), nw = ns - Us.sk[s];
       const bool turns = kPingPong && Us.lo[0] == Us.lo[1] && Us.hi[0] == Us.hi[1];
-      const int n = Us.kv_hi - Us.kv_lo + 1;
+      const int n = ring_len(Us);
       // ring index of this slot's first tile (only the Evoformer kinds read
       // the ring from here; their units are never key-split: stride 1)
       const uint32_t idx0 = it + static_cast<uint32_t>(ring_first(Us, s));
@@ -1293,6 +1323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ic = i < p.Lq ? i : p.Lq - 1;
       int lo, hi;
       row_bounds(p, u_b, ic, lo, hi);
+      // the tiles after the window's are the sinks': there the row sees [0, min(sink, lo))
+      int sink_hi = 0;
+      if (KIND == KIND_ATTN) sink_hi = min(p.sink, lo) - 1;
       float slope2 = 0.f;
       if (SCORE == SCORE_ALIBI) slope2 = __ldg(p.slopes + u_hq) * kLog2e;
       float m = -CUDART_INF_F, l = 0.f;
@@ -1311,7 +1344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       for (int k = 0; k < ns; ++k, ++scnt) {
-        const int t = u_hi - k;
+        int t = u_hi - k;
+        if (KIND == KIND_ATTN && k >= nw) {
+          t = ns - 1 - k;
+          lo = 0;
+          hi = sink_hi;
+        }
         const int j0 = t * kBlockN + c_off;   // key of this thread's first column
         const uint32_t idx = idx0 + k;
         if (kDefer) release_pending();

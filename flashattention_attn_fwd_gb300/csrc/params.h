@@ -56,6 +56,13 @@ __host__ __device__
 #endif
 constexpr bool key_split_ok(int d, int dv) { return dv <= d && d <= 64 && kRowSplit == 1; }
 
+// Window with sinks: a slot may skip a key tile that only the other slot
+// walks when the ring has three stages (as above).
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr bool sink_skip_ok(int d, int dv) { return d <= 64 && dv <= 64; }
+
 struct KParams {
   // problem (Evoformer row-wise: B is B * N_seq, Hq == Hkv == H;
   // column-wise: Hq == Hkv == H * N_res, rows are MSA rows)
@@ -76,6 +83,7 @@ struct KParams {
 
   // mask
   int mask_kind, doc_causal, window, prefix;
+  int sink;             // window: keys [0, sink) stay visible to later rows
   const int32_t* doc_offsets;
   int num_docs;
 

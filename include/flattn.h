@@ -84,7 +84,7 @@ typedef enum {
                                       (normally only the units of a last,
                                       partial wave over the SMs are), so that
                                       small problems exercise the split and
-                                      its merge */
+                                      its merge; no effect with sinks */
 
 /*
  * Problem descriptor for fl_attn_fwd / fl_diffattn_fwd.
@@ -370,7 +370,9 @@ FL_API int32_t fl_kv_append_desc_size(void);
  *                      aligned): an fp32 dq accumulator and two per-row vectors
  * desc: the forward's descriptor; d == dv in {32, 64, 128}, or d 64 with
  * dv 128 (v, dv: [B, Hkv, Lk, dv]; out, dout: [B, Hq, Lq, dv]); Lq a
- * multiple of 4, strides zero.  Masks, ALiBi and softcap as in fl_attn_fwd.
+ * multiple of 4 (any Lq with sink > 0, whose workspace pads the per-row
+ * vectors), strides zero.  Masks, ALiBi and softcap as in fl_attn_fwd.  dq is
+ * summed with fp32 atomics in no fixed order; dk and dv in a fixed one.
  */
 FL_API fl_status fl_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
                              const float* lse, void* dq, void* dk, void* dv, void* workspace,
