@@ -526,6 +526,7 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   const fl_status st = device_state(&ds);
   if (st != FL_OK) return st;
   fl::BwdParams p{};
+  p.q = q; p.k = k; p.v = v;
   p.out = out; p.dout = dout; p.lse = lse; p.dq = dq; p.dk = dk; p.dv = dv;
   p.rows = static_cast<int64_t>(d.B) * d.Hq * d.Lq;
   p.dq_acc = static_cast<float*>(workspace);

@@ -585,7 +585,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(p_full);
-      // dS^T = P^T (dP^T - D_q) (* sech^2 for softcap)
+      // dS^T = P^T (dP^T - D_q) (* sech^2 for softcap).  With sinks query 0 is
+      // the one row that sees a single key: its softmax has no gradient, and
+      // the difference's rounding must not stand in for it.
+      if (p.sink && q0 == 0) x[0] = 0.f;
       if (!__all_sync(0xffffffffu, wait_bar(dp_full, ph, ctl, 61))) { ok = false; break; }
       // the previous dQ product must have read the dS tile in shared memory
       if (n > 0 && !__all_sync(0xffffffffu, wait_bar(dq_full, ph ^ 1u, ctl, 62))) { ok = false; break; }
@@ -814,10 +817,9 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < ZPL / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (sub == 0) {
-    const int64_t vrow = p.Lq_pad == p.Lq ? row : row / p.Lq * p.Lq_pad + row % p.Lq;
-    p.dvec[vrow] = s * p.dout_scale;
+    p.dvec[row] = s * p.dout_scale;
     const float l = p.lse[row];
-    p.l2[vrow] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+    p.l2[row] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
   }
 }
 
@@ -869,9 +871,14 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   }();
   if (checked != cudaSuccess) return checked;
-  const int rgrid = static_cast<int>((p.rows + 256 / (DV / 8) - 1) / (256 / (DV / 8)));
-  attn_bwd_pre_kernel<D, DV><<<rgrid, 256, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.sink) {
+    e = launch_bwd_dot(D, DV, SCORE, p, s);
+  } else {
+    const int rgrid = static_cast<int>((p.rows + 256 / (DV / 8) - 1) / (256 / (DV / 8)));
+    attn_bwd_pre_kernel<D, DV><<<rgrid, 256, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   const int walks = p.B * p.Hkv * (p.n_ktiles + p.far_chunks * p.sink_tiles);
   kern<<<walks, kBwdThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], p);

@@ -10,6 +10,9 @@
 namespace fl {
 
 struct BwdParams {
+  const void* q;          // bf16 [B, Hq, Lq, D]
+  const void* k;          // bf16 [B, Hkv, Lk, D]
+  const void* v;          // bf16 [B, Hkv, Lk, DV]
   const void* out;        // bf16 [B, Hq, Lq, DV] forward output
   const void* dout;       // bf16 [B, Hq, Lq, DV] gradient of the output
   const float* lse;       // fp32 [B, Hq, Lq] forward log-sum-exp (natural log)
@@ -72,6 +75,10 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
   s.chunks = (far + s.len - 1) / s.len;
   return s;
 }
+
+// D, L2 and a zeroed dQ accumulator with sinks (sum P dP from the scores; the
+// plain backward's pre-kernel takes dO . O); (d, dv) as below.
+cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
 
 // (d, dv): (32, 32), (64, 64), (128, 128) or (64, 128)
 cudaError_t launch_bwd(int d, int dv, int score_mod, const CUtensorMap* maps, const BwdParams& p, cudaStream_t s);

@@ -9,11 +9,12 @@ ds = (d + 8) 2^-22 mag + 2^-20 cap + 2^-18.
 Forward.  P is rounded to bf16 (2^-8) before P V, the sum of weights carries ds
 too, and the result is rounded: (2 ds + 2^-8) sum P |v| + 2^-8 |out|.
 Backward.  dV = P^T dO with P in bf16: (ds + 2^-8) sum P |dO| + 2^-8 |dv|.
-dS = P (dP - D) (1 - tanh^2): D = sum dO O with the bf16 O that the forward
-returned, off by the forward's bound on O, eO, so by eD = sum |dO| eO; dP
-is an fp32 sum, 2^-22 (d + 8) sum |dO v|; the difference and sech^2 (fp16 pairs,
-2^-11 of 1) and dS itself (bf16, 2^-8) are rounded:
-eS = P (eD + 2^-22 (dv + 8) sum |dO v|) + (ds + 2^-8 + 2^-20) |dS| + 2^-11 P |dP - D| (softcap).
+dS = P (dP - D) (1 - tanh^2): dP is an fp32 sum, off by eP = 2^-22 (dv + 8) sum
+|dO v|; D = sum P dP is summed in fp32 from such products, off by eD = sum P
+(2 ds |dP| + eP); the difference and sech^2 (fp16 pairs, 2^-11 of 1) and dS
+itself (bf16, 2^-8) are rounded:
+eS = P (eD + eP) + (ds + 2^-8 + 2^-20) |dS| + 2^-11 P |dP - D| (softcap).
+Query 0 sees one key: its dS is zero.
 dQ and dK are scale sum eS |k|, scale sum eS |q|, rounded to bf16 (2^-8).
 5 % for products of errors and fp32 sums over rows.
 """
@@ -63,10 +64,13 @@ def _bounds(q, k, v, dout, window, sink, score_mod="none", slopes=None, softcap=
             df = dP - (P * dP).sum(1, keepdims=True)
             sech = 1.0 - np.tanh(s / softcap) ** 2 if softcap else 1.0
             dS = P * df * sech
-            eD = (np.abs(D0) * eo).sum(1, keepdims=True)
-            eS = P * (eD + 2.0 ** -22 * (dv + 8) * (np.abs(D0) @ np.abs(v[b, g]).T)) + (ds + 2.0 ** -8 + 2.0 ** -20) * np.abs(dS)
+            dS[0] = 0.0
+            eP = 2.0 ** -22 * (dv + 8) * (np.abs(D0) @ np.abs(v[b, g]).T)
+            eD = (P * (2 * ds * np.abs(dP) + eP)).sum(1, keepdims=True)
+            eS = P * (eD + eP) + (ds + 2.0 ** -8 + 2.0 ** -20) * np.abs(dS)
             if softcap:
                 eS = eS + 2.0 ** -11 * P * np.abs(df)
+            eS[0] = 0.0
             r["dq"][b, h], e["dq"][b, h] = scale * dS @ k[b, g], scale * eS @ np.abs(k[b, g])
             r["dk"][b, g] += scale * dS.T @ q[b, h]
             e["dk"][b, g] += scale * eS.T @ np.abs(q[b, h])
@@ -146,6 +150,38 @@ def test_backward(case):
     r, e = _bounds(q, k, v, dout, window, sink, **okw)
     for n, g in zip(("dq", "dk", "dv"), grads):
         _within(g, r[n], e[n], n)
+
+
+@gpu
+@pytest.mark.parametrize("L,window,sink", [(2, 1, 1), (3, 1, 1), (5, 2, 1), (40, 1, 1), (300, 2, 1), (300, 4, 4), (64, 200, 1)])
+def test_gradients_of_few_keys_keep_their_precision(L, window, sink):
+    """Rows that see few keys: dS cancels, and the gradients stay within what
+    the two bf16 roundings (dS, then the result: 2^-8 each at most) and fp32
+    allow in the 2-norm."""
+    q, k, v, dout = _inputs(2, 4, 2, L, 64, 64, seed=L)
+    kw = dict(mask="window", window=window, sink=sink)
+    qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
+    out, lse = attn_fwd(qd, kd, vd, **kw)
+    grads = attn_bwd(qd, kd, vd, out, dout.to(DEV), lse, **kw)
+    sync_status()
+    r, e = _bounds(q, k, v, dout, window, sink)
+    for n, g in zip(("dq", "dk", "dv"), grads):
+        _within(g, r[n], e[n], n)
+        assert np.linalg.norm(g.double().cpu().numpy() - r[n]) <= 2.0 ** -7 * np.linalg.norm(r[n]), n
+    assert (grads[0][:, :, 0] == 0).all()
+
+
+@gpu
+def test_one_token_has_no_gradient_but_v():
+    q, k, v, dout = _inputs(2, 4, 2, 1, 128, 128, seed=5)
+    kw = dict(mask="window", window=3, sink=2)
+    out, lse = attn_fwd(q.to(DEV), k.to(DEV), v.to(DEV), **kw)
+    dq, dk, dv = attn_bwd(q.to(DEV), k.to(DEV), v.to(DEV), out, dout.to(DEV), lse, **kw)
+    sync_status()
+    assert (dq == 0).all() and (dk == 0).all()
+    assert torch.equal(out.cpu(), v.repeat_interleave(2, 1))
+    want = dout.double().reshape(2, 2, 2, 1, 128).sum(2).numpy()
+    assert (np.abs(dv.double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20).all()
 
 
 @gpu
