@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libflattn.so")
@@ -103,6 +104,23 @@ class KvAppendDesc(ctypes.Structure):
     ]
 
 
+# The structures as one packed bytes object (native alignment): a fraction of
+# the time of setting ctypes fields one by one.
+_ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i 6i")
+_APPEND = struct.Struct("@4i 3P q 2P 4i 4P 12q P")
+_ZERO4 = (0, 0, 0, 0)
+APPEND_PACK = _APPEND.pack
+
+
+def desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, *, scale=0.0, mask_kind=0, doc_causal=0, window=0, prefix=0, score_mod=0,
+              softcap=0.0, slopes=0, doc_offsets=0, num_docs=0, q_strides=_ZERO4, k_strides=_ZERO4,
+              v_strides=_ZERO4, o_strides=_ZERO4, stream=0, debug_flags=0, debug_arg=-1, wait_limit_ms=0, sink=0):
+    """fl_attn_desc as bytes."""
+    return _ATTN.pack(B, Hq, Hkv, Lq, Lk, d, dv, scale, mask_kind, doc_causal, window, prefix, score_mod, softcap,
+                      slopes, doc_offsets, num_docs, *q_strides, *k_strides, *v_strides, *o_strides, stream,
+                      debug_flags, debug_arg, wait_limit_ms, sink, 0, 0, 0, 0, 0, 0)
+
+
 class FlattnError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -124,31 +142,32 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with __graft_entry__.build() "
                 "(the CUDA library is required; there is no CPU fallback)")
         L = ctypes.CDLL(LIB_PATH)
+        # structures are passed as pointers, ctypes.byref(...) or packed bytes
         vp, i32, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
         L.fl_attn_desc_init.argtypes = [ctypes.POINTER(AttnDesc)]
         L.fl_attn_desc_init.restype = None
-        L.fl_attn_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp]
         L.fl_attn_fwd.restype = i32
-        L.fl_attn_fwd_noalloc.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_fwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp]
         L.fl_attn_fwd_noalloc.restype = i32
-        L.fl_diffattn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, ctypes.POINTER(AttnDesc)]
+        L.fl_diffattn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp]
         L.fl_diffattn_fwd.restype = i32
         L.fl_evoformer_gated_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp]
         L.fl_evoformer_gated_attn_fwd.restype = i32
         L.fl_evoformer_col_gated_attn_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp]
         L.fl_evoformer_col_gated_attn_fwd.restype = i32
-        L.fl_attn_decode_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_decode_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
         L.fl_attn_decode_fwd.restype = i32
-        L.fl_attn_decode_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+        L.fl_attn_decode_workspace_size.argtypes = [vp]
         L.fl_attn_decode_workspace_size.restype = ctypes.c_size_t
-        L.fl_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
         L.fl_attn_bwd.restype = i32
-        L.fl_attn_bwd_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+        L.fl_attn_bwd_workspace_size.argtypes = [vp]
         L.fl_attn_bwd_workspace_size.restype = ctypes.c_size_t
         L.fl_diffattn_bwd.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp, vp,
-                                      ctypes.c_size_t, ctypes.POINTER(AttnDesc)]
+                                      ctypes.c_size_t, vp]
         L.fl_diffattn_bwd.restype = i32
-        L.fl_diffattn_bwd_workspace_size.argtypes = [ctypes.POINTER(AttnDesc)]
+        L.fl_diffattn_bwd_workspace_size.argtypes = [vp]
         L.fl_diffattn_bwd_workspace_size.restype = ctypes.c_size_t
         L.fl_sync_status.argtypes = [vp]
         L.fl_sync_status.restype = i32
@@ -160,12 +179,12 @@ def lib() -> ctypes.CDLL:
         L.fl_status_string.restype = ctypes.c_char_p
         L.fl_abi_version.argtypes = []
         L.fl_abi_version.restype = i32
-        L.fl_kv_append.argtypes = [vp, vp, ctypes.POINTER(KvCache), ctypes.POINTER(KvAppendDesc)]
+        L.fl_kv_append.argtypes = [vp, vp, vp, vp]
         L.fl_kv_append.restype = i32
-        L.fl_attn_paged_decode_fwd.argtypes = [vp, ctypes.POINTER(KvCache), vp, vp, ctypes.c_int64, vp, vp, vp,
-                                               ctypes.c_size_t, ctypes.POINTER(AttnDesc)]
+        L.fl_attn_paged_decode_fwd.argtypes = [vp, vp, vp, vp, ctypes.c_int64, vp, vp, vp,
+                                               ctypes.c_size_t, vp]
         L.fl_attn_paged_decode_fwd.restype = i32
-        L.fl_attn_paged_decode_workspace_size.argtypes = [ctypes.POINTER(AttnDesc), ctypes.POINTER(KvCache)]
+        L.fl_attn_paged_decode_workspace_size.argtypes = [vp, vp]
         L.fl_attn_paged_decode_workspace_size.restype = ctypes.c_size_t
         L.fl_kv_cache_size.argtypes = []
         L.fl_kv_cache_size.restype = i32
@@ -173,10 +192,11 @@ def lib() -> ctypes.CDLL:
         L.fl_kv_append_desc_size.restype = i32
         L.fl_attn_desc_size.argtypes = []
         L.fl_attn_desc_size.restype = i32
-        if L.fl_attn_desc_size() != ctypes.sizeof(AttnDesc):
+        if L.fl_attn_desc_size() != ctypes.sizeof(AttnDesc) or ctypes.sizeof(AttnDesc) != _ATTN.size:
             raise RuntimeError("fl_attn_desc layout mismatch between flattn.h and the binding")
         if L.fl_kv_cache_size() != ctypes.sizeof(KvCache) or \
-                L.fl_kv_append_desc_size() != ctypes.sizeof(KvAppendDesc):
+                L.fl_kv_append_desc_size() != ctypes.sizeof(KvAppendDesc) or \
+                ctypes.sizeof(KvAppendDesc) != _APPEND.size:
             raise RuntimeError("paged cache layout mismatch between flattn.h and the binding")
         _lib = L
     return _lib

@@ -17,11 +17,25 @@ from ._lib import FL_DEBUG_KEY_SPLIT, FL_DEBUG_SKIP_KV_LOAD, MASKS, SCORE_MODS, 
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
+    """A tensor from the pool of the stream that the kernels run on (memory
+    that is freed while they run is not handed out on another stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -32,37 +46,27 @@ def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):
         raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
 
 
-def _strides4(t: torch.Tensor):
-    s = t.stride()
-    return (ctypes.c_int64 * 4)(*[int(x) for x in s])
-
-
 def _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, *, mask="none", window=None, prefix=None, doc_offsets=None,
-                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None, sink=None):
-    desc = _lib.new_desc()
-    desc.B, desc.Hq, desc.Hkv, desc.Lq, desc.Lk, desc.d, desc.dv = B, Hq, Hkv, Lq, Lk, d, dv
-    desc.scale = 0.0 if scale is None else float(scale)
+                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None, sink=None, **kw):
+    """fl_attn_desc of the variant arguments (packed); `kw`: its other fields."""
     if mask not in MASKS:
         raise ValueError(f"unknown mask {mask!r}")
-    desc.mask_kind = MASKS[mask]
-    desc.doc_causal = 1 if doc_causal else 0
-    desc.window = 0 if window is None else int(window)
-    desc.sink = 0 if sink is None else int(sink)
-    desc.prefix_len = 0 if prefix is None else int(prefix)
     if score_mod not in SCORE_MODS:
         raise ValueError(f"unknown score_mod {score_mod!r}")
-    desc.score_mod = SCORE_MODS[score_mod]
-    desc.softcap = 0.0 if softcap is None else float(softcap)
     if alibi_slopes is not None:
         _need(alibi_slopes, "alibi_slopes", 1, torch.float32)
-        desc.alibi_slopes = alibi_slopes.data_ptr()
+        kw["slopes"] = alibi_slopes.data_ptr()
     if doc_offsets is not None:
         _need(doc_offsets, "doc_offsets", 2, torch.int32)
         if not doc_offsets.is_contiguous():
             raise ValueError("doc_offsets must be contiguous")
-        desc.doc_offsets = doc_offsets.data_ptr()
-        desc.num_docs = doc_offsets.shape[1] - 1
-    return desc
+        kw["doc_offsets"] = doc_offsets.data_ptr()
+        kw["num_docs"] = doc_offsets.shape[1] - 1
+    return _lib.desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, scale=0.0 if scale is None else float(scale),
+                          mask_kind=MASKS[mask], doc_causal=1 if doc_causal else 0,
+                          window=0 if window is None else int(window), sink=0 if sink is None else int(sink),
+                          prefix=0 if prefix is None else int(prefix), score_mod=SCORE_MODS[score_mod],
+                          softcap=0.0 if softcap is None else float(softcap), **kw)
 
 
 def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, sink: int | None = None,
@@ -85,23 +89,22 @@ def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, sink: in
     _, Hkv, Lk, _ = k.shape
     dv = v.shape[-1]
     if out is None:
-        out = torch.empty((B, Hq, Lq, dv), device=q.device, dtype=torch.bfloat16)
+        out = _empty_on(stream, (B, Hq, Lq, dv), torch.bfloat16, q.device)
     _need(out, "out", 4)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, Lq), device=q.device, dtype=torch.float32)
+        lse = _empty_on(stream, (B, Hq, Lq), torch.float32, q.device)
     if lse is not None:
         _need(lse, "lse", 3, torch.float32)
         if not lse.is_contiguous():
             raise ValueError("lse must be contiguous")
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
-                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink)
-    desc.q_strides, desc.k_strides = _strides4(q), _strides4(k)
-    desc.v_strides, desc.o_strides = _strides4(v), _strides4(out)
-    desc.stream = _stream_ptr(stream)
-    desc.debug_flags, desc.debug_arg, desc.wait_limit_ms = int(debug_flags), int(debug_arg), int(wait_limit_ms)
+                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink, q_strides=q.stride(),
+                         k_strides=k.stride(), v_strides=v.stride(), o_strides=out.stride(),
+                         stream=_stream_ptr(stream), debug_flags=int(debug_flags), debug_arg=int(debug_arg),
+                         wait_limit_ms=int(wait_limit_ms))
     st = _lib.lib().fl_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                0 if lse is None else lse.data_ptr(), ctypes.byref(desc))
+                                0 if lse is None else lse.data_ptr(), desc)
     _lib.check(st, "fl_attn_fwd")
     return out, lse
 
@@ -286,19 +289,19 @@ def attn_bwd(q, k, v, out, dout, lse, *, mask: str = "none", window: int | None 
     _need(lse, "lse", 3, torch.float32)
     B, Hq, Lq, d = q.shape
     _, Hkv, Lk, _ = k.shape
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty_on(stream, q.shape, q.dtype, q.device) if dq is None else dq
+    dk = _empty_on(stream, k.shape, k.dtype, k.device) if dk is None else dk
+    dv = _empty_on(stream, v.shape, v.dtype, v.device) if dv is None else dv
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, v.shape[-1], mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
-                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink)
-    desc.stream = _stream_ptr(stream)
-    need = int(_lib.lib().fl_attn_bwd_workspace_size(ctypes.byref(desc)))
+                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink,
+                         stream=_stream_ptr(stream))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), device=q.device, dtype=torch.uint8)
+        need = int(_lib.lib().fl_attn_bwd_workspace_size(desc))
+        workspace = _empty_on(stream, (max(need, 16),), torch.uint8, q.device)
     st = _lib.lib().fl_attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dout.data_ptr(),
                                 lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-                                ctypes.c_size_t(workspace.numel() * workspace.element_size()), ctypes.byref(desc))
+                                workspace.numel() * workspace.element_size(), desc)
     _lib.check(st, "fl_attn_bwd")
     return dq, dk, dv
 

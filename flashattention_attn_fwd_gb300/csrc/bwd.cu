@@ -823,25 +823,25 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
   }
 }
 
-// dQ = scale * accumulator, rounded to bf16; eight elements per thread.
-template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_post_kernel(const __grid_constant__ BwdParams p) {
-  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (e >= p.rows * D) return;
-  const float4 a = *reinterpret_cast<const float4*>(p.dq_acc + e);
-  const float4 c = *reinterpret_cast<const float4*>(p.dq_acc + e + 4);
-  const float f = p.scale;
-  *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.dq) + e) =
-      make_uint4(ptx::pack_bf16x2(a.x * f, a.y * f), ptx::pack_bf16x2(a.z * f, a.w * f),
-                 ptx::pack_bf16x2(c.x * f, c.y * f), ptx::pack_bf16x2(c.z * f, c.w * f));
-}
-
-// dV and dK of the sink tiles' keys: the partial sums of their walks, in
-// order, rounded to bf16; four channels per thread.
+// dQ = scale * accumulator, rounded to bf16; eight elements per thread of the
+// first `dq_blocks` blocks.  The blocks after them (sinks): dV and dK of the
+// sink tiles' keys, the partial sums of their walks in order, rounded to bf16;
+// four channels per thread.
 template <int D, int DV>
-__global__ void __launch_bounds__(256) attn_bwd_sink_kernel(const __grid_constant__ BwdParams p) {
+__global__ void __launch_bounds__(256) attn_bwd_post_kernel(const __grid_constant__ BwdParams p, int dq_blocks) {
+  if (static_cast<int>(blockIdx.x) < dq_blocks) {
+    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (e >= p.rows * D) return;
+    const float4 a = *reinterpret_cast<const float4*>(p.dq_acc + e);
+    const float4 c = *reinterpret_cast<const float4*>(p.dq_acc + e + 4);
+    const float f = p.scale;
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.dq) + e) =
+        make_uint4(ptx::pack_bf16x2(a.x * f, a.y * f), ptx::pack_bf16x2(a.z * f, a.w * f),
+                   ptx::pack_bf16x2(c.x * f, c.y * f), ptx::pack_bf16x2(c.z * f, c.w * f));
+    return;
+  }
   constexpr int W4 = (D + DV) / 4;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) - dq_blocks) * 256 + threadIdx.x;
   const int c = static_cast<int>(e % W4) * 4;
   const int64_t krow = e / W4;                 // (batch * head, key of the sink tiles)
   const int keys = p.sink_tiles * 128;
@@ -885,11 +885,8 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int pgrid = static_cast<int>((p.rows * D / 8 + 255) / 256);
-  attn_bwd_post_kernel<D><<<pgrid, 256, 0, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || p.far_chunks == 0) return e;
-  const int64_t quads = static_cast<int64_t>(p.B) * p.Hkv * p.sink_tiles * 128 * ((D + DV) / 4);
-  attn_bwd_sink_kernel<D, DV><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, s>>>(p);
+  const int64_t quads = p.far_chunks ? static_cast<int64_t>(p.B) * p.Hkv * p.sink_tiles * 128 * ((D + DV) / 4) : 0;
+  attn_bwd_post_kernel<D, DV><<<pgrid + static_cast<int>((quads + 255) / 256), 256, 0, s>>>(p, pgrid);
   return cudaGetLastError();
 }
 

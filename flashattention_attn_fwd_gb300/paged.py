@@ -9,38 +9,23 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import _need
+from .api import _empty_on, _need, _stream_ptr
 from ._lib import KV_FORMATS, MASKS, SCORE_MODS
 
 _SCALE_BLOCK = 16
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _call_device(device: torch.device) -> None:
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+def _check(t, name: str, ndim: int, dtype, index: int) -> None:
+    """`t` is a tensor of this rank and type on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != index:
+        _need(t, name, ndim, dtype)
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
-
-
-def _stream(stream, device: torch.device) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
-    """A tensor from the pool of the stream that the kernels run on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream),
-                                           device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _current(index: int) -> None:
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
 
 
 class PagedKVCache:
@@ -74,12 +59,14 @@ class PagedKVCache:
         for name, t in (("k", k), ("v", v), ("k_scales", k_scales), ("v_scales", v_scales)):
             if t is not None and not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-        _same_device(k.device, v=v, k_scales=k_scales, v_scales=v_scales)
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}, got {t.device}")
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.format = "e2m1" if quantised else "bf16"
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         self.num_pages, self.page_size, self.Hkv, self.d = pages, page, Hkv, d
         self.device = k.device
+        self.index = k.get_device()
         c = _lib.KvCache()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         if quantised:
@@ -88,7 +75,7 @@ class PagedKVCache:
         c.format = KV_FORMATS[self.format]
         c.num_pages, c.page_size, c.Hkv, c.d = pages, page, Hkv, d
         self._c = c
-        self._ref = ctypes.byref(c)
+        self._ref = ctypes.addressof(c)
 
     @classmethod
     def allocate(cls, num_pages: int, page_size: int, Hkv: int, d: int, *, format: str = "bf16",
@@ -104,30 +91,31 @@ class PagedKVCache:
         return cls(k, v, ks, vs, k_scale=k_scale, v_scale=v_scale)
 
 
-def _need_table(cache, kv_len, block_table) -> int:
-    """Checks the length and table arrays; returns B."""
-    _need(kv_len, "kv_len", 1, torch.int32)
-    _need(block_table, "block_table", 2, torch.int32)
-    B = kv_len.shape[0]
+def _need_table(cache, kv_len, block_table) -> tuple[int, int, int]:
+    """Checks the length and table arrays; returns (B, columns, row stride)."""
+    _check(kv_len, "kv_len", 1, _I32, cache.index)
+    _check(block_table, "block_table", 2, _I32, cache.index)
+    B, n = block_table.shape
+    if kv_len.shape[0] != B:
+        raise ValueError("block_table must have one row per sequence of kv_len")
     if not kv_len.is_contiguous():
         raise ValueError("kv_len must be contiguous")
-    if block_table.shape[0] != B:
-        raise ValueError("block_table must have one row per sequence of kv_len")
-    if block_table.stride(1) != 1 and block_table.shape[1] > 1:
+    row, col = block_table.stride()
+    if col != 1 and n > 1:
         raise ValueError("block_table must have contiguous rows")
-    return B
+    return B, n, row if B > 1 else n
 
 
-def _rows(t, name, T, H, d):
+def _rows(t, name, T, H, d, index):
     """Checks a [T, H, d] bf16 row tensor; returns its (token, head) strides."""
-    _need(t, name, 3)
-    if tuple(t.shape) != (T, H, d):
+    _check(t, name, 3, _BF16, index)
+    if t.shape != (T, H, d):
         raise ValueError(f"{name} must be {[T, H, d]}, got {list(t.shape)}")
     st, sh, sc = t.stride()
     if sc != 1:
         raise ValueError(f"{name} must have a contiguous head dimension")
     # the stride of a single token or head is never used to step
-    return (st if T > 1 else H * d, sh if H > 1 else d)
+    return (st if T > 1 else H * d), (sh if H > 1 else d)
 
 
 def kv_append(cache: PagedKVCache, k, v, kv_len, block_table, *, seq_offsets=None, rope_cos=None, rope_sin=None,
@@ -142,86 +130,76 @@ def kv_append(cache: PagedKVCache, k, v, kv_len, block_table, *, seq_offsets=Non
     rotation).  q_out (allocated when q is given without it) takes the rotated
     queries; k_out and v_out, if given, the values that the cache now holds for
     the new tokens.  Returns q_out."""
-    B = _need_table(cache, kv_len, block_table)
+    index = cache.index
+    _current(index)
+    B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
     _need(k, "k", 3)
     T, Hkv, d = k.shape
     if Hkv != cache.Hkv or d != cache.d:
         raise ValueError(f"k must be [T, {cache.Hkv}, {cache.d}] for this cache, got {list(k.shape)}")
-    a = _lib.KvAppendDesc()
-    a.T, a.B, a.max_pages = T, B, block_table.shape[1]
-    a.k_strides[:] = _rows(k, "k", T, Hkv, d)
-    a.v_strides[:] = _rows(v, "v", T, Hkv, d)
-    device = cache.device
-    _call_device(device)
+    ks, vs = _rows(k, "k", T, Hkv, d, index), _rows(v, "v", T, Hkv, d, index)
+    offsets = 0
     if seq_offsets is not None:
-        _need(seq_offsets, "seq_offsets", 1, torch.int32)
+        _check(seq_offsets, "seq_offsets", 1, _I32, index)
         if seq_offsets.shape[0] != B + 1 or not seq_offsets.is_contiguous():
             raise ValueError("seq_offsets must be contiguous [B + 1]")
-        a.seq_offsets = seq_offsets.data_ptr()
+        offsets = seq_offsets.data_ptr()
     elif T != B:
         raise ValueError("without seq_offsets every sequence has one new token")
     if (rope_cos is None) != (rope_sin is None):
         raise ValueError("rope_cos and rope_sin come together")
+    cos = sin = positions = rot = 0
     if rope_cos is not None:
-        for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-            _need(t, name, 2, torch.float32)
-            if not t.is_contiguous() or t.shape != rope_cos.shape:
-                raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
-        a.rope_cos, a.rope_sin = rope_cos.data_ptr(), rope_sin.data_ptr()
-        a.rope_positions, a.rope_dim = rope_cos.shape[0], 2 * rope_cos.shape[1]
-        a.rope_interleaved = 1 if rope_interleaved else 0
+        _check(rope_cos, "rope_cos", 2, _F32, index)
+        _check(rope_sin, "rope_sin", 2, _F32, index)
+        if rope_sin.shape != rope_cos.shape or not rope_cos.is_contiguous() or not rope_sin.is_contiguous():
+            raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
+        positions, rot = rope_cos.shape
+        cos, sin, rot = rope_cos.data_ptr(), rope_sin.data_ptr(), 2 * rot
+    Hq = qp = qop = 0
+    qs = qos = kos = vos = (0, 0)
     if q is not None:
         _need(q, "q", 3)
         Hq = q.shape[1]
         if q_out is None:
-            q_out = _empty_on(stream, (T, Hq, d), torch.bfloat16, device)
-        a.Hq = Hq
-        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-        a.q_strides[:] = _rows(q, "q", T, Hq, d)
-        a.q_out_strides[:] = _rows(q_out, "q_out", T, Hq, d)
+            q_out = _empty_on(stream, (T, Hq, d), _BF16, cache.device)
+        qs, qos = _rows(q, "q", T, Hq, d, index), _rows(q_out, "q_out", T, Hq, d, index)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
+    kop = vop = 0
     if (k_out is None) != (v_out is None):
         raise ValueError("k_out and v_out come together")
     if k_out is not None:
-        a.k_out, a.v_out = k_out.data_ptr(), v_out.data_ptr()
-        a.k_out_strides[:] = _rows(k_out, "k_out", T, Hkv, d)
-        a.v_out_strides[:] = _rows(v_out, "v_out", T, Hkv, d)
-    _same_device(device, k=k, v=v, kv_len=kv_len, block_table=block_table, seq_offsets=seq_offsets,
-                 rope_cos=rope_cos, rope_sin=rope_sin, q=q, q_out=q_out, k_out=k_out, v_out=v_out)
-    a.kv_len, a.block_table = kv_len.data_ptr(), block_table.data_ptr()
-    a.table_stride = block_table.stride(0) if B > 1 else block_table.shape[1]
-    a.stream = _stream(stream, device)
-    st = _lib.lib().fl_kv_append(k.data_ptr(), v.data_ptr(), cache._ref, ctypes.byref(a))
-    _lib.check(st, "fl_kv_append")
+        kos, vos = _rows(k_out, "k_out", T, Hkv, d, index), _rows(v_out, "v_out", T, Hkv, d, index)
+        kop, vop = k_out.data_ptr(), v_out.data_ptr()
+    desc = _lib.APPEND_PACK(T, B, Hq, max_pages, offsets, kv_len.data_ptr(), block_table.data_ptr(), table_stride,
+                            cos, sin, positions, rot, 1 if rope_interleaved else 0, 0, qp, qop, kop, vop,
+                            *qs, *ks, *vs, *qos, *kos, *vos, _stream_ptr(stream))
+    st = _lib.lib().fl_kv_append(k.data_ptr(), v.data_ptr(), cache._ref, desc)
+    if st:
+        _lib.check(st, "fl_kv_append")
     return q_out
-
-
-def _decode_desc(q, cache, block_table):
-    _need(q, "q", 4)
-    B, Hq, Lq, d = q.shape
-    desc = _lib.AttnDesc()
-    desc.B, desc.Hq, desc.Hkv, desc.Lq, desc.d, desc.dv = B, Hq, cache.Hkv, Lq, d, d
-    desc.Lk = block_table.shape[1] * cache.page_size
-    return desc
 
 
 def _strides(t, name):
     """(b, h, l, c) strides; those of axes of length 1 are never used to step."""
-    s, n = t.stride(), t.shape
-    if s[3] != 1:
+    sb, sh, sl, sc = t.stride()
+    if sc != 1:
         raise ValueError(f"{name} must have a contiguous head dimension")
-    full = (n[1] * n[2] * n[3], n[2] * n[3], n[3])
-    return [x if m > 1 else f for x, m, f in zip(s, n, full)] + [1]
+    B, H, L, d = t.shape
+    return (sb if B > 1 else H * L * d, sh if H > 1 else L * d, sl if L > 1 else d, 1)
 
 
 def attn_paged_decode_workspace_size(q, cache: PagedKVCache, block_table) -> int:
     """fl_attn_paged_decode_workspace_size: bytes of workspace that a call
     with these arguments needs."""
-    _need(block_table, "block_table", 2, torch.int32)
-    _call_device(cache.device)
-    return int(_lib.lib().fl_attn_paged_decode_workspace_size(ctypes.byref(_decode_desc(q, cache, block_table)),
-                                                              cache._ref))
+    _check(q, "q", 4, _BF16, cache.index)
+    _check(block_table, "block_table", 2, _I32, cache.index)
+    _current(cache.index)
+    B, Hq, Lq, d = q.shape
+    desc = _lib.desc_pack(B, Hq, cache.Hkv, Lq, block_table.shape[1] * cache.page_size, d, d)
+    return int(_lib.lib().fl_attn_paged_decode_workspace_size(desc, cache._ref))
 
 
 def attn_paged_decode_fwd(q, cache: PagedKVCache, kv_len, block_table, *, mask: str = "none",
@@ -233,52 +211,49 @@ def attn_paged_decode_fwd(q, cache: PagedKVCache, kv_len, block_table, *, mask: 
     sequence; mask "none", "causal" or "window" (with ``window`` and ``sink``).
     The workspace is allocated with torch when not given.  Returns (out
     [B, Hq, Lq, d] bf16, lse [B, Hq, Lq] fp32 or None)."""
-    B = _need_table(cache, kv_len, block_table)
-    desc = _decode_desc(q, cache, block_table)
-    if q.shape[0] != B:
+    index = cache.index
+    _current(index)
+    B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
+    _check(q, "q", 4, _BF16, index)
+    shape = q.shape
+    _, Hq, Lq, d = shape
+    if shape[0] != B:
         raise ValueError("q must have one entry per sequence of kv_len")
-    device = cache.device
-    _call_device(device)
     if mask not in MASKS:
         raise ValueError(f"unknown mask {mask!r}")
     if score_mod not in SCORE_MODS:
         raise ValueError(f"unknown score_mod {score_mod!r}")
-    desc.mask_kind, desc.score_mod = MASKS[mask], SCORE_MODS[score_mod]
-    desc.window = 0 if window is None else int(window)
-    desc.sink = 0 if sink is None else int(sink)
-    desc.softcap = 0.0 if softcap is None else float(softcap)
-    desc.scale = 0.0 if scale is None else float(scale)
+    slopes = 0
     if alibi_slopes is not None:
-        _need(alibi_slopes, "alibi_slopes", 1, torch.float32)
-        if alibi_slopes.shape[0] != q.shape[1] or not alibi_slopes.is_contiguous():
+        _check(alibi_slopes, "alibi_slopes", 1, _F32, index)
+        if alibi_slopes.shape[0] != Hq or not alibi_slopes.is_contiguous():
             raise ValueError("alibi_slopes must be contiguous [Hq]")
-        desc.alibi_slopes = alibi_slopes.data_ptr()
+        slopes = alibi_slopes.data_ptr()
     if out is None:
-        out = _empty_on(stream, q.shape, torch.bfloat16, device)
+        out = _empty_on(stream, shape, _BF16, cache.device)
     else:
-        _need(out, "out", 4)
-        if out.shape != q.shape:
+        _check(out, "out", 4, _BF16, index)
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
     if lse is None and return_lse:
-        lse = _empty_on(stream, q.shape[:3], torch.float32, device)
+        lse = _empty_on(stream, shape[:3], _F32, cache.device)
     elif lse is not None:
-        _need(lse, "lse", 3, torch.float32)
-        if lse.shape != q.shape[:3] or not lse.is_contiguous():
+        _check(lse, "lse", 3, _F32, index)
+        if lse.shape != shape[:3] or not lse.is_contiguous():
             raise ValueError("lse must be contiguous [B, Hq, Lq]")
-    desc.q_strides[:] = _strides(q, "q")
-    desc.o_strides[:] = _strides(out, "out")
+    desc = _lib.desc_pack(B, Hq, cache.Hkv, Lq, max_pages * cache.page_size, d, d, scale=scale or 0.0,
+                          mask_kind=MASKS[mask], window=window or 0, sink=sink or 0, score_mod=SCORE_MODS[score_mod],
+                          softcap=softcap or 0.0, slopes=slopes, q_strides=_strides(q, "q"),
+                          o_strides=_strides(out, "out"), stream=_stream_ptr(stream))
+    L = _lib.lib()
     if workspace is None:
-        n = int(_lib.lib().fl_attn_paged_decode_workspace_size(ctypes.byref(desc), cache._ref))
-        workspace = _empty_on(stream, (max(n, 16),), torch.uint8, device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _same_device(device, q=q, kv_len=kv_len, block_table=block_table, alibi_slopes=alibi_slopes, out=out, lse=lse,
-                 workspace=workspace)
-    desc.stream = _stream(stream, device)
-    st = _lib.lib().fl_attn_paged_decode_fwd(
-        q.data_ptr(), cache._ref, kv_len.data_ptr(), block_table.data_ptr(),
-        block_table.stride(0) if B > 1 else block_table.shape[1], out.data_ptr(),
-        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        ctypes.byref(desc))
-    _lib.check(st, "fl_attn_paged_decode_fwd")
+        n = int(L.fl_attn_paged_decode_workspace_size(desc, cache._ref))
+        workspace = _empty_on(stream, (max(n, 16),), torch.uint8, cache.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
+    st = L.fl_attn_paged_decode_fwd(q.data_ptr(), cache._ref, kv_len.data_ptr(), block_table.data_ptr(), table_stride,
+                                    out.data_ptr(), 0 if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel() * workspace.element_size(), desc)
+    if st:
+        _lib.check(st, "fl_attn_paged_decode_fwd")
     return out, lse

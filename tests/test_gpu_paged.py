@@ -56,7 +56,7 @@ def check_decode(out, lse, ref, fmt, q):
         gl = lse.double().cpu().numpy()
         live = np.isfinite(rl)
         assert np.array_equal(live, np.isfinite(gl)) and (gl[~live] == -np.inf).all()
-        assert (np.abs(gl - rl)[live] <= (2 * ds[..., 0] + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(live, rl, 0)))[live]).all()
+        assert (np.abs(gl[live] - rl[live]) <= (2 * ds[..., 0] + 2.0 ** -20)[live] + 2.0 ** -22 * np.abs(rl[live])).all()
 
 
 DECODE = [
