@@ -61,7 +61,7 @@ struct PagedDecodeParams {
   int64_t table_stride;
   const float* slopes;
   int B, Hq, Lq, G, M;       // M = G * Lq rows per key/value head
-  int row_blocks;            // ceil(M / rows per CTA)
+  int row_warps;             // warps that share a tile for different rows: 1, 2 or 4
   int max_pages, cap;        // cap = max_pages * page_size
   float scale_log2;          // scale * log2(e) * k_scale
   float softcap;             // in log2 units (cap * log2(e))
@@ -69,19 +69,16 @@ struct PagedDecodeParams {
   // workspace: the plan (tiles per CTA, then for every sequence the tiles of
   // one head before it) and two partial results for every CTA
   int64_t* plan;
-  float* opart;              // [grid][2][rows][d], normalised
-  float* lpart;              // [grid][2][rows], log2
+  float* opart;              // [grid][2][M][d], normalised
+  float* lpart;              // [grid][2][M], log2
   int grid;
   uint32_t* status;
 };
 
-// Rows per CTA of the decode kernel for M rows: the smallest of 8, 16, 32
-// that holds them (32 with several row blocks beyond).
-inline int paged_rows(int M) { return M <= 8 ? 8 : M <= 16 ? 16 : 32; }
+// CTAs of the decode kernel for M rows (every one resident at once), < 0 on a
+// CUDA error.
+int paged_decode_grid(int format, int d, int M, int sm_count);
 
-// CTAs of the decode kernel (every one resident at once), < 0 on a CUDA error.
-int paged_decode_grid(int format, int d, int rows, int sm_count);
-
-cudaError_t launch_paged_decode(int format, int d, int rows, const PagedDecodeParams& p, cudaStream_t s);
+cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s);
 
 }  // namespace fl

@@ -136,11 +136,11 @@ fl_status decode_desc_check(const fl_kv_cache* cache, const fl_attn_desc* desc) 
 struct WorkspaceLayout {
   size_t opart, lpart, bytes;
 };
-WorkspaceLayout workspace_layout(const fl_attn_desc& d, int rows, int grid) {
+WorkspaceLayout workspace_layout(const fl_attn_desc& d, int M, int grid) {
   WorkspaceLayout w;
   w.opart = ((2 + static_cast<size_t>(d.B)) * sizeof(int64_t) + 15) / 16 * 16;
-  w.lpart = w.opart + static_cast<size_t>(grid) * 2 * rows * d.d * sizeof(float);
-  w.bytes = w.lpart + static_cast<size_t>(grid) * 2 * rows * sizeof(float);
+  w.lpart = w.opart + static_cast<size_t>(grid) * 2 * M * d.d * sizeof(float);
+  w.bytes = w.lpart + static_cast<size_t>(grid) * 2 * M * sizeof(float);
   return w;
 }
 
@@ -187,9 +187,9 @@ size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv
   int sm_count = 0;
   uint32_t* status = nullptr;
   if (fl::device_info(&sm_count, &status) != FL_OK) return 0;
-  const int rows = fl::paged_rows(desc->Hq / desc->Hkv * desc->Lq);
-  const int grid = fl::paged_decode_grid(cache->format, cache->d, rows, sm_count);
-  return grid < 1 ? 0 : workspace_layout(*desc, rows, grid).bytes;
+  const int M = desc->Hq / desc->Hkv * desc->Lq;
+  const int grid = fl::paged_decode_grid(cache->format, cache->d, M, sm_count);
+  return grid < 1 ? 0 : workspace_layout(*desc, M, grid).bytes;
 }
 
 fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, const int32_t* kv_len,
@@ -215,17 +215,16 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   if (st != FL_OK) return st;
   p.G = d.Hq / d.Hkv;
   p.M = p.G * d.Lq;
-  const int rows = fl::paged_rows(p.M);
-  p.grid = fl::paged_decode_grid(cache->format, cache->d, rows, sm_count);
+  p.row_warps = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+  p.grid = fl::paged_decode_grid(cache->format, cache->d, p.M, sm_count);
   if (p.grid < 1) return fl::launch_result("paged decode occupancy", cudaErrorInvalidDeviceFunction);
-  const WorkspaceLayout w = workspace_layout(d, rows, p.grid);
+  const WorkspaceLayout w = workspace_layout(d, p.M, p.grid);
   if (workspace_bytes < w.bytes) return FL_ERR_INVALID_ARG;
   p.c = cache_params(*cache);
   p.q = q; p.out = out; p.lse = lse;
   p.kv_len = kv_len; p.table = block_table; p.table_stride = table_stride;
   p.slopes = d.alibi_slopes;
   p.B = d.B; p.Hq = d.Hq; p.Lq = d.Lq;
-  p.row_blocks = (p.M + rows - 1) / rows;
   p.cap = d.Lk;
   const float scale = d.scale > 0.f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.d));
   p.scale_log2 = scale * static_cast<float>(kLog2e) * cache->k_scale;
@@ -240,7 +239,7 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   p.plan = reinterpret_cast<int64_t*>(ws);
   p.opart = reinterpret_cast<float*>(ws + w.opart);
   p.lpart = reinterpret_cast<float*>(ws + w.lpart);
-  return fl::launch_result("paged decode launch", fl::launch_paged_decode(cache->format, cache->d, rows, p,
+  return fl::launch_result("paged decode launch", fl::launch_paged_decode(cache->format, cache->d, p,
                                                                          static_cast<cudaStream_t>(d.stream)));
 }
 

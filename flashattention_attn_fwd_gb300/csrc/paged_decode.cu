@@ -16,8 +16,9 @@
 // 2^(LSE_piece - LSE).  The cut depends on the lengths alone, so the result of
 // a call is the same every time.
 //
-// Inner loop.  Each warp takes every fourth tile of its CTA's piece.  Both
-// products are warp-level m16n8k16 tiles with the keys' side as the 16-row
+// Inner loop.  The CTA's four warps take the tiles of its piece in turn (with
+// more than 16 rows, groups of two or four warps take the same tile for
+// different rows; the second reading comes from L1).  Both products are warp-level m16n8k16 tiles with the keys' side as the 16-row
 // operand, so that 8 query rows fill the tile:
 //   S^T (16 keys x 8 rows)      = K (16 keys x 16 channels) Q^T
 //   O^T (16 channels x 8 rows) += V^T (16 channels x 16 keys) P^T
@@ -50,10 +51,13 @@ namespace {
 
 constexpr int kPdWarps = 4;
 constexpr int kPdThreads = 32 * kPdWarps;
-constexpr int kTileKeys = 16;
-constexpr int64_t kMinTiles = 8;  // tiles per CTA: two per warp
 constexpr float kPLog2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
+
+// 16-key halves of a tile: one for bf16 heads of 128 channels, whose 16 keys
+// fill 64 registers, else two, which share the bookkeeping of a tile.
+template <int FMT, int D>
+constexpr int kHalves = FMT == KV_BF16 && D == 128 ? 1 : 2;
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -84,53 +88,55 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return r;
 }
 
-// Tiles of one head of sequence b: `count` of them (at least one), tile i at
-// key 16 * (i < sink ? i : i + skip).
+// Tiles of KT keys of one head of sequence b: `count` of them (at least one),
+// tile i at key KT * (i < sink ? i : i + skip).
 struct SeqTiles {
   int n;        // keys in the cache
   int count, sink, skip;
 };
+template <int KT>
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeParams& p, int b) {
   SeqTiles s;
   s.n = min(max(__ldg(p.kv_len + b), 0), p.cap);
   int first = 0;
   s.sink = 0;
   if (p.window) {
-    first = max(s.n - p.Lq - p.window + 1, 0) / kTileKeys;  // of the first row's window
-    s.sink = min((p.sink + kTileKeys - 1) / kTileKeys, first);
+    first = max(s.n - p.Lq - p.window + 1, 0) / KT;  // of the first row's window
+    s.sink = min((p.sink + KT - 1) / KT, first);
   }
   s.skip = first - s.sink;
-  s.count = max((s.n + kTileKeys - 1) / kTileKeys - s.skip, 1);
+  s.count = max((s.n + KT - 1) / KT - s.skip, 1);
   return s;
 }
 
-// The raw cache bytes of one 16-key tile held by a lane.
+// The raw cache bytes of 16 keys held by a lane: two keys of K (a quarter of
+// the channels) and four of V (an eighth).
 template <int FMT, int D>
-struct TileRegs;
+struct HalfRegs;
 template <int D>
-struct TileRegs<KV_E2M1, D> {
-  static constexpr int KW = D / 32;  // words of a quarter row (K)
-  static constexpr int VW = D / 64;  // words of an eighth row (V)
-  uint32_t k[2][KW], v[4][VW], ks[2], vs;
+struct HalfRegs<KV_E2M1, D> {
+  uint32_t k[2][D / 32], v[4][D / 64], ks[2], vs;
 };
 template <int D>
-struct TileRegs<KV_BF16, D> {
-  static constexpr int KC = D / 32;  // 16-byte chunks of a quarter row
-  static constexpr int VC = D / 64;  // 16-byte chunks of an eighth row
-  uint4 k[2][KC], v[4][VC];
+struct HalfRegs<KV_BF16, D> {
+  uint4 k[2][D / 32], v[4][D / 64];
 };
 
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int KS = D / 16;        // k-steps of S, and 16-channel row tiles of O
-  constexpr int ROWS = 8 * NT;      // query rows per CTA
-  extern __shared__ float psm[];    // merge: O [warp][ROWS][D], then m, l [warp][ROWS][2]
-  __shared__ int64_t scan_sm[kPdWarps + 2];
+  constexpr int HV = kHalves<FMT, D>;
+  constexpr int KT = 16 * HV;       // keys per tile
+  constexpr int WR = 8 * NT;        // query rows per warp
+  // weights carry 2^kLift in fp16 (see above)
+  constexpr float kLift = FMT == KV_E2M1 ? 7.f : 0.f;
+  extern __shared__ float psm[];    // merge: O [warp][WR][D], then m, l [warp][WR][2]
+  __shared__ int64_t scan_sm[kPdWarps];
   __shared__ int found_sm;
   __shared__ int64_t base_sm;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int64_t HR = static_cast<int64_t>(p.c.Hkv) * p.row_blocks;  // units per sequence
+  const int64_t H = p.c.Hkv;        // units (key/value heads) per sequence
 
   // ---- the plan: tiles per CTA, and this CTA's first sequence
   auto warp_incl = [&](int64_t v) {
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   };
   int64_t total = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-    const int64_t c = b0 + tid < p.B ? seq_tiles(p, b0 + tid).count : 0;
+    const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
     const int64_t s = warp_incl(c);
     if (lane == 31) scan_sm[warp] = s;
     __syncthreads();
@@ -151,16 +157,13 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     for (int i = 0; i < kPdWarps; ++i) total += scan_sm[i];
     __syncthreads();
   }
-  const int64_t all = total * HR;
-  int64_t per = (all + gridDim.x - 1) / gridDim.x;
-  per = per < kMinTiles ? kMinTiles : (per + kPdWarps - 1) / kPdWarps * kPdWarps;
+  const int64_t all = total * H;
+  const int64_t per = ((all + gridDim.x - 1) / gridDim.x + kPdWarps - 1) / kPdWarps * kPdWarps;
   const int64_t begin = blockIdx.x * per;
   const int64_t end = begin + per < all ? begin + per : all;
   int64_t carry = 0;  // tiles of one head before the chunk's sequences
-  if (tid == 0) found_sm = -1;
-  __syncthreads();
   for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-    const int64_t c = b0 + tid < p.B ? seq_tiles(p, b0 + tid).count : 0;
+    const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
     int64_t s = warp_incl(c);
     if (lane == 31) scan_sm[warp] = s;
     __syncthreads();
@@ -172,9 +175,9 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     }
     const int64_t before = carry + s - c;
     if (blockIdx.x == 0 && b0 + tid < p.B) p.plan[2 + b0 + tid] = before;
-    if (c > 0 && before * HR <= begin && begin < (before + c) * HR) {
+    if (c > 0 && before * H <= begin && begin < (before + c) * H) {
       found_sm = b0 + tid;
-      base_sm = before * HR;
+      base_sm = before * H;
     }
     carry += chunk;
     __syncthreads();
@@ -187,55 +190,132 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   if (begin >= end) return;
   int b = found_sm;
   int64_t base = base_sm;  // line position of sequence b's first unit
-  SeqTiles sq = seq_tiles(p, b);
+  SeqTiles sq = seq_tiles<KT>(p, b);
 
-  const int page_mask = (1 << p.c.page_shift) - 1;
+  const int shift = p.c.page_shift;
+  const int page_mask = (1 << shift) - 1;
+  // warps by row group and by key group
+  const int rw = warp & (p.row_warps - 1);
+  const int kw = warp / p.row_warps, n_kw = kPdWarps / p.row_warps;
+  const int row0 = rw * WR;         // this warp's first row
+  // K keys of this lane: 4 (g / 2) + g % 2 and two further; V keys 4 t4 ..
+  const int kkey = 4 * (g >> 1) + (g & 1);
+  constexpr int KB = FMT == KV_E2M1 ? D / 2 : 2 * D;  // bytes of one key's row
+  const uint8_t* k_lane = static_cast<const uint8_t*>(p.c.k) + kkey * KB + (FMT == KV_E2M1 ? t4 * (D / 8) : 16 * t4);
+  const uint8_t* v_lane = static_cast<const uint8_t*>(p.c.v) + 4 * t4 * KB + (FMT == KV_E2M1 ? g * (D / 16) : 16 * g);
+  const uint8_t* ks_lane = FMT == KV_E2M1 ? p.c.ks + kkey * (D / 16) + t4 * (D / 64) : nullptr;
+  const uint8_t* vs_lane = FMT == KV_E2M1 ? p.c.vs + ((D == 128 ? g : g >> 1) << shift) + 4 * t4 : nullptr;
+
   for (int64_t cur = begin; cur < end;) {
     // ---- the unit at `cur`
-    while (cur >= base + sq.count * HR) {
-      base += sq.count * HR;
-      sq = seq_tiles(p, ++b);
+    while (cur >= base + sq.count * H) {
+      base += sq.count * H;
+      sq = seq_tiles<KT>(p, ++b);
     }
     const int64_t local = cur - base;
-    const int unit = static_cast<int>(local / sq.count);
-    const int t0 = static_cast<int>(local - static_cast<int64_t>(unit) * sq.count);
+    const int hkv = static_cast<int>(local / sq.count);
+    const int t0 = static_cast<int>(local - static_cast<int64_t>(hkv) * sq.count);
     const int64_t room = t0 + (end - cur);
     const int t1 = room < sq.count ? static_cast<int>(room) : sq.count;
-    const int hkv = unit / p.row_blocks, rb = unit % p.row_blocks;
-    const int row0 = rb * ROWS;
-    const int nrows = min(ROWS, p.M - row0);
     const bool whole = t0 == 0 && t1 == sq.count;
     const int slot = cur == begin ? 0 : 1;
+
+    // ---- pages and bytes of the first tile
+    const int32_t* trow = p.table + b * p.table_stride;
+    auto key_of = [&](int t) { return KT * (t < sq.sink ? t : t + sq.skip); };
+    // page of key j; -1: none (past the cache, or out of the pool)
+    auto page_of = [&](int t, int hf) {
+      const int j = key_of(t) + 16 * hf;
+      return t < t1 && j < sq.n ? __ldg(trow + (j >> shift)) : -1;
+    };
+    // token index of a half's first key in the pool (page 0 stands in for none)
+    auto token_of = [&](int t, int hf, int page) {
+      const int pg = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages) ? page : 0;
+      return ((static_cast<int64_t>(pg) * p.c.Hkv + hkv) << shift) + ((key_of(t) + 16 * hf) & page_mask);
+    };
+    HalfRegs<FMT, D> r[HV];
+    auto load_k = [&](HalfRegs<FMT, D>& x, int64_t tok) {
+      const uint8_t* kp = k_lane + tok * KB;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (FMT == KV_E2M1) {
+          const uint8_t* sp = ks_lane + tok * (D / 16);
+          if constexpr (D == 128) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(kp + 2 * i * KB));
+            x.k[i][0] = w.x; x.k[i][1] = w.y; x.k[i][2] = w.z; x.k[i][3] = w.w;
+            x.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(sp + 2 * i * (D / 16)));
+          } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(kp + 2 * i * KB));
+            x.k[i][0] = w.x; x.k[i][1] = w.y;
+            x.ks[i] = __ldg(sp + 2 * i * (D / 16));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) x.k[i][j] = __ldg(reinterpret_cast<const uint4*>(kp + 2 * i * KB + 64 * j));
+        }
+      }
+    };
+    auto load_v = [&](HalfRegs<FMT, D>& x, int64_t tok) {
+      const uint8_t* vp = v_lane + tok * KB;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (FMT == KV_E2M1) {
+          if constexpr (D == 128) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(vp + i * KB));
+            x.v[i][0] = w.x; x.v[i][1] = w.y;
+          } else {
+            x.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(vp + i * KB));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) x.v[i][j] = __ldg(reinterpret_cast<const uint4*>(vp + i * KB + 128 * j));
+        }
+      }
+      if constexpr (FMT == KV_E2M1) {
+        const int off = static_cast<int>(tok) & page_mask;  // runs are page-aligned
+        x.vs = __ldg(reinterpret_cast<const uint32_t*>(vs_lane + (tok - off) * (D / 16) + off));
+      }
+    };
+    int t = t0 + kw;
+    int page[HV], page_n[HV];
+#pragma unroll
+    for (int hf = 0; hf < HV; ++hf) page[hf] = page_of(t, hf);
+#pragma unroll
+    for (int hf = 0; hf < HV; ++hf) page_n[hf] = page_of(t + n_kw, hf);
 
     // ---- queries: row g of every 8-row tile, channels in the order of K's
     // fragments; fp16 rows scaled to magnitude [1, 2) by a power of two
     uint32_t qf[NT][KS][2];
     float sc[NT][2];   // factor of S (log2 units) of rows 2 t4, 2 t4 + 1
     int pos[NT][2];    // their positions
-    float slope[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + 8 * nt + g;
-      const bool rv = r < p.M;
-      const int hq = hkv * p.G + (rv ? r : 0) / p.Lq, i = (rv ? r : 0) % p.Lq;
+      const int rr = row0 + 8 * nt + g;
+      const bool rv = rr < p.M;
+      const int hq = hkv * p.G + (rv ? rr : 0) / p.Lq, i = (rv ? rr : 0) % p.Lq;
       const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_b + hq * p.q_h + i * p.q_l;
+      // channels: bf16 32 j + 8 t4 .., 4-bit t4 d / 4 + 8 j ..
+#pragma unroll
+      for (int j = 0; j < KS / 2; ++j) {
+        const uint4 w = rv ? __ldg(reinterpret_cast<const uint4*>(qr + (FMT == KV_E2M1 ? t4 * (D / 4) + 8 * j : 32 * j + 8 * t4)))
+                           : make_uint4(0u, 0u, 0u, 0u);
+        qf[nt][2 * j][0] = w.x; qf[nt][2 * j][1] = w.y;
+        qf[nt][2 * j + 1][0] = w.z; qf[nt][2 * j + 1][1] = w.w;
+      }
+    }
+    if (t < t1) {
+#pragma unroll
+      for (int hf = 0; hf < HV; ++hf) {
+        const int64_t tok = token_of(t, hf, page[hf]);
+        load_k(r[hf], tok);
+        load_v(r[hf], tok);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
       float undo = 1.f;
-      if (FMT == KV_BF16) {
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-          const uint4 w = rv ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * j + 8 * t4)) : make_uint4(0u, 0u, 0u, 0u);
-          qf[nt][2 * j][0] = w.x; qf[nt][2 * j][1] = w.y;
-          qf[nt][2 * j + 1][0] = w.z; qf[nt][2 * j + 1][1] = w.w;
-        }
-      } else {
-        // a lane's channels are t4 * d / 4 + 4 kk + {0, 1}, {2, 3}
+      if (FMT == KV_E2M1) {
         float a = 0.f;
-#pragma unroll
-        for (int j = 0; j < KS / 2; ++j) {
-          const uint4 w = rv ? __ldg(reinterpret_cast<const uint4*>(qr + t4 * (D / 4) + 8 * j)) : make_uint4(0u, 0u, 0u, 0u);
-          qf[nt][2 * j][0] = w.x; qf[nt][2 * j][1] = w.y;
-          qf[nt][2 * j + 1][0] = w.z; qf[nt][2 * j + 1][1] = w.w;
-        }
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
@@ -257,242 +337,249 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         sc[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, undo, 4 * (2 * t4 + e));
         const int rc = row0 + 8 * nt + 2 * t4 + e;
         pos[nt][e] = sq.n - p.Lq + (rc < p.M ? rc % p.Lq : 0);
-        slope[nt][e] = p.score_mod == 1 && rc < p.M ? __ldg(p.slopes + hkv * p.G + rc / p.Lq) * kPLog2e : 0.f;
       }
     }
     const int pos_lo = sq.n - p.Lq, pos_hi = sq.n - 1;
+    // first keys of tiles that every row sees whole: at most full_hi, and from
+    // full_lo on or within the sinks
+    const int full_hi = (p.causal ? pos_lo + 1 : sq.n) - KT;
+    const int full_lo = p.window ? pos_hi - p.window + 1 : 0;
+    const int full_sink = p.window ? p.sink - KT : -1;
 
-    float o[NT][KS][4], m[NT][2], l[NT][2];
+    // online softmax: reference maximum m, the offset of the exponent
+    // (2^kLift in fp16) and the bound beyond which m moves
+    float o[NT][KS][4], m[NT][2], l[NT][2], off[NT][2], bound[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -CUDART_INF_F;
-      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = bound[nt][e] = -CUDART_INF_F;
+        l[nt][e] = off[nt][e] = 0.f;
+      }
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
     }
 
-    // ---- tiles: page ids two ahead, bytes one ahead of the products
-    const int32_t* trow = p.table + b * p.table_stride;
-    auto key_of = [&](int t) { return kTileKeys * (t < sq.sink ? t : t + sq.skip); };
-    auto page_of = [&](int t) {
+    for (; t < t1; t += n_kw) {
       const int key0 = key_of(t);
-      return t < t1 && key0 < sq.n ? __ldg(trow + (key0 >> p.c.page_shift)) : -1;
-    };
-    // K keys of this lane: 4 (g / 2) + g % 2 and two further; V keys 4 t4 ..
-    const int kkey = 4 * (g >> 1) + (g & 1);
-    auto load = [&](TileRegs<FMT, D>& r, int t, int page) {
-      const bool ok = page >= 0 && page < p.c.num_pages;
-      const int off = key_of(t) & page_mask;
-      const int64_t run = (static_cast<int64_t>(page) * p.c.Hkv + hkv) << p.c.page_shift;  // tokens before
-      if constexpr (FMT == KV_E2M1) {
-        const uint8_t* kp = static_cast<const uint8_t*>(p.c.k) + (run + off + kkey) * (D / 2) + t4 * (D / 8);
-        const uint8_t* vp = static_cast<const uint8_t*>(p.c.v) + (run + off + 4 * t4) * (D / 2) + g * (D / 16);
-        const uint8_t* ksp = p.c.ks + (run + off + kkey) * (D / 16) + t4 * (D / 64);
-        const uint8_t* vsp = p.c.vs + run * (D / 16) + (static_cast<int64_t>(D == 128 ? g : g >> 1) << p.c.page_shift) + off + 4 * t4;
+      // page ids two tiles ahead; K a tile ahead once S is done, V once O is
+      int page_nn[HV];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if constexpr (D == 128) {
-            const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(kp + 2 * i * (D / 2))) : make_uint4(0u, 0u, 0u, 0u);
-            r.k[i][0] = w.x; r.k[i][1] = w.y; r.k[i][2] = w.z; r.k[i][3] = w.w;
-            r.ks[i] = ok ? __ldg(reinterpret_cast<const uint16_t*>(ksp + 2 * i * (D / 16))) : 0u;
-          } else {
-            const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(kp + 2 * i * (D / 2))) : make_uint2(0u, 0u);
-            r.k[i][0] = w.x; r.k[i][1] = w.y;
-            r.ks[i] = ok ? __ldg(ksp + 2 * i * (D / 16)) : 0u;
-          }
-        }
+      for (int hf = 0; hf < HV; ++hf) page_nn[hf] = page_of(t + 2 * n_kw, hf);
+      bool pages_ok = true;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (D == 128) {
-            const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(vp + i * (D / 2))) : make_uint2(0u, 0u);
-            r.v[i][0] = w.x; r.v[i][1] = w.y;
-          } else {
-            r.v[i][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(vp + i * (D / 2))) : 0u;
-          }
-        }
-        r.vs = ok ? __ldg(reinterpret_cast<const uint32_t*>(vsp)) : 0u;
-      } else {
-        const uint4* kp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.c.k) + (run + off + kkey) * D + 8 * t4);
-        const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.c.v) + (run + off + 4 * t4) * D + 8 * g);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) r.k[i][j] = ok ? __ldg(kp + 2 * i * (D / 8) + 4 * j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) r.v[i][j] = ok ? __ldg(vp + i * (D / 8) + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    int t = t0 + warp;
-    int page = page_of(t), page_n = page_of(t + kPdWarps);
-    TileRegs<FMT, D> cur_r, nxt_r;
-    load(cur_r, t, page);
-    for (; t < t1; t += kPdWarps) {
-      const int page_nn = page_of(t + 2 * kPdWarps);
-      load(nxt_r, t + kPdWarps, page_n);
-      const int key0 = key_of(t);
-      const bool page_ok = page >= 0 && page < p.c.num_pages;
-      if (!page_ok && key0 < sq.n && lane == 0) atomicOr(p.status, 2u);
-      // every key of the tile visible to every row?
-      const bool full = page_ok && key0 + kTileKeys <= sq.n && (!p.causal || key0 + kTileKeys - 1 <= pos_lo) &&
-                        (!p.window || key0 > pos_hi - p.window || key0 + kTileKeys <= p.sink);
-      // keys that no row sees may hold anything: their V must not reach the
-      // product (0 * NaN)
-      auto any_sees = [&](int j) {
-        return page_ok && j < sq.n && (!p.window || j > pos_lo - p.window || j < p.sink);
-      };
+      for (int hf = 0; hf < HV; ++hf) pages_ok = pages_ok && static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
+      const bool full = pages_ok && key0 <= full_hi && (key0 >= full_lo || key0 <= full_sink);
       // ---- S^T = K Q^T
-      float s[NT][4];
+      float s[HV][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-      if constexpr (FMT == KV_E2M1) {
-        uint32_t ksc[2][2];  // [key][block of the lane's channels] fp16 pairs
+      for (int hf = 0; hf < HV; ++hf)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t h2 = cvt4::from_e4m3x2(cur_r.ks[i]);
-          ksc[i][0] = __byte_perm(h2, 0u, 0x1010);
-          ksc[i][1] = D == 128 ? __byte_perm(h2, 0u, 0x3232) : ksc[i][0];
-        }
+        for (int nt = 0; nt < NT; ++nt) s[hf][nt][0] = s[hf][nt][1] = s[hf][nt][2] = s[hf][nt][3] = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          uint32_t ha[4], hb[4];
-          cvt4::from_e2m1x8(cur_r.k[0][w], ha);
-          cvt4::from_e2m1x8(cur_r.k[1][w], hb);
-          const int bl = D == 128 ? w >> 1 : 0;
+      for (int hf = 0; hf < HV; ++hf) {
+        const HalfRegs<FMT, D>& x = r[hf];
+        if constexpr (FMT == KV_E2M1) {
+          uint32_t ksc[2][2];  // [key][block of the lane's channels] fp16 pairs
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            ha[e] = cvt4::hmul2(ha[e], ksc[0][bl]);
-            hb[e] = cvt4::hmul2(hb[e], ksc[1][bl]);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t h2 = cvt4::from_e4m3x2(x.ks[i]);
+            ksc[i][0] = __byte_perm(h2, 0u, 0x1010);
+            ksc[i][1] = D == 128 ? __byte_perm(h2, 0u, 0x3232) : ksc[i][0];
           }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {ha[2 * h], hb[2 * h], ha[2 * h + 1], hb[2 * h + 1]};
+          for (int w = 0; w < D / 32; ++w) {
+            uint32_t ha[4], hb[4];
+            cvt4::from_e2m1x8(x.k[0][w], ha);
+            cvt4::from_e2m1x8(x.k[1][w], hb);
+            const int bl = D == 128 ? w >> 1 : 0;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(s[nt], a, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
+            for (int e = 0; e < 4; ++e) {
+              ha[e] = cvt4::hmul2(ha[e], ksc[0][bl]);
+              hb[e] = cvt4::hmul2(hb[e], ksc[1][bl]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {ha[2 * h], hb[2 * h], ha[2 * h + 1], hb[2 * h + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(s[hf][nt], a, qf[nt][2 * w + h][0], qf[nt][2 * w + h][1]);
+            }
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint32_t a0[4] = {cur_r.k[0][j].x, cur_r.k[1][j].x, cur_r.k[0][j].y, cur_r.k[1][j].y};
-          const uint32_t a1[4] = {cur_r.k[0][j].z, cur_r.k[1][j].z, cur_r.k[0][j].w, cur_r.k[1][j].w};
+          for (int j = 0; j < D / 32; ++j) {
+            const uint32_t a0[4] = {x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y};
+            const uint32_t a1[4] = {x.k[0][j].z, x.k[1][j].z, x.k[0][j].w, x.k[1][j].w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma16816<FMT>(s[nt], a0, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-            mma16816<FMT>(s[nt], a1, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816<FMT>(s[hf][nt], a0, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+              mma16816<FMT>(s[hf][nt], a1, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+            }
           }
         }
       }
-      // ---- scores (log2 units): key kkey rows 2 t4, +1; key kkey + 2 the same
-      uint32_t pb[NT][2];
+      const bool more = t + n_kw < t1;
+      int64_t tok_n[HV];
+      if (more) {
+#pragma unroll
+        for (int hf = 0; hf < HV; ++hf) {
+          tok_n[hf] = token_of(t + n_kw, hf, page_n[hf]);
+          load_k(r[hf], tok_n[hf]);
+        }
+      }
+      // ---- scores (log2 units) of key kkey (e < 2) and kkey + 2, rows 2 t4, +1
+      uint32_t pb[HV][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+        float x[HV][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = s[nt][e] * sc[nt][e & 1];
-          const int j = key0 + kkey + (e & 2);
-          if (p.score_mod == 2) x[e] = p.softcap * tanhf(x[e] / p.softcap);
-          else if (p.score_mod == 1) x[e] = fmaf(slope[nt][e & 1], static_cast<float>(j - pos[nt][e & 1]), x[e]);
-          if (!full) {
-            const int ps = pos[nt][e & 1];
-            const bool vis = page_ok && j < sq.n && (!p.causal || j <= ps) && (!p.window || j > ps - p.window || j < p.sink);
-            x[e] = vis ? x[e] : -CUDART_INF_F;
+        for (int hf = 0; hf < HV; ++hf)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[hf][e] = s[hf][nt][e] * sc[nt][e & 1];
+        if (p.score_mod != 0) {
+          const int rc = row0 + 8 * nt + 2 * t4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float slope = p.score_mod == 1 && rc + (e & 1) < p.M
+                                    ? __ldg(p.slopes + hkv * p.G + (rc + (e & 1)) / p.Lq) * kPLog2e : 0.f;
+#pragma unroll
+            for (int hf = 0; hf < HV; ++hf) {
+              if (p.score_mod == 2) x[hf][e] = p.softcap * tanhf(x[hf][e] / p.softcap);
+              else x[hf][e] = fmaf(slope, static_cast<float>(key0 + 16 * hf + kkey + (e & 2) - pos[nt][e & 1]), x[hf][e]);
+            }
+          }
+        }
+        if (!full) {
+#pragma unroll
+          for (int hf = 0; hf < HV; ++hf) {
+            const bool pok = static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = key0 + 16 * hf + kkey + (e & 2), ps = pos[nt][e & 1];
+              const bool vis = pok && j < sq.n && (!p.causal || j <= ps) && (!p.window || j > ps - p.window || j < p.sink);
+              x[hf][e] = vis ? x[hf][e] : -CUDART_INF_F;
+            }
           }
         }
         // the reference maximum moves only by more than 2^8 (O rescaled then)
-        const float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
-        if (__any_sync(0xffffffffu, m0 > m[nt][0] + 8.f || m1 > m[nt][1] + 8.f)) {
-          float mx[2] = {m0, m1};
+        float mx[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(x[0][e], x[0][2 + e]);
+#pragma unroll
+          for (int hf = 1; hf < HV; ++hf) mx[e] = ptx::max3(mx[e], x[hf][e], x[hf][2 + e]);
+        }
+        if (__any_sync(0xffffffffu, mx[0] > bound[nt][0] || mx[1] > bound[nt][1])) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
             const float mn = fmaxf(m[nt][e], mx[e]);
-            const float alpha = mn == -CUDART_INF_F ? 1.f : ptx::ex2(m[nt][e] - mn);
-            m[nt][e] = mn;
-            l[nt][e] *= alpha;
+            if (mn != -CUDART_INF_F) {
+              const float alpha = ptx::ex2(m[nt][e] - mn);
+              m[nt][e] = mn;
+              off[nt][e] = kLift - mn;
+              bound[nt][e] = mn + 8.f;
+              l[nt][e] *= alpha;
 #pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-              o[nt][mt][e] *= alpha;
-              o[nt][mt][2 + e] *= alpha;
+              for (int mt = 0; mt < KS; ++mt) {
+                o[nt][mt][e] *= alpha;
+                o[nt][mt][2 + e] *= alpha;
+              }
             }
           }
         }
-        constexpr float kLift = FMT == KV_E2M1 ? 7.f : 0.f;
-        const float r0 = m[nt][0] == -CUDART_INF_F ? 0.f : kLift - m[nt][0];
-        const float r1 = m[nt][1] == -CUDART_INF_F ? 0.f : kLift - m[nt][1];
-        x[0] = ptx::ex2(x[0] + r0);
-        x[1] = ptx::ex2(x[1] + r1);
-        x[2] = ptx::ex2(x[2] + r0);
-        x[3] = ptx::ex2(x[3] + r1);
-        l[nt][0] += x[0] + x[2];
-        l[nt][1] += x[1] + x[3];
-        if (FMT == KV_E2M1) {
-          pb[nt][0] = transpose8(pack_f16(x[0], x[1]));
-          pb[nt][1] = transpose8(pack_f16(x[2], x[3]));
-        } else {
-          pb[nt][0] = transpose8(ptx::pack_bf16x2(x[0], x[1]));
-          pb[nt][1] = transpose8(ptx::pack_bf16x2(x[2], x[3]));
+#pragma unroll
+        for (int hf = 0; hf < HV; ++hf) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[hf][e] = ptx::ex2(x[hf][e] + off[nt][e & 1]);
+            l[nt][e & 1] += x[hf][e];
+          }
+          if (FMT == KV_E2M1) {
+            pb[hf][nt][0] = transpose8(pack_f16(x[hf][0], x[hf][1]));
+            pb[hf][nt][1] = transpose8(pack_f16(x[hf][2], x[hf][3]));
+          } else {
+            pb[hf][nt][0] = transpose8(ptx::pack_bf16x2(x[hf][0], x[hf][1]));
+            pb[hf][nt][1] = transpose8(ptx::pack_bf16x2(x[hf][2], x[hf][3]));
+          }
+        }
+      }
+      if (!full) {
+        // keys that no row sees may hold anything: their V must not reach the
+        // product (0 * NaN)
+#pragma unroll
+        for (int hf = 0; hf < HV; ++hf) {
+          const bool pok = static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
+          const int h0 = key0 + 16 * hf;
+          const bool seen = h0 < sq.n && (!p.window || h0 + 15 > pos_lo - p.window || h0 < p.sink);
+          if (!pok && seen && lane == 0) atomicOr(p.status, 2u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = key0 + 16 * hf + 4 * t4 + i;
+            if (pok && j < sq.n && (!p.window || j > pos_lo - p.window || j < p.sink)) continue;
+            if constexpr (FMT == KV_E2M1) {
+              r[hf].vs &= ~(0xffu << (8 * i));
+            } else {
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c) r[hf].v[i][c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
         }
       }
       // ---- O^T += V^T P^T
-      if constexpr (FMT == KV_E2M1) {
-        uint32_t vs = cur_r.vs;
-        if (!full) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!any_sees(key0 + 4 * t4 + i)) vs &= ~(0xffu << (8 * i));
-        }
-        const uint32_t s01 = cvt4::from_e4m3x2(vs & 0xffffu), s23 = cvt4::from_e4m3x2(vs >> 16);
+      for (int hf = 0; hf < HV; ++hf) {
+        const HalfRegs<FMT, D>& x = r[hf];
+        if constexpr (FMT == KV_E2M1) {
+          const uint32_t s01 = cvt4::from_e4m3x2(x.vs & 0xffffu), s23 = cvt4::from_e4m3x2(x.vs >> 16);
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) {
-          // nibble pairs (key 0, key 1) of even and of odd channels
-          const uint32_t v0 = cur_r.v[0][w], v1 = cur_r.v[1][w], v2 = cur_r.v[2][w], v3 = cur_r.v[3][w];
-          uint32_t e01[4], o01[4], e23[4], o23[4];
-          cvt4::from_e2m1x8((v0 & 0x0f0f0f0fu) | ((v1 << 4) & 0xf0f0f0f0u), e01);
-          cvt4::from_e2m1x8(((v0 >> 4) & 0x0f0f0f0fu) | (v1 & 0xf0f0f0f0u), o01);
-          cvt4::from_e2m1x8((v2 & 0x0f0f0f0fu) | ((v3 << 4) & 0xf0f0f0f0u), e23);
-          cvt4::from_e2m1x8(((v2 >> 4) & 0x0f0f0f0fu) | (v3 & 0xf0f0f0f0u), o23);
+          for (int w = 0; w < D / 64; ++w) {
+            // nibble pairs (key 0, key 1) of even and of odd channels
+            const uint32_t v0 = x.v[0][w], v1 = x.v[1][w], v2 = x.v[2][w], v3 = x.v[3][w];
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            cvt4::from_e2m1x8((v0 & 0x0f0f0f0fu) | ((v1 << 4) & 0xf0f0f0f0u), e01);
+            cvt4::from_e2m1x8(((v0 >> 4) & 0x0f0f0f0fu) | (v1 & 0xf0f0f0f0u), o01);
+            cvt4::from_e2m1x8((v2 & 0x0f0f0f0fu) | ((v3 << 4) & 0xf0f0f0f0u), e23);
+            cvt4::from_e2m1x8(((v2 >> 4) & 0x0f0f0f0fu) | (v3 & 0xf0f0f0f0u), o23);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a[4] = {cvt4::hmul2(e01[i], s01), cvt4::hmul2(o01[i], s01), cvt4::hmul2(e23[i], s23),
-                                   cvt4::hmul2(o23[i], s23)};
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a[4] = {cvt4::hmul2(e01[i], s01), cvt4::hmul2(o01[i], s01), cvt4::hmul2(e23[i], s23),
+                                     cvt4::hmul2(o23[i], s23)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(o[nt][4 * w + i], a, pb[nt][0], pb[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(o[nt][4 * w + i], a, pb[hf][nt][0], pb[hf][nt][1]);
+            }
           }
-        }
-      } else {
-        if (!full) {
+        } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!any_sees(key0 + 4 * t4 + i))
+          for (int j = 0; j < D / 64; ++j) {
+            const uint32_t v0[4] = {x.v[0][j].x, x.v[0][j].y, x.v[0][j].z, x.v[0][j].w};
+            const uint32_t v1[4] = {x.v[1][j].x, x.v[1][j].y, x.v[1][j].z, x.v[1][j].w};
+            const uint32_t v2[4] = {x.v[2][j].x, x.v[2][j].y, x.v[2][j].z, x.v[2][j].w};
+            const uint32_t v3[4] = {x.v[3][j].x, x.v[3][j].y, x.v[3][j].z, x.v[3][j].w};
 #pragma unroll
-              for (int j = 0; j < D / 64; ++j) cur_r.v[i][j] = make_uint4(0u, 0u, 0u, 0u);
-        }
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
+                                     __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const uint32_t v0[4] = {cur_r.v[0][j].x, cur_r.v[0][j].y, cur_r.v[0][j].z, cur_r.v[0][j].w};
-          const uint32_t v1[4] = {cur_r.v[1][j].x, cur_r.v[1][j].y, cur_r.v[1][j].z, cur_r.v[1][j].w};
-          const uint32_t v2[4] = {cur_r.v[2][j].x, cur_r.v[2][j].y, cur_r.v[2][j].z, cur_r.v[2][j].w};
-          const uint32_t v3[4] = {cur_r.v[3][j].x, cur_r.v[3][j].y, cur_r.v[3][j].z, cur_r.v[3][j].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
-                                   __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(o[nt][4 * j + i], a, pb[nt][0], pb[nt][1]);
+              for (int nt = 0; nt < NT; ++nt) mma16816<FMT>(o[nt][4 * j + i], a, pb[hf][nt][0], pb[hf][nt][1]);
+            }
           }
         }
       }
-      cur_r = nxt_r;
-      page = page_n;
-      page_n = page_nn;
+      if (more) {
+#pragma unroll
+        for (int hf = 0; hf < HV; ++hf) load_v(r[hf], tok_n[hf]);
+      }
+#pragma unroll
+      for (int hf = 0; hf < HV; ++hf) {
+        page[hf] = page_n[hf];
+        page_n[hf] = page_nn[hf];
+      }
     }
 
     // ---- the warps' states meet: weights 2^(m_w - m)
-    float* msm = psm + kPdWarps * ROWS * D;
+    float* msm = psm + kPdWarps * WR * D;
     __syncthreads();  // the previous unit's results have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -502,11 +589,11 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
         if (g == 0) {
-          msm[(warp * ROWS + 8 * nt + 2 * t4 + e) * 2] = m[nt][e];
-          msm[(warp * ROWS + 8 * nt + 2 * t4 + e) * 2 + 1] = v;
+          msm[(warp * WR + 8 * nt + 2 * t4 + e) * 2] = m[nt][e];
+          msm[(warp * WR + 8 * nt + 2 * t4 + e) * 2 + 1] = v;
         }
         // O's channel of row tile mt, half hf, lane group g
-        float* od = psm + (warp * ROWS + 8 * nt + 2 * t4 + e) * D;
+        float* od = psm + (warp * WR + 8 * nt + 2 * t4 + e) * D;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
           const int c = FMT == KV_E2M1 ? g * (D / 8) + 2 * mt : 64 * (mt >> 2) + 8 * g + 2 * (mt & 3);
@@ -515,34 +602,32 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       }
     }
     __syncthreads();
-    constexpr float kLift = FMT == KV_E2M1 ? 7.f : 0.f;
     constexpr int CP = D / 2;
-    for (int e = tid; e < nrows * CP; e += kPdThreads) {
-      const int r = e / CP, c2 = e % CP;
+    for (int e = tid; e < p.M * CP; e += kPdThreads) {
+      const int rr = e / CP, c2 = e % CP;
+      // row rr of warp group rr / WR: warps rr / WR + w * row_warps
+      const int w0 = rr / WR, rl = rr % WR;
       float mr = -CUDART_INF_F;
-#pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) mr = fmaxf(mr, msm[(w * ROWS + r) * 2]);
+      for (int w = w0; w < kPdWarps; w += p.row_warps) mr = fmaxf(mr, msm[(w * WR + rl) * 2]);
       const float ms = mr == -CUDART_INF_F ? 0.f : mr;
       float ls = 0.f;
       float2 ov = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kPdWarps; ++w) {
-        const float mw = msm[(w * ROWS + r) * 2];
+      for (int w = w0; w < kPdWarps; w += p.row_warps) {
+        const float mw = msm[(w * WR + rl) * 2];
         const float wt = mw == -CUDART_INF_F ? 0.f : ptx::ex2(mw - ms);
-        ls = fmaf(wt, msm[(w * ROWS + r) * 2 + 1], ls);
-        const float2 ow = *reinterpret_cast<const float2*>(psm + (w * ROWS + r) * D + 2 * c2);
+        ls = fmaf(wt, msm[(w * WR + rl) * 2 + 1], ls);
+        const float2 ow = *reinterpret_cast<const float2*>(psm + (w * WR + rl) * D + 2 * c2);
         ov = make_float2(fmaf(wt, ow.x, ov.x), fmaf(wt, ow.y, ov.y));
       }
       const float inv = ls == 0.f ? 0.f : p.c.v_scale / ls;
       const float lse2 = ls == 0.f ? -CUDART_INF_F : ms - kLift + __log2f(ls);
       if (whole) {
-        const int rr = row0 + r;
         const int hq = hkv * p.G + rr / p.Lq, i = rr % p.Lq;
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + hq * p.o_h + i * p.o_l;
         reinterpret_cast<__nv_bfloat162*>(orow)[c2] = __floats2bfloat162_rn(ov.x * inv, ov.y * inv);
         if (c2 == 0 && p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = lse2 * kPLn2;
       } else {
-        const int64_t pr = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS + r;
+        const int64_t pr = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.M + rr;
         reinterpret_cast<float2*>(p.opart)[pr * CP + c2] = make_float2(ov.x * inv, ov.y * inv);
         if (c2 == 0) p.lpart[pr] = lse2;
       }
@@ -555,27 +640,26 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 // per query row, its warps taking the pieces in turn.
 constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedDecodeParams p, int rows) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedDecodeParams p) {
   __shared__ float osm[kMergeWarps][D];
   __shared__ float wsm[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t HR = static_cast<int64_t>(p.c.Hkv) * p.row_blocks;
+  const int64_t H = p.c.Hkv;
   const int64_t row = blockIdx.x;  // (sequence, key/value head, row of the group)
   const int m = static_cast<int>(row % p.M);
   const int hkv = static_cast<int>(row / p.M % p.c.Hkv);
   const int b = static_cast<int>(row / p.M / p.c.Hkv);
   const int64_t per = p.plan[0];
   const int64_t before = p.plan[2 + b];
-  const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : p.plan[1] / HR) - before;
-  const int64_t first = before * HR + (static_cast<int64_t>(hkv) * p.row_blocks + m / rows) * count;
+  const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : p.plan[1] / H) - before;
+  const int64_t first = before * H + hkv * count;
   const int64_t c0 = first / per, c1 = (first + count - 1) / per;
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rl = m % rows;
   // piece i: CTA c0 + i; the first CTA's piece is its second one unless it starts there
   const int n = static_cast<int>(c1 - c0) + 1;
-  const int64_t head = (c0 * 2 + (first == c0 * per ? 0 : 1)) * rows + rl;
-  auto part = [&](int i) { return i == 0 ? head : (c0 + i) * 2 * rows + rl; };
+  const int64_t head = (c0 * 2 + (first == c0 * per ? 0 : 1)) * p.M + m;
+  auto part = [&](int i) { return i == 0 ? head : (c0 + i) * 2 * p.M + m; };
   float L = -CUDART_INF_F;
   for (int i = lane; i < n; i += 32) L = fmaxf(L, p.lpart[part(i)]);
 #pragma unroll
@@ -651,26 +735,29 @@ cudaError_t launch_fdn(const PagedDecodeParams& p, cudaStream_t s) {
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p, 8 * NT);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p);
 }
 
 }  // namespace
 
-#define FL_PAGED_DISPATCH(CALL)                                      \
-  if (format == KV_BF16) {                                           \
-    if (d == 64) return rows == 8 ? CALL(KV_BF16, 64, 1) : rows == 16 ? CALL(KV_BF16, 64, 2) : CALL(KV_BF16, 64, 4);       \
-    return rows == 8 ? CALL(KV_BF16, 128, 1) : rows == 16 ? CALL(KV_BF16, 128, 2) : CALL(KV_BF16, 128, 4);                 \
-  }                                                                  \
-  if (d == 64) return rows == 8 ? CALL(KV_E2M1, 64, 1) : rows == 16 ? CALL(KV_E2M1, 64, 2) : CALL(KV_E2M1, 64, 4);         \
-  return rows == 8 ? CALL(KV_E2M1, 128, 1) : rows == 16 ? CALL(KV_E2M1, 128, 2) : CALL(KV_E2M1, 128, 4);
+// 8-row tiles per warp: one up to 8 rows, two beyond
+#define FL_PAGED_DISPATCH(CALL)                                                                            \
+  const bool two = M > 8;                                                                                  \
+  if (format == KV_BF16) {                                                                                 \
+    if (d == 64) return two ? CALL(KV_BF16, 64, 2) : CALL(KV_BF16, 64, 1);                                 \
+    return two ? CALL(KV_BF16, 128, 2) : CALL(KV_BF16, 128, 1);                                            \
+  }                                                                                                        \
+  if (d == 64) return two ? CALL(KV_E2M1, 64, 2) : CALL(KV_E2M1, 64, 1);                                   \
+  return two ? CALL(KV_E2M1, 128, 2) : CALL(KV_E2M1, 128, 1);
 
-int paged_decode_grid(int format, int d, int rows, int sm_count) {
+int paged_decode_grid(int format, int d, int M, int sm_count) {
 #define FL_CALL(F, D, N) grid_of<F, D, N>(sm_count)
   FL_PAGED_DISPATCH(FL_CALL)
 #undef FL_CALL
 }
 
-cudaError_t launch_paged_decode(int format, int d, int rows, const PagedDecodeParams& p, cudaStream_t s) {
+cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s) {
+  const int M = p.M;
 #define FL_CALL(F, D, N) launch_fdn<F, D, N>(p, s)
   FL_PAGED_DISPATCH(FL_CALL)
 #undef FL_CALL
