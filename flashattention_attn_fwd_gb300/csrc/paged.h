@@ -61,7 +61,6 @@ struct PagedDecodeParams {
   int64_t table_stride;
   const float* slopes;
   int B, Hq, Lq, G, M;       // M = G * Lq rows per key/value head
-  int row_warps;             // warps that share a tile for different rows: 1, 2 or 4
   int max_pages, cap;        // cap = max_pages * page_size
   float scale_log2;          // scale * log2(e) * k_scale
   float softcap;             // in log2 units (cap * log2(e))

@@ -215,7 +215,6 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   if (st != FL_OK) return st;
   p.G = d.Hq / d.Hkv;
   p.M = p.G * d.Lq;
-  p.row_warps = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
   p.grid = fl::paged_decode_grid(cache->format, cache->d, p.M, sm_count);
   if (p.grid < 1) return fl::launch_result("paged decode occupancy", cudaErrorInvalidDeviceFunction);
   const WorkspaceLayout w = workspace_layout(d, p.M, p.grid);

@@ -16,21 +16,24 @@
 // 2^(LSE_piece - LSE).  The cut depends on the lengths alone, so the result of
 // a call is the same every time.
 //
-// Inner loop.  The CTA's four warps take the tiles of its piece in turn (with
-// more than 16 rows, groups of two or four warps take the same tile for
-// different rows; the second reading comes from L1).  Both products are warp-level m16n8k16 tiles with the keys' side as the 16-row
+// Inner loop.  The CTA's four warps take the tiles of its piece in turn; with
+// more than 16 rows, groups of two or four warps share a tile, each for its own
+// rows.  A group copies its tiles with 16-byte cp.async into a ring of stages of
+// its own (one barrier per tile), so that a few stages per group, well above
+// the SM's share of bandwidth times latency, are always on the way.  Both
+// products are warp-level m16n8k16 tiles with the keys' side as the 16-row
 // operand, so that 8 query rows fill the tile:
 //   S^T (16 keys x 8 rows)      = K (16 keys x 16 channels) Q^T
 //   O^T (16 channels x 8 rows) += V^T (16 channels x 16 keys) P^T
 // (tcgen05's 64/128-row tiles would be mostly padding.)  The order of the
 // channels inside S's contraction, of the channels among O's rows and of the
 // keys inside a tile is free, and is chosen so that a lane's fragments are
-// contiguous bytes of the cache: lane (g, t) = (lane / 4, lane % 4) loads a
+// contiguous bytes of the cache: lane (g, t) = (lane / 4, lane % 4) takes a
 // quarter of the channels of two keys of K and an eighth of the channels of four
-// consecutive keys of V, straight from global memory into registers, with no
-// pass through shared memory.  The two 4-bit codes of a byte are neighbouring
-// channels of one key, which is a K fragment's pair as it stands; V's pairs are
-// two keys of one channel, so the nibbles of two keys are interleaved first.
+// consecutive keys of V, with wide loads and no shuffles.  The two 4-bit codes
+// of a byte are neighbouring channels of one key, which is a K fragment's pair
+// as it stands; V's pairs are two keys of one channel, so the nibbles of two
+// keys are interleaved first.
 // 4-bit values times their block scale have at most six significant bits and
 // are exact in fp16; the products run in fp16 with fp32 sums.  The query row
 // is scaled to fp16's range by a power of two (undone in the score), P carries a
@@ -109,20 +112,60 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeParams& p, int b)
   return s;
 }
 
-// The raw cache bytes of 16 keys held by a lane: two keys of K (a quarter of
-// the channels) and four of V (an eighth).
+// Ring of one warp group.  A stage holds the tile's K rows, its V rows and
+// (4 bits) its scales: K's [key][d / 16], V's [d / 16][16 keys] per half.  The
+// 16-byte chunks of a row are permuted within their 128-byte line (swz_k,
+// swz_v of the key) so that the fragment loads meet no bank twice.
+template <int FMT, int D, int RW>
+struct Ring {
+  static constexpr int HV = kHalves<FMT, D>;
+  static constexpr int KB = FMT == KV_E2M1 ? D / 2 : 2 * D;      // bytes of one key's row
+  static constexpr int ROWS = 16 * HV * KB;                      // bytes of K (or V) per stage
+  static constexpr int SC = FMT == KV_E2M1 ? D : 0;              // bytes of K (or V) scales per half
+  static constexpr int STAGE = 2 * ROWS + 2 * HV * SC;
+  static constexpr int STAGES = RW * (FMT == KV_E2M1 && D == 64 ? 4 : 3);
+  static constexpr int BYTES = kPdWarps / RW * STAGES * STAGE;   // of the CTA's groups
+};
 template <int FMT, int D>
-struct HalfRegs;
-template <int D>
-struct HalfRegs<KV_E2M1, D> {
-  uint32_t k[2][D / 32], v[4][D / 64], ks[2], vs;
-};
-template <int D>
-struct HalfRegs<KV_BF16, D> {
-  uint4 k[2][D / 32], v[4][D / 64];
-};
+__device__ __forceinline__ int swz_k(int j) {
+  return FMT == KV_BF16 ? 4 * (j & 1) : D == 128 ? 2 * ((j >> 2) & 3) : 4 * ((j >> 2) & 1);
+}
+__device__ __forceinline__ int swz_v(int j) { return 2 * ((j >> 2) & 3); }
 
-template <int FMT, int D, int NT>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+
+template <int FMT, int D, int NT, int RW>
 __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int KS = D / 16;        // k-steps of S, and 16-channel row tiles of O
   constexpr int HV = kHalves<FMT, D>;
@@ -130,7 +173,12 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   constexpr int WR = 8 * NT;        // query rows per warp
   // weights carry 2^kLift in fp16 (see above)
   constexpr float kLift = FMT == KV_E2M1 ? 7.f : 0.f;
-  extern __shared__ float psm[];    // merge: O [warp][WR][D], then m, l [warp][WR][2]
+  using L = Ring<FMT, D, RW>;
+  constexpr int S = L::STAGES;
+  constexpr int GT = 32 * RW;       // threads of a group
+  // rings of the groups; after a unit's tiles O [warp][WR][D], then m, l
+  // [warp][WR][2] for the merge
+  extern __shared__ __align__(128) float psm[];
   __shared__ int64_t scan_sm[kPdWarps];
   __shared__ int found_sm;
   __shared__ int64_t base_sm;
@@ -195,16 +243,27 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   const int shift = p.c.page_shift;
   const int page_mask = (1 << shift) - 1;
   // warps by row group and by key group
-  const int rw = warp & (p.row_warps - 1);
-  const int kw = warp / p.row_warps, n_kw = kPdWarps / p.row_warps;
+  const int rw = warp % RW, kw = warp / RW;
+  constexpr int n_kw = kPdWarps / RW;
   const int row0 = rw * WR;         // this warp's first row
-  // K keys of this lane: 4 (g / 2) + g % 2 and two further; V keys 4 t4 ..
+  const int gt = rw * 32 + lane;    // thread of the group
+  const uint32_t ring = ptx::smem_u32(psm) + kw * (S * L::STAGE);
+  auto group_sync = [&]() {
+    if (RW == 1) __syncwarp();
+    else ptx::named_bar_sync(1 + kw, GT);
+  };
+  // fragments: K keys 4 (g / 2) + g % 2 and two further, V keys 4 t4 ..; byte
+  // offsets within a stage's K and V, whose swizzle depends on the lane alone
+  // (kx: 4 bits the two keys, bf16 even and odd 64-byte chunks of a row)
+  constexpr int KB = L::KB;
   const int kkey = 4 * (g >> 1) + (g & 1);
-  constexpr int KB = FMT == KV_E2M1 ? D / 2 : 2 * D;  // bytes of one key's row
-  const uint8_t* k_lane = static_cast<const uint8_t*>(p.c.k) + kkey * KB + (FMT == KV_E2M1 ? t4 * (D / 8) : 16 * t4);
-  const uint8_t* v_lane = static_cast<const uint8_t*>(p.c.v) + 4 * t4 * KB + (FMT == KV_E2M1 ? g * (D / 16) : 16 * g);
-  const uint8_t* ks_lane = FMT == KV_E2M1 ? p.c.ks + kkey * (D / 16) + t4 * (D / 64) : nullptr;
-  const uint8_t* vs_lane = FMT == KV_E2M1 ? p.c.vs + ((D == 128 ? g : g >> 1) << shift) + 4 * t4 : nullptr;
+  uint32_t kx[2], vx[4];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    kx[q] = (FMT == KV_E2M1 ? (kkey + 2 * q) * KB + t4 * (D / 8) : kkey * KB + 16 * t4 + 64 * q) ^ (16 * swz_k<FMT, D>(kkey));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) vx[i] = ((4 * t4 + i) * KB + g * (FMT == KV_E2M1 ? D / 16 : 16)) ^ (16 * swz_v(4 * t4));
+  const uint32_t ksx = kkey * (D / 16) + t4 * (D / 64), vsx = D + 16 * (D == 128 ? g : g >> 1) + 4 * t4;
 
   for (int64_t cur = begin; cur < end;) {
     // ---- the unit at `cur`
@@ -220,68 +279,66 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     const bool whole = t0 == 0 && t1 == sq.count;
     const int slot = cur == begin ? 0 : 1;
 
-    // ---- pages and bytes of the first tile
+    // ---- the ring: tile i of this group is t0 + kw + i * n_kw
     const int32_t* trow = p.table + b * p.table_stride;
     auto key_of = [&](int t) { return KT * (t < sq.sink ? t : t + sq.skip); };
-    // page of key j; -1: none (past the cache, or out of the pool)
+    // page of a tile's half; -1: none (past the piece, the cache or the pool)
     auto page_of = [&](int t, int hf) {
       const int j = key_of(t) + 16 * hf;
-      return t < t1 && j < sq.n ? __ldg(trow + (j >> shift)) : -1;
+      const int pg = t < t1 && j < sq.n ? __ldg(trow + (j >> shift)) : -1;
+      return static_cast<unsigned>(pg) < static_cast<unsigned>(p.c.num_pages) ? pg : -1;
     };
-    // token index of a half's first key in the pool (page 0 stands in for none)
-    auto token_of = [&](int t, int hf, int page) {
-      const int pg = static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages) ? page : 0;
-      return ((static_cast<int64_t>(pg) * p.c.Hkv + hkv) << shift) + ((key_of(t) + 16 * hf) & page_mask);
-    };
-    HalfRegs<FMT, D> r[HV];
-    auto load_k = [&](HalfRegs<FMT, D>& x, int64_t tok) {
-      const uint8_t* kp = k_lane + tok * KB;
+    // Copies tile t (pages pg) into a stage; page 0 stands in for a missing
+    // one, whose keys are masked.
+    auto copy = [&](int t, const int (&pg)[HV], uint32_t st) {
+      int64_t tok[HV];  // tokens in the pool before each half
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (FMT == KV_E2M1) {
-          const uint8_t* sp = ks_lane + tok * (D / 16);
-          if constexpr (D == 128) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(kp + 2 * i * KB));
-            x.k[i][0] = w.x; x.k[i][1] = w.y; x.k[i][2] = w.z; x.k[i][3] = w.w;
-            x.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(sp + 2 * i * (D / 16)));
-          } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(kp + 2 * i * KB));
-            x.k[i][0] = w.x; x.k[i][1] = w.y;
-            x.ks[i] = __ldg(sp + 2 * i * (D / 16));
-          }
-        } else {
+      for (int hf = 0; hf < HV; ++hf)
+        tok[hf] = ((static_cast<int64_t>(max(pg[hf], 0)) * p.c.Hkv + hkv) << shift) + ((key_of(t) + 16 * hf) & page_mask);
+      const uint8_t* kp = static_cast<const uint8_t*>(p.c.k);
+      const uint8_t* vp = static_cast<const uint8_t*>(p.c.v);
+      constexpr int CH = KB;           // chunks of one half's K
+      constexpr int N = HV * CH;
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) x.k[i][j] = __ldg(reinterpret_cast<const uint4*>(kp + 2 * i * KB + 64 * j));
-        }
-      }
-    };
-    auto load_v = [&](HalfRegs<FMT, D>& x, int64_t tok) {
-      const uint8_t* vp = v_lane + tok * KB;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (FMT == KV_E2M1) {
-          if constexpr (D == 128) {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(vp + i * KB));
-            x.v[i][0] = w.x; x.v[i][1] = w.y;
-          } else {
-            x.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(vp + i * KB));
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) x.v[i][j] = __ldg(reinterpret_cast<const uint4*>(vp + i * KB + 128 * j));
+      for (int i = 0; i < (N + GT - 1) / GT; ++i) {
+        const int c = gt + GT * i;
+        if (N % GT == 0 || c < N) {
+          const int hf = CH % GT == 0 ? GT * i / CH : c / CH;
+          const int64_t at = (HV == 1 || hf == 0 ? tok[0] : tok[HV - 1]) * KB + (c % CH) * 16;
+          const int j = c / (KB / 16);
+          cp_async16(st + 16 * (c ^ swz_k<FMT, D>(j)), kp + at);
+          cp_async16(st + L::ROWS + 16 * (c ^ swz_v(j)), vp + at);
         }
       }
       if constexpr (FMT == KV_E2M1) {
-        const int off = static_cast<int>(tok) & page_mask;  // runs are page-aligned
-        x.vs = __ldg(reinterpret_cast<const uint32_t*>(vs_lane + (tok - off) * (D / 16) + off));
+        constexpr int SH = D / 8;      // scale chunks per half: K's, then V's
+        if (gt < HV * SH) {
+          const int hf = gt / SH, x = gt % SH;
+          const int64_t tk = hf == 0 ? tok[0] : tok[HV - 1];
+          const int off = static_cast<int>(tk) & page_mask;  // runs are page-aligned
+          const uint8_t* src = x < SH / 2 ? p.c.ks + tk * (D / 16) + 16 * x
+                                          : p.c.vs + (tk - off) * (D / 16) + (static_cast<int64_t>(x - SH / 2) << shift) + off;
+          cp_async16(st + 2 * L::ROWS + 16 * gt, src);
+        }
       }
     };
-    int t = t0 + kw;
-    int page[HV], page_n[HV];
+    const int n_tiles = (t1 - t0 - kw + n_kw - 1) / n_kw;  // of this group (0 or less: none)
+    // pages of the next tile to copy, and which pages of the tiles under way
+    // exist: HV bits a tile, the current tile's lowest
+    int pg[HV];
+    uint64_t have = 0;
+    auto fetch = [&](int i) {
 #pragma unroll
-    for (int hf = 0; hf < HV; ++hf) page[hf] = page_of(t, hf);
+      for (int hf = 0; hf < HV; ++hf) pg[hf] = page_of(t0 + kw + i * n_kw, hf);
+    };
+    auto issue = [&](int i, int ahead, uint32_t st) {  // tile i into stage st
+      if (i < n_tiles) {
+        copy(t0 + kw + i * n_kw, pg, st);
 #pragma unroll
-    for (int hf = 0; hf < HV; ++hf) page_n[hf] = page_of(t + n_kw, hf);
+        for (int hf = 0; hf < HV; ++hf) have |= static_cast<uint64_t>(pg[hf] >= 0) << (HV * ahead + hf);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 
     // ---- queries: row g of every 8-row tile, channels in the order of K's
     // fragments; fp16 rows scaled to magnitude [1, 2) by a power of two
@@ -303,14 +360,11 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         qf[nt][2 * j + 1][0] = w.z; qf[nt][2 * j + 1][1] = w.w;
       }
     }
-    if (t < t1) {
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf) {
-        const int64_t tok = token_of(t, hf, page[hf]);
-        load_k(r[hf], tok);
-        load_v(r[hf], tok);
-      }
+    for (int i = 0; i < S - 1; ++i) {
+      fetch(i);
+      issue(i, i, ring + i * L::STAGE);
     }
+    fetch(S - 1);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float undo = 1.f;
@@ -360,16 +414,17 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
     }
 
-    for (; t < t1; t += n_kw) {
-      const int key0 = key_of(t);
-      // page ids two tiles ahead; K a tile ahead once S is done, V once O is
-      int page_nn[HV];
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf) page_nn[hf] = page_of(t + 2 * n_kw, hf);
-      bool pages_ok = true;
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf) pages_ok = pages_ok && static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
-      const bool full = pages_ok && key0 <= full_hi && (key0 >= full_lo || key0 <= full_sink);
+    uint32_t stage = 0, ahead = S - 1;  // ring positions of tile i and tile i + S - 1
+    for (int i = 0; i < n_tiles; ++i) {
+      cp_async_wait<S - 2>();
+      group_sync();  // tile i is here, and its predecessor's stage is free
+      issue(i + S - 1, S - 1, ring + ahead * L::STAGE);
+      fetch(i + S);
+      const uint32_t st = ring + stage * L::STAGE;
+      const int key0 = key_of(t0 + kw + i * n_kw);
+      const uint32_t got = static_cast<uint32_t>(have) & ((1u << HV) - 1);
+      have >>= HV;
+      const bool full = got == (1u << HV) - 1 && key0 <= full_hi && (key0 >= full_lo || key0 <= full_sink);
       // ---- S^T = K Q^T
       float s[HV][NT][4];
 #pragma unroll
@@ -378,20 +433,29 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         for (int nt = 0; nt < NT; ++nt) s[hf][nt][0] = s[hf][nt][1] = s[hf][nt][2] = s[hf][nt][3] = 0.f;
 #pragma unroll
       for (int hf = 0; hf < HV; ++hf) {
-        const HalfRegs<FMT, D>& x = r[hf];
+        const uint32_t kt = st + hf * 16 * KB;
         if constexpr (FMT == KV_E2M1) {
           uint32_t ksc[2][2];  // [key][block of the lane's channels] fp16 pairs
+          uint32_t kw4[2][D / 32];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t h2 = cvt4::from_e4m3x2(x.ks[i]);
-            ksc[i][0] = __byte_perm(h2, 0u, 0x1010);
-            ksc[i][1] = D == 128 ? __byte_perm(h2, 0u, 0x3232) : ksc[i][0];
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t sa = st + 2 * L::ROWS + hf * 2 * D + ksx + 2 * q * (D / 16);
+            const uint32_t h2 = cvt4::from_e4m3x2(D == 128 ? lds16(sa) : lds8(sa));
+            ksc[q][0] = __byte_perm(h2, 0u, 0x1010);
+            ksc[q][1] = D == 128 ? __byte_perm(h2, 0u, 0x3232) : ksc[q][0];
+            if constexpr (D == 128) {
+              const uint4 w = lds128(kt + kx[q]);
+              kw4[q][0] = w.x; kw4[q][1] = w.y; kw4[q][2] = w.z; kw4[q][3] = w.w;
+            } else {
+              const uint2 w = lds64(kt + kx[q]);
+              kw4[q][0] = w.x; kw4[q][1] = w.y;
+            }
           }
 #pragma unroll
           for (int w = 0; w < D / 32; ++w) {
             uint32_t ha[4], hb[4];
-            cvt4::from_e2m1x8(x.k[0][w], ha);
-            cvt4::from_e2m1x8(x.k[1][w], hb);
+            cvt4::from_e2m1x8(kw4[0][w], ha);
+            cvt4::from_e2m1x8(kw4[1][w], hb);
             const int bl = D == 128 ? w >> 1 : 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -408,23 +472,16 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         } else {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
-            const uint32_t a0[4] = {x.k[0][j].x, x.k[1][j].x, x.k[0][j].y, x.k[1][j].y};
-            const uint32_t a1[4] = {x.k[0][j].z, x.k[1][j].z, x.k[0][j].w, x.k[1][j].w};
+            const uint4 ka = lds128(kt + kx[j & 1] + 128 * (j >> 1));
+            const uint4 kb = lds128(kt + kx[j & 1] + 128 * (j >> 1) + 2 * KB);
+            const uint32_t a0[4] = {ka.x, kb.x, ka.y, kb.y};
+            const uint32_t a1[4] = {ka.z, kb.z, ka.w, kb.w};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16816<FMT>(s[hf][nt], a0, qf[nt][2 * j][0], qf[nt][2 * j][1]);
               mma16816<FMT>(s[hf][nt], a1, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
             }
           }
-        }
-      }
-      const bool more = t + n_kw < t1;
-      int64_t tok_n[HV];
-      if (more) {
-#pragma unroll
-        for (int hf = 0; hf < HV; ++hf) {
-          tok_n[hf] = token_of(t + n_kw, hf, page_n[hf]);
-          load_k(r[hf], tok_n[hf]);
         }
       }
       // ---- scores (log2 units) of key kkey (e < 2) and kkey + 2, rows 2 t4, +1
@@ -452,7 +509,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         if (!full) {
 #pragma unroll
           for (int hf = 0; hf < HV; ++hf) {
-            const bool pok = static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
+            const bool pok = (got >> hf) & 1u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int j = key0 + 16 * hf + kkey + (e & 2), ps = pos[nt][e & 1];
@@ -505,38 +562,49 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           }
         }
       }
+      // keys that no row sees may hold anything: their V must not reach the
+      // product (0 * NaN)
+      uint32_t drop = 0;  // of V keys 4 t4 .. of each half, one bit each
       if (!full) {
-        // keys that no row sees may hold anything: their V must not reach the
-        // product (0 * NaN)
 #pragma unroll
         for (int hf = 0; hf < HV; ++hf) {
-          const bool pok = static_cast<unsigned>(page[hf]) < static_cast<unsigned>(p.c.num_pages);
+          const bool pok = (got >> hf) & 1u;
           const int h0 = key0 + 16 * hf;
           const bool seen = h0 < sq.n && (!p.window || h0 + 15 > pos_lo - p.window || h0 < p.sink);
           if (!pok && seen && lane == 0) atomicOr(p.status, 2u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = key0 + 16 * hf + 4 * t4 + i;
-            if (pok && j < sq.n && (!p.window || j > pos_lo - p.window || j < p.sink)) continue;
-            if constexpr (FMT == KV_E2M1) {
-              r[hf].vs &= ~(0xffu << (8 * i));
-            } else {
-#pragma unroll
-              for (int c = 0; c < D / 64; ++c) r[hf].v[i][c] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            const int j = h0 + 4 * t4 + i;
+            if (!pok || j >= sq.n || (p.window && j <= pos_lo - p.window && j >= p.sink)) drop |= 1u << (4 * hf + i);
           }
         }
       }
       // ---- O^T += V^T P^T
 #pragma unroll
       for (int hf = 0; hf < HV; ++hf) {
-        const HalfRegs<FMT, D>& x = r[hf];
+        const uint32_t vt = st + L::ROWS + hf * 16 * KB;
         if constexpr (FMT == KV_E2M1) {
-          const uint32_t s01 = cvt4::from_e4m3x2(x.vs & 0xffffu), s23 = cvt4::from_e4m3x2(x.vs >> 16);
+          uint32_t vs = lds32(st + 2 * L::ROWS + hf * 2 * D + vsx);
+          if (drop) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((drop >> (4 * hf + i)) & 1u) vs &= ~(0xffu << (8 * i));
+          }
+          const uint32_t s01 = cvt4::from_e4m3x2(vs & 0xffffu), s23 = cvt4::from_e4m3x2(vs >> 16);
+          uint32_t vw[4][D / 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (D == 128) {
+              const uint2 w = lds64(vt + vx[i]);
+              vw[i][0] = w.x; vw[i][1] = w.y;
+            } else {
+              vw[i][0] = lds32(vt + vx[i]);
+            }
+          }
 #pragma unroll
           for (int w = 0; w < D / 64; ++w) {
             // nibble pairs (key 0, key 1) of even and of odd channels
-            const uint32_t v0 = x.v[0][w], v1 = x.v[1][w], v2 = x.v[2][w], v3 = x.v[3][w];
+            const uint32_t v0 = vw[0][w], v1 = vw[1][w], v2 = vw[2][w], v3 = vw[3][w];
             uint32_t e01[4], o01[4], e23[4], o23[4];
             cvt4::from_e2m1x8((v0 & 0x0f0f0f0fu) | ((v1 << 4) & 0xf0f0f0f0u), e01);
             cvt4::from_e2m1x8(((v0 >> 4) & 0x0f0f0f0fu) | (v1 & 0xf0f0f0f0u), o01);
@@ -553,10 +621,14 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         } else {
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
-            const uint32_t v0[4] = {x.v[0][j].x, x.v[0][j].y, x.v[0][j].z, x.v[0][j].w};
-            const uint32_t v1[4] = {x.v[1][j].x, x.v[1][j].y, x.v[1][j].z, x.v[1][j].w};
-            const uint32_t v2[4] = {x.v[2][j].x, x.v[2][j].y, x.v[2][j].z, x.v[2][j].w};
-            const uint32_t v3[4] = {x.v[3][j].x, x.v[3][j].y, x.v[3][j].z, x.v[3][j].w};
+            uint4 vv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              vv[i] = lds128(vt + vx[i] + 128 * j);
+              if ((drop >> (4 * hf + i)) & 1u) vv[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            const uint32_t v0[4] = {vv[0].x, vv[0].y, vv[0].z, vv[0].w}, v1[4] = {vv[1].x, vv[1].y, vv[1].z, vv[1].w};
+            const uint32_t v2[4] = {vv[2].x, vv[2].y, vv[2].z, vv[2].w}, v3[4] = {vv[3].x, vv[3].y, vv[3].z, vv[3].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t a[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
@@ -567,20 +639,14 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           }
         }
       }
-      if (more) {
-#pragma unroll
-        for (int hf = 0; hf < HV; ++hf) load_v(r[hf], tok_n[hf]);
-      }
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf) {
-        page[hf] = page_n[hf];
-        page_n[hf] = page_nn[hf];
-      }
+      stage = stage + 1 == S ? 0 : stage + 1;
+      ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
 
     // ---- the warps' states meet: weights 2^(m_w - m)
     float* msm = psm + kPdWarps * WR * D;
-    __syncthreads();  // the previous unit's results have been read
+    cp_async_wait<0>();
+    __syncthreads();  // the rings are idle: their memory takes the states
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -605,14 +671,14 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     constexpr int CP = D / 2;
     for (int e = tid; e < p.M * CP; e += kPdThreads) {
       const int rr = e / CP, c2 = e % CP;
-      // row rr of warp group rr / WR: warps rr / WR + w * row_warps
+      // row rr belongs to row warp rr / WR of every group
       const int w0 = rr / WR, rl = rr % WR;
       float mr = -CUDART_INF_F;
-      for (int w = w0; w < kPdWarps; w += p.row_warps) mr = fmaxf(mr, msm[(w * WR + rl) * 2]);
+      for (int w = w0; w < kPdWarps; w += RW) mr = fmaxf(mr, msm[(w * WR + rl) * 2]);
       const float ms = mr == -CUDART_INF_F ? 0.f : mr;
       float ls = 0.f;
       float2 ov = make_float2(0.f, 0.f);
-      for (int w = w0; w < kPdWarps; w += p.row_warps) {
+      for (int w = w0; w < kPdWarps; w += RW) {
         const float mw = msm[(w * WR + rl) * 2];
         const float wt = mw == -CUDART_INF_F ? 0.f : ptx::ex2(mw - ms);
         ls = fmaf(wt, msm[(w * WR + rl) * 2 + 1], ls);
@@ -633,6 +699,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       }
     }
     cur += t1 - t0;
+    if (cur < end) __syncthreads();  // the results have been read: the rings may fill again
   }
 }
 
@@ -701,28 +768,29 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = tot == 0.f ? -CUDART_INF_F : (Ls + __log2f(tot)) * kPLn2;
 }
 
-template <int D, int NT>
+template <int FMT, int D, int NT, int RW>
 constexpr int decode_smem() {
-  return kPdWarps * 8 * NT * (D + 2) * 4;
+  constexpr int merge = kPdWarps * 8 * NT * (D + 2) * 4, ring = Ring<FMT, D, RW>::BYTES;
+  return merge > ring ? merge : ring;
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, int RW>
 int grid_of(int sm_count) {
   static const int per_sm = [] {
     int n = 0;
-    if (cudaFuncSetAttribute(paged_decode_kernel<FMT, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             decode_smem<D, NT>()) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_decode_kernel<FMT, D, NT>, kPdThreads,
-                                                      decode_smem<D, NT>()) != cudaSuccess)
+    if (cudaFuncSetAttribute(paged_decode_kernel<FMT, D, NT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             decode_smem<FMT, D, NT, RW>()) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_decode_kernel<FMT, D, NT, RW>, kPdThreads,
+                                                      decode_smem<FMT, D, NT, RW>()) != cudaSuccess)
       return -1;
     return n;
   }();
   return per_sm < 1 ? -1 : per_sm * sm_count;
 }
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, int RW>
 cudaError_t launch_fdn(const PagedDecodeParams& p, cudaStream_t s) {
-  paged_decode_kernel<FMT, D, NT><<<p.grid, kPdThreads, decode_smem<D, NT>(), s>>>(p);
+  paged_decode_kernel<FMT, D, NT, RW><<<p.grid, kPdThreads, decode_smem<FMT, D, NT, RW>(), s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the merge's launch overlaps the tiles' work; it waits for it before it reads
@@ -740,25 +808,27 @@ cudaError_t launch_fdn(const PagedDecodeParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// 8-row tiles per warp: one up to 8 rows, two beyond
-#define FL_PAGED_DISPATCH(CALL)                                                                            \
-  const bool two = M > 8;                                                                                  \
-  if (format == KV_BF16) {                                                                                 \
-    if (d == 64) return two ? CALL(KV_BF16, 64, 2) : CALL(KV_BF16, 64, 1);                                 \
-    return two ? CALL(KV_BF16, 128, 2) : CALL(KV_BF16, 128, 1);                                            \
-  }                                                                                                        \
-  if (d == 64) return two ? CALL(KV_E2M1, 64, 2) : CALL(KV_E2M1, 64, 1);                                   \
-  return two ? CALL(KV_E2M1, 128, 2) : CALL(KV_E2M1, 128, 1);
+// 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
+// (2, 2) and (2, 4)
+#define FL_PAGED_ROWS(CALL, F, D) \
+  return M <= 8 ? CALL(F, D, 1, 1) : M <= 16 ? CALL(F, D, 2, 1) : M <= 32 ? CALL(F, D, 2, 2) : CALL(F, D, 2, 4);
+#define FL_PAGED_DISPATCH(CALL)                    \
+  if (format == KV_BF16) {                         \
+    if (d == 64) FL_PAGED_ROWS(CALL, KV_BF16, 64)  \
+    FL_PAGED_ROWS(CALL, KV_BF16, 128)              \
+  }                                                \
+  if (d == 64) FL_PAGED_ROWS(CALL, KV_E2M1, 64)    \
+  FL_PAGED_ROWS(CALL, KV_E2M1, 128)
 
 int paged_decode_grid(int format, int d, int M, int sm_count) {
-#define FL_CALL(F, D, N) grid_of<F, D, N>(sm_count)
+#define FL_CALL(F, D, N, R) grid_of<F, D, N, R>(sm_count)
   FL_PAGED_DISPATCH(FL_CALL)
 #undef FL_CALL
 }
 
 cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s) {
   const int M = p.M;
-#define FL_CALL(F, D, N) launch_fdn<F, D, N>(p, s)
+#define FL_CALL(F, D, N, R) launch_fdn<F, D, N, R>(p, s)
   FL_PAGED_DISPATCH(FL_CALL)
 #undef FL_CALL
 }
