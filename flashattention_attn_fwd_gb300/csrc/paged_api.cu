@@ -16,6 +16,9 @@ constexpr double kLog2e = 1.4426950408889634;
 // within 32 bits.
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
+// Rows (heads times tokens) of a page: its bytes stay below 2^31.
+constexpr int64_t kMaxPageRows = int64_t(1) << 22;
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 bool normal_scale(float x) { return x > 0.f && std::isnormal(x) && std::isnormal(1.0f / x); }
@@ -33,6 +36,7 @@ fl_status cache_check(const fl_kv_cache* c) {
     return FL_ERR_INVALID_ARG;
   }
   if (c->d != 64 && c->d != 128) return FL_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->Hkv) * c->page_size > kMaxPageRows) return FL_ERR_UNSUPPORTED;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return FL_ERR_UNSUPPORTED;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return FL_ERR_ALIGNMENT;
   if (c->format == FL_KV_E2M1 && (!aligned(c->k_scales, 16) || !aligned(c->v_scales, 16))) return FL_ERR_ALIGNMENT;

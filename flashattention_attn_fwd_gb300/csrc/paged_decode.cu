@@ -123,7 +123,7 @@ struct Ring {
   static constexpr int ROWS = 16 * HV * KB;                      // bytes of K (or V) per stage
   static constexpr int SC = FMT == KV_E2M1 ? D : 0;              // bytes of K (or V) scales per half
   static constexpr int STAGE = 2 * ROWS + 2 * HV * SC;
-  static constexpr int STAGES = RW * (FMT == KV_E2M1 && D == 64 ? 4 : 3);
+  static constexpr int STAGES = RW * (FMT == KV_BF16 ? 2 : D == 64 ? 4 : 3);
   static constexpr int BYTES = kPdWarps / RW * STAGES * STAGE;   // of the CTA's groups
 };
 template <int FMT, int D>
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 
   const int shift = p.c.page_shift;
   const int page_mask = (1 << shift) - 1;
+  const uint32_t page_bytes = static_cast<uint32_t>(p.c.Hkv << shift) * L::KB;  // of K, of V
   // warps by row group and by key group
   const int rw = warp % RW, kw = warp / RW;
   constexpr int n_kw = kPdWarps / RW;
@@ -282,43 +283,55 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     // ---- the ring: tile i of this group is t0 + kw + i * n_kw
     const int32_t* trow = p.table + b * p.table_stride;
     auto key_of = [&](int t) { return KT * (t < sq.sink ? t : t + sq.skip); };
-    // page of a tile's half; -1: none (past the piece, the cache or the pool)
+    // page of a tile's half; -1: none (past the piece, the cache or the pool).
+    // From 32-key pages on a tile lies in one page.
     auto page_of = [&](int t, int hf) {
       const int j = key_of(t) + 16 * hf;
       const int pg = t < t1 && j < sq.n ? __ldg(trow + (j >> shift)) : -1;
       return static_cast<unsigned>(pg) < static_cast<unsigned>(p.c.num_pages) ? pg : -1;
     };
+    // Addresses: a page is `stride` bytes (of K, of V), a head's run in it starts
+    // `head` bytes on; the scales' are those over KB / (D / 16).
+    const uint8_t* kh = static_cast<const uint8_t*>(p.c.k) + (static_cast<int64_t>(hkv) << shift) * KB + 16 * gt;
+    const uint8_t* vh = static_cast<const uint8_t*>(p.c.v) + (static_cast<int64_t>(hkv) << shift) * KB + 16 * gt;
+    constexpr int SH = D / 8;          // scale chunks per half: K's, then V's
+    const int sx = gt % SH;
+    const bool sv = sx >= SH / 2;
+    const uint8_t* sh = nullptr;
+    if (FMT == KV_E2M1)
+      sh = (sv ? p.c.vs + ((sx - SH / 2) << shift) : p.c.ks + 16 * sx) + (static_cast<int64_t>(hkv) << shift) * (D / 16);
     // Copies tile t (pages pg) into a stage; page 0 stands in for a missing
     // one, whose keys are masked.
     auto copy = [&](int t, const int (&pg)[HV], uint32_t st) {
-      int64_t tok[HV];  // tokens in the pool before each half
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf)
-        tok[hf] = ((static_cast<int64_t>(max(pg[hf], 0)) * p.c.Hkv + hkv) << shift) + ((key_of(t) + 16 * hf) & page_mask);
-      const uint8_t* kp = static_cast<const uint8_t*>(p.c.k);
-      const uint8_t* vp = static_cast<const uint8_t*>(p.c.v);
+      const uint32_t off = key_of(t) & page_mask;
+      const uint32_t p0 = max(pg[0], 0);
+      const int64_t a0 = static_cast<int64_t>(static_cast<uint64_t>(p0) * page_bytes + off * KB);
+      int64_t a1 = a0 + 16 * KB;
+      uint32_t p1 = p0, off1 = off + 16;
+      if (HV == 2 && shift == 4) {
+        p1 = max(pg[HV - 1], 0);
+        off1 = 0;
+        a1 = static_cast<int64_t>(static_cast<uint64_t>(p1) * page_bytes);
+      }
       constexpr int CH = KB;           // chunks of one half's K
       constexpr int N = HV * CH;
 #pragma unroll
       for (int i = 0; i < (N + GT - 1) / GT; ++i) {
         const int c = gt + GT * i;
         if (N % GT == 0 || c < N) {
-          const int hf = CH % GT == 0 ? GT * i / CH : c / CH;
-          const int64_t at = (HV == 1 || hf == 0 ? tok[0] : tok[HV - 1]) * KB + (c % CH) * 16;
+          // within a half the chunks of consecutive i are GT chunks on
+          const bool second = CH % GT == 0 ? GT * i >= CH : c >= CH;
+          const int64_t at = (second ? a1 - 16 * CH : a0) + 16 * GT * i;
           const int j = c / (KB / 16);
-          cp_async16(st + 16 * (c ^ swz_k<FMT, D>(j)), kp + at);
-          cp_async16(st + L::ROWS + 16 * (c ^ swz_v(j)), vp + at);
+          cp_async16(st + 16 * (c ^ swz_k<FMT, D>(j)), kh + at);
+          cp_async16(st + L::ROWS + 16 * (c ^ swz_v(j)), vh + at);
         }
       }
       if constexpr (FMT == KV_E2M1) {
-        constexpr int SH = D / 8;      // scale chunks per half: K's, then V's
         if (gt < HV * SH) {
-          const int hf = gt / SH, x = gt % SH;
-          const int64_t tk = hf == 0 ? tok[0] : tok[HV - 1];
-          const int off = static_cast<int>(tk) & page_mask;  // runs are page-aligned
-          const uint8_t* src = x < SH / 2 ? p.c.ks + tk * (D / 16) + 16 * x
-                                          : p.c.vs + (tk - off) * (D / 16) + (static_cast<int64_t>(x - SH / 2) << shift) + off;
-          cp_async16(st + 2 * L::ROWS + 16 * gt, src);
+          const uint32_t pp = gt < SH ? p0 : p1, oo = gt < SH ? off : off1;
+          cp_async16(st + 2 * L::ROWS + 16 * gt,
+                     sh + static_cast<int64_t>(static_cast<uint64_t>(pp) * (page_bytes / (KB / (D / 16))) + oo * (sv ? 1 : D / 16)));
         }
       }
     };
@@ -326,16 +339,17 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     // pages of the next tile to copy, and which pages of the tiles under way
     // exist: HV bits a tile, the current tile's lowest
     int pg[HV];
-    uint64_t have = 0;
+    uint32_t have = 0;
+    static_assert(HV * S <= 32, "a bit per half under way");
     auto fetch = [&](int i) {
-#pragma unroll
-      for (int hf = 0; hf < HV; ++hf) pg[hf] = page_of(t0 + kw + i * n_kw, hf);
+      pg[0] = page_of(t0 + kw + i * n_kw, 0);
+      if (HV == 2) pg[HV - 1] = shift == 4 ? page_of(t0 + kw + i * n_kw, 1) : pg[0];
     };
     auto issue = [&](int i, int ahead, uint32_t st) {  // tile i into stage st
       if (i < n_tiles) {
         copy(t0 + kw + i * n_kw, pg, st);
 #pragma unroll
-        for (int hf = 0; hf < HV; ++hf) have |= static_cast<uint64_t>(pg[hf] >= 0) << (HV * ahead + hf);
+        for (int hf = 0; hf < HV; ++hf) have |= (pg[hf] >= 0 ? 1u : 0u) << (HV * ahead + hf);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -422,7 +436,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       fetch(i + S);
       const uint32_t st = ring + stage * L::STAGE;
       const int key0 = key_of(t0 + kw + i * n_kw);
-      const uint32_t got = static_cast<uint32_t>(have) & ((1u << HV) - 1);
+      const uint32_t got = have & ((1u << HV) - 1);
       have >>= HV;
       const bool full = got == (1u << HV) - 1 && key0 <= full_hi && (key0 >= full_lo || key0 <= full_sink);
       // ---- S^T = K Q^T

@@ -244,8 +244,8 @@ FL_API size_t fl_attn_decode_workspace_size(const fl_attn_desc* desc);
  *                v_scales : e4m3 [num_pages, Hkv, d / 16, page_size]
  *                A stored value is code * block scale * k_scale (v_scale),
  *                one e4m3 block scale per 16 channels of one token.
- * page_size is a power of two from 16 to 256, d is 64 or 128.  v_scales is
- * block-major so that one load brings the scales of consecutive tokens.
+ * page_size is a power of two from 16 to 256, d is 64 or 128, Hkv * page_size
+ * at most 2^22.  v_scales is block-major so that one load brings the scales of consecutive tokens.
  */
 typedef enum { FL_KV_BF16 = 0, FL_KV_E2M1 = 1 } fl_kv_format;
 

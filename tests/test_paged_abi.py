@@ -58,7 +58,7 @@ CACHES = [
     (dict(k_scale=-1.0, format=1), INV), (dict(k_scale=float("inf"), format=1), INV),
     (dict(k_scale=1e-40, format=1), INV), (dict(k_scale=2.0), INV), (dict(k_scales=P), INV),
     (dict(format=1, v_scales=0), INV), (dict(d=32), UNS), (dict(d=96), UNS), (dict(page_size=24), UNS),
-    (dict(page_size=8), UNS), (dict(page_size=512), UNS), (dict(k=P + 8), ALI), (dict(format=1, k_scales=P + 4), ALI),
+    (dict(page_size=8), UNS), (dict(page_size=512), UNS), (dict(Hkv=1 << 19), UNS), (dict(k=P + 8), ALI), (dict(format=1, k_scales=P + 4), ALI),
 ]
 
 
@@ -66,7 +66,7 @@ CACHES = [
 def test_bad_cache_is_refused_by_both_calls(L, kw, expect):
     c = cache(**kw)
     assert append(L, c, append_desc()) == expect
-    d = decode_desc(d=max(c.d, 1), dv=max(c.d, 1), Lk=max(4 * c.page_size, 1), Hkv=max(c.Hkv, 1))
+    d = decode_desc(d=max(c.d, 1), dv=max(c.d, 1), Lk=max(4 * c.page_size, 1), Hkv=max(c.Hkv, 1), Hq=2 * max(c.Hkv, 1))
     assert decode(L, c, d) == expect
     assert L.fl_attn_paged_decode_workspace_size(ctypes.byref(d), ctypes.byref(c)) == 0
 
