@@ -71,13 +71,41 @@ struct PagedDecodeParams {
   float* opart;              // [grid][2][M][d], normalised
   float* lpart;              // [grid][2][M], log2
   int grid;
+  int cluster;               // CTAs of a cluster that share a unit; 0: the line is cut evenly
   uint32_t* status;
 };
 
-// CTAs of the decode kernel for M rows (every one resident at once), < 0 on a
-// CUDA error.
-int paged_decode_grid(int format, int d, int M, int sm_count);
+// CTAs of a cluster that takes one unit of at most `keys` keys, 0 for the line:
+// a power of two up to the portable 8, no more than one 128-key round of a CTA's
+// warps needs, and all units' clusters resident at once if possible (a second
+// wave costs as much as the first).  Past kClusterKeys per CTA the line's even
+// cut is worth its plan and merge (4 us).
+constexpr int kClusterMax = 8;
+constexpr int64_t kClusterKeys = 1024;
+inline int paged_cluster(int64_t keys, int64_t units, int64_t resident) {
+  int c = 1;
+  while (c < kClusterMax && keys > 128 * static_cast<int64_t>(c) && units * 2 * c <= resident) c *= 2;
+  return keys <= kClusterKeys * c ? c : 0;
+}
 
-cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s);
+// Per format and head dim: resident CTAs per SM of the cluster's or the line's
+// kernel for M rows (< 1 on a CUDA error; call before a launch), and the launch.
+#define FL_DECLARE_PAGED(NAME)                     \
+  int paged_resident_##NAME(int M, bool cluster);  \
+  cudaError_t launch_paged_##NAME(const PagedDecodeParams& p, cudaStream_t s);
+FL_DECLARE_PAGED(bf16_d64)
+FL_DECLARE_PAGED(bf16_d128)
+FL_DECLARE_PAGED(e2m1_d64)
+FL_DECLARE_PAGED(e2m1_d128)
+#undef FL_DECLARE_PAGED
+
+inline int paged_resident(int format, int d, int M, bool cluster) {
+  if (format == KV_BF16) return d == 64 ? paged_resident_bf16_d64(M, cluster) : paged_resident_bf16_d128(M, cluster);
+  return d == 64 ? paged_resident_e2m1_d64(M, cluster) : paged_resident_e2m1_d128(M, cluster);
+}
+inline cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s) {
+  if (format == KV_BF16) return d == 64 ? launch_paged_bf16_d64(p, s) : launch_paged_bf16_d128(p, s);
+  return d == 64 ? launch_paged_e2m1_d64(p, s) : launch_paged_e2m1_d128(p, s);
+}
 
 }  // namespace fl

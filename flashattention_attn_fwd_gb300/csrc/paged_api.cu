@@ -192,7 +192,7 @@ size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv
   uint32_t* status = nullptr;
   if (fl::device_info(&sm_count, &status) != FL_OK) return 0;
   const int M = desc->Hq / desc->Hkv * desc->Lq;
-  const int grid = fl::paged_decode_grid(cache->format, cache->d, M, sm_count);
+  const int grid = fl::paged_resident(cache->format, cache->d, M, false) * sm_count;
   return grid < 1 ? 0 : workspace_layout(*desc, M, grid).bytes;
 }
 
@@ -219,7 +219,7 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   if (st != FL_OK) return st;
   p.G = d.Hq / d.Hkv;
   p.M = p.G * d.Lq;
-  p.grid = fl::paged_decode_grid(cache->format, cache->d, p.M, sm_count);
+  p.grid = fl::paged_resident(cache->format, cache->d, p.M, false) * sm_count;
   if (p.grid < 1) return fl::launch_result("paged decode occupancy", cudaErrorInvalidDeviceFunction);
   const WorkspaceLayout w = workspace_layout(d, p.M, p.grid);
   if (workspace_bytes < w.bytes) return FL_ERR_INVALID_ARG;
@@ -238,6 +238,15 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
     p.window = d.window < kMaxTokens ? d.window : static_cast<int>(kMaxTokens);
     p.sink = d.sink < kMaxTokens ? d.sink : static_cast<int>(kMaxTokens);
   }
+  // keys that one unit reads at most: the table's, or the window's and the sinks'
+  int64_t keys = d.Lk;
+  if (p.window) {
+    const int64_t seen = static_cast<int64_t>(p.window) + d.Lq + p.sink + 64;  // whole tiles at three borders
+    keys = seen < keys ? seen : keys;
+  }
+  const int resident = fl::paged_resident(cache->format, cache->d, p.M, true) * sm_count;
+  if (resident < 1) return fl::launch_result("paged decode occupancy", cudaErrorInvalidDeviceFunction);
+  p.cluster = fl::paged_cluster(keys, static_cast<int64_t>(d.B) * d.Hkv, resident);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.plan = reinterpret_cast<int64_t*>(ws);
   p.opart = reinterpret_cast<float*>(ws + w.opart);

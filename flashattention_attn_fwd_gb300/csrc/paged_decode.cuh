@@ -7,8 +7,12 @@
 // bits.  Bound by reading the cache: per key and head 2 (d / 2 + d / 16)
 // bytes in 4 bits, 4 d in bf16, against 4 d M operations.
 //
-// Work split.  The tiles of 16 keys that some row sees, over all (sequence,
-// key/value head, row block) units, form one line that is cut into equal
+// Work split.  With at most a few thousand keys to read per key/value head (a
+// short cache, or a window), a cluster of CTAs takes each (sequence, head) unit,
+// cuts its tiles evenly and joins the results through distributed shared memory:
+// one launch and no workspace traffic, 6 us against 10 at the smallest sizes.
+// Beyond that lengths matter more: the tiles of 16 keys that some row sees, over all (sequence,
+// key/value head) units, form one line that is cut into equal
 // pieces, one per resident CTA: lengths may differ as they like and every CTA
 // reads the same amount.  A unit inside one piece is finished by its CTA; a
 // unit that pieces share leaves one normalised partial result and log-sum-exp
@@ -38,6 +42,8 @@
 // are exact in fp16; the products run in fp16 with fp32 sums.  The query row
 // is scaled to fp16's range by a power of two (undone in the score), P carries a
 // factor 2^7 so that weights down to 2^-31 of the largest survive in fp16.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -89,6 +95,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
   return r;
+}
+
+// All threads of the cluster's CTAs, with their shared memory made visible.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at shared address `a` of cluster rank `rank`
+__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+               : "=f"(v)
+               : "r"(a), "r"(rank)
+               : "memory");
+  return v;
 }
 
 // Tiles of KT keys of one head of sequence b: `count` of them (at least one),
@@ -165,7 +185,8 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   return v;
 }
 
-template <int FMT, int D, int NT, int RW>
+// CL: a cluster of p.cluster CTAs per unit; else pieces of the line.
+template <int FMT, int D, int NT, int RW, bool CL>
 __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int KS = D / 16;        // k-steps of S, and 16-channel row tiles of O
   constexpr int HV = kHalves<FMT, D>;
@@ -186,59 +207,73 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   const int g = lane >> 2, t4 = lane & 3;
   const int64_t H = p.c.Hkv;        // units (key/value heads) per sequence
 
-  // ---- the plan: tiles per CTA, and this CTA's first sequence
-  auto warp_incl = [&](int64_t v) {
+  int b;                // current sequence
+  int64_t base;         // line position of its first unit
+  int64_t begin, end;   // this CTA's piece of the line
+  SeqTiles sq;
+  if constexpr (CL) {
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+    b = unit / p.c.Hkv;
+    sq = seq_tiles<KT>(p, b);
+    base = 0;
+    const int64_t u0 = static_cast<int64_t>(unit % p.c.Hkv) * sq.count;
+    begin = u0 + static_cast<int64_t>(sq.count) * rank / p.cluster;
+    end = u0 + static_cast<int64_t>(sq.count) * (rank + 1) / p.cluster;
+  } else {
+    // ---- the plan: tiles per CTA, and this CTA's first sequence
+    auto warp_incl = [&](int64_t v) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += u;
-    }
-    return v;
-  };
-  int64_t total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-    const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
-    const int64_t s = warp_incl(c);
-    if (lane == 31) scan_sm[warp] = s;
-    __syncthreads();
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      return v;
+    };
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
+      const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
+      const int64_t s = warp_incl(c);
+      if (lane == 31) scan_sm[warp] = s;
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kPdWarps; ++i) total += scan_sm[i];
-    __syncthreads();
-  }
-  const int64_t all = total * H;
-  const int64_t per = ((all + gridDim.x - 1) / gridDim.x + kPdWarps - 1) / kPdWarps * kPdWarps;
-  const int64_t begin = blockIdx.x * per;
-  const int64_t end = begin + per < all ? begin + per : all;
-  int64_t carry = 0;  // tiles of one head before the chunk's sequences
-  for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-    const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
-    int64_t s = warp_incl(c);
-    if (lane == 31) scan_sm[warp] = s;
-    __syncthreads();
-    int64_t chunk = 0;
+      for (int i = 0; i < kPdWarps; ++i) total += scan_sm[i];
+      __syncthreads();
+    }
+    const int64_t all = total * H;
+    const int64_t per = ((all + gridDim.x - 1) / gridDim.x + kPdWarps - 1) / kPdWarps * kPdWarps;
+    begin = blockIdx.x * per;
+    end = begin + per < all ? begin + per : all;
+    int64_t carry = 0;  // tiles of one head before the chunk's sequences
+    for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
+      const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
+      int64_t s = warp_incl(c);
+      if (lane == 31) scan_sm[warp] = s;
+      __syncthreads();
+      int64_t chunk = 0;
 #pragma unroll
-    for (int i = 0; i < kPdWarps; ++i) {
-      if (i < warp) s += scan_sm[i];
-      chunk += scan_sm[i];
+      for (int i = 0; i < kPdWarps; ++i) {
+        if (i < warp) s += scan_sm[i];
+        chunk += scan_sm[i];
+      }
+      const int64_t before = carry + s - c;
+      if (blockIdx.x == 0 && b0 + tid < p.B) p.plan[2 + b0 + tid] = before;
+      if (c > 0 && before * H <= begin && begin < (before + c) * H) {
+        found_sm = b0 + tid;
+        base_sm = before * H;
+      }
+      carry += chunk;
+      __syncthreads();
     }
-    const int64_t before = carry + s - c;
-    if (blockIdx.x == 0 && b0 + tid < p.B) p.plan[2 + b0 + tid] = before;
-    if (c > 0 && before * H <= begin && begin < (before + c) * H) {
-      found_sm = b0 + tid;
-      base_sm = before * H;
+    if (blockIdx.x == 0 && tid == 0) {
+      p.plan[0] = per;
+      p.plan[1] = all;
     }
-    carry += chunk;
-    __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (begin >= end) return;
+    b = found_sm;
+    base = base_sm;
+    sq = seq_tiles<KT>(p, b);
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    p.plan[0] = per;
-    p.plan[1] = all;
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (begin >= end) return;
-  int b = found_sm;
-  int64_t base = base_sm;  // line position of sequence b's first unit
-  SeqTiles sq = seq_tiles<KT>(p, b);
 
   const int shift = p.c.page_shift;
   const int page_mask = (1 << shift) - 1;
@@ -266,18 +301,19 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   for (int i = 0; i < 4; ++i) vx[i] = ((4 * t4 + i) * KB + g * (FMT == KV_E2M1 ? D / 16 : 16)) ^ (16 * swz_v(4 * t4));
   const uint32_t ksx = kkey * (D / 16) + t4 * (D / 64), vsx = D + 16 * (D == 128 ? g : g >> 1) + 4 * t4;
 
-  for (int64_t cur = begin; cur < end;) {
+  // a rank without tiles still leaves its (empty) part for the cluster
+  for (int64_t cur = begin; cur < end || (CL && cur == begin);) {
     // ---- the unit at `cur`
-    while (cur >= base + sq.count * H) {
+    while (!CL && cur >= base + sq.count * H) {
       base += sq.count * H;
       sq = seq_tiles<KT>(p, ++b);
     }
     const int64_t local = cur - base;
-    const int hkv = static_cast<int>(local / sq.count);
+    const int hkv = CL ? static_cast<int>(blockIdx.x / p.cluster % p.c.Hkv) : static_cast<int>(local / sq.count);
     const int t0 = static_cast<int>(local - static_cast<int64_t>(hkv) * sq.count);
     const int64_t room = t0 + (end - cur);
     const int t1 = room < sq.count ? static_cast<int>(room) : sq.count;
-    const bool whole = t0 == 0 && t1 == sq.count;
+    const bool whole = CL ? p.cluster == 1 : t0 == 0 && t1 == sq.count;
     const int slot = cur == begin ? 0 : 1;
 
     // ---- the ring: tile i of this group is t0 + kw + i * n_kw
@@ -706,12 +742,56 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + hq * p.o_h + i * p.o_l;
         reinterpret_cast<__nv_bfloat162*>(orow)[c2] = __floats2bfloat162_rn(ov.x * inv, ov.y * inv);
         if (c2 == 0 && p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = lse2 * kPLn2;
+      } else if (CL) {
+        float* part = msm + kPdWarps * WR * 2;  // O [M][D], then log-sum-exp [M]
+        *reinterpret_cast<float2*>(part + rr * D + 2 * c2) = make_float2(ov.x * inv, ov.y * inv);
+        if (c2 == 0) part[p.M * D + rr] = lse2;
       } else {
         const int64_t pr = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.M + rr;
         reinterpret_cast<float2*>(p.opart)[pr * CP + c2] = make_float2(ov.x * inv, ov.y * inv);
         if (c2 == 0) p.lpart[pr] = lse2;
       }
     }
+    if (CL && p.cluster > 1) {
+      // ---- the cluster's parts meet: every CTA joins a share of the outputs
+      cluster_barrier();
+      const uint32_t part = ptx::smem_u32(msm + kPdWarps * WR * 2);
+      const int rank = blockIdx.x % p.cluster;
+      for (int e = rank + p.cluster * tid; e < p.M * CP; e += p.cluster * kPdThreads) {
+        const int rr = e / CP, c2 = e % CP;
+        float lse[kClusterMax], Lm = -CUDART_INF_F;
+        float2 ow[kClusterMax];
+#pragma unroll
+        for (int c = 0; c < kClusterMax; ++c) {
+          if (c < p.cluster) {
+            lse[c] = ld_cluster(part + (p.M * D + rr) * 4, c);
+            ow[c] = make_float2(ld_cluster(part + (rr * D + 2 * c2) * 4, c), ld_cluster(part + (rr * D + 2 * c2) * 4 + 4, c));
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kClusterMax; ++c)
+          if (c < p.cluster) Lm = fmaxf(Lm, lse[c]);
+        const float Ls = Lm == -CUDART_INF_F ? 0.f : Lm;
+        float tot = 0.f;
+        float2 ov = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kClusterMax; ++c) {
+          if (c < p.cluster) {
+            const float w = ptx::ex2(lse[c] - Ls);
+            tot += w;
+            ov = make_float2(fmaf(w, ow[c].x, ov.x), fmaf(w, ow[c].y, ov.y));
+          }
+        }
+        const float inv = tot == 0.f ? 0.f : 1.f / tot;
+        const int hq = hkv * p.G + rr / p.Lq, i = rr % p.Lq;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + hq * p.o_h + i * p.o_l;
+        reinterpret_cast<__nv_bfloat162*>(orow)[c2] = __floats2bfloat162_rn(ov.x * inv, ov.y * inv);
+        if (c2 == 0 && p.lse)
+          p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = tot == 0.f ? -CUDART_INF_F : (Ls + __log2f(tot)) * kPLn2;
+      }
+      cluster_barrier();  // no CTA leaves while another reads its part
+    }
+    if (CL) return;
     cur += t1 - t0;
     if (cur < end) __syncthreads();  // the results have been read: the rings may fill again
   }
@@ -782,69 +862,81 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
     p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = tot == 0.f ? -CUDART_INF_F : (Ls + __log2f(tot)) * kPLn2;
 }
 
-template <int FMT, int D, int NT, int RW>
+template <int FMT, int D, int NT, int RW, bool CL>
 constexpr int decode_smem() {
-  constexpr int merge = kPdWarps * 8 * NT * (D + 2) * 4, ring = Ring<FMT, D, RW>::BYTES;
+  // the warps' states, and the CTA's part of a cluster's result
+  constexpr int merge = kPdWarps * 8 * NT * (D + 2) * 4 + (CL ? 8 * NT * RW * (D + 1) * 4 : 0);
+  constexpr int ring = Ring<FMT, D, RW>::BYTES;
   return merge > ring ? merge : ring;
 }
 
-template <int FMT, int D, int NT, int RW>
-int grid_of(int sm_count) {
+// Resident CTAs per SM; sets the kernel's shared-memory limit (< 1 on a CUDA
+// error).
+template <int FMT, int D, int NT, int RW, bool CL>
+int resident() {
   static const int per_sm = [] {
+    constexpr int smem = decode_smem<FMT, D, NT, RW, CL>();
+    auto* kernel = paged_decode_kernel<FMT, D, NT, RW, CL>;
     int n = 0;
-    if (cudaFuncSetAttribute(paged_decode_kernel<FMT, D, NT, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             decode_smem<FMT, D, NT, RW>()) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, paged_decode_kernel<FMT, D, NT, RW>, kPdThreads,
-                                                      decode_smem<FMT, D, NT, RW>()) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kPdThreads, smem) != cudaSuccess)
       return -1;
     return n;
   }();
-  return per_sm < 1 ? -1 : per_sm * sm_count;
+  return per_sm;
 }
 
 template <int FMT, int D, int NT, int RW>
-cudaError_t launch_fdn(const PagedDecodeParams& p, cudaStream_t s) {
-  paged_decode_kernel<FMT, D, NT, RW><<<p.grid, kPdThreads, decode_smem<FMT, D, NT, RW>(), s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the merge's launch overlaps the tiles' work; it waits for it before it reads
+cudaError_t launch_rows(const PagedDecodeParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.Hkv * p.M));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = s;
   cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kPdThreads);
+  cfg.stream = s;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
+  if (p.cluster) {
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.c.Hkv * p.cluster));
+    cfg.dynamicSmemBytes = decode_smem<FMT, D, NT, RW, true>();
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    return cudaLaunchKernelEx(&cfg, paged_decode_kernel<FMT, D, NT, RW, true>, p);
+  }
+  paged_decode_kernel<FMT, D, NT, RW, false><<<p.grid, kPdThreads, decode_smem<FMT, D, NT, RW, false>(), s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the merge's launch overlaps the tiles' work; it waits for it before it reads
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.Hkv * p.M));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p);
+}
+
+// 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
+// (2, 2) and (2, 4)
+template <int FMT, int D, bool CL>
+int resident_ctas(int M) {
+  return M <= 8    ? resident<FMT, D, 1, 1, CL>()
+         : M <= 16 ? resident<FMT, D, 2, 1, CL>()
+         : M <= 32 ? resident<FMT, D, 2, 2, CL>()
+                   : resident<FMT, D, 2, 4, CL>();
+}
+template <int FMT, int D>
+cudaError_t launch_paged(const PagedDecodeParams& p, cudaStream_t s) {
+  return p.M <= 8    ? launch_rows<FMT, D, 1, 1>(p, s)
+         : p.M <= 16 ? launch_rows<FMT, D, 2, 1>(p, s)
+         : p.M <= 32 ? launch_rows<FMT, D, 2, 2>(p, s)
+                     : launch_rows<FMT, D, 2, 4>(p, s);
 }
 
 }  // namespace
 
-// 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
-// (2, 2) and (2, 4)
-#define FL_PAGED_ROWS(CALL, F, D) \
-  return M <= 8 ? CALL(F, D, 1, 1) : M <= 16 ? CALL(F, D, 2, 1) : M <= 32 ? CALL(F, D, 2, 2) : CALL(F, D, 2, 4);
-#define FL_PAGED_DISPATCH(CALL)                    \
-  if (format == KV_BF16) {                         \
-    if (d == 64) FL_PAGED_ROWS(CALL, KV_BF16, 64)  \
-    FL_PAGED_ROWS(CALL, KV_BF16, 128)              \
-  }                                                \
-  if (d == 64) FL_PAGED_ROWS(CALL, KV_E2M1, 64)    \
-  FL_PAGED_ROWS(CALL, KV_E2M1, 128)
-
-int paged_decode_grid(int format, int d, int M, int sm_count) {
-#define FL_CALL(F, D, N, R) grid_of<F, D, N, R>(sm_count)
-  FL_PAGED_DISPATCH(FL_CALL)
-#undef FL_CALL
-}
-
-cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParams& p, cudaStream_t s) {
-  const int M = p.M;
-#define FL_CALL(F, D, N, R) launch_fdn<F, D, N, R>(p, s)
-  FL_PAGED_DISPATCH(FL_CALL)
-#undef FL_CALL
-}
+// The launch functions of one format and head width (a translation unit each).
+#define FL_DEFINE_PAGED(NAME, FMT, D)                                                                             \
+  int paged_resident_##NAME(int M, bool cluster) {                                                                \
+    return cluster ? resident_ctas<FMT, D, true>(M) : resident_ctas<FMT, D, false>(M);                            \
+  }                                                                                                               \
+  cudaError_t launch_paged_##NAME(const PagedDecodeParams& p, cudaStream_t s) { return launch_paged<FMT, D>(p, s); }
 
 }  // namespace fl

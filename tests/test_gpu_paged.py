@@ -87,15 +87,21 @@ DECODE = [
 ]
 
 
+# a table this wide (with missing pages) lets a sequence grow past what a
+# cluster of CTAs takes: the call then cuts all units' tiles as one line
+WIDE = 9000
+
+
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
 @pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(str(x) for x in c[:7]) + "-" + str(c[7][-1]) + "-" +
                          "-".join(f"{a}{b}" for a, b in c[8].items()))
-def test_decode_against_the_oracle(case):
+def test_decode_against_the_oracle(case, wide):
     fmt, B, Hq, Hkv, Lq, d, page, lens, kw = case
     pages = sum(-(-n // page) for n in lens) + 3
     parts, K, V = pool(fmt, pages, Hkv, page, d, seed=d + page, k_scale=0.75 if fmt == "e2m1" else 1.0,
                        v_scale=1.5 if fmt == "e2m1" else 1.0)
     cache = make_cache(parts, k_scale=0.75, v_scale=1.5) if fmt == "e2m1" else make_cache(parts)
-    table = table_for(lens, page, pages, seed=1)
+    table = table_for(lens, page, pages, seed=1, width=-(-WIDE // page) if wide else None)
     g = synth.generator(len(lens) + Hq)
     q = synth.randn_bf16((B, Hq, Lq, d), g)
     if fmt == "e2m1":
@@ -110,15 +116,16 @@ def test_decode_against_the_oracle(case):
     check_decode(out, lse, ref, fmt, q)
 
 
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
-def test_decode_many_pieces_and_row_blocks(fmt):
+def test_decode_many_pieces_and_row_blocks(fmt, wide):
     """Long ragged lengths: units shared by several CTAs, CTAs with several
     units, and M = 64 rows in two row blocks."""
     lens = [4000, 1, 0, 2777, 16, 900, 3333]
     page, Hkv, d = 16, 2, 64
     pages = sum(-(-n // page) for n in lens) + 1
     parts, K, V = pool(fmt, pages, Hkv, page, d, seed=4)
-    table = table_for(lens, page, pages, seed=2)
+    table = table_for(lens, page, pages, seed=2, width=-(-WIDE // page) if wide else None)
     cache = make_cache(parts)
     for G, Lq in ((4, 1), (32, 2)):
         q = (synth.randn_bf16((len(lens), Hkv * G, Lq, d), synth.generator(3)).float() * 0.2).bfloat16()
@@ -135,17 +142,46 @@ def test_decode_many_pieces_and_row_blocks(fmt):
                 check_decode(out[:, h:h + 1], lse[:, h:h + 1], ref, fmt, q[:, h:h + 1])
 
 
-def test_decode_more_sequences_than_threads():
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
+def test_decode_more_sequences_than_threads(wide):
     """B = 300 (the plan scans several chunks), lengths 0 to 70."""
     B, page, Hkv, d = 300, 16, 1, 64
     lens = [(7 * b) % 71 for b in range(B)]
     pages = sum(-(-n // page) for n in lens) + 1
     parts, K, V = pool("bf16", pages, Hkv, page, d, seed=5)
-    table = table_for(lens, page, pages, seed=3)
+    table = table_for(lens, page, pages, seed=3, width=-(-WIDE // page) if wide else None)
     q = synth.randn_bf16((B, 4, 1, d), synth.generator(9))
     out, lse = attn_paged_decode_fwd(q.to(DEV), make_cache(parts), dev(lens, torch.int32), dev(table))
     sync_status()
     check_decode(out, lse, oracle.paged_attention(q, K, V, lens, np.maximum(table, 0)), "bf16", q)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_decode_long_window_cut_as_a_line(fmt):
+    """A window and sinks of more keys than a cluster takes, over stale pages
+    (NaNs) before and between them, several sequences."""
+    B, Hq, Hkv, Lq, d, page = 2, 4, 1, 2, 64, 32
+    W, S = 9000, 70
+    lens, kw = [9400, 300], dict(mask="window", window=W, sink=S)
+    pages = sum(-(-n // page) for n in lens) + 2
+    parts, K, V = pool(fmt, pages, Hkv, page, d, seed=13)
+    table = table_for(lens, page, pages, seed=12)
+    q = (synth.randn_bf16((B, Hq, Lq, d), synth.generator(14)).float() * 0.2).bfloat16()
+    ref = oracle.paged_attention(q, K, V, lens, np.maximum(table, 0), **kw)
+    parts = [t.clone() if t is not None else None for t in parts]
+    for j in range(S, lens[0] - Lq - W + 1):  # keys that no row of sequence 0 sees
+        pg, at = table[0, j // page], j % page
+        if fmt == "bf16":
+            parts[0][pg, :, at] = float("nan")
+            parts[1][pg, :, at] = float("nan")
+        else:
+            parts[2][pg, :, at] = 0x7f
+            parts[3][pg, :, :, at] = 0x7f
+    t2 = table.copy()
+    t2[0, 4:12] = -7
+    out, lse = attn_paged_decode_fwd(q.to(DEV), make_cache(parts), dev(lens, torch.int32), dev(t2), **kw)
+    sync_status()
+    check_decode(out, lse, ref, fmt, q)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
@@ -180,10 +216,11 @@ def test_decode_ignores_what_no_row_sees(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
-def test_decode_reports_a_bad_page_and_recovers(fmt):
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
+def test_decode_reports_a_bad_page_and_recovers(fmt, wide):
     lens, page = [100, 64], 16
     parts, K, V = pool(fmt, 16, 2, page, 64, seed=7)
-    table = table_for(lens, page, 16, seed=5)
+    table = table_for(lens, page, 16, seed=5, width=WIDE // page if wide else None)
     q = (synth.randn_bf16((2, 4, 1, 64), synth.generator(2)).float() * 0.2).bfloat16()
     cache = make_cache(parts)
     for bad in (-1, 16, 2 ** 31 - 1, -2 ** 31):
@@ -211,13 +248,14 @@ def test_decode_lengths_past_the_table_are_clamped():
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
-def test_decode_strides_streams_workspace_and_repeatability(fmt):
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
+def test_decode_strides_streams_workspace_and_repeatability(fmt, wide):
     """Token-major q and out, a table with padded rows, a given workspace with
     a guard, another stream; the same call gives the same bits."""
     B, Hq, Hkv, Lq, d, page = 3, 8, 2, 2, 128, 32
     lens = [1000, 37, 513]
     parts, K, V = pool(fmt, 64, Hkv, page, d, seed=9)
-    table = table_for(lens, page, 64, seed=6)
+    table = table_for(lens, page, 64, seed=6, width=WIDE // page + 1 if wide else None)
     wide = np.full((B, table.shape[1] + 5), 10 ** 7, np.int32)
     wide[:, :table.shape[1]] = table
     tq = (synth.randn_bf16((B, Lq, Hq, d), synth.generator(4)).float() * 0.2).bfloat16()
