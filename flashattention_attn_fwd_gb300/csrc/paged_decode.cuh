@@ -65,6 +65,12 @@ constexpr float kPLn2 = 0.6931471805599453f;
 
 // 16-key halves of a tile: one for bf16 heads of 128 channels, whose 16 keys
 // fill 64 registers, else two, which share the bookkeeping of a tile.
+// Starting a unit (queries, pages, the first copies, the join at its end) costs
+// a CTA about as long as this many tiles; the line counts them before each
+// unit's own, so that a CTA that starts a second unit gets fewer tiles.
+template <int FMT, int D>
+constexpr int kLead = FMT == KV_BF16 ? 28 : 16;
+
 template <int FMT, int D>
 constexpr int kHalves = FMT == KV_BF16 && D == 128 ? 1 : 2;
 
@@ -206,6 +212,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   const int64_t H = p.c.Hkv;        // units (key/value heads) per sequence
+  constexpr int LEAD = kLead<FMT, D>;
 
   int b;                // current sequence
   int64_t base;         // line position of its first unit
@@ -216,9 +223,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     b = unit / p.c.Hkv;
     sq = seq_tiles<KT>(p, b);
     base = 0;
-    const int64_t u0 = static_cast<int64_t>(unit % p.c.Hkv) * sq.count;
-    begin = u0 + static_cast<int64_t>(sq.count) * rank / p.cluster;
-    end = u0 + static_cast<int64_t>(sq.count) * (rank + 1) / p.cluster;
+    begin = static_cast<int64_t>(sq.count) * rank / p.cluster;
+    end = static_cast<int64_t>(sq.count) * (rank + 1) / p.cluster;
   } else {
     // ---- the plan: tiles per CTA, and this CTA's first sequence
     auto warp_incl = [&](int64_t v) {
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     };
     int64_t total = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-      const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
+      const int64_t c = b0 + tid < p.B ? LEAD + seq_tiles<KT>(p, b0 + tid).count : 0;
       const int64_t s = warp_incl(c);
       if (lane == 31) scan_sm[warp] = s;
       __syncthreads();
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     end = begin + per < all ? begin + per : all;
     int64_t carry = 0;  // tiles of one head before the chunk's sequences
     for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-      const int64_t c = b0 + tid < p.B ? seq_tiles<KT>(p, b0 + tid).count : 0;
+      const int64_t c = b0 + tid < p.B ? LEAD + seq_tiles<KT>(p, b0 + tid).count : 0;
       int64_t s = warp_incl(c);
       if (lane == 31) scan_sm[warp] = s;
       __syncthreads();
@@ -268,7 +274,6 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       p.plan[0] = per;
       p.plan[1] = all;
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (begin >= end) return;
     b = found_sm;
     base = base_sm;
@@ -304,15 +309,32 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
   // a rank without tiles still leaves its (empty) part for the cluster
   for (int64_t cur = begin; cur < end || (CL && cur == begin);) {
     // ---- the unit at `cur`
-    while (!CL && cur >= base + sq.count * H) {
-      base += sq.count * H;
-      sq = seq_tiles<KT>(p, ++b);
+    int hkv, t0, t1;
+    int64_t next;
+    if constexpr (CL) {
+      hkv = blockIdx.x / p.cluster % p.c.Hkv;
+      t0 = static_cast<int>(begin);
+      t1 = static_cast<int>(end);
+      next = end;
+    } else {
+      while (cur >= base + (LEAD + sq.count) * H) {
+        base += (LEAD + sq.count) * H;
+        sq = seq_tiles<KT>(p, ++b);
+      }
+      const int64_t local = cur - base;
+      const int len = LEAD + sq.count;
+      hkv = static_cast<int>(local / len);
+      const int at = static_cast<int>(local - static_cast<int64_t>(hkv) * len);
+      const int64_t room = at + (end - cur);
+      const int to = room < len ? static_cast<int>(room) : len;
+      t0 = max(at - LEAD, 0);
+      t1 = to - LEAD;
+      next = cur + (to - at);
+      if (t1 <= t0) {  // the piece ends within a unit's lead
+        cur = next;
+        continue;
+      }
     }
-    const int64_t local = cur - base;
-    const int hkv = CL ? static_cast<int>(blockIdx.x / p.cluster % p.c.Hkv) : static_cast<int>(local / sq.count);
-    const int t0 = static_cast<int>(local - static_cast<int64_t>(hkv) * sq.count);
-    const int64_t room = t0 + (end - cur);
-    const int t1 = room < sq.count ? static_cast<int>(room) : sq.count;
     const bool whole = CL ? p.cluster == 1 : t0 == 0 && t1 == sq.count;
     const int slot = cur == begin ? 0 : 1;
 
@@ -792,7 +814,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       cluster_barrier();  // no CTA leaves while another reads its part
     }
     if (CL) return;
-    cur += t1 - t0;
+    cur = next;
     if (cur < end) __syncthreads();  // the results have been read: the rings may fill again
   }
 }
@@ -801,10 +823,9 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 // per query row, its warps taking the pieces in turn.
 constexpr int kMergeWarps = 4;
 template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ PagedDecodeParams p, int lead) {
   __shared__ float osm[kMergeWarps][D];
   __shared__ float wsm[kMergeWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t H = p.c.Hkv;
   const int64_t row = blockIdx.x;  // (sequence, key/value head, row of the group)
   const int m = static_cast<int>(row % p.M);
@@ -813,13 +834,13 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   const int64_t per = p.plan[0];
   const int64_t before = p.plan[2 + b];
   const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : p.plan[1] / H) - before;
-  const int64_t first = before * H + hkv * count;
-  const int64_t c0 = first / per, c1 = (first + count - 1) / per;
+  const int64_t first = before * H + hkv * count;  // count: the unit's lead, then its tiles
+  const int64_t c0 = (first + lead) / per, c1 = (first + count - 1) / per;
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // piece i: CTA c0 + i; the first CTA's piece is its second one unless it starts there
   const int n = static_cast<int>(c1 - c0) + 1;
-  const int64_t head = (c0 * 2 + (first == c0 * per ? 0 : 1)) * p.M + m;
+  const int64_t head = (c0 * 2 + (first <= c0 * per ? 0 : 1)) * p.M + m;
   auto part = [&](int i) { return i == 0 ? head : (c0 + i) * 2 * p.M + m; };
   float L = -CUDART_INF_F;
   for (int i = lane; i < n; i += 32) L = fmaxf(L, p.lpart[part(i)]);
@@ -888,15 +909,15 @@ int resident() {
 
 template <int FMT, int D, int NT, int RW>
 cudaError_t launch_rows(const PagedDecodeParams& p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute at{};
-  cfg.blockDim = dim3(kPdThreads);
-  cfg.stream = s;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
   if (p.cluster) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.c.Hkv * p.cluster));
+    cfg.blockDim = dim3(kPdThreads);
     cfg.dynamicSmemBytes = decode_smem<FMT, D, NT, RW, true>();
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
     at.id = cudaLaunchAttributeClusterDimension;
     at.val.clusterDim.x = static_cast<unsigned>(p.cluster);
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
@@ -905,12 +926,8 @@ cudaError_t launch_rows(const PagedDecodeParams& p, cudaStream_t s) {
   paged_decode_kernel<FMT, D, NT, RW, false><<<p.grid, kPdThreads, decode_smem<FMT, D, NT, RW, false>(), s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // the merge's launch overlaps the tiles' work; it waits for it before it reads
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * p.c.Hkv * p.M));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<D>, p);
+  paged_merge_kernel<D><<<static_cast<unsigned>(p.B * p.c.Hkv * p.M), 32 * kMergeWarps, 0, s>>>(p, kLead<FMT, D>);
+  return cudaGetLastError();
 }
 
 // 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
