@@ -817,9 +817,10 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
 #pragma unroll
   for (int i = 0; i < ZPL / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (sub == 0) {
-    p.dvec[row] = s * p.dout_scale;
+    const int64_t vrow = p.Lq_pad == p.Lq ? row : row / p.Lq * p.Lq_pad + row % p.Lq;
+    p.dvec[vrow] = s * p.dout_scale;
     const float l = p.lse[row];
-    p.l2[row] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+    p.l2[vrow] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
   }
 }
 
@@ -872,7 +873,7 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
   }();
   if (checked != cudaSuccess) return checked;
   cudaError_t e;
-  if (p.sink) {
+  if (p.sink && few_keys(p.window, p.sink, p.Lq)) {
     e = launch_bwd_dot(D, DV, SCORE, p, s);
   } else {
     const int rgrid = static_cast<int>((p.rows + 256 / (DV / 8) - 1) / (256 / (DV / 8)));

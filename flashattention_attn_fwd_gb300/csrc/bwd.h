@@ -66,18 +66,30 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
   s.tiles = ((sink < Lk ? sink : Lk) + 127) / 128;
   const int far = nq - far_begin(0, window);
   if (far <= 0) return SinkSplit{0, 0, 0};  // every query is within the first tile's window
-  // walks about as long as a window tile's, on no more CTAs than a few waves
+  // A walk costs its tiles and, at its two ends, about three more, so runs are
+  // as long as balance allows: half of an SM's share of all tiles (they start
+  // first), and no shorter than a window tile's walk.
   const int near = far_begin(0, window);
-  int64_t want = (far + near - 1) / near;
-  const int64_t most = (608 + static_cast<int64_t>(B) * Hkv * s.tiles - 1) / (static_cast<int64_t>(B) * Hkv * s.tiles);
-  want = want < most ? want : most;
+  const int64_t steps = static_cast<int64_t>(B) * Hkv * ((Lk + 127) / 128 * static_cast<int64_t>(near) + static_cast<int64_t>(far) * s.tiles);
+  const int64_t share = steps / (2 * 152);
+  const int64_t most = share > near ? share : near;
+  const int64_t want = (far + most - 1) / most;
   s.len = static_cast<int>((far + want - 1) / want);
   s.chunks = (far + s.len - 1) / s.len;
   return s;
 }
 
-// D, L2 and a zeroed dQ accumulator with sinks (sum P dP from the scores; the
-// plain backward's pre-kernel takes dO . O); (d, dv) as below.
+// With sinks: does D need the scores (launch_bwd_dot), or does dO . O do?  Where
+// rows see few keys the rounding of O shows: relative error of dQ against 64 bits
+// 2.4e-3 from the scores at any size; from O 4.6e-3 at 4 tokens, 3.0e-3 at 16,
+// 2.7e-3 at windows of 8, 2.5e-3 at windows of 64 and 2.4e-3 at 256 (the first
+// rows of a short sequence count as such a window).  The scores cost 40 us of
+// 200 at B 4 H 16 L 2048 window 256, 3 us at 300 tokens.
+inline bool few_keys(int window, int sink, int Lq) {
+  return static_cast<int64_t>(window) + sink <= 64 || Lq <= 512;
+}
+
+// D, L2 and a zeroed dQ accumulator from the scores (sum P dP); (d, dv) as below.
 cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
 
 // (d, dv): (32, 32), (64, 64), (128, 128) or (64, 128)

@@ -1,18 +1,19 @@
 // D_i = sum_j P_ij dP_ij of the windowed backward with sinks, from the scores.
 //
 // dS = P (dP - D) cancels where a row's weight sits on one key: dP of that key
-// and D are then nearly equal.  D is commonly taken as dO . O with the output
+// and D are then nearly equal.  D is otherwise taken as dO . O with the output
 // that the forward returned, whose bf16 rounding (2^-9 of |O|, and that of P
-// before it) then is the error of the difference; windows of a few keys, which
-// leave a row little else to attend to, bring that out (relative error of dQ
-// 5e-3 against 2.4e-3 with D from here, at windows of one to four keys).  So
-// this kernel forms S = Q K^T and dP = dO V^T once more over the visible keys
-// and sums P dP in 32 bits: P = 2^(t log2 e - L2) needs no running maximum, as
-// the log-sum-exp is known.
+// before it) then is the error of the difference; rows of a few keys, which
+// have little else to attend to, bring that out (few_keys in bwd.h has the
+// figures and the rule).  So this kernel forms S = Q K^T and dP = dO V^T once
+// more over the visible keys and sums P dP in 32 bits: P = 2^(t log2 e - L2) needs
+// no running maximum, as the log-sum-exp is known.
 //
-// One CTA takes 64 query rows of one head, 16 per warp; keys come in tiles of
-// 64 through a two-stage cp.async ring; both products are warp-level m16n8k16
-// tiles whose accumulators (16 x 64 of S and of dP) stay in registers.  No
+// One CTA takes 64 query rows of one head, 16 per warp; keys come in tiles of 64
+// through a two-stage cp.async ring; both products are warp-level m16n8k16
+// tiles whose accumulators stay in registers.  Larger blocks read K and V less
+// often but leave fewer of them to hide each other's waits: 128 rows in 8 warps
+// and 32 rows per warp were 15 and 20 us slower at B 4 H 16 L 2048 d 64.  No
 // accumulator outlives a tile, so there is nothing for TMEM to hold; bound by
 // the tensor core's warp-level rate and by the exponentials.
 #include <cuda_bf16.h>
@@ -136,7 +137,13 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
   const float kcap = p.softcap * kDotLog2e, zmul = SCORE == 2 ? 2.0f * sc / p.softcap : 0.f;
   if (SCORE == 1) slope2 = __ldg(p.slopes + h) * kDotLog2e;
 
+  // P = 2^(t log2 e - L2) of a raw score x, key j, row[w]
   float sum[2] = {0.f, 0.f};
+  auto weight = [&](float x, int j, int w) {
+    if (SCORE == 1) return ptx::ex2(fmaf(x, sc, fmaf(slope2, static_cast<float>(j - row[w]), -l2[w])));
+    if (SCORE == 2) return ptx::ex2(fmaf(-2.0f * kcap, ptx::rcp(1.0f + ptx::ex2(x * zmul)), kcap - l2[w]));
+    return ptx::ex2(fmaf(x, sc, -l2[w]));
+  };
   for (int i = 0; i < n_tiles; ++i) {
     if (i + 1 < n_tiles) {
       load(i + 1);
@@ -147,21 +154,25 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
     __syncthreads();
     const uint32_t ks = sm + (i & 1) * STAGE, vs = ks + kDotKeys * D * 2;
     const int j0 = (i < nw ? w0 + i : i - nw) * kDotKeys;
-    // the interval that each of this lane's two rows sees in this tile
+    // the interval that each of this lane's two rows sees in this tile, and the
+    // warp's 16 rows' smallest and largest ends
+    const bool win_tile = i < nw;
     int lo[2], hi[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int first = max(row[e] - win + 1, 0);
-      lo[e] = i < nw ? first : 0;
-      hi[e] = !live[e] ? -1 : i < nw ? row[e] : min(p.sink, first) - 1;
+      lo[e] = win_tile ? first : 0;
+      hi[e] = !live[e] ? -1 : win_tile ? row[e] : min(p.sink, first) - 1;
     }
-    const int first_row = r0 + warp * 16, last_row = min(first_row + 15, p.Lq - 1);
-    const int lo_min = i < nw ? max(first_row - win + 1, 0) : 0;
-    const int hi_max = i < nw ? last_row : min(p.sink, max(last_row - win + 1, 0)) - 1;
-#pragma unroll
+    const int ra = r0 + warp * 16, rz = min(ra + 15, p.Lq - 1);
+    const int fa = max(ra - win + 1, 0), fz = max(rz - win + 1, 0);
+    const int lo_min = win_tile ? fa : 0, lo_max = win_tile ? fz : 0;
+    const int hi_min = ra + 15 >= p.Lq ? -1 : win_tile ? ra : min(p.sink, fa) - 1;
+    const int hi_max = win_tile ? rz : min(p.sink, fz) - 1;
+#pragma unroll 1
     for (int n2 = 0; n2 < kDotKeys / 16; ++n2) {
-      // blocks that none of the warp's 16 rows sees (warp-uniform): a third of
-      // them at a window of 256 and few sinks
+      // blocks that none of the warp's rows sees (a third of them at a window of
+      // 256 and few sinks)
       const int jb = j0 + n2 * 16;
       if (jb > hi_max || jb + 15 < lo_min) continue;
       // 16 keys: matrices (keys 0-7 | 8-15) x (channels 0-7 | 8-15) of a k-step
@@ -181,17 +192,22 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
         mma(dp[0], da[kk], r[0], r[1]);
         mma(dp[1], da[kk], r[2], r[3]);
       }
+      if (jb >= lo_max && jb + 15 <= hi_min) {  // all of the warp's rows see all of it
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = j0 + n2 * 16 + m * 8 + 2 * t4 + (e & 1), w = e >> 1;
-          float t = s[m][e] * sc;
-          if (SCORE == 1) t = fmaf(slope2, static_cast<float>(j - row[w]), t);
-          if (SCORE == 2) t = fmaf(-2.0f * kcap, ptx::rcp(1.0f + ptx::ex2(s[m][e] * zmul)), kcap);
-          const float pv = j >= lo[w] && j <= hi[w] ? ptx::ex2(t - l2[w]) : 0.f;
-          sum[w] = fmaf(pv, dp[m][e], sum[w]);
-        }
+          for (int e = 0; e < 4; ++e)
+            sum[e >> 1] = fmaf(weight(s[n][e], jb + n * 8 + 2 * t4 + (e & 1), e >> 1), dp[n][e], sum[e >> 1]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = jb + n * 8 + 2 * t4 + (e & 1), w = e >> 1;
+            const float pv = j >= lo[w] && j <= hi[w] ? weight(s[n][e], j, w) : 0.f;
+            sum[w] = fmaf(pv, dp[n][e], sum[w]);
+          }
+      }
     }
     __syncthreads();  // the stage may be refilled
   }

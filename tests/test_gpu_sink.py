@@ -11,7 +11,9 @@ too, and the result is rounded: (2 ds + 2^-8) sum P |v| + 2^-8 |out|.
 Backward.  dV = P^T dO with P in bf16: (ds + 2^-8) sum P |dO| + 2^-8 |dv|.
 dS = P (dP - D) (1 - tanh^2): dP is an fp32 sum, off by eP = 2^-22 (dv + 8) sum
 |dO v|; D = sum P dP is summed in fp32 from such products, off by eD = sum P
-(2 ds |dP| + eP); the difference and sech^2 (fp16 pairs, 2^-11 of 1) and dS
+(2 ds |dP| + eP) where rows see few keys (window + sink <= 64, or L <= 512), else
+it is dO . O with the forward's O, off by the forward's bound: eD = sum |dO| eO;
+the difference and sech^2 (fp16 pairs, 2^-11 of 1) and dS
 itself (bf16, 2^-8) are rounded:
 eS = P (eD + eP) + (ds + 2^-8 + 2^-20) |dS| + 2^-11 P |dP - D| (softcap).
 Query 0 sees one key: its dS is zero.
@@ -66,7 +68,8 @@ def _bounds(q, k, v, dout, window, sink, score_mod="none", slopes=None, softcap=
             dS = P * df * sech
             dS[0] = 0.0
             eP = 2.0 ** -22 * (dv + 8) * (np.abs(D0) @ np.abs(v[b, g]).T)
-            eD = (P * (2 * ds * np.abs(dP) + eP)).sum(1, keepdims=True)
+            few = window + sink <= 64 or L <= 512
+            eD = (P * (2 * ds * np.abs(dP) + eP)).sum(1, keepdims=True) if few else (np.abs(D0) * eo).sum(1, keepdims=True)
             eS = P * (eD + eP) + (ds + 2.0 ** -8 + 2.0 ** -20) * np.abs(dS)
             if softcap:
                 eS = eS + 2.0 ** -11 * P * np.abs(df)
