@@ -18,7 +18,11 @@
 //
 // A product and a sum are rounded separately (no fused multiply-add), so that
 // a value next to a rounding border of the 4-bit code falls to the side that
-// the definition says.
+// the definition says.  The code of u / s is decided on the correctly rounded
+// quotient: with r = 1 / s correctly rounded, q = u r and one residual step q +
+// r (u - q s) give it (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990), three operations where the general
+// division takes a dozen.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,6 +37,11 @@ namespace {
 
 constexpr int kAppThreads = 128;
 constexpr float kSixth = 1.0f / 6.0f;
+// Above this a block saturates its scale: its values are clamped first, so that
+// an infinite one goes through the quotient's residual.
+constexpr float kBlockMax = 448.0f * 6.0f;
+
+enum Rope : int { ROPE_NONE = 0, ROPE_HALF = 1, ROPE_PAIRS = 2 };
 
 // Sequence of row t: the number of seq_offsets[1..] that are <= t, found by
 // narrowing 32-fold (a warp-wide count a step); B when t is past the last.
@@ -49,7 +58,17 @@ __device__ __forceinline__ int sequence_of(const int32_t* offsets, int B, int t,
   return lo;
 }
 
-template <int FMT, int D>
+__device__ __forceinline__ void unpack8(const uint4& w, float2 (&x)[4]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
+  return make_uint4(ptx::pack_bf16x2(x[0].x, x[0].y), ptx::pack_bf16x2(x[1].x, x[1].y), ptx::pack_bf16x2(x[2].x, x[2].y),
+                    ptx::pack_bf16x2(x[3].x, x[3].y));
+}
+
+template <int FMT, int D, int ROPE>
 __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPS = 32 / LPR;     // rows a warp handles at once
@@ -72,7 +91,7 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const __grid_con
   const int page_size = 1 << p.c.page_shift;
   const int col = pos >> p.c.page_shift;
   int page = -1;
-  if (col < p.max_pages && (p.rope_dim == 0 || pos < p.rope_positions)) page = __ldg(p.table + b * p.table_stride + col);
+  if (col < p.max_pages && (ROPE == ROPE_NONE || pos < p.rope_positions)) page = __ldg(p.table + b * p.table_stride + col);
   if (page < 0 || page >= p.c.num_pages) {
     if (lane == 0 && part == 0) atomicOr(p.status, 2u);
     return;
@@ -80,144 +99,158 @@ __global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const __grid_con
   const int at = pos & (page_size - 1);
   const int sub = lane / LPR, c8 = lane % LPR;
   const int c0 = 8 * c8;
-  // this lane's rotation: cs[e], sn[e] of channel c0 + e, the sign of sin
-  // folded in (y = x cos + partner * sn; the partner of the first channel of
-  // a pair enters with -sin)
-  const bool turn = c0 < p.rope_dim;
+  // this lane's rotation: cs, sn of channels c0 .. c0 + 7 in pairs, the sign of
+  // sin folded in (y = x cos + partner * sn; the partner of the first channel
+  // of a pair enters with -sin)
+  const bool turn = ROPE != ROPE_NONE && c0 < p.rope_dim;
   const int half = p.rope_dim >> 1;
-  const bool second = !p.interleaved && c0 >= half;
-  const int partner = turn && !p.interleaved ? sub * LPR + (second ? c0 - half : c0 + half) / 8 : lane;
-  float cs[8], sn[8];
+  const bool second = ROPE == ROPE_HALF && c0 >= half;
+  const int partner = turn && ROPE == ROPE_HALF ? sub * LPR + (second ? c0 - half : c0 + half) / 8 : lane;
+  float2 cs[4], sn[4];
   if (turn) {
     const int64_t row = static_cast<int64_t>(pos) * half;
-    if (p.interleaved) {
+    if (ROPE == ROPE_PAIRS) {
       const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cos + row + c0 / 2));
       const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sin + row + c0 / 2));
-      cs[0] = cs[1] = c4.x; cs[2] = cs[3] = c4.y; cs[4] = cs[5] = c4.z; cs[6] = cs[7] = c4.w;
-      sn[1] = s4.x; sn[3] = s4.y; sn[5] = s4.z; sn[7] = s4.w;
-      sn[0] = -s4.x; sn[2] = -s4.y; sn[4] = -s4.z; sn[6] = -s4.w;
+      const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        cs[e] = make_float2(cc[e], cc[e]);
+        sn[e] = make_float2(-ss[e], ss[e]);
+      }
     } else {
       const float4* cp = reinterpret_cast<const float4*>(p.cos + row + (second ? c0 - half : c0));
       const float4* sp = reinterpret_cast<const float4*>(p.sin + row + (second ? c0 - half : c0));
       const float4 ca = __ldg(cp), cb = __ldg(cp + 1), sa = __ldg(sp), sb = __ldg(sp + 1);
       const float f = second ? 1.f : -1.f;
-      cs[0] = ca.x; cs[1] = ca.y; cs[2] = ca.z; cs[3] = ca.w; cs[4] = cb.x; cs[5] = cb.y; cs[6] = cb.z; cs[7] = cb.w;
-      sn[0] = f * sa.x; sn[1] = f * sa.y; sn[2] = f * sa.z; sn[3] = f * sa.w;
-      sn[4] = f * sb.x; sn[5] = f * sb.y; sn[6] = f * sb.z; sn[7] = f * sb.w;
+      cs[0] = make_float2(ca.x, ca.y); cs[1] = make_float2(ca.z, ca.w);
+      cs[2] = make_float2(cb.x, cb.y); cs[3] = make_float2(cb.z, cb.w);
+      sn[0] = make_float2(f * sa.x, f * sa.y); sn[1] = make_float2(f * sa.z, f * sa.w);
+      sn[2] = make_float2(f * sb.x, f * sb.y); sn[3] = make_float2(f * sb.z, f * sb.w);
     }
   }
-  const int Hkv = p.c.Hkv;
-  const int rows = p.Hq + 2 * Hkv;  // q heads, then k heads, then v heads
-  const int groups = (rows + RPS - 1) / RPS;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_t;
-  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + t * p.k_t;
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v) + t * p.v_t;
-  for (int g0 = part; g0 < groups; g0 += NB * p.splits) {
-    uint4 raw[NB];
+  auto rotate = [&](const uint4& raw, float2 (&x)[4]) {
+    float2 y[4];
+    if (ROPE == ROPE_HALF) {
+      const uint4 o = make_uint4(__shfl_sync(0xffffffffu, raw.x, partner), __shfl_sync(0xffffffffu, raw.y, partner),
+                                 __shfl_sync(0xffffffffu, raw.z, partner), __shfl_sync(0xffffffffu, raw.w, partner));
+      unpack8(o, y);
+    } else if (ROPE == ROPE_PAIRS) {
 #pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      const int r = (g0 + u * p.splits) * RPS + sub;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        const __nv_bfloat16* src = r < p.Hq ? q + r * p.q_h
-                                   : r < p.Hq + Hkv ? k + (r - p.Hq) * p.k_h
-                                                    : v + (r - p.Hq - Hkv) * p.v_h;
-        raw[u] = *reinterpret_cast<const uint4*>(src + c0);
-      }
+      for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].y, x[e].x);
     }
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      if (g0 + u * p.splits >= groups) break;
-      const int r = (g0 + u * p.splits) * RPS + sub;
-      const uint32_t own[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-      float x[8];
+    if (ROPE != ROPE_NONE && turn) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(own[e] << 16);
-        x[2 * e + 1] = __uint_as_float(own[e] & 0xffff0000u);
-      }
-      const bool is_v = r >= p.Hq + Hkv;
-      if (p.rope_dim) {
-        float y[8];
-        if (p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t o = __shfl_sync(0xffffffffu, own[e], partner);
-            y[2 * e] = __uint_as_float(o << 16);
-            y[2 * e + 1] = __uint_as_float(o & 0xffff0000u);
-          }
-        }
-        if (turn && !is_v) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __fadd_rn(__fmul_rn(x[e], cs[e]), __fmul_rn(y[e], sn[e]));
-        }
-      }
-      const uint4 rounded = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
-                                       ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
-      const int h = is_v ? r - p.Hq - Hkv : r - p.Hq;  // key/value head
-      if (FMT == KV_BF16) {
-        if (r < p.Hq) {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + t * p.qo_t + r * p.qo_h + c0) = rounded;
-        } else if (r < rows) {
-          const int64_t slot = ((static_cast<int64_t>(page) * Hkv + h) << p.c.page_shift) + at;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.c.v : p.c.k) + slot * D + c0) = rounded;
-          if (p.k_out) {
-            __nv_bfloat16* o = is_v ? static_cast<__nv_bfloat16*>(p.v_out) + t * p.vo_t + h * p.vo_h
-                                    : static_cast<__nv_bfloat16*>(p.k_out) + t * p.ko_t + h * p.ko_h;
-            *reinterpret_cast<uint4*>(o + c0) = rounded;
-          }
-        }
-      } else {
-        const float inv = is_v ? p.inv_v_scale : p.inv_k_scale;
-        float a = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          // q rows keep x (stored below); their u is not used
-          a = fmaxf(a, fabsf(__fmul_rn(x[e], inv)));
-        }
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        if (r < p.Hq) {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) + t * p.qo_t + r * p.qo_h + c0) = rounded;
-        } else if (r < rows) {
-          const uint32_t s8 = cvt4::to_e4m3(__fmul_rn(a, kSixth));
-          const float s = cvt4::unpack_f16x2(cvt4::from_e4m3x2(s8)).x;
-          float z[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = s > 0.f ? __fdiv_rn(__fmul_rn(x[e], inv), s) : 0.f;
-          const uint32_t code = cvt4::to_e2m1x8(z);
-          const int64_t run = (static_cast<int64_t>(page) * Hkv + h) << p.c.page_shift;  // tokens before this head
-          const int64_t slot = run + at;
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + slot * (D / 2) + c0 / 2) = code;
-          if ((c8 & 1) == 0) {
-            if (is_v) p.c.vs[run * (D / kScaleBlock) + (static_cast<int64_t>(c8 >> 1) << p.c.page_shift) + at] = s8;
-            else p.c.ks[slot * (D / kScaleBlock) + (c8 >> 1)] = s8;
-          }
-          if (p.k_out) {
-            const float g = is_v ? p.c.v_scale : p.c.k_scale;
-            uint32_t hv[4], o4[4];
-            cvt4::from_e2m1x8(code, hv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = cvt4::unpack_f16x2(hv[e]);
-              o4[e] = ptx::pack_bf16x2(__fmul_rn(__fmul_rn(f.x, s), g), __fmul_rn(__fmul_rn(f.y, s), g));
-            }
-            __nv_bfloat16* o = is_v ? static_cast<__nv_bfloat16*>(p.v_out) + t * p.vo_t + h * p.vo_h
-                                    : static_cast<__nv_bfloat16*>(p.k_out) + t * p.ko_t + h * p.ko_h;
-            *reinterpret_cast<uint4*>(o + c0) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-          }
-        }
+        // scalar: the packed product and sum came out fused
+        x[e].x = __fadd_rn(__fmul_rn(x[e].x, cs[e].x), __fmul_rn(y[e].x, sn[e].x));
+        x[e].y = __fadd_rn(__fmul_rn(x[e].y, cs[e].y), __fmul_rn(y[e].y, sn[e].y));
       }
     }
+  };
+  // Rows r = part-th, (part + splits)-th ... group of `heads` rows of a tensor,
+  // NB groups in flight; `first`: groups before this tensor's.
+  auto for_rows = [&](const void* base, int64_t st, int64_t sh, int heads, int first, auto&& row) {
+    const int groups = (heads + RPS - 1) / RPS;
+    int g = (part - first) % p.splits;
+    if (g < 0) g += p.splits;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(base) + t * st + c0;
+    for (; g < groups; g += NB * p.splits) {
+      uint4 raw[NB];
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const int r = (g + u * p.splits) * RPS + sub;
+        raw[u] = r < heads ? *reinterpret_cast<const uint4*>(src + r * sh) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        if (g + u * p.splits >= groups) break;
+        const int r = (g + u * p.splits) * RPS + sub;
+        row(raw[u], r, r < heads);
+      }
+    }
+  };
+  const int Hkv = p.c.Hkv;
+  const int q_groups = (p.Hq + RPS - 1) / RPS, k_groups = (Hkv + RPS - 1) / RPS;
+  if (p.Hq) {
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.q_out) + t * p.qo_t + c0;
+    for_rows(p.q, p.q_t, p.q_h, p.Hq, 0, [&](const uint4& raw, int r, bool ok) {
+      float2 x[4];
+      unpack8(raw, x);
+      rotate(raw, x);
+      if (ok) *reinterpret_cast<uint4*>(dst + r * p.qo_h) = pack8(x);
+    });
   }
+  // stores row h of K or V: cache (and the values that it now holds)
+  auto store = [&](float2 (&x)[4], int h, bool ok, bool is_v, void* pool, uint8_t* scales, float inv, float scale,
+                   void* out, int64_t ot, int64_t oh) {
+    const int64_t run = (static_cast<int64_t>(page) * Hkv + h) << p.c.page_shift;  // tokens before this head
+    const int64_t slot = run + at;
+    uint4 held;
+    if constexpr (FMT == KV_BF16) {
+      held = pack8(x);
+      if (ok) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + slot * D + c0) = held;
+    } else {
+      const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = ptx::mul2(x[e], inv2);
+      float a = fmaxf(fabsf(x[0].x), fabsf(x[0].y));
+#pragma unroll
+      for (int e = 1; e < 4; ++e) a = ptx::max3(a, fabsf(x[e].x), fabsf(x[e].y));
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      const uint32_t s8 = cvt4::to_e4m3(__fmul_rn(a, kSixth));
+      const float s = cvt4::unpack_f16x2(cvt4::from_e4m3x2(s8)).x;
+      if (a > kBlockMax) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = make_float2(fminf(fmaxf(x[e].x, -2.f * kBlockMax), 2.f * kBlockMax),
+                             fminf(fmaxf(x[e].y, -2.f * kBlockMax), 2.f * kBlockMax));
+      }
+      const float rs = s > 0.f ? __frcp_rn(s) : 0.f;  // a zero scale: all codes zero
+      const float2 rs2 = make_float2(rs, rs), ns2 = make_float2(-s, -s);
+      float z[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 q = ptx::mul2(x[e], rs2);
+        const float2 f = ptx::fma2(ptx::fma2(q, ns2, x[e]), rs2, q);
+        z[2 * e] = s > 0.f ? f.x : 0.f;
+        z[2 * e + 1] = s > 0.f ? f.y : 0.f;
+      }
+      const uint32_t code = cvt4::to_e2m1x8(z);
+      if (ok) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(pool) + slot * (D / 2) + c0 / 2) = code;
+        if ((c8 & 1) == 0)
+          scales[is_v ? run * (D / kScaleBlock) + (static_cast<int64_t>(c8 >> 1) << p.c.page_shift) + at
+                      : slot * (D / kScaleBlock) + (c8 >> 1)] = s8;
+      }
+      if (out) {
+        uint32_t hv[4];
+        cvt4::from_e2m1x8(code, hv);
+        const float2 s2 = make_float2(s, s), g2 = make_float2(scale, scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = ptx::mul2(ptx::mul2(cvt4::unpack_f16x2(hv[e]), s2), g2);
+        held = pack8(x);
+      }
+    }
+    if (out && ok) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + t * ot + h * oh + c0) = held;
+  };
+  for_rows(p.k, p.k_t, p.k_h, Hkv, q_groups, [&](const uint4& raw, int h, bool ok) {
+    float2 x[4];
+    unpack8(raw, x);
+    rotate(raw, x);
+    store(x, h, ok, false, p.c.k, p.c.ks, p.inv_k_scale, p.c.k_scale, p.k_out, p.ko_t, p.ko_h);
+  });
+  for_rows(p.v, p.v_t, p.v_h, Hkv, q_groups + k_groups, [&](const uint4& raw, int h, bool ok) {
+    float2 x[4];
+    unpack8(raw, x);
+    store(x, h, ok, true, p.c.v, p.c.vs, p.inv_v_scale, p.c.v_scale, p.v_out, p.vo_t, p.vo_h);
+  });
 }
 
-template <int FMT, int D>
+template <int FMT, int D, int ROPE>
 cudaError_t launch_append(AppendParams& p, int sm_count, cudaStream_t s) {
   constexpr int RPS = 32 / (D / 8);
-  const int groups = (p.Hq + 2 * p.c.Hkv + RPS - 1) / RPS;
+  const int groups = (p.Hq + RPS - 1) / RPS + 2 * ((p.c.Hkv + RPS - 1) / RPS);
   // spread a token's rows over more warps while that leaves fewer than 32
   // warps an SM
   const int64_t want = static_cast<int64_t>(sm_count) * 32;
@@ -227,15 +260,21 @@ cudaError_t launch_append(AppendParams& p, int sm_count, cudaStream_t s) {
   const int64_t warps = splits * p.T;
   const int64_t blocks = (warps + kAppThreads / 32 - 1) / (kAppThreads / 32);
   if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  kv_append_kernel<FMT, D><<<static_cast<unsigned>(blocks), kAppThreads, 0, s>>>(p);
+  kv_append_kernel<FMT, D, ROPE><<<static_cast<unsigned>(blocks), kAppThreads, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+template <int FMT, int D>
+cudaError_t launch_append_d(AppendParams& p, int sm_count, cudaStream_t s) {
+  if (!p.rope_dim) return launch_append<FMT, D, ROPE_NONE>(p, sm_count, s);
+  return p.interleaved ? launch_append<FMT, D, ROPE_PAIRS>(p, sm_count, s) : launch_append<FMT, D, ROPE_HALF>(p, sm_count, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append(int format, int d, AppendParams& p, int sm_count, cudaStream_t s) {
-  if (format == KV_BF16) return d == 64 ? launch_append<KV_BF16, 64>(p, sm_count, s) : launch_append<KV_BF16, 128>(p, sm_count, s);
-  return d == 64 ? launch_append<KV_E2M1, 64>(p, sm_count, s) : launch_append<KV_E2M1, 128>(p, sm_count, s);
+  if (format == KV_BF16) return d == 64 ? launch_append_d<KV_BF16, 64>(p, sm_count, s) : launch_append_d<KV_BF16, 128>(p, sm_count, s);
+  return d == 64 ? launch_append_d<KV_E2M1, 64>(p, sm_count, s) : launch_append_d<KV_E2M1, 128>(p, sm_count, s);
 }
 
 }  // namespace fl

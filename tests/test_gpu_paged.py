@@ -479,6 +479,39 @@ def test_append_reports_what_is_out_of_range_and_leaves_it():
     assert (cache.k == 0).all()
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.7, 3.3e-5, 4096.0])
+def test_append_rounding_borders_of_every_scale(scale):
+    """For every e4m3 scale s, blocks whose largest magnitude fixes it (6 s) and
+    whose other values sit on a border of the 4-bit codes, or one bf16 step to
+    either side: the codes are those of the correctly rounded quotient."""
+    e4 = oracle.paged.e4m3_values()[1:]
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    blocks = []
+    for s in e4:
+        m = torch.from_numpy(mids * s * scale).bfloat16()
+        bits = m.view(torch.int16)
+        up, dn = (bits + 1).view(torch.bfloat16), (bits - 1).view(torch.bfloat16)
+        top = torch.tensor([6 * s * scale]).bfloat16()
+        for v in (torch.cat((top, m, -m, m[:1])), torch.cat((top, up, -dn, up[:1])), torch.cat((-top, -up, dn, dn[:1]))):
+            blocks.append(v)
+    rng = np.random.default_rng(3)
+    blocks += [torch.from_numpy(rng.normal(size=16) * 10.0 ** rng.uniform(-8, 6)).bfloat16() for _ in range(2000)]
+    x = torch.stack(blocks)
+    x = torch.cat((x, torch.zeros(-len(x) % 8, 16, dtype=torch.bfloat16))).reshape(-1, 1, 128)  # [T, 1, 128]
+    T, page = x.shape[0], 256
+    pages = -(-T // page)
+    cache = PagedKVCache.allocate(pages, page, 1, 128, format="e2m1", k_scale=scale, v_scale=scale)
+    table = np.arange(pages, dtype=np.int32)[None]
+    kv_append(cache, x.to(DEV), x.to(DEV), dev([T], torch.int32), dev(table), seq_offsets=dev([0, T], torch.int32))
+    sync_status()
+    with np.errstate(over="ignore"):
+        code, s8 = oracle.quantise(x.float().numpy(), np.float32(scale), np.float32)
+    _, _, (kc, vc, ks, vs) = unpack(cache)
+    for got_c, got_s in ((kc, ks), (vc, vs)):
+        got_c, got_s = got_c.reshape(-1, 1, 128)[:T], got_s.reshape(-1, 1, 8)[:T]
+        assert np.array_equal(got_s, s8) and np.array_equal(got_c, code)
+
+
 def test_append_infinities_saturate_their_block():
     cache = PagedKVCache.allocate(2, 16, 1, 64, format="e2m1")
     k = torch.ones((1, 1, 64), dtype=torch.bfloat16, device=DEV)
