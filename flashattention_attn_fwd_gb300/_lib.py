@@ -110,6 +110,7 @@ _ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i 6i")
 _APPEND = struct.Struct("@4i 3P q 2P 4i 4P 12q P")
 _ZERO4 = (0, 0, 0, 0)
 APPEND_PACK = _APPEND.pack
+ATTN_PACK = _ATTN.pack
 
 
 def desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, *, scale=0.0, mask_kind=0, doc_causal=0, window=0, prefix=0, score_mod=0,

@@ -15,10 +15,14 @@ from . import _lib
 from ._lib import FL_DEBUG_KEY_SPLIT, FL_DEBUG_SKIP_KV_LOAD, MASKS, SCORE_MODS, FlattnError  # noqa: F401
 
 
+# the current stream's handle of a device, without a Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:
-        # the current stream's handle without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -47,26 +51,28 @@ def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):
 
 
 def _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, *, mask="none", window=None, prefix=None, doc_offsets=None,
-                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None, sink=None, **kw):
-    """fl_attn_desc of the variant arguments (packed); `kw`: its other fields."""
+                  doc_causal=False, score_mod="none", alibi_slopes=None, softcap=None, scale=None, sink=None,
+                  strides=(0,) * 16, stream=0, debug=(0, -1, 0)):
+    """fl_attn_desc of the variant arguments (packed); strides: q, k, v, out."""
+    slopes = offsets = num_docs = 0
     if mask not in MASKS:
         raise ValueError(f"unknown mask {mask!r}")
     if score_mod not in SCORE_MODS:
         raise ValueError(f"unknown score_mod {score_mod!r}")
     if alibi_slopes is not None:
         _need(alibi_slopes, "alibi_slopes", 1, torch.float32)
-        kw["slopes"] = alibi_slopes.data_ptr()
+        slopes = alibi_slopes.data_ptr()
     if doc_offsets is not None:
         _need(doc_offsets, "doc_offsets", 2, torch.int32)
         if not doc_offsets.is_contiguous():
             raise ValueError("doc_offsets must be contiguous")
-        kw["doc_offsets"] = doc_offsets.data_ptr()
-        kw["num_docs"] = doc_offsets.shape[1] - 1
-    return _lib.desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, scale=0.0 if scale is None else float(scale),
-                          mask_kind=MASKS[mask], doc_causal=1 if doc_causal else 0,
-                          window=0 if window is None else int(window), sink=0 if sink is None else int(sink),
-                          prefix=0 if prefix is None else int(prefix), score_mod=SCORE_MODS[score_mod],
-                          softcap=0.0 if softcap is None else float(softcap), **kw)
+        offsets = doc_offsets.data_ptr()
+        num_docs = doc_offsets.shape[1] - 1
+    return _lib.ATTN_PACK(B, Hq, Hkv, Lq, Lk, d, dv, 0.0 if scale is None else float(scale), MASKS[mask],
+                          1 if doc_causal else 0, 0 if window is None else int(window),
+                          0 if prefix is None else int(prefix), SCORE_MODS[score_mod],
+                          0.0 if softcap is None else float(softcap), slopes, offsets, num_docs, *strides, stream,
+                          *debug, 0 if sink is None else int(sink), 0, 0, 0, 0, 0, 0)
 
 
 def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, sink: int | None = None,
@@ -99,10 +105,9 @@ def attn_fwd(q, k, v, *, mask: str = "none", window: int | None = None, sink: in
             raise ValueError("lse must be contiguous")
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, dv, mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
-                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink, q_strides=q.stride(),
-                         k_strides=k.stride(), v_strides=v.stride(), o_strides=out.stride(),
-                         stream=_stream_ptr(stream), debug_flags=int(debug_flags), debug_arg=int(debug_arg),
-                         wait_limit_ms=int(wait_limit_ms))
+                         alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink,
+                         strides=q.stride() + k.stride() + v.stride() + out.stride(), stream=_stream_ptr(stream),
+                         debug=(int(debug_flags), int(debug_arg), int(wait_limit_ms)))
     st = _lib.lib().fl_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                 0 if lse is None else lse.data_ptr(), desc)
     _lib.check(st, "fl_attn_fwd")
@@ -289,9 +294,10 @@ def attn_bwd(q, k, v, out, dout, lse, *, mask: str = "none", window: int | None 
     _need(lse, "lse", 3, torch.float32)
     B, Hq, Lq, d = q.shape
     _, Hkv, Lk, _ = k.shape
-    dq = _empty_on(stream, q.shape, q.dtype, q.device) if dq is None else dq
-    dk = _empty_on(stream, k.shape, k.dtype, k.device) if dk is None else dk
-    dv = _empty_on(stream, v.shape, v.dtype, v.device) if dv is None else dv
+    like = torch.empty_like if stream is None else lambda t: _empty_on(stream, t.shape, t.dtype, t.device)
+    dq = like(q) if dq is None else dq
+    dk = like(k) if dk is None else dk
+    dv = like(v) if dv is None else dv
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, v.shape[-1], mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
                          alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink,

@@ -69,7 +69,7 @@ __device__ __forceinline__ uint4 pack8(const float2 (&x)[4]) {
 }
 
 template <int FMT, int D, int ROPE>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppThreads, 6) kv_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8;        // lanes per row
   constexpr int RPS = 32 / LPR;     // rows a warp handles at once
   constexpr int NB = 4;             // row groups in flight per warp

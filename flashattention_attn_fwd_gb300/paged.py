@@ -9,7 +9,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import _empty_on, _need, _stream_ptr
+from .api import _empty_on, _need, _raw_stream, _stream_ptr
 from ._lib import KV_FORMATS, MASKS, SCORE_MODS
 
 _SCALE_BLOCK = 16
@@ -108,7 +108,8 @@ def _need_table(cache, kv_len, block_table) -> tuple[int, int, int]:
 
 def _rows(t, name, T, H, d, index):
     """Checks a [T, H, d] bf16 row tensor; returns its (token, head) strides."""
-    _check(t, name, 3, _BF16, index)
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
+        _check(t, name, 3, _BF16, index)
     if t.shape != (T, H, d):
         raise ValueError(f"{name} must be {[T, H, d]}, got {list(t.shape)}")
     st, sh, sc = t.stride()
@@ -133,7 +134,7 @@ def kv_append(cache: PagedKVCache, k, v, kv_len, block_table, *, seq_offsets=Non
     index = cache.index
     _current(index)
     B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
-    _need(k, "k", 3)
+    _check(k, "k", 3, _BF16, index)
     T, Hkv, d = k.shape
     if Hkv != cache.Hkv or d != cache.d:
         raise ValueError(f"k must be [T, {cache.Hkv}, {cache.d}] for this cache, got {list(k.shape)}")
@@ -159,7 +160,7 @@ def kv_append(cache: PagedKVCache, k, v, kv_len, block_table, *, seq_offsets=Non
     Hq = qp = qop = 0
     qs = qos = kos = vos = (0, 0)
     if q is not None:
-        _need(q, "q", 3)
+        _check(q, "q", 3, _BF16, index)
         Hq = q.shape[1]
         if q_out is None:
             q_out = _empty_on(stream, (T, Hq, d), _BF16, cache.device)
@@ -175,7 +176,7 @@ def kv_append(cache: PagedKVCache, k, v, kv_len, block_table, *, seq_offsets=Non
         kop, vop = k_out.data_ptr(), v_out.data_ptr()
     desc = _lib.APPEND_PACK(T, B, Hq, max_pages, offsets, kv_len.data_ptr(), block_table.data_ptr(), table_stride,
                             cos, sin, positions, rot, 1 if rope_interleaved else 0, 0, qp, qop, kop, vop,
-                            *qs, *ks, *vs, *qos, *kos, *vos, _stream_ptr(stream))
+                            *qs, *ks, *vs, *qos, *kos, *vos, _raw_stream(index) if stream is None else _stream_ptr(stream))
     st = _lib.lib().fl_kv_append(k.data_ptr(), v.data_ptr(), cache._ref, desc)
     if st:
         _lib.check(st, "fl_kv_append")
@@ -244,7 +245,8 @@ def attn_paged_decode_fwd(q, cache: PagedKVCache, kv_len, block_table, *, mask: 
     desc = _lib.desc_pack(B, Hq, cache.Hkv, Lq, max_pages * cache.page_size, d, d, scale=scale or 0.0,
                           mask_kind=MASKS[mask], window=window or 0, sink=sink or 0, score_mod=SCORE_MODS[score_mod],
                           softcap=softcap or 0.0, slopes=slopes, q_strides=_strides(q, "q"),
-                          o_strides=_strides(out, "out"), stream=_stream_ptr(stream))
+                          o_strides=_strides(out, "out"),
+                          stream=_raw_stream(index) if stream is None else _stream_ptr(stream))
     L = _lib.lib()
     if workspace is None:
         n = int(L.fl_attn_paged_decode_workspace_size(desc, cache._ref))
