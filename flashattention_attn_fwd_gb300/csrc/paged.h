@@ -77,14 +77,14 @@ struct PagedDecodeParams {
 
 // CTAs of a cluster that takes one unit of at most `keys` keys, 0 for the line:
 // a power of two up to the portable 8, no more than one 128-key round of a CTA's
-// warps needs, and all units' clusters resident at once if possible (a second
-// wave costs as much as the first).  Past kClusterKeys per CTA the line's even
-// cut is worth its plan and merge (4 us).
+// warps needs, and no more than fill half of the places for CTAs (128 units of
+// 1092 keys: 12.0 us in pairs, 13.2 in fours and 13.0 alone).  Past kClusterKeys
+// per CTA the line's even cut is worth its plan and merge (5 us).
 constexpr int kClusterMax = 8;
-constexpr int64_t kClusterKeys = 1024;
+constexpr int64_t kClusterKeys = 2048;
 inline int paged_cluster(int64_t keys, int64_t units, int64_t resident) {
   int c = 1;
-  while (c < kClusterMax && keys > 128 * static_cast<int64_t>(c) && units * 2 * c <= resident) c *= 2;
+  while (c < kClusterMax && keys > 128 * static_cast<int64_t>(c) && units * 4 * c <= resident) c *= 2;
   return keys <= kClusterKeys * c ? c : 0;
 }
 

@@ -50,6 +50,7 @@
 #include <math_constants.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "cvt4.cuh"
 #include "paged.h"
@@ -63,16 +64,18 @@ constexpr int kPdThreads = 32 * kPdWarps;
 constexpr float kPLog2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
 
-// 16-key halves of a tile: one for bf16 heads of 128 channels, whose 16 keys
-// fill 64 registers, else two, which share the bookkeeping of a tile.
+// A tile is kSteps steps of 16 keys, which share its bookkeeping (four of a 4-bit
+// head of 64 channels: 7.2 us against 6.1 at one sequence of 701 tokens, and no
+// gain over long ones).
+template <int FMT, int D>
+constexpr int kSteps = FMT == KV_BF16 && D == 128 ? 1 : 2;
+
 // Starting a unit (queries, pages, the first copies, the join at its end) costs
 // a CTA about as long as this many tiles; the line counts them before each
 // unit's own, so that a CTA that starts a second unit gets fewer tiles.
 template <int FMT, int D>
 constexpr int kLead = FMT == KV_BF16 ? 28 : 16;
 
-template <int FMT, int D>
-constexpr int kHalves = FMT == KV_BF16 && D == 128 ? 1 : 2;
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -139,17 +142,17 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedDecodeParams& p, int b)
 }
 
 // Ring of one warp group.  A stage holds the tile's K rows, its V rows and
-// (4 bits) its scales: K's [key][d / 16], V's [d / 16][16 keys] per half.  The
+// (4 bits) its scales: K's [key][d / 16], V's [d / 16][16 keys] per step.  The
 // 16-byte chunks of a row are permuted within their 128-byte line (swz_k,
 // swz_v of the key) so that the fragment loads meet no bank twice.
 template <int FMT, int D, int RW>
 struct Ring {
-  static constexpr int HV = kHalves<FMT, D>;
+  static constexpr int HV = kSteps<FMT, D>;
   static constexpr int KB = FMT == KV_E2M1 ? D / 2 : 2 * D;      // bytes of one key's row
   static constexpr int ROWS = 16 * HV * KB;                      // bytes of K (or V) per stage
-  static constexpr int SC = FMT == KV_E2M1 ? D : 0;              // bytes of K (or V) scales per half
+  static constexpr int SC = FMT == KV_E2M1 ? D : 0;              // bytes of K (or V) scales per step
   static constexpr int STAGE = 2 * ROWS + 2 * HV * SC;
-  static constexpr int STAGES = RW * (FMT == KV_BF16 ? 2 : D == 64 ? 4 : 3);
+  static constexpr int STAGES = RW * (FMT == KV_BF16 ? 2 : 3);
   static constexpr int BYTES = kPdWarps / RW * STAGES * STAGE;   // of the CTA's groups
 };
 template <int FMT, int D>
@@ -195,7 +198,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 template <int FMT, int D, int NT, int RW, bool CL>
 __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   constexpr int KS = D / 16;        // k-steps of S, and 16-channel row tiles of O
-  constexpr int HV = kHalves<FMT, D>;
+  constexpr int HV = kSteps<FMT, D>;
   constexpr int KT = 16 * HV;       // keys per tile
   constexpr int WR = 8 * NT;        // query rows per warp
   // weights carry 2^kLift in fp16 (see above)
@@ -341,13 +344,14 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     // ---- the ring: tile i of this group is t0 + kw + i * n_kw
     const int32_t* trow = p.table + b * p.table_stride;
     auto key_of = [&](int t) { return KT * (t < sq.sink ? t : t + sq.skip); };
-    // page of a tile's half; -1: none (past the piece, the cache or the pool).
-    // From 32-key pages on a tile lies in one page.
+    // page of a tile's step; -1: none (past the piece, the cache or the pool)
     auto page_of = [&](int t, int hf) {
       const int j = key_of(t) + 16 * hf;
       const int pg = t < t1 && j < sq.n ? __ldg(trow + (j >> shift)) : -1;
       return static_cast<unsigned>(pg) < static_cast<unsigned>(p.c.num_pages) ? pg : -1;
     };
+    // does a tile's step hf > 0 start a page of its own?
+    auto fresh = [&](int hf) { return ((16 * hf) & page_mask) == 0; };
     // Addresses: a page is `stride` bytes (of K, of V), a head's run in it starts
     // `head` bytes on; the scales' are those over KB / (D / 16).
     const uint8_t* kh = static_cast<const uint8_t*>(p.c.k) + (static_cast<int64_t>(hkv) << shift) * KB + 16 * gt;
@@ -361,33 +365,49 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     // Copies tile t (pages pg) into a stage; page 0 stands in for a missing
     // one, whose keys are masked.
     auto copy = [&](int t, const int (&pg)[HV], uint32_t st) {
-      const uint32_t off = key_of(t) & page_mask;
-      const uint32_t p0 = max(pg[0], 0);
-      const int64_t a0 = static_cast<int64_t>(static_cast<uint64_t>(p0) * page_bytes + off * KB);
-      int64_t a1 = a0 + 16 * KB;
-      uint32_t p1 = p0, off1 = off + 16;
-      if (HV == 2 && shift == 4) {
-        p1 = max(pg[HV - 1], 0);
-        off1 = 0;
-        a1 = static_cast<int64_t>(static_cast<uint64_t>(p1) * page_bytes);
+      uint32_t pn[HV], off[HV];
+      int64_t at[HV];
+      pn[0] = max(pg[0], 0);
+      off[0] = key_of(t) & page_mask;
+      at[0] = static_cast<int64_t>(static_cast<uint64_t>(pn[0]) * page_bytes + off[0] * KB);
+#pragma unroll
+      for (int hf = 1; hf < HV; ++hf) {
+        pn[hf] = pn[hf - 1];
+        off[hf] = off[hf - 1] + 16;
+        at[hf] = at[hf - 1] + 16 * KB;
+        if (fresh(hf)) {
+          pn[hf] = max(pg[hf], 0);
+          off[hf] = 0;
+          at[hf] = static_cast<int64_t>(static_cast<uint64_t>(pn[hf]) * page_bytes);
+        }
       }
-      constexpr int CH = KB;           // chunks of one half's K
+      constexpr int CH = KB;           // chunks of one step's K
       constexpr int N = HV * CH;
 #pragma unroll
       for (int i = 0; i < (N + GT - 1) / GT; ++i) {
         const int c = gt + GT * i;
         if (N % GT == 0 || c < N) {
-          // within a half the chunks of consecutive i are GT chunks on
-          const bool second = CH % GT == 0 ? GT * i >= CH : c >= CH;
-          const int64_t at = (second ? a1 - 16 * CH : a0) + 16 * GT * i;
+          int64_t a;
+          if constexpr (CH % GT == 0) {
+            a = at[GT * i / CH] + 16 * (GT * i % CH);
+          } else {  // a group's round covers several steps
+            a = at[0] + 16 * GT * i;
+#pragma unroll
+            for (int hf = 1; hf < HV; ++hf)
+              if (c >= hf * CH) a = at[hf] + 16 * (GT * i - hf * CH);
+          }
           const int j = c / (KB / 16);
-          cp_async16(st + 16 * (c ^ swz_k<FMT, D>(j)), kh + at);
-          cp_async16(st + L::ROWS + 16 * (c ^ swz_v(j)), vh + at);
+          cp_async16(st + 16 * (c ^ swz_k<FMT, D>(j)), kh + a);
+          cp_async16(st + L::ROWS + 16 * (c ^ swz_v(j)), vh + a);
         }
       }
       if constexpr (FMT == KV_E2M1) {
+        static_assert(HV * SH <= 32, "a scale chunk per lane");
         if (gt < HV * SH) {
-          const uint32_t pp = gt < SH ? p0 : p1, oo = gt < SH ? off : off1;
+          uint32_t pp = pn[0], oo = off[0];
+#pragma unroll
+          for (int hf = 1; hf < HV; ++hf)
+            if (gt >= hf * SH) pp = pn[hf], oo = off[hf];
           cp_async16(st + 2 * L::ROWS + 16 * gt,
                      sh + static_cast<int64_t>(static_cast<uint64_t>(pp) * (page_bytes / (KB / (D / 16))) + oo * (sv ? 1 : D / 16)));
         }
@@ -397,17 +417,19 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     // pages of the next tile to copy, and which pages of the tiles under way
     // exist: HV bits a tile, the current tile's lowest
     int pg[HV];
-    uint32_t have = 0;
-    static_assert(HV * S <= 32, "a bit per half under way");
+    using Bits = std::conditional_t<(HV * S > 32), uint64_t, uint32_t>;
+    static_assert(HV * S <= 64, "a bit per step under way");
+    Bits have = 0;
     auto fetch = [&](int i) {
       pg[0] = page_of(t0 + kw + i * n_kw, 0);
-      if (HV == 2) pg[HV - 1] = shift == 4 ? page_of(t0 + kw + i * n_kw, 1) : pg[0];
+#pragma unroll
+      for (int hf = 1; hf < HV; ++hf) pg[hf] = fresh(hf) ? page_of(t0 + kw + i * n_kw, hf) : pg[hf - 1];
     };
     auto issue = [&](int i, int ahead, uint32_t st) {  // tile i into stage st
       if (i < n_tiles) {
         copy(t0 + kw + i * n_kw, pg, st);
 #pragma unroll
-        for (int hf = 0; hf < HV; ++hf) have |= (pg[hf] >= 0 ? 1u : 0u) << (HV * ahead + hf);
+        for (int hf = 0; hf < HV; ++hf) have |= static_cast<Bits>(pg[hf] >= 0) << (HV * ahead + hf);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -486,6 +508,30 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       for (int mt = 0; mt < KS; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
     }
 
+    const bool plain = p.score_mod == 0;
+    // The reference maximum moves only when a score exceeds it by more than 2^8
+    // (O rescaled then); m0, m1: the lane's largest scores of its two rows.
+    auto raise = [&](int nt, float m0, float m1) {
+      float mx[2] = {m0, m1};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
+        const float mn = fmaxf(m[nt][e], mx[e]);
+        if (mn != -CUDART_INF_F) {
+          const float alpha = ptx::ex2(m[nt][e] - mn);
+          m[nt][e] = mn;
+          off[nt][e] = kLift - mn;
+          bound[nt][e] = mn + 8.f;
+          l[nt][e] *= alpha;
+#pragma unroll
+          for (int mt = 0; mt < KS; ++mt) {
+            o[nt][mt][e] *= alpha;
+            o[nt][mt][2 + e] *= alpha;
+          }
+        }
+      }
+    };
     uint32_t stage = 0, ahead = S - 1;  // ring positions of tile i and tile i + S - 1
     for (int i = 0; i < n_tiles; ++i) {
       cp_async_wait<S - 2>();
@@ -494,7 +540,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       fetch(i + S);
       const uint32_t st = ring + stage * L::STAGE;
       const int key0 = key_of(t0 + kw + i * n_kw);
-      const uint32_t got = have & ((1u << HV) - 1);
+      const uint32_t got = static_cast<uint32_t>(have) & ((1u << HV) - 1);
       have >>= HV;
       const bool full = got == (1u << HV) - 1 && key0 <= full_hi && (key0 >= full_lo || key0 <= full_sink);
       // ---- S^T = K Q^T
@@ -561,68 +607,75 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float x[HV][4];
-#pragma unroll
-        for (int hf = 0; hf < HV; ++hf)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[hf][e] = s[hf][nt][e] * sc[nt][e & 1];
-        if (p.score_mod != 0) {
-          const int rc = row0 + 8 * nt + 2 * t4;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float slope = p.score_mod == 1 && rc + (e & 1) < p.M
-                                    ? __ldg(p.slopes + hkv * p.G + (rc + (e & 1)) / p.Lq) * kPLog2e : 0.f;
-#pragma unroll
-            for (int hf = 0; hf < HV; ++hf) {
-              if (p.score_mod == 2) x[hf][e] = p.softcap * tanhf(x[hf][e] / p.softcap);
-              else x[hf][e] = fmaf(slope, static_cast<float>(key0 + 16 * hf + kkey + (e & 2) - pos[nt][e & 1]), x[hf][e]);
-            }
-          }
-        }
-        if (!full) {
-#pragma unroll
-          for (int hf = 0; hf < HV; ++hf) {
-            const bool pok = (got >> hf) & 1u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = key0 + 16 * hf + kkey + (e & 2), ps = pos[nt][e & 1];
-              const bool vis = pok && j < sq.n && (!p.causal || j <= ps) && (!p.window || j > ps - p.window || j < p.sink);
-              x[hf][e] = vis ? x[hf][e] : -CUDART_INF_F;
-            }
-          }
-        }
-        // the reference maximum moves only by more than 2^8 (O rescaled then)
-        float mx[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[e] = fmaxf(x[0][e], x[0][2 + e]);
-#pragma unroll
-          for (int hf = 1; hf < HV; ++hf) mx[e] = ptx::max3(mx[e], x[hf][e], x[hf][2 + e]);
-        }
-        if (__any_sync(0xffffffffu, mx[0] > bound[nt][0] || mx[1] > bound[nt][1])) {
+        if (NT == 1 && plain && full) {
+          // the maximum of the raw scores against the bound in their units, then
+          // scale and offset in one packed step
+          float mx[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], d));
-            const float mn = fmaxf(m[nt][e], mx[e]);
-            if (mn != -CUDART_INF_F) {
-              const float alpha = ptx::ex2(m[nt][e] - mn);
-              m[nt][e] = mn;
-              off[nt][e] = kLift - mn;
-              bound[nt][e] = mn + 8.f;
-              l[nt][e] *= alpha;
+            for (int hf = 1; hf < HV; ++hf) mx[e] = ptx::max3(mx[e], s[hf][nt][e], s[hf][nt][2 + e]);
+          }
+          if (__any_sync(0xffffffffu, mx[0] * sc[nt][0] > bound[nt][0] || mx[1] * sc[nt][1] > bound[nt][1]))
+            raise(nt, mx[0] * sc[nt][0], mx[1] * sc[nt][1]);
+          const float2 sc2 = make_float2(sc[nt][0], sc[nt][1]), off2 = make_float2(off[nt][0], off[nt][1]);
 #pragma unroll
-              for (int mt = 0; mt < KS; ++mt) {
-                o[nt][mt][e] *= alpha;
-                o[nt][mt][2 + e] *= alpha;
+          for (int hf = 0; hf < HV; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float2 v = ptx::fma2(make_float2(s[hf][nt][e], s[hf][nt][e + 1]), sc2, off2);
+              x[hf][e] = v.x;
+              x[hf][e + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < HV; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[hf][e] = s[hf][nt][e] * sc[nt][e & 1];
+          if (p.score_mod != 0) {
+            const int rc = row0 + 8 * nt + 2 * t4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float slope = p.score_mod == 1 && rc + (e & 1) < p.M
+                                      ? __ldg(p.slopes + hkv * p.G + (rc + (e & 1)) / p.Lq) * kPLog2e : 0.f;
+#pragma unroll
+              for (int hf = 0; hf < HV; ++hf) {
+                if (p.score_mod == 2) x[hf][e] = p.softcap * tanhf(x[hf][e] / p.softcap);
+                else x[hf][e] = fmaf(slope, static_cast<float>(key0 + 16 * hf + kkey + (e & 2) - pos[nt][e & 1]), x[hf][e]);
               }
             }
           }
+          if (!full) {
+#pragma unroll
+            for (int hf = 0; hf < HV; ++hf) {
+              const bool pok = (got >> hf) & 1u;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = key0 + 16 * hf + kkey + (e & 2), ps = pos[nt][e & 1];
+                const bool vis = pok && j < sq.n && (!p.causal || j <= ps) && (!p.window || j > ps - p.window || j < p.sink);
+                x[hf][e] = vis ? x[hf][e] : -CUDART_INF_F;
+              }
+            }
+          }
+          float mx[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[e] = fmaxf(x[0][e], x[0][2 + e]);
+#pragma unroll
+            for (int hf = 1; hf < HV; ++hf) mx[e] = ptx::max3(mx[e], x[hf][e], x[hf][2 + e]);
+          }
+          if (__any_sync(0xffffffffu, mx[0] > bound[nt][0] || mx[1] > bound[nt][1])) raise(nt, mx[0], mx[1]);
+#pragma unroll
+          for (int hf = 0; hf < HV; ++hf)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[hf][e] += off[nt][e & 1];
         }
 #pragma unroll
         for (int hf = 0; hf < HV; ++hf) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[hf][e] = ptx::ex2(x[hf][e] + off[nt][e & 1]);
+            x[hf][e] = ptx::ex2(x[hf][e]);
             l[nt][e & 1] += x[hf][e];
           }
           if (FMT == KV_E2M1) {
