@@ -238,15 +238,25 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       }
       return v;
     };
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-      const int64_t c = b0 + tid < p.B ? LEAD + seq_tiles<KT>(p, b0 + tid).count : 0;
-      const int64_t s = warp_incl(c);
+    // tiles and lead of sequence b0 + tid, and of the chunk's up to it
+    int64_t c = 0, s = 0, chunk = 0;
+    auto scan = [&](int b0) {
+      c = b0 + tid < p.B ? LEAD + seq_tiles<KT>(p, b0 + tid).count : 0;
+      s = warp_incl(c);
       if (lane == 31) scan_sm[warp] = s;
       __syncthreads();
+      chunk = 0;
 #pragma unroll
-      for (int i = 0; i < kPdWarps; ++i) total += scan_sm[i];
+      for (int i = 0; i < kPdWarps; ++i) {
+        if (i < warp) s += scan_sm[i];
+        chunk += scan_sm[i];
+      }
       __syncthreads();
+    };
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
+      scan(b0);
+      total += chunk;
     }
     const int64_t all = total * H;
     const int64_t per = ((all + gridDim.x - 1) / gridDim.x + kPdWarps - 1) / kPdWarps * kPdWarps;
@@ -254,16 +264,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     end = begin + per < all ? begin + per : all;
     int64_t carry = 0;  // tiles of one head before the chunk's sequences
     for (int b0 = 0; b0 < p.B; b0 += kPdThreads) {
-      const int64_t c = b0 + tid < p.B ? LEAD + seq_tiles<KT>(p, b0 + tid).count : 0;
-      int64_t s = warp_incl(c);
-      if (lane == 31) scan_sm[warp] = s;
-      __syncthreads();
-      int64_t chunk = 0;
-#pragma unroll
-      for (int i = 0; i < kPdWarps; ++i) {
-        if (i < warp) s += scan_sm[i];
-        chunk += scan_sm[i];
-      }
+      if (p.B > kPdThreads) scan(b0);  // else the one chunk's is at hand
       const int64_t before = carry + s - c;
       if (blockIdx.x == 0 && b0 + tid < p.B) p.plan[2 + b0 + tid] = before;
       if (c > 0 && before * H <= begin && begin < (before + c) * H) {
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         base_sm = before * H;
       }
       carry += chunk;
-      __syncthreads();
     }
+    __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
       p.plan[0] = per;
       p.plan[1] = all;
@@ -352,11 +353,11 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     };
     // does a tile's step hf > 0 start a page of its own?
     auto fresh = [&](int hf) { return ((16 * hf) & page_mask) == 0; };
-    // Addresses: a page is `stride` bytes (of K, of V), a head's run in it starts
-    // `head` bytes on; the scales' are those over KB / (D / 16).
+    // A page is page_bytes (of K, of V); a head's run in it starts at kh, vh; the
+    // scales' counts are those over KB / (D / 16).
     const uint8_t* kh = static_cast<const uint8_t*>(p.c.k) + (static_cast<int64_t>(hkv) << shift) * KB + 16 * gt;
     const uint8_t* vh = static_cast<const uint8_t*>(p.c.v) + (static_cast<int64_t>(hkv) << shift) * KB + 16 * gt;
-    constexpr int SH = D / 8;          // scale chunks per half: K's, then V's
+    constexpr int SH = D / 8;          // scale chunks per step: K's, then V's
     const int sx = gt % SH;
     const bool sv = sx >= SH / 2;
     const uint8_t* sh = nullptr;
