@@ -554,7 +554,7 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   p.window = d.window; p.prefix = d.prefix_len; p.num_docs = d.num_docs;
   if (static_cast<int64_t>(d.B) * d.Hkv * (p.n_ktiles + static_cast<int64_t>(p.far_chunks) * p.sink_tiles) > 0x7fffffff)
     return FL_ERR_UNSUPPORTED;
-  CUtensorMap maps[7];
+  CUtensorMap maps[9];
   const int bw = box_width(d.d), bwv = box_width(d.dv);
   const int64_t sl = d.d, slv = d.dv;
   // the fp32 dQ accumulator as [B * Hq][Lq][d], boxes of 32 channels x 128
@@ -574,7 +574,11 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
       !encode_rows_f32(&maps[4], p.l2, static_cast<int64_t>(d.B) * d.Hq, d.Lq, p.Lq_pad) ||
       !encode_rows_f32(&maps[5], p.dvec, static_cast<int64_t>(d.B) * d.Hq, d.Lq, p.Lq_pad) ||
       !encode(&maps[6], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p.dq_acc, qa_dims, qa_str, qa_box,
-              CU_TENSOR_MAP_SWIZZLE_128B))
+              CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_bhlc(&maps[7], dk, d.d, d.Lk, d.Hkv, d.B, sl, static_cast<int64_t>(d.Lk) * d.d,
+                   static_cast<int64_t>(d.Hkv) * d.Lk * d.d, bw) ||
+      !encode_bhlc(&maps[8], dv, d.dv, d.Lk, d.Hkv, d.B, slv, static_cast<int64_t>(d.Lk) * d.dv,
+                   static_cast<int64_t>(d.Hkv) * d.Lk * d.dv, bwv))
     return cuda_fail("cuTensorMapEncodeTiled", cudaSuccess);
   return launched("backward kernel launch", fl::launch_bwd(d.d, d.dv, d.score_mod, maps, p, static_cast<cudaStream_t>(d.stream)));
 }

@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                     const __grid_constant__ CUtensorMap tmL2, const __grid_constant__ CUtensorMap tmDv,
-                    const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ BwdParams p) {
+                    const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmDK,
+                    const __grid_constant__ CUtensorMap tmGV, const __grid_constant__ BwdParams p) {
   using L = BwdLayout<D, DV>;
   // d = dv <= 64: S^T [0,128), K V or sech^2 [128,192), dP^T [192,320), dV,
   // dK, dQ after.  d = 128 (dV and dK take 256 columns): S^T [0,128), dP^T
@@ -229,6 +230,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int nq = it_hi - it_lo + 1;
   const int n_tiles = nq > 0 ? nq * group : 0;
 
+  // Q, the query rows' vectors and (with two buffers) dO of walk step n
+  auto load_q = [&](int n, uint64_t pol_keep) {
+    const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
+    const int buf = n & 1;
+    ptx::mbar_arrive_expect_tx(&q_full[buf], static_cast<uint32_t>(L::TILE + (L::NDO == 2 ? L::TILE_V : 0)) + 2u * 512u);
+#pragma unroll
+    for (int bx = 0; bx < L::NBOX; ++bx)
+      ptx::tma_load_4d(smem + L::OFF_Q + buf * L::TILE + bx * L::BOX, &tmQ, &q_full[buf], bx * L::BOXW, i0, h, b, pol_keep);
+    if (L::NDO == 2) {
+#pragma unroll
+      for (int bx = 0; bx < L::NBOX_V; ++bx)
+        ptx::tma_load_4d(smem + L::OFF_DO + buf * L::TILE_V + bx * L::BOX_V, &tmDO, &q_full[buf], bx * L::BOXW_V, i0, h, b,
+                         pol_keep);
+    }
+    const int row = b * p.Hq + h;
+    ptx::tma_load_2d(vec + buf * 128, &tmL2, &q_full[buf], i0, row, pol_keep);
+    ptx::tma_load_2d(vec + 256 + buf * 128, &tmDv, &q_full[buf], i0, row, pol_keep);
+  };
+
   if (threadIdx.x == 0) {
     ptx::mbar_init(kv_full, 1);
     for (int i = 0; i < 2; ++i) {
@@ -248,6 +268,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     misc[1] = 0u;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
+    // this thread issues every copy: K, V and the first query tile set out while
+    // TMEM is allocated (0.5 us of a short walk's 11)
+    if (n_tiles > 0) {
+      const uint64_t pol_keep = ptx::policy_evict_last();
+      ptx::mbar_arrive_expect_tx(kv_full, static_cast<uint32_t>(L::TILE + L::TILE_V));
+#pragma unroll
+      for (int bx = 0; bx < L::NBOX; ++bx)
+        ptx::tma_load_4d(smem + L::OFF_K + bx * L::BOX, &tmK, kv_full, bx * L::BOXW, j0, hkv, b, pol_keep);
+#pragma unroll
+      for (int bx = 0; bx < L::NBOX_V; ++bx)
+        ptx::tma_load_4d(smem + L::OFF_V + bx * L::BOX_V, &tmV, kv_full, bx * L::BOXW_V, j0, hkv, b, pol_keep);
+      load_q(0, pol_keep);
+    }
   }
   if (warp == 1) {
     ptx::tmem_alloc(&misc[0], 512);
@@ -264,37 +297,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ptx::setmaxnreg_dec<kBwdCtlRegs>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------------- TMA
+      // (K, V and the first tile are under way already)
       const uint64_t pol_keep = ptx::policy_evict_last();
-      if (n_tiles > 0) {
-        ptx::mbar_arrive_expect_tx(kv_full, static_cast<uint32_t>(L::TILE + L::TILE_V));
-#pragma unroll
-        for (int bx = 0; bx < L::NBOX; ++bx)
-          ptx::tma_load_4d(smem + L::OFF_K + bx * L::BOX, &tmK, kv_full, bx * L::BOXW, j0, hkv, b, pol_keep);
-#pragma unroll
-        for (int bx = 0; bx < L::NBOX_V; ++bx)
-          ptx::tma_load_4d(smem + L::OFF_V + bx * L::BOX_V, &tmV, kv_full, bx * L::BOXW_V, j0, hkv, b, pol_keep);
-      }
-      int issued = 0, do_issued = 0;
+      int issued = n_tiles > 0 ? 1 : 0, do_issued = 0;
       bool ok = true;
       for (int n = 0; n < n_tiles && ok; ++n) {
         const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
-        const int buf = n & 1;
-        if (!wait_bar(&q_empty[buf], ((n >> 1) & 1u) ^ 1u, ctl, 50)) { ok = false; break; }
-        ptx::mbar_arrive_expect_tx(&q_full[buf],
-                                   static_cast<uint32_t>(L::TILE + (L::NDO == 2 ? L::TILE_V : 0)) + 2u * 512u);
-#pragma unroll
-        for (int bx = 0; bx < L::NBOX; ++bx)
-          ptx::tma_load_4d(smem + L::OFF_Q + buf * L::TILE + bx * L::BOX, &tmQ, &q_full[buf], bx * L::BOXW, i0, h, b,
-                           pol_keep);
-        if (L::NDO == 2) {
-#pragma unroll
-          for (int bx = 0; bx < L::NBOX_V; ++bx)
-            ptx::tma_load_4d(smem + L::OFF_DO + buf * L::TILE_V + bx * L::BOX_V, &tmDO, &q_full[buf], bx * L::BOXW_V,
-                             i0, h, b, pol_keep);
+        if (n > 0) {
+          if (!wait_bar(&q_empty[n & 1], ((n >> 1) & 1u) ^ 1u, ctl, 50)) { ok = false; break; }
+          load_q(n, pol_keep);
         }
-        const int row = b * p.Hq + h;
-        ptx::tma_load_2d(vec + buf * 128, &tmL2, &q_full[buf], i0, row, pol_keep);
-        ptx::tma_load_2d(vec + 256 + buf * 128, &tmDv, &q_full[buf], i0, row, pol_keep);
         issued = n + 1;
         if (L::NDO == 1) {
           // one dO buffer: tile n's once dV(n - 1) has read tile n - 1's
@@ -645,18 +657,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) ptx::mbar_arrive(ds_full);
     }
     // dV (half 0) or dK (half 1) of this thread's key row, once every product
-    // is done (the TMEM loads are warp-wide; only the stores depend on the row)
-    if (ok && __all_sync(0xffffffffu, wait_bar(done, 0u, ctl, 63))) {
+    // is done (the TMEM loads are warp-wide; only the stores depend on the row).
+    // The row goes through the idle V (K) tile in shared memory and out by TMA,
+    // which clips rows past Lk; a thread's own stores of its row, 16 bytes in
+    // each of 32 lines a time, take 1 us longer.  Partial sums and additions to
+    // dv are stored directly.  Whether to go on is decided jointly by the half's
+    // four warps, as below.
+    const bool finished = ok && __all_sync(0xffffffffu, wait_bar(done, 0u, ctl, 63));
+    if (ptx::named_bar_and(2 + hf, 128, finished)) {
       ptx::tc_fence_after();
       const bool z = n_tiles == 0;
       const int64_t row = (static_cast<int64_t>(b) * p.Hkv + hkv) * p.Lk + kg;
-      // NC columns of TMEM from col, times f, as bf16 into base's row (plus
-      // what is there with acc)
       float* prow = part ? p.part + (((static_cast<int64_t>(bh) * p.sink_tiles + jt) * (1 + p.far_chunks) + chunk + 1) * 128 + r) * (D + DV)
                          : nullptr;
-      auto write_row = [&](auto nc, uint32_t col, void* base, float f, bool acc, int pcol) {
+      // NC columns of TMEM from col, times f: fp32 into prow, added to the bf16
+      // row of base with acc, or bf16 into the staged tile
+      auto write_row = [&](auto nc, uint32_t col, void* base, float f, bool acc, int pcol, uint8_t* tile) {
         constexpr int NC = decltype(nc)::value;
-        constexpr int EC = NC < 64 ? NC : 64;  // columns per TMEM read-out
+        constexpr int EC = NC < 64 ? NC : 64;  // columns per TMEM read-out, and per staged box
         uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + row * NC);
 #pragma unroll
         for (int c0 = 0; c0 < NC; c0 += EC) {
@@ -671,30 +689,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int c = 0; c < EC; c += 4)
               *reinterpret_cast<float4*>(prow + pcol + c0 + c) =
                   z ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
-          } else if (kg < p.Lk) {
+            continue;
+          }
 #pragma unroll
-            for (int c = 0; c < EC; c += 8) {
-              float o[8];
+          for (int c = 0; c < EC; c += 8) {
+            float o[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = z ? 0.f : a[c + e] * f;
-              if (acc) {
-                const uint4 prev = dst[(c0 + c) / 8];
-                const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&prev);
+            for (int e = 0; e < 8; ++e) o[e] = z ? 0.f : a[c + e] * f;
+            if (acc) {
+              if (kg >= p.Lk) continue;
+              const uint4 prev = dst[(c0 + c) / 8];
+              const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&prev);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 pf = __bfloat1622float2(p2[e]);
-                  o[2 * e] += pf.x;
-                  o[2 * e + 1] += pf.y;
-                }
+              for (int e = 0; e < 4; ++e) {
+                const float2 pf = __bfloat1622float2(p2[e]);
+                o[2 * e] += pf.x;
+                o[2 * e + 1] += pf.y;
               }
-              dst[(c0 + c) / 8] = make_uint4(ptx::pack_bf16x2(o[0], o[1]), ptx::pack_bf16x2(o[2], o[3]),
-                                             ptx::pack_bf16x2(o[4], o[5]), ptx::pack_bf16x2(o[6], o[7]));
             }
+            const uint4 w = make_uint4(ptx::pack_bf16x2(o[0], o[1]), ptx::pack_bf16x2(o[2], o[3]),
+                                       ptx::pack_bf16x2(o[4], o[5]), ptx::pack_bf16x2(o[6], o[7]));
+            // box c0 / EC of the tile: 16-byte chunks at the swizzled positions
+            const int k = c / 8, sw = EC == 64 ? (k ^ (r & 7)) : (k ^ ((r >> 1) & 3));
+            if (acc) dst[(c0 + c) / 8] = w;
+            else *reinterpret_cast<uint4*>(tile + (c0 / EC) * (128 * EC * 2) + r * (EC * 2) + (sw << 4)) = w;
           }
         }
       };
-      if (hf) write_row(std::integral_constant<int, D>{}, kColDK, p.dk, n_tiles > 0 ? p.scale : 1.0f, false, DV);
-      else write_row(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, p.dv_accumulate != 0, 0);
+      const bool acc = hf == 0 && p.dv_accumulate != 0;
+      if (hf) write_row(std::integral_constant<int, D>{}, kColDK, p.dk, n_tiles > 0 ? p.scale : 1.0f, false, DV, smem + L::OFF_K);
+      else write_row(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, acc, 0, smem + L::OFF_V);
+      if (!prow && !acc) {
+        ptx::fence_proxy_async_smem();
+        ptx::named_bar_sync(2 + hf, 128);
+        if (lane == 0 && quad == 0) {
+          if (hf) {
+#pragma unroll
+            for (int bx = 0; bx < L::NBOX; ++bx)
+              ptx::tma_store_4d(&tmDK, smem + L::OFF_K + bx * L::BOX, bx * L::BOXW, j0, hkv, b);
+          } else {
+#pragma unroll
+            for (int bx = 0; bx < L::NBOX_V; ++bx)
+              ptx::tma_store_4d(&tmGV, smem + L::OFF_V + bx * L::BOX_V, bx * L::BOXW_V, j0, hkv, b);
+          }
+          ptx::bulk_commit_group();
+          ptx::bulk_wait_group_read0();
+        }
+      }
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -882,7 +923,8 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
   }
   if (e != cudaSuccess) return e;
   const int walks = p.B * p.Hkv * (p.n_ktiles + p.far_chunks * p.sink_tiles);
-  kern<<<walks, kBwdThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], p);
+  kern<<<walks, kBwdThreads, smem, s>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6],
+                                         maps[7], maps[8], p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int pgrid = static_cast<int>((p.rows * D / 8 + 255) / 256);
