@@ -9,10 +9,15 @@
 //   dP^T = V dO^T                  dS^T = P^T * (dP^T - D) * dT/dS
 //   dK  += dS^T Q                  dQ  += dS K        (D = rowsum(dO * O))
 //
-// One CTA owns one (batch, key/value head, 128-key tile) and walks every
-// query tile of every query head of its GQA group that sees those keys;
-// dK and dV stay in TMEM for the whole walk, and each query tile's dQ
-// contribution is added to an fp32 accumulator in global memory.  All five
+// A walk is one (batch, key/value head, 128-key tile) with every query tile of
+// every query head of its GQA group that sees those keys; dK and dV stay in
+// TMEM for the whole walk, and each query tile's dQ contribution is added to an
+// fp32 accumulator in global memory.  The grid has a block per walk; with d = dv
+// <= 64, where shared memory holds K and V twice, a block that nears the end of
+// its walk takes over one that has not started (cluster launch control), so
+// that the next walk's loads and first products run under the last one's end:
+// B 4, H 16, L 2048, d 64: causal 173 -> 160 us, window of 256 104 -> 92, with
+// 4 sinks 126 -> 108.  All five
 // products run on tcgen05 with accumulators in TMEM:
 //   S^T  = K Q^T   (A = K, B = Q smem)              TMEM [0,128)
 //   P^T  (bf16, written by the compute warps)        over S^T: [0,32), [64,96)
@@ -36,7 +41,8 @@
 // output gradient (dout_scale, applied to dP, D and dV), and dV may be added
 // to what dv holds: the differential backward's second branch takes
 // -lambda dout and adds its dV to the first branch's.
-// Warp roles (512 threads): warp 0 TMA, warp 1 TMEM + MMA issue, warps 4-11
+// Warp roles (512 threads): warp 0 TMA loads, warp 1 TMEM + MMA issue, warp 2
+// dK and dV stores, warp 3 the next walk, warps 4-11
 // compute P and dS (one thread per key row and half of the query columns:
 // two warps per scheduler), warps 12-15 add dQ into the accumulator (one
 // thread per query row): they stage the fp32 tile in shared memory and one
@@ -66,11 +72,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
-// registers: 128 per thread at launch, then 56 (TMA / MMA warps), 168 (P and
-// dS), 120 (dQ) -- together exactly the launch's 512 x 128
-constexpr int kBwdLaunchRegs = 128, kBwdCtlRegs = 56, kBwdComputeRegs = 168, kBwdDQRegs = 120;
-static_assert(128 * kBwdCtlRegs + 256 * kBwdComputeRegs + 128 * kBwdDQRegs <= kBwdThreads * kBwdLaunchRegs,
-              "backward register split");
+// registers: 128 per thread at launch, then 56 (TMA / MMA warps) and, for P and
+// dS and for dQ (a row's channels), 168 and 120 with d = 128, else 176 and 104
+// -- together exactly the launch's 512 x 128
+constexpr int kBwdLaunchRegs = 128;
 
 template <int D, int DV>
 struct BwdLayout {
@@ -93,9 +98,15 @@ struct BwdLayout {
   // d = 128: one dO buffer and one 32-channel dQ staging box; two of each
   // would not fit in a block's 227 KB
   static constexpr int NDO = D == 128 ? 1 : 2;
-  static constexpr int OFF_K = 0;
+  // d = dv <= 64: K and V twice, the next walk's beside this one's
+  static constexpr int NKV = D == DV && D <= 64 ? 2 : 1;
+  static constexpr int KV = TILE + TILE_V;
+  static constexpr int CTL_REGS = 56, COMPUTE_REGS = D <= 64 ? 176 : 168, DQ_REGS = D <= 64 ? 104 : 120;
+  static_assert(128 * CTL_REGS + 256 * COMPUTE_REGS + 128 * DQ_REGS <= kBwdThreads * kBwdLaunchRegs,
+                "backward register split");
+  static constexpr int OFF_K = 0;                      // K and V, [NKV]
   static constexpr int OFF_V = TILE;
-  static constexpr int OFF_Q = TILE + TILE_V;          // Q[2]
+  static constexpr int OFF_Q = NKV * KV;               // Q[2]
   static constexpr int OFF_DO = OFF_Q + 2 * TILE;      // dO[NDO]
   static constexpr int OFF_DS = OFF_DO + NDO * TILE_V; // dS tile: 2 boxes [128 keys][64 queries], 128B swizzle
   static constexpr int DQS = D == 128 ? 128 * 32 * 4 : 128 * D * 4;  // fp32 boxes [128 rows][32], 128B swizzle
@@ -103,9 +114,11 @@ struct BwdLayout {
                                                           // has a whole tile period to read it out)
   static constexpr int OFF_VEC = OFF_DQS + DQS;        // fp32 L2[2][128], Dv[2][128]
   static constexpr int OFF_BAR = OFF_VEC + 4 * 128 * 4;
-  static constexpr int NBARS = 16;
-  static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;
-  static constexpr int SMEM = OFF_MISC + 64 + 1024;
+  static constexpr int NBARS = 28;
+  static constexpr int OFF_MISC = OFF_BAR + NBARS * 8;  // TMEM base, abort flag
+  static constexpr int OFF_NEXT = OFF_MISC + 16;        // answers of the launch control [2]
+  static constexpr int OFF_WALK = OFF_NEXT + 32;        // walks [2]
+  static constexpr int SMEM = OFF_WALK + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "backward shared memory");
   static_assert(OFF_Q % 1024 == 0 && OFF_DO % 1024 == 0 && OFF_DS % 1024 == 0 && OFF_DQS % 1024 == 0,
                 "swizzled tiles on 1024-byte boundaries");
@@ -173,87 +186,142 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t kColKT = 128, kColVT = 128 + D / 2;
   // softcap: sech^2, fp16 pairs, 32 columns per half
   constexpr uint32_t kColSech = kSechInS ? 32 : 128, kSechHalf = kSechInS ? 64 : 32;
+  // a CTA takes walk after walk from the launch's own queue
+  constexpr bool kMany = L::NKV == 2;
   // sech^2 in the S^T columns: the next S^T waits for the dS step
   constexpr bool kLateS = kSechInS && SCORE == SCORE_SOFTCAP;
   extern __shared__ uint8_t bsm_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(bsm_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* kv_full = bars + 0;
-  uint64_t* q_full = bars + 1;    // [2]
-  uint64_t* q_empty = bars + 3;   // [2]
-  uint64_t* s_full = bars + 5;
-  uint64_t* dp_full = bars + 6;
-  uint64_t* p_full = bars + 7;
-  uint64_t* ds_full = bars + 8;
-  uint64_t* dq_full = bars + 9;
-  uint64_t* dq_free = bars + 10;
-  uint64_t* done = bars + 11;
-  uint64_t* kvt_ready = bars + 12;  // K and V copied into TMEM
-  uint64_t* do_full = bars + 13;    // d = 128: the single dO buffer loaded ...
-  uint64_t* do_empty = bars + 14;   // ... and read by dV
+  uint64_t* q_full = bars + 0;    // [2]
+  uint64_t* q_empty = bars + 2;   // [2]
+  uint64_t* s_full = bars + 4;
+  uint64_t* dp_full = bars + 5;
+  uint64_t* p_full = bars + 6;
+  uint64_t* ds_full = bars + 7;
+  uint64_t* dq_full = bars + 8;
+  uint64_t* dq_free = bars + 9;
+  uint64_t* done = bars + 10;       // every product of a walk
+  uint64_t* kvt_ready = bars + 11;  // K and V copied into TMEM
+  uint64_t* do_full = bars + 12;    // d = 128: the single dO buffer loaded ...
+  uint64_t* do_empty = bars + 13;   // ... and read by dV
+  uint64_t* last = bars + 14;       // the CTA's last products
+  uint64_t* kv_full = bars + 15;    // [2]
+  uint64_t* kv_empty = bars + 17;   // [2]
+  uint64_t* out_full = bars + 19;   // [2] dK and dV staged over K and V (or stored)
+  uint64_t* dv_done = bars + 21;    // a walk's last dV
+  uint64_t* next_full = bars + 22;  // [2] the launch control's answer
+  uint64_t* walk_full = bars + 24;  // [2] a walk in shared memory
+  uint64_t* walk_empty = bars + 26;  // [2]
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   float* vec = reinterpret_cast<float*>(smem + L::OFF_VEC);  // L2[buf][128] then Dv[buf][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA: (batch b, key/value head hkv, key tile jt), key tiles in the
-  // outer order so that the first tiles of every head (the longest walks
-  // under causal and prefix masks) start first and the short ones end the grid
-  // (the far runs of the sink tiles come before them: each is as long as a
-  // window tile's walk)
-  const int n_far = p.far_chunks * p.sink_tiles * p.B * p.Hkv;
-  const bool far = static_cast<int>(blockIdx.x) < n_far;
-  const int unit = far ? blockIdx.x % (p.sink_tiles * p.B * p.Hkv) : blockIdx.x - n_far;
-  const int chunk = far ? blockIdx.x / (p.sink_tiles * p.B * p.Hkv) : -1;
-  const int jt = unit / (p.B * p.Hkv);
-  const int bh = unit % (p.B * p.Hkv);
-  const int hkv = bh % p.Hkv, b = bh / p.Hkv;
-  const int j0 = jt * 128;
   const int group = p.Hq / p.Hkv;
-  // query tiles that see any key of the tile (intervals are monotone in k)
-  int qlo0, qhi0, qlo1, qhi1;
-  col_bounds(p, b, j0, qlo0, qhi0);
-  col_bounds(p, b, min(j0 + 127, p.Lk - 1), qlo1, qhi1);
-  // with sinks an early key of the tile may reach further than its last one
-  qhi1 = max(qhi0, qhi1);
-  int it_lo = qlo0 / 128;
-  int it_hi = qhi1 >= qlo0 ? qhi1 / 128 : it_lo - 1;
-  const bool part = jt < p.sink_tiles && p.far_chunks > 0;  // this walk leaves partial dV, dK
-  if (part) {
-    const int f0 = far_begin(jt, p.window) + max(chunk, 0) * p.far_len;
-    if (far) {
-      it_lo = f0;
-      it_hi = min(it_hi, f0 + p.far_len - 1);
-    } else {
-      it_hi = min(it_hi, f0 - 1);
+  // Walk w: (batch b, key/value head hkv, key tile jt), key tiles in the outer
+  // order so that the first tiles of every head (the longest walks under causal
+  // and prefix masks) start first and the short ones end the grid (the far runs
+  // of the sink tiles come before them: each is as long as a window tile's
+  // walk).  Its query tiles [it_lo, it_lo + nq) are walked for each query head
+  // of the group.
+  struct __align__(16) Walk {
+    int b, hkv, jt, chunk;  // chunk: of a far run, else -1
+    int it_lo, nq, n_tiles;
+    int part;               // this walk leaves partial dV, dK
+  };
+  Walk* walks = reinterpret_cast<Walk*>(smem + L::OFF_WALK);
+  auto walk_of = [&](int w) {
+    Walk W;
+    const int n_far = p.far_chunks * p.sink_tiles * p.B * p.Hkv;
+    const bool far = w < n_far;
+    const int unit = far ? w % (p.sink_tiles * p.B * p.Hkv) : w - n_far;
+    W.chunk = far ? w / (p.sink_tiles * p.B * p.Hkv) : -1;
+    W.jt = unit / (p.B * p.Hkv);
+    const int bh = unit % (p.B * p.Hkv);
+    W.hkv = bh % p.Hkv;
+    W.b = bh / p.Hkv;
+    const int j0 = W.jt * 128;
+    // query tiles that see any key of the tile (intervals are monotone in k)
+    int qlo0, qhi0, qlo1, qhi1;
+    col_bounds(p, W.b, j0, qlo0, qhi0);
+    col_bounds(p, W.b, min(j0 + 127, p.Lk - 1), qlo1, qhi1);
+    // with sinks an early key of the tile may reach further than its last one
+    qhi1 = max(qhi0, qhi1);
+    W.it_lo = qlo0 / 128;
+    int it_hi = qhi1 >= qlo0 ? qhi1 / 128 : W.it_lo - 1;
+    W.part = W.jt < p.sink_tiles && p.far_chunks > 0;
+    if (W.part) {
+      const int f0 = far_begin(W.jt, p.window) + max(W.chunk, 0) * p.far_len;
+      if (far) {
+        W.it_lo = f0;
+        it_hi = min(it_hi, f0 + p.far_len - 1);
+      } else {
+        it_hi = min(it_hi, f0 - 1);
+      }
     }
-  }
-  const int nq = it_hi - it_lo + 1;
-  const int n_tiles = nq > 0 ? nq * group : 0;
+    W.nq = it_hi - W.it_lo + 1;
+    W.n_tiles = W.nq > 0 ? W.nq * group : 0;
+    return W;
+  };
+  // The steps of a walk: (query head, query tile), tiles in the inner order
+  struct Step {
+    int h, i0;
+  };
+  auto first_step = [&](const Walk& W) { return Step{W.hkv * group, W.it_lo * 128}; };
+  auto next_step = [&](const Walk& W, Step& x) {
+    x.i0 += 128;
+    if (x.i0 == (W.it_lo + W.nq) * 128) {
+      x.i0 = W.it_lo * 128;
+      ++x.h;
+    }
+  };
+  // The CTA's walks: walk k lies in walks[k & 1], the first one written below,
+  // the others by warp 3; n_tiles is -1 after the last.  Every role waits for
+  // the next walk and then lets go of the one it has done.
+  const Ctl ctl{reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC + 4), p.status, p.timeout_ns};
+  auto walk_here = [&](int k) { return wait_bar(&walk_full[k & 1], ((k - 1) >> 1) & 1u, ctl, 71); };
+  auto walk_done = [&](int k) { ptx::mbar_arrive(&walk_empty[k & 1]); };
 
-  // Q, the query rows' vectors and (with two buffers) dO of walk step n
-  auto load_q = [&](int n, uint64_t pol_keep) {
-    const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
-    const int buf = n & 1;
+  // K and V of the CTA's c-th walk with products; Q, the query rows' vectors and
+  // (with two buffers) dO of its t-th step
+  auto load_kv = [&](const Walk& W, int c, uint64_t pol_keep) {
+    uint64_t* bar = &kv_full[c & (L::NKV - 1)];
+    uint8_t* dst = smem + (c & (L::NKV - 1)) * L::KV;
+    ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(L::KV));
+#pragma unroll
+    for (int bx = 0; bx < L::NBOX; ++bx)
+      ptx::tma_load_4d(dst + L::OFF_K + bx * L::BOX, &tmK, bar, bx * L::BOXW, W.jt * 128, W.hkv, W.b, pol_keep);
+#pragma unroll
+    for (int bx = 0; bx < L::NBOX_V; ++bx)
+      ptx::tma_load_4d(dst + L::OFF_V + bx * L::BOX_V, &tmV, bar, bx * L::BOXW_V, W.jt * 128, W.hkv, W.b, pol_keep);
+  };
+  auto load_q = [&](const Walk& W, const Step& x, int t, uint64_t pol_keep) {
+    const int buf = t & 1;
     ptx::mbar_arrive_expect_tx(&q_full[buf], static_cast<uint32_t>(L::TILE + (L::NDO == 2 ? L::TILE_V : 0)) + 2u * 512u);
 #pragma unroll
     for (int bx = 0; bx < L::NBOX; ++bx)
-      ptx::tma_load_4d(smem + L::OFF_Q + buf * L::TILE + bx * L::BOX, &tmQ, &q_full[buf], bx * L::BOXW, i0, h, b, pol_keep);
+      ptx::tma_load_4d(smem + L::OFF_Q + buf * L::TILE + bx * L::BOX, &tmQ, &q_full[buf], bx * L::BOXW, x.i0, x.h, W.b, pol_keep);
     if (L::NDO == 2) {
 #pragma unroll
       for (int bx = 0; bx < L::NBOX_V; ++bx)
-        ptx::tma_load_4d(smem + L::OFF_DO + buf * L::TILE_V + bx * L::BOX_V, &tmDO, &q_full[buf], bx * L::BOXW_V, i0, h, b,
-                         pol_keep);
+        ptx::tma_load_4d(smem + L::OFF_DO + buf * L::TILE_V + bx * L::BOX_V, &tmDO, &q_full[buf], bx * L::BOXW_V, x.i0, x.h,
+                         W.b, pol_keep);
     }
-    const int row = b * p.Hq + h;
-    ptx::tma_load_2d(vec + buf * 128, &tmL2, &q_full[buf], i0, row, pol_keep);
-    ptx::tma_load_2d(vec + 256 + buf * 128, &tmDv, &q_full[buf], i0, row, pol_keep);
+    const int row = W.b * p.Hq + x.h;
+    ptx::tma_load_2d(vec + buf * 128, &tmL2, &q_full[buf], x.i0, row, pol_keep);
+    ptx::tma_load_2d(vec + 256 + buf * 128, &tmDv, &q_full[buf], x.i0, row, pol_keep);
   };
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(kv_full, 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&q_full[i], 1);
       ptx::mbar_init(&q_empty[i], 1);
+      ptx::mbar_init(&kv_full[i], 1);
+      ptx::mbar_init(&kv_empty[i], 1);
+      ptx::mbar_init(&out_full[i], 8);
+      ptx::mbar_init(&next_full[i], 1);
+      ptx::mbar_init(&walk_full[i], 1);
+      ptx::mbar_init(&walk_empty[i], 15);  // TMA, MMA, store, 8 compute warps, 4 dQ warps
     }
     ptx::mbar_init(s_full, 1);
     ptx::mbar_init(dp_full, 1);
@@ -262,6 +330,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ptx::mbar_init(dq_full, 1);
     ptx::mbar_init(dq_free, 4);
     ptx::mbar_init(done, 1);
+    ptx::mbar_init(last, 1);
+    ptx::mbar_init(dv_done, 1);
     ptx::mbar_init(kvt_ready, 8);
     ptx::mbar_init(do_full, 1);
     ptx::mbar_init(do_empty, 1);
@@ -270,16 +340,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     ptx::fence_proxy_async_smem();
     // this thread issues every copy: K, V and the first query tile set out while
     // TMEM is allocated (0.5 us of a short walk's 11)
-    if (n_tiles > 0) {
+    const Walk W = walk_of(blockIdx.x);
+    walks[0] = W;
+    if (W.n_tiles > 0) {
       const uint64_t pol_keep = ptx::policy_evict_last();
-      ptx::mbar_arrive_expect_tx(kv_full, static_cast<uint32_t>(L::TILE + L::TILE_V));
-#pragma unroll
-      for (int bx = 0; bx < L::NBOX; ++bx)
-        ptx::tma_load_4d(smem + L::OFF_K + bx * L::BOX, &tmK, kv_full, bx * L::BOXW, j0, hkv, b, pol_keep);
-#pragma unroll
-      for (int bx = 0; bx < L::NBOX_V; ++bx)
-        ptx::tma_load_4d(smem + L::OFF_V + bx * L::BOX_V, &tmV, kv_full, bx * L::BOXW_V, j0, hkv, b, pol_keep);
-      load_q(0, pol_keep);
+      load_kv(W, 0, pol_keep);
+      load_q(W, first_step(W), 0, pol_keep);
     }
   }
   if (warp == 1) {
@@ -290,37 +356,65 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
-  const Ctl ctl{reinterpret_cast<volatile uint32_t*>(&misc[1]), p.status, p.timeout_ns};
   const uint64_t drain_ns = 50ull * 1000ull * 1000ull;
 
   if (warp < 4) {
-    ptx::setmaxnreg_dec<kBwdCtlRegs>();
+    ptx::setmaxnreg_dec<L::CTL_REGS>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------------- TMA
       // (K, V and the first tile are under way already)
       const uint64_t pol_keep = ptx::policy_evict_last();
-      int issued = n_tiles > 0 ? 1 : 0, do_issued = 0;
+      int t = 0, c = 0, asked = 1;        // steps, walks with products, walks asked for (or had), so far
+      int t_issued = walks[0].n_tiles > 0 ? 1 : 0, c_issued = t_issued, do_issued = 0;
       bool ok = true;
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
-        if (n > 0) {
-          if (!wait_bar(&q_empty[n & 1], ((n >> 1) & 1u) ^ 1u, ctl, 50)) { ok = false; break; }
-          load_q(n, pol_keep);
+      for (int k = 0;; ++k) {
+        const Walk W = walks[k & 1];
+        if (W.n_tiles < 0) break;
+        // the next walk is asked for when this one's last step has been asked
+        // for, about two steps before its end: the answer is there in time, and
+        // a CTA holds no walk long that another could start
+        auto ask = [&]() -> bool {
+          if (!kMany) return true;
+          if (!wait_bar(&walk_empty[asked & 1], ((asked >> 1) & 1u) ^ 1u, ctl, 72)) return false;
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive_expect_tx(&next_full[asked & 1], 16u);
+          ptx::launch_next(smem + L::OFF_NEXT + 16 * (asked & 1), &next_full[asked & 1]);
+          ++asked;
+          return true;
+        };
+        if (W.n_tiles > 0 && c == c_issued) {
+          if (!wait_bar(&kv_empty[c & (L::NKV - 1)], ((c / L::NKV) & 1u) ^ 1u, ctl, 49)) break;
+          load_kv(W, c, pol_keep);
+          c_issued = c + 1;
         }
-        issued = n + 1;
-        if (L::NDO == 1) {
-          // one dO buffer: tile n's once dV(n - 1) has read tile n - 1's
-          if (!wait_bar(do_empty, (n & 1u) ^ 1u, ctl, 56)) { ok = false; break; }
-          ptx::mbar_arrive_expect_tx(do_full, L::TILE_V);
+        Step x = first_step(W);
+        for (int n = 0; n < W.n_tiles && ok; ++n, ++t, next_step(W, x)) {
+          if (t == t_issued) {
+            if (!wait_bar(&q_empty[t & 1], ((t >> 1) & 1u) ^ 1u, ctl, 50)) { ok = false; break; }
+            load_q(W, x, t, pol_keep);
+            t_issued = t + 1;
+          }
+          if (L::NDO == 1) {
+            // one dO buffer: tile n's once dV(n - 1) has read tile n - 1's
+            if (!wait_bar(do_empty, (t & 1u) ^ 1u, ctl, 56)) { ok = false; break; }
+            ptx::mbar_arrive_expect_tx(do_full, L::TILE_V);
 #pragma unroll
-          for (int bx = 0; bx < L::NBOX_V; ++bx)
-            ptx::tma_load_4d(smem + L::OFF_DO + bx * L::BOX_V, &tmDO, do_full, bx * L::BOXW_V, i0, h, b, pol_keep);
-          do_issued = n + 1;
+            for (int bx = 0; bx < L::NBOX_V; ++bx)
+              ptx::tma_load_4d(smem + L::OFF_DO + bx * L::BOX_V, &tmDO, do_full, bx * L::BOXW_V, x.i0, x.h, W.b, pol_keep);
+            do_issued = t + 1;
+          }
+          if (n + 1 == W.n_tiles && !ask()) { ok = false; break; }
         }
+        if (W.n_tiles > 0) ++c;
+        else if (ok) ok = ask();
+        if (!kMany || !ok || !walk_here(k + 1)) break;
+        walk_done(k);
       }
       if (*ctl.abort) {
-        if (n_tiles > 0) wait_drain(kv_full, 0u, drain_ns);
-        for (int n = issued - 2 < 0 ? 0 : issued - 2; n < issued; ++n) wait_drain(&q_full[n & 1], (n >> 1) & 1u, drain_ns);
+        for (int i = max(c_issued - L::NKV, 0); i < c_issued; ++i)
+          wait_drain(&kv_full[i & (L::NKV - 1)], (i / L::NKV) & 1u, drain_ns);
+        for (int i = max(t_issued - 2, 0); i < t_issued; ++i) wait_drain(&q_full[i & 1], (i >> 1) & 1u, drain_ns);
+        for (int i = max(asked - 2, 1); i < asked; ++i) wait_drain(&next_full[i & 1], ((i - 1) >> 1) & 1u, drain_ns);
         if (do_issued > 0) wait_drain(do_full, (do_issued - 1) & 1u, drain_ns);
       }
     } else if (warp == 1 && lane == 0) {
@@ -329,25 +423,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       constexpr uint32_t ID_DV = ptx::idesc_bf16_f32(128, DV, true);         // dV (B = dO, N-major)
       constexpr uint32_t ID_DK = ptx::idesc_bf16_f32(128, D, true);          // dK (B = Q, N-major)
       constexpr uint32_t ID_DQ = ptx::idesc_bf16_f32(128, D, true) | (1u << 15);  // dQ: A = dS, M-major
-      const uint32_t k_a = ptx::smem_u32(smem + L::OFF_K), v_a = ptx::smem_u32(smem + L::OFF_V);
       const uint32_t ds_a = ptx::smem_u32(smem + L::OFF_DS);
       const uint64_t dsa = ptx::smem_desc(ds_a, 128 * 128, 1024, 2u);
       // N-major B operands (N = D channels across NBOX boxes, LBO = box
       // stride) and K-major operands (k-steps through ::koff)
-      const uint64_t kn = ptx::smem_desc(k_a, L::BOX, 8 * L::BOXB, L::SWZ);
-      const uint64_t ka = ptx::smem_desc(k_a, 16, 8 * L::BOXB, L::SWZ);
-      const uint64_t va = ptx::smem_desc(v_a, 16, 8 * L::BOXB_V, L::SWZ_V);
-      // S^T = K Q^T and dP^T = V dO^T of query tile n (K-major, k-steps of 16
-      // channels), each once its Q / dO tile has landed
+      uint64_t kn = 0, ka = 0, va = 0;
+      // a descriptor's k-steps are formed where they are used: kept over the
+      // whole walk they would take more registers than the warp has
+      auto here = [](uint64_t d) {
+        asm volatile("" : "+l"(d));
+        return d;
+      };
+      // S^T = K Q^T and dP^T = V dO^T of the CTA's n-th step (K-major, k-steps
+      // of 16 channels), each once its Q / dO tile has landed
       auto issue_s = [&](int n) -> bool {
         const int buf = n & 1;
         if (!wait_bar(&q_full[buf], (n >> 1) & 1u, ctl, 52)) return false;
         ptx::tc_fence_after();
+        const uint64_t kd = here(ka);
         const uint64_t qb = ptx::smem_desc(ptx::smem_u32(smem + L::OFF_Q + buf * L::TILE), 16, 8 * L::BOXB, L::SWZ);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
           if (kKVT) ptx::mma_ts(tmem + kColS, tmem + kColKT + kb * 8, qb + L::koff(kb), ID_SS, kb > 0);
-          else ptx::mma_ss(tmem + kColS, ka + L::koff(kb), qb + L::koff(kb), ID_SS, kb > 0);
+          else ptx::mma_ss(tmem + kColS, kd + L::koff(kb), qb + L::koff(kb), ID_SS, kb > 0);
         }
         ptx::mma_commit(s_full);
         return true;
@@ -357,12 +455,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!wait_bar(do_full, n & 1u, ctl, 57)) return false;
           ptx::tc_fence_after();
         }
+        const uint64_t vd = here(va);
         const uint64_t dob = ptx::smem_desc(
             ptx::smem_u32(smem + L::OFF_DO + (L::NDO == 2 ? (n & 1) : 0) * L::TILE_V), 16, 8 * L::BOXB_V, L::SWZ_V);
 #pragma unroll
         for (int kb = 0; kb < DV / 16; ++kb) {
           if (kKVT) ptx::mma_ts(tmem + kColDP, tmem + kColVT + kb * 8, dob + L::koff_v(kb), ID_SS, kb > 0);
-          else ptx::mma_ss(tmem + kColDP, va + L::koff_v(kb), dob + L::koff_v(kb), ID_SS, kb > 0);
+          else ptx::mma_ss(tmem + kColDP, vd + L::koff_v(kb), dob + L::koff_v(kb), ID_SS, kb > 0);
         }
         ptx::mma_commit(dp_full);
         return true;
@@ -376,12 +475,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // (over the S^T columns) and dK(n) dS^T before the next products
       // overwrite those columns, and a commit covers every product issued
       // before it.
-      bool ok = n_tiles == 0 ||
-                (wait_bar(kv_full, 0u, ctl, 51) && (!kKVT || wait_bar(kvt_ready, 0u, ctl, 58)) && issue_s(0) &&
-                 issue_dp(0));
-      for (int n = 0; n < n_tiles && ok; ++n) {
-        const int buf = n & 1;
-        const uint32_t ph = n & 1;
+      bool ok = true;
+      int t = 0, c = 0;  // steps and walks with products so far
+      for (int k = 0; ok; ++k) {
+      const int n_tiles = walks[k & 1].n_tiles;
+      if (n_tiles < 0) break;
+      if (n_tiles > 0) {
+        const int kb = c & (L::NKV - 1);
+        const uint32_t k_a = ptx::smem_u32(smem + kb * L::KV + L::OFF_K), v_a = ptx::smem_u32(smem + kb * L::KV + L::OFF_V);
+        kn = ptx::smem_desc(k_a, L::BOX, 8 * L::BOXB, L::SWZ);
+        ka = ptx::smem_desc(k_a, 16, 8 * L::BOXB, L::SWZ);
+        va = ptx::smem_desc(v_a, 16, 8 * L::BOXB_V, L::SWZ_V);
+        ok = wait_bar(&kv_full[kb], (c / L::NKV) & 1u, ctl, 51) && (!kKVT || wait_bar(kvt_ready, c & 1u, ctl, 58)) &&
+             issue_s(t) && issue_dp(t);
+      }
+      for (int n = 0; n < n_tiles && ok; ++n, ++t) {
+        const int buf = t & 1;
+        const uint32_t ph = t & 1;
         const bool more = n + 1 < n_tiles;
         const uint32_t q_a = ptx::smem_u32(smem + L::OFF_Q + buf * L::TILE);
         const uint32_t do_a = ptx::smem_u32(smem + L::OFF_DO + (L::NDO == 2 ? buf : 0) * L::TILE_V);
@@ -394,33 +504,85 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           ptx::mma_ts(tmem + kColDV, tmem + kColS + kb * 8 + (kb >= 4 ? 32 : 0), don + ((kb * 16 * L::BOXB_V) >> 4),
                       ID_DV, (n > 0 || kb > 0));
         if (L::NDO == 1) ptx::mma_commit(do_empty);
-        if (!kLateS && more && !issue_s(n + 1)) { ok = false; break; }
+        if (!more) ptx::mma_commit(dv_done);
+        if (!kLateS && more && !issue_s(t + 1)) { ok = false; break; }
         // dK += dS^T Q (dS^T of queries 64-127 sits 64 columns further on)
         if (!wait_bar(ds_full, ph, ctl, 54)) { ok = false; break; }
         ptx::tc_fence_after();
-        if (kLateS && more && !issue_s(n + 1)) { ok = false; break; }
+        if (kLateS && more && !issue_s(t + 1)) { ok = false; break; }
         const uint64_t qn = ptx::smem_desc(q_a, L::BOX, 8 * L::BOXB, L::SWZ);
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb)
           ptx::mma_ts(tmem + kColDK, tmem + kColDP + kb * 8 + (kb >= 4 ? 32 : 0), qn + ((kb * 16 * L::BOXB) >> 4),
                       ID_DK, (n > 0 || kb > 0));
-        if (!kWide && more) issue_dp(n + 1);
+        if (!kWide && more) issue_dp(t + 1);
         // dQ = dS K once the dQ warps have read the previous one
         if (!wait_bar(dq_free, ph ^ 1u, ctl, 55)) { ok = false; break; }
         ptx::tc_fence_after();
+        const uint64_t dsd = here(dsa), knd = here(kn);
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb)
-          ptx::mma_ss(tmem + kColDQ, dsa + ((kb * 16 * 128) >> 4), kn + ((kb * 16 * L::BOXB) >> 4), ID_DQ, kb > 0);
+          ptx::mma_ss(tmem + kColDQ, dsd + ((kb * 16 * 128) >> 4), knd + ((kb * 16 * L::BOXB) >> 4), ID_DQ, kb > 0);
         ptx::mma_commit(dq_full);
         ptx::mma_commit(&q_empty[buf]);
         if (kWide && more) {
           if (!wait_bar(dq_free, ph, ctl, 59)) { ok = false; break; }
           ptx::tc_fence_after();
-          if (!issue_dp(n + 1)) { ok = false; break; }
+          if (!issue_dp(t + 1)) { ok = false; break; }
         }
       }
-      ptx::mma_commit(done);
-      wait_drain(done, 0u, drain_ns);
+      if (!ok) break;
+      if (n_tiles > 0) {
+        ptx::mma_commit(done);
+        ++c;
+      }
+      if (!kMany || !walk_here(k + 1)) break;
+      walk_done(k);
+      }
+      // the products in flight end before TMEM is freed
+      ptx::mma_commit(last);
+      wait_drain(last, 0u, drain_ns);
+    } else if (warp == 2 && lane == 0) {
+      // -------------------------------------------------------------- stores
+      // dK and dV of each walk, staged over its K and V, go out by TMA (rows
+      // past Lk are clipped); then the next walk but one may load there
+      int c = 0;
+      for (int k = 0;; ++k) {
+        const Walk W = walks[k & 1];
+        if (W.n_tiles < 0) break;
+        if (W.n_tiles > 0) {
+          const int kb = c & (L::NKV - 1);
+          if (!wait_bar(&out_full[kb], (c / L::NKV) & 1u, ctl, 74)) break;
+          if (!W.part) {
+#pragma unroll
+            for (int bx = 0; bx < L::NBOX; ++bx)
+              ptx::tma_store_4d(&tmDK, smem + kb * L::KV + L::OFF_K + bx * L::BOX, bx * L::BOXW, W.jt * 128, W.hkv, W.b);
+            if (!p.dv_accumulate) {
+#pragma unroll
+              for (int bx = 0; bx < L::NBOX_V; ++bx)
+                ptx::tma_store_4d(&tmGV, smem + kb * L::KV + L::OFF_V + bx * L::BOX_V, bx * L::BOXW_V, W.jt * 128, W.hkv, W.b);
+            }
+            ptx::bulk_commit_group();
+            ptx::bulk_wait_group_read0();
+          }
+          ptx::mbar_arrive(&kv_empty[kb]);
+          ++c;
+        }
+        if (!kMany || !walk_here(k + 1)) break;
+        walk_done(k);
+      }
+    } else if (kMany && warp == 3 && lane == 0) {
+      // --------------------------------------------------------------- walks
+      // from the launch control's answers to walks in shared memory, once for
+      // all roles (the divisions and bounds take 0.8 us)
+      for (int k = 1;; ++k) {
+        if (!wait_bar(&next_full[k & 1], ((k - 1) >> 1) & 1u, ctl, 73)) break;
+        const int w = ptx::launch_query(smem + L::OFF_NEXT + 16 * (k & 1));
+        if (w >= 0) walks[k & 1] = walk_of(w);
+        else walks[k & 1].n_tiles = -1;
+        ptx::mbar_arrive(&walk_full[k & 1]);
+        if (w < 0) break;
+      }
     }
     __syncwarp();
     ptx::tc_fence_before();
@@ -433,19 +595,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ---------------------------------------- P and dS (key rows, half tiles)
     // Thread (quad, lane) of half hf owns key row r and the query columns
     // [64 hf, 64 hf + 64) of every query tile: its S^T, P^T and dP^T columns.
-    ptx::setmaxnreg_inc<kBwdComputeRegs>();
+    ptx::setmaxnreg_inc<L::COMPUTE_REGS>();
     const int quad = warp & 3;
     const int hf = (warp - 4) >> 2;
     const int r = quad * 32 + lane;          // key row of the tile
-    const int kg = j0 + r;                   // key index
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t cS = kColS + 64 * hf;     // S^T
     const uint32_t cP = cS;                  // P^T, bf16 pairs, over the S^T just read
     const uint32_t cSech = kColSech + kSechHalf * hf;  // softcap: sech^2, fp16 pairs
     const uint32_t cDP = kColDP + 64 * hf;   // dP^T; dS^T as bf16 pairs over its first 32 columns
-    int cqlo, cqhi;
-    col_bounds(p, b, kg < p.Lk ? kg : p.Lk - 1, cqlo, cqhi);
-    if (kg >= p.Lk) { cqlo = 1; cqhi = 0; }  // keys past the end see nothing
     const float scale_log2 = p.scale * kLog2e;
     const float2 sc2 = make_float2(scale_log2, scale_log2);
     const float kcap = p.softcap * kLog2e;
@@ -455,21 +613,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float ikc = SCORE == SCORE_SOFTCAP ? 1.0f / kcap : 0.f;
     const float gsc = p.dout_scale;  // dP of the scaled dO (D comes scaled from the pre-kernel)
     const float2 ikc2 = make_float2(ikc, ikc);
-    bool ok = true;
-    if constexpr (kKVT) if (n_tiles > 0) {
-      // this thread's key row of K (half 0) or V (half 1) into TMEM: 16-byte
-      // chunk c of row r sits at c ^ (r & 7) (128-byte rows) or
-      // c ^ ((r >> 1) & 3) (64-byte rows) of the swizzled tile
-      ok = __all_sync(0xffffffffu, wait_bar(kv_full, 0u, ctl, 65));
-      if (ok) {
-        const uint8_t* row = smem + (hf ? L::OFF_V : L::OFF_K) + r * L::ROWB;
-        uint32_t kv[D / 2];
+    // this thread's key row of K (half 0) or V (half 1) of the CTA's c-th walk
+    // into registers, and from there into TMEM: 16-byte chunk c of row r sits at
+    // c ^ (r & 7) (128-byte rows) or c ^ ((r >> 1) & 3) (64-byte rows) of the
+    // swizzled tile
+    constexpr int KVR = kKVT ? D / 2 : 1;
+    auto read_kv = [&](int c, uint32_t (&kv)[KVR]) -> bool {
+      if constexpr (kKVT) {
+        if (!__all_sync(0xffffffffu, wait_bar(&kv_full[c & (L::NKV - 1)], (c / L::NKV) & 1u, ctl, 65))) return false;
+        const uint8_t* row = smem + (c & (L::NKV - 1)) * L::KV + (hf ? L::OFF_V : L::OFF_K) + r * L::ROWB;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const int sc = L::ROWB == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+        for (int c8 = 0; c8 < D / 8; ++c8) {
+          const int sc = L::ROWB == 128 ? (c8 ^ (r & 7)) : (c8 ^ ((r >> 1) & 3));
           const uint4 v4 = *reinterpret_cast<const uint4*>(row + (sc << 4));
-          kv[4 * c] = v4.x; kv[4 * c + 1] = v4.y; kv[4 * c + 2] = v4.z; kv[4 * c + 3] = v4.w;
+          kv[4 * c8] = v4.x; kv[4 * c8 + 1] = v4.y; kv[4 * c8 + 2] = v4.z; kv[4 * c8 + 3] = v4.w;
         }
+      }
+      return true;
+    };
+    auto put_kv = [&](const uint32_t (&kv)[KVR]) {
+      if constexpr (kKVT) {
         const uint32_t ta = tl + (hf ? kColVT : kColKT);
         if constexpr (D == 64) ptx::tmem_st32(ta, kv);
         else ptx::tmem_st16(ta, kv);
@@ -478,17 +641,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(kvt_ready);
       }
+    };
+    int t = 0, c = 0;  // steps and walks with products so far
+    bool ok = true;
+    if (walks[0].n_tiles > 0) {
+      uint32_t kv[KVR];
+      ok = read_kv(0, kv);
+      if (ok) put_kv(kv);
     }
-    for (int n = 0; n < n_tiles && ok; ++n) {
-      const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
+    for (int k = 0; ok; ++k) {
+    const int n_tiles = walks[k & 1].n_tiles;
+    if (n_tiles < 0) break;
+    const int kg = walks[k & 1].jt * 128 + r;  // key index
+    int cqlo, cqhi;
+    col_bounds(p, walks[k & 1].b, kg < p.Lk ? kg : p.Lk - 1, cqlo, cqhi);
+    if (kg >= p.Lk) { cqlo = 1; cqhi = 0; }  // keys past the end see nothing
+    const int i_lo = walks[k & 1].it_lo * 128, i_end = i_lo + walks[k & 1].nq * 128;
+    int h = walks[k & 1].hkv * group, i0 = i_lo;
+    for (int n = 0; n < n_tiles && ok; ++n, ++t) {
       const int q0 = i0 + 64 * hf;           // first query column of this half
-      const int buf = n & 1;
-      const uint32_t ph = n & 1;
+      const int buf = t & 1;
+      const uint32_t ph = t & 1;
       const float* l2 = vec + buf * 128 + 64 * hf;
       const float* dvec = vec + 256 + buf * 128 + 64 * hf;
       if (!__all_sync(0xffffffffu, wait_bar(s_full, ph, ctl, 60))) { ok = false; break; }
       // this tile's LSE and D rows came with Q (TMA); observe that barrier too
-      if (!__all_sync(0xffffffffu, wait_bar(&q_full[buf], (n >> 1) & 1u, ctl, 64))) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, wait_bar(&q_full[buf], (t >> 1) & 1u, ctl, 64))) { ok = false; break; }
       ptx::tc_fence_after();
       float x[64];
       ptx::tmem_ld32f(tl + cS, &x[0]);
@@ -655,87 +833,112 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ds_full);
+      i0 += 128;
+      if (i0 == i_end) {
+        i0 = i_lo;
+        ++h;
+      }
     }
-    // dV (half 0) or dK (half 1) of this thread's key row, once every product
-    // is done (the TMEM loads are warp-wide; only the stores depend on the row).
-    // The row goes through the idle V (K) tile in shared memory and out by TMA,
-    // which clips rows past Lk; a thread's own stores of its row, 16 bytes in
-    // each of 32 lines a time, take 1 us longer.  Partial sums and additions to
-    // dv are stored directly.  Whether to go on is decided jointly by the half's
-    // four warps, as below.
-    const bool finished = ok && __all_sync(0xffffffffu, wait_bar(done, 0u, ctl, 63));
-    if (ptx::named_bar_and(2 + hf, 128, finished)) {
-      ptx::tc_fence_after();
-      const bool z = n_tiles == 0;
-      const int64_t row = (static_cast<int64_t>(b) * p.Hkv + hkv) * p.Lk + kg;
-      float* prow = part ? p.part + (((static_cast<int64_t>(bh) * p.sink_tiles + jt) * (1 + p.far_chunks) + chunk + 1) * 128 + r) * (D + DV)
-                         : nullptr;
-      // NC columns of TMEM from col, times f: fp32 into prow, added to the bf16
-      // row of base with acc, or bf16 into the staged tile
-      auto write_row = [&](auto nc, uint32_t col, void* base, float f, bool acc, int pcol, uint8_t* tile) {
-        constexpr int NC = decltype(nc)::value;
-        constexpr int EC = NC < 64 ? NC : 64;  // columns per TMEM read-out, and per staged box
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + row * NC);
+    // The walk's dV and dK, half of the channels of its key row per thread (the
+    // TMEM loads are warp-wide; only the stores depend on the row).  What needs
+    // no more products comes first, while the last ones run: the next walk, dV,
+    // the next K and V into registers; then, with every product done, K and V
+    // into TMEM, so that the next walk's first S^T and dP^T start, and dK.  Rows
+    // are staged over the walk's V and K in shared memory and the store warp
+    // sends the tiles out by TMA; a thread's own stores of its row, 16 bytes in
+    // each of 32 lines a time, take 1 us longer.  Partial sums, additions to dv
+    // and the zeros of a walk without steps are stored directly.  (B 4, H 16, L
+    // 2048, window 256: 2.0 us a step, three steps a walk, and 2.4 us between
+    // two walks' steps; 5.1 us with a launch per walk.)
+    if (!ok) break;
+    const bool z = n_tiles == 0;
+    const Walk P = walks[k & 1];
+    if (kMany && !__all_sync(0xffffffffu, walk_here(k + 1))) break;
+    const int kb = c & (L::NKV - 1);
+    const int bh = P.b * p.Hkv + P.hkv, key = P.jt * 128 + r;
+    const int64_t row = static_cast<int64_t>(bh) * p.Lk + key;
+    // partial sums: [(DV + D) / 4][128 rows][4], so that a warp's stores are whole lines
+    float4* prow = P.part ? reinterpret_cast<float4*>(p.part) +
+                                ((static_cast<int64_t>(bh) * p.sink_tiles + P.jt) * (1 + p.far_chunks) + P.chunk + 1) *
+                                    (128 * ((D + DV) / 4)) + r
+                          : nullptr;
+    // this half's NC / 2 columns of TMEM from col, times f: fp32 into prow, added
+    // to the bf16 row of base with acc, or bf16 into the staged tile
+    auto write_half = [&](auto nc, uint32_t col, void* base, float f, bool acc, int pcol, uint8_t* tile) {
+      constexpr int NC = decltype(nc)::value, HC = NC / 2;
+      constexpr int BW = NC < 64 ? NC : 64;  // columns of a staged box
+      const int c0 = HC * hf;
+      float a[HC];
+      if constexpr (HC == 16) {
+        uint32_t u[16];
+        ptx::tmem_ld16(tl + col + c0, u);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence16(u);
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += EC) {
-          float a[EC];
+        for (int c = 0; c < 16; ++c) a[c] = __uint_as_float(u[c]);
+      } else {
 #pragma unroll
-          for (int c = 0; c < EC; c += 32) ptx::tmem_ld32f(tl + col + c0 + c, &a[c]);
-          ptx::tmem_ld_wait();
+        for (int c = 0; c < HC; c += 32) ptx::tmem_ld32f(tl + col + c0 + c, &a[c]);
+        ptx::tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < EC; c += 32) ptx::reg_fence32f(&a[c]);
-          if (prow) {
+        for (int c = 0; c < HC; c += 32) ptx::reg_fence32f(&a[c]);
+      }
+      if (prow) {
 #pragma unroll
-            for (int c = 0; c < EC; c += 4)
-              *reinterpret_cast<float4*>(prow + pcol + c0 + c) =
-                  z ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
-            continue;
-          }
+        for (int c = 0; c < HC; c += 4)
+          prow[((pcol + c0 + c) / 4) * 128] =
+              z ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(a[c] * f, a[c + 1] * f, a[c + 2] * f, a[c + 3] * f);
+        return;
+      }
+      uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + row * NC + c0);
 #pragma unroll
-          for (int c = 0; c < EC; c += 8) {
-            float o[8];
+      for (int c = 0; c < HC; c += 8) {
+        float o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = z ? 0.f : a[c + e] * f;
-            if (acc) {
-              if (kg >= p.Lk) continue;
-              const uint4 prev = dst[(c0 + c) / 8];
-              const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&prev);
+        for (int e = 0; e < 8; ++e) o[e] = z ? 0.f : a[c + e] * f;
+        if (acc) {
+          if (key >= p.Lk) continue;
+          const uint4 prev = dst[c / 8];
+          const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&prev);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 pf = __bfloat1622float2(p2[e]);
-                o[2 * e] += pf.x;
-                o[2 * e + 1] += pf.y;
-              }
-            }
-            const uint4 w = make_uint4(ptx::pack_bf16x2(o[0], o[1]), ptx::pack_bf16x2(o[2], o[3]),
-                                       ptx::pack_bf16x2(o[4], o[5]), ptx::pack_bf16x2(o[6], o[7]));
-            // box c0 / EC of the tile: 16-byte chunks at the swizzled positions
-            const int k = c / 8, sw = EC == 64 ? (k ^ (r & 7)) : (k ^ ((r >> 1) & 3));
-            if (acc) dst[(c0 + c) / 8] = w;
-            else *reinterpret_cast<uint4*>(tile + (c0 / EC) * (128 * EC * 2) + r * (EC * 2) + (sw << 4)) = w;
+          for (int e = 0; e < 4; ++e) {
+            const float2 pf = __bfloat1622float2(p2[e]);
+            o[2 * e] += pf.x;
+            o[2 * e + 1] += pf.y;
           }
         }
-      };
-      const bool acc = hf == 0 && p.dv_accumulate != 0;
-      if (hf) write_row(std::integral_constant<int, D>{}, kColDK, p.dk, n_tiles > 0 ? p.scale : 1.0f, false, DV, smem + L::OFF_K);
-      else write_row(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, acc, 0, smem + L::OFF_V);
-      if (!prow && !acc) {
-        ptx::fence_proxy_async_smem();
-        ptx::named_bar_sync(2 + hf, 128);
-        if (lane == 0 && quad == 0) {
-          if (hf) {
-#pragma unroll
-            for (int bx = 0; bx < L::NBOX; ++bx)
-              ptx::tma_store_4d(&tmDK, smem + L::OFF_K + bx * L::BOX, bx * L::BOXW, j0, hkv, b);
-          } else {
-#pragma unroll
-            for (int bx = 0; bx < L::NBOX_V; ++bx)
-              ptx::tma_store_4d(&tmGV, smem + L::OFF_V + bx * L::BOX_V, bx * L::BOXW_V, j0, hkv, b);
-          }
-          ptx::bulk_commit_group();
-          ptx::bulk_wait_group_read0();
+        const uint4 v = make_uint4(ptx::pack_bf16x2(o[0], o[1]), ptx::pack_bf16x2(o[2], o[3]),
+                                   ptx::pack_bf16x2(o[4], o[5]), ptx::pack_bf16x2(o[6], o[7]));
+        // 16-byte chunks at the swizzled positions of their box
+        const int k = (c0 + c) % BW / 8, sw = BW == 64 ? (k ^ (r & 7)) : (k ^ ((r >> 1) & 3));
+        if (acc || z) {
+          if (key < p.Lk) dst[c / 8] = v;
+        } else {
+          *reinterpret_cast<uint4*>(tile + ((c0 + c) / BW) * (128 * BW * 2) + r * (BW * 2) + (sw << 4)) = v;
         }
       }
+    };
+    if (!z && !__all_sync(0xffffffffu, wait_bar(dv_done, c & 1u, ctl, 66))) break;
+    ptx::tc_fence_after();
+    write_half(std::integral_constant<int, DV>{}, kColDV, p.dv, p.dout_scale, p.dv_accumulate != 0, 0,
+               smem + kb * L::KV + L::OFF_V);
+    const bool more_kv = kMany && walks[(k + 1) & 1].n_tiles > 0;
+    uint32_t kv[KVR] = {};
+    if (more_kv && !read_kv(z ? c : c + 1, kv)) break;
+    if (!z && !__all_sync(0xffffffffu, wait_bar(done, c & 1u, ctl, 63))) break;
+    ptx::tc_fence_after();
+    if (more_kv) put_kv(kv);
+    write_half(std::integral_constant<int, D>{}, kColDK, p.dk, p.scale, false, DV, smem + kb * L::KV + L::OFF_K);
+    if (!z) {
+      ptx::fence_proxy_async_smem();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&out_full[kb]);
+      ++c;
+    }
+    if (!kMany) break;
+    __syncwarp();
+    if (lane == 0) walk_done(k);
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -747,16 +950,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // tensor reduction (rows past Lq skipped by the map).  Whether to go on is
     // decided jointly by the four warps (barrier with an AND), so that every
     // warp takes the same named barriers.
-    ptx::setmaxnreg_dec<kBwdDQRegs>();
+    ptx::setmaxnreg_dec<L::DQ_REGS>();
     const int quad = warp & 3;
     const int r = quad * 32 + lane;          // query row of the tile
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const bool issuer = warp == 12 && lane == 0;
     constexpr uint32_t kBarDQ = 1, kDQThreads = 128;
     bool ok = true;
-    for (int n = 0; n < n_tiles && ok; ++n) {
-      const int h = hkv * group + n / nq, i0 = (it_lo + n % nq) * 128;
-      const bool got = __all_sync(0xffffffffu, wait_bar(dq_full, n & 1u, ctl, 70));
+    int t = 0;
+    for (int k = 0;; ++k) {
+    const Walk W = walks[k & 1];
+    if (W.n_tiles < 0) break;
+    Step st = first_step(W);
+    for (int n = 0; n < W.n_tiles; ++n, ++t, next_step(W, st)) {
+      const int h = st.h, i0 = st.i0, b = W.b;
+      const bool got = __all_sync(0xffffffffu, wait_bar(dq_full, t & 1u, ctl, 70));
       if (!ptx::named_bar_and(kBarDQ, kDQThreads, got)) { ok = false; break; }
       ptx::tc_fence_after();
       uint8_t* sb = smem + L::OFF_DQS;
@@ -824,6 +1032,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     }
+    if (!kMany || !ok) break;
+    const bool got = __all_sync(0xffffffffu, walk_here(k + 1));
+    if (!ptx::named_bar_and(kBarDQ, kDQThreads, got)) break;
+    if (lane == 0) walk_done(k);
+    }
     if (issuer) ptx::bulk_wait_group0();
     ptx::tc_fence_before();
     __syncthreads();
@@ -884,16 +1097,15 @@ __global__ void __launch_bounds__(256) attn_bwd_post_kernel(const __grid_constan
   }
   constexpr int W4 = (D + DV) / 4;
   const int64_t e = (static_cast<int64_t>(blockIdx.x) - dq_blocks) * 256 + threadIdx.x;
-  const int c = static_cast<int>(e % W4) * 4;
-  const int64_t krow = e / W4;                 // (batch * head, key of the sink tiles)
-  const int keys = p.sink_tiles * 128;
-  const int64_t bh = krow / keys;
-  const int k = static_cast<int>(krow % keys);
+  const int r = static_cast<int>(e % 128), c = static_cast<int>(e / 128 % W4) * 4;
+  const int64_t tile = e / (128 * W4);         // (batch * head, sink tile)
+  const int64_t bh = tile / p.sink_tiles;
+  const int k = static_cast<int>(tile % p.sink_tiles) * 128 + r;
   if (bh >= static_cast<int64_t>(p.B) * p.Hkv || k >= p.Lk) return;
-  const float* src = p.part + ((bh * p.sink_tiles + k / 128) * (1 + p.far_chunks) * 128 + k % 128) * (D + DV) + c;
+  const float4* src = reinterpret_cast<const float4*>(p.part) + tile * (1 + p.far_chunks) * (128 * W4) + (c / 4) * 128 + r;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i <= p.far_chunks; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(i) * 128 * (D + DV));
+    const float4 v = src[static_cast<int64_t>(i) * (128 * W4)];
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
   __nv_bfloat16* dst = c < DV ? static_cast<__nv_bfloat16*>(p.dv) + (bh * p.Lk + k) * DV + c

@@ -46,7 +46,7 @@ struct BwdParams {
   // far more tiles than a window's.  The query tiles from far0(tile) on are
   // cut into far_chunks runs of far_len tiles, one CTA each; those CTAs and
   // the tile's own leave fp32 partial dV and dK, [B * Hkv * sink_tiles][1 +
-  // far_chunks][128][DV + D], summed in order by a last kernel.  0: no split.
+  // far_chunks][(DV + D) / 4][128][4], summed in order by a last kernel.  0: no split.
   int sink, sink_tiles, far_chunks, far_len;
 };
 
