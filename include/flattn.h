@@ -304,8 +304,9 @@ typedef struct fl_kv_append_desc {
  * rest passes through.  A bf16 cache takes y rounded once.  An e2m1 cache
  * takes, per 16 channels of u = y * (1 / k_scale): block scale s = e4m3(max|u|
  * * (1/6)), codes e2m1(u / s), all rounded to nearest even and saturating; a
- * block whose scale rounds to 0 is stored as zeros.  Values are stored the
- * same way without rotation.  k_out and v_out receive the stored values (for
+ * block whose scale rounds to 0 is stored as zeros; what a block with a NaN in
+ * it holds is not specified (other blocks are not touched by it).  Values are
+ * stored the same way without rotation.  k_out and v_out receive the stored values (for
  * the new tokens' own attention); q_out may be q, k_out k and v_out v (same
  * strides) to work in place.
  * Left as they are: rows from seq_offsets[B] on, and rows whose position is

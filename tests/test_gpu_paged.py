@@ -614,3 +614,24 @@ def test_captured_step_replays_and_graphs_with_own_workspaces_overlap():
             K, V, _ = unpack(s.cache)
             ref = oracle.paged_attention(s.qo.unsqueeze(2).cpu(), K, V, s.kv.cpu().numpy(), s.table.cpu().numpy(), mask="causal")
             check_decode(s.out, s.lse, ref, "e2m1", s.qo.unsqueeze(2))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("wide", [False, True], ids=["cluster", "line"])
+def test_decode_sequences_that_share_pages(fmt, wide):
+    """Pages may be read through several rows of the table, and twice through one
+    row: the same queries over the same pages give the same result, and a page
+    named twice counts twice."""
+    page, n = 16, 100
+    parts, K, V = pool(fmt, 8, 2, page, 64, seed=31)
+    row = [3, 5, 3, 1, 0, 3, 7]
+    width = WIDE // page if wide else len(row)
+    table = np.zeros((3, width), np.int32)
+    table[:, :len(row)] = row
+    lens = [n, n, 37]
+    q = (synth.randn_bf16((1, 4, 1, 64), synth.generator(8)).float() * 0.3).bfloat16().expand(3, 4, 1, 64).contiguous()
+    out, lse = attn_paged_decode_fwd(q.to(DEV), make_cache(parts), dev(lens, torch.int32), dev(table))
+    sync_status()
+    check_decode(out, lse, oracle.paged_attention(q, K, V, lens, table), fmt, q)
+    if not wide:
+        assert torch.equal(out[0], out[1]) and torch.equal(lse[0], lse[1])
