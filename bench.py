@@ -160,7 +160,10 @@ def make_calls(api, bufs, slopes):
 # Each kernel family is built from every source file except the ones only
 # another family uses, so a change to (say) the backward leaves the forward
 # kernels' counters valid.
-KERNEL_FAMILY_EXCLUDES = {"forward": ("bwd.", "decode."), "backward": ("decode.",), "decode": ("bwd.",)}
+PAGED_SOURCES = ("paged", "kv_append.", "cvt4.")
+KERNEL_FAMILY_EXCLUDES = {"forward": ("bwd.", "bwd_dot.", "decode.", *PAGED_SOURCES),
+                          "backward": ("decode.", *PAGED_SOURCES),
+                          "decode": ("bwd.", "bwd_dot.", *PAGED_SOURCES)}
 TRAFFIC_FAMILY = {"decode": "decode", "backward": "backward", "backward_d128": "backward",
                   "diffattn_backward": "backward"}  # every other entry: forward
 

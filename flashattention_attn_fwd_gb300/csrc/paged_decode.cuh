@@ -106,6 +106,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return r;
 }
 
+// floats between the rows of O that the warps leave for their join
+template <int D>
+constexpr int kORow = D + 2;
+
 // All threads of the cluster's CTAs, with their shared memory made visible.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -426,11 +430,11 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
       for (int hf = 1; hf < HV; ++hf) pg[hf] = fresh(hf) ? page_of(t0 + kw + i * n_kw, hf) : pg[hf - 1];
     };
-    auto issue = [&](int i, int ahead, uint32_t st) {  // tile i into stage st
+    auto issue = [&](int i, int ahead, uint32_t st, const int (&page)[HV]) {  // tile i into stage st
       if (i < n_tiles) {
-        copy(t0 + kw + i * n_kw, pg, st);
+        copy(t0 + kw + i * n_kw, page, st);
 #pragma unroll
-        for (int hf = 0; hf < HV; ++hf) have |= static_cast<Bits>(pg[hf] >= 0) << (HV * ahead + hf);
+        for (int hf = 0; hf < HV; ++hf) have |= static_cast<Bits>(page[hf] >= 0) << (HV * ahead + hf);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -455,11 +459,18 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         qf[nt][2 * j + 1][0] = w.z; qf[nt][2 * j + 1][1] = w.w;
       }
     }
+    // the first tiles' pages all at once, then their copies (a page after the
+    // copy before it costs a table read's latency each: 0.7 us)
+    int first[S - 1][HV];
+#pragma unroll
     for (int i = 0; i < S - 1; ++i) {
       fetch(i);
-      issue(i, i, ring + i * L::STAGE);
+#pragma unroll
+      for (int hf = 0; hf < HV; ++hf) first[i][hf] = pg[hf];
     }
     fetch(S - 1);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) issue(i, i, ring + i * L::STAGE, first[i]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float undo = 1.f;
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     for (int i = 0; i < n_tiles; ++i) {
       cp_async_wait<S - 2>();
       group_sync();  // tile i is here, and its predecessor's stage is free
-      issue(i + S - 1, S - 1, ring + ahead * L::STAGE);
+      issue(i + S - 1, S - 1, ring + ahead * L::STAGE, pg);
       fetch(i + S);
       const uint32_t st = ring + stage * L::STAGE;
       const int key0 = key_of(t0 + kw + i * n_kw);
@@ -769,8 +780,10 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
 
-    // ---- the warps' states meet: weights 2^(m_w - m)
-    float* msm = psm + kPdWarps * WR * D;
+    // ---- the warps' states meet: weights 2^(m_w - m), found once a row.  Rows of
+    // O lie kORow apart, which spreads a warp's stores over the banks.
+    constexpr int OW = kORow<D>;
+    float* msm = psm + kPdWarps * WR * OW;
     cp_async_wait<0>();
     __syncthreads();  // the rings are idle: their memory takes the states
 #pragma unroll
@@ -785,7 +798,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
           msm[(warp * WR + 8 * nt + 2 * t4 + e) * 2 + 1] = v;
         }
         // O's channel of row tile mt, half hf, lane group g
-        float* od = psm + (warp * WR + 8 * nt + 2 * t4 + e) * D;
+        float* od = psm + (warp * WR + 8 * nt + 2 * t4 + e) * OW;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
           const int c = FMT == KV_E2M1 ? g * (D / 8) + 2 * mt : 64 * (mt >> 2) + 8 * g + 2 * (mt & 3);
@@ -795,43 +808,62 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     }
     __syncthreads();
     constexpr int CP = D / 2;
-    for (int e = tid; e < p.M * CP; e += kPdThreads) {
-      const int rr = e / CP, c2 = e % CP;
+    float* part = msm + kPdWarps * WR * 2;  // CL: O [M][D], then log-sum-exp [M]
+    const int64_t piece = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.M;
+    static_assert(kPagedMaxRows <= kPdThreads, "a thread per row");
+    if (tid < p.M) {
       // row rr belongs to row warp rr / WR of every group
-      const int w0 = rr / WR, rl = rr % WR;
+      const int rr = tid, w0 = rr / WR, rl = rr % WR;
       float mr = -CUDART_INF_F;
-      for (int w = w0; w < kPdWarps; w += RW) mr = fmaxf(mr, msm[(w * WR + rl) * 2]);
+#pragma unroll
+      for (int i = 0; i < n_kw; ++i) mr = fmaxf(mr, msm[((w0 + i * RW) * WR + rl) * 2]);
       const float ms = mr == -CUDART_INF_F ? 0.f : mr;
       float ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < n_kw; ++i) {
+        float* st = msm + ((w0 + i * RW) * WR + rl) * 2;
+        const float wt = st[0] == -CUDART_INF_F ? 0.f : ptx::ex2(st[0] - ms);
+        ls = fmaf(wt, st[1], ls);
+        st[0] = wt;
+      }
+      msm[(w0 * WR + rl) * 2 + 1] = ls == 0.f ? 0.f : p.c.v_scale / ls;
+      const float lse2 = ls == 0.f ? -CUDART_INF_F : ms - kLift + __log2f(ls);
+      if (whole) {
+        if (p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + hkv * p.G + rr / p.Lq) * p.Lq + rr % p.Lq] = lse2 * kPLn2;
+      } else if (CL) {
+        part[p.M * D + rr] = lse2;
+      } else {
+        p.lpart[piece + rr] = lse2;
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < p.M * CP; e += kPdThreads) {
+      const int rr = e / CP, c2 = e % CP;
+      const int w0 = rr / WR, rl = rr % WR;
       float2 ov = make_float2(0.f, 0.f);
-      for (int w = w0; w < kPdWarps; w += RW) {
-        const float mw = msm[(w * WR + rl) * 2];
-        const float wt = mw == -CUDART_INF_F ? 0.f : ptx::ex2(mw - ms);
-        ls = fmaf(wt, msm[(w * WR + rl) * 2 + 1], ls);
-        const float2 ow = *reinterpret_cast<const float2*>(psm + (w * WR + rl) * D + 2 * c2);
+#pragma unroll
+      for (int i = 0; i < n_kw; ++i) {
+        const int at = (w0 + i * RW) * WR + rl;
+        const float wt = msm[at * 2];
+        const float2 ow = *reinterpret_cast<const float2*>(psm + at * OW + 2 * c2);
         ov = make_float2(fmaf(wt, ow.x, ov.x), fmaf(wt, ow.y, ov.y));
       }
-      const float inv = ls == 0.f ? 0.f : p.c.v_scale / ls;
-      const float lse2 = ls == 0.f ? -CUDART_INF_F : ms - kLift + __log2f(ls);
+      const float inv = msm[(w0 * WR + rl) * 2 + 1];
+      ov = make_float2(ov.x * inv, ov.y * inv);
       if (whole) {
         const int hq = hkv * p.G + rr / p.Lq, i = rr % p.Lq;
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) + b * p.o_b + hq * p.o_h + i * p.o_l;
-        reinterpret_cast<__nv_bfloat162*>(orow)[c2] = __floats2bfloat162_rn(ov.x * inv, ov.y * inv);
-        if (c2 == 0 && p.lse) p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = lse2 * kPLn2;
+        reinterpret_cast<__nv_bfloat162*>(orow)[c2] = __floats2bfloat162_rn(ov.x, ov.y);
       } else if (CL) {
-        float* part = msm + kPdWarps * WR * 2;  // O [M][D], then log-sum-exp [M]
-        *reinterpret_cast<float2*>(part + rr * D + 2 * c2) = make_float2(ov.x * inv, ov.y * inv);
-        if (c2 == 0) part[p.M * D + rr] = lse2;
+        *reinterpret_cast<float2*>(part + rr * D + 2 * c2) = ov;
       } else {
-        const int64_t pr = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * p.M + rr;
-        reinterpret_cast<float2*>(p.opart)[pr * CP + c2] = make_float2(ov.x * inv, ov.y * inv);
-        if (c2 == 0) p.lpart[pr] = lse2;
+        reinterpret_cast<float2*>(p.opart)[(piece + rr) * CP + c2] = ov;
       }
     }
     if (CL && p.cluster > 1) {
       // ---- the cluster's parts meet: every CTA joins a share of the outputs
       cluster_barrier();
-      const uint32_t part = ptx::smem_u32(msm + kPdWarps * WR * 2);
+      const uint32_t pa = ptx::smem_u32(part);
       const int rank = blockIdx.x % p.cluster;
       for (int e = rank + p.cluster * tid; e < p.M * CP; e += p.cluster * kPdThreads) {
         const int rr = e / CP, c2 = e % CP;
@@ -840,8 +872,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < kClusterMax; ++c) {
           if (c < p.cluster) {
-            lse[c] = ld_cluster(part + (p.M * D + rr) * 4, c);
-            ow[c] = make_float2(ld_cluster(part + (rr * D + 2 * c2) * 4, c), ld_cluster(part + (rr * D + 2 * c2) * 4 + 4, c));
+            lse[c] = ld_cluster(pa + (p.M * D + rr) * 4, c);
+            ow[c] = make_float2(ld_cluster(pa + (rr * D + 2 * c2) * 4, c), ld_cluster(pa + (rr * D + 2 * c2) * 4 + 4, c));
           }
         }
 #pragma unroll
@@ -940,7 +972,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
 template <int FMT, int D, int NT, int RW, bool CL>
 constexpr int decode_smem() {
   // the warps' states, and the CTA's part of a cluster's result
-  constexpr int merge = kPdWarps * 8 * NT * (D + 2) * 4 + (CL ? 8 * NT * RW * (D + 1) * 4 : 0);
+  constexpr int merge = kPdWarps * 8 * NT * (kORow<D> + 2) * 4 + (CL ? 8 * NT * RW * (D + 1) * 4 : 0);
   constexpr int ring = Ring<FMT, D, RW>::BYTES;
   return merge > ring ? merge : ring;
 }
