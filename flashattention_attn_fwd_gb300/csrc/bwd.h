@@ -66,8 +66,9 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
   s.tiles = ((sink < Lk ? sink : Lk) + 127) / 128;
   const int far = nq - far_begin(0, window);
   if (far <= 0) return SinkSplit{0, 0, 0};  // every query is within the first tile's window
-  // A walk costs its tiles and, at its two ends, about three more, so runs are
-  // as long as balance allows: half of an SM's share of all tiles (they start
+  // A walk costs its tiles and, at its two ends, about one more (three where
+  // blocks take one walk), and its partial sums, so runs are as long as balance
+  // allows: half of an SM's share of all tiles (they start
   // first), and no shorter than a window tile's walk.
   const int near = far_begin(0, window);
   const int64_t steps = static_cast<int64_t>(B) * Hkv * ((Lk + 127) / 128 * static_cast<int64_t>(near) + static_cast<int64_t>(far) * s.tiles);
@@ -83,8 +84,8 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
 // rows see few keys the rounding of O shows: relative error of dQ against 64 bits
 // 2.4e-3 from the scores at any size; from O 4.6e-3 at 4 tokens, 3.0e-3 at 16,
 // 2.7e-3 at windows of 8, 2.5e-3 at windows of 64 and 2.4e-3 at 256 (the first
-// rows of a short sequence count as such a window).  The scores cost 40 us of
-// 200 at B 4 H 16 L 2048 window 256, 3 us at 300 tokens.
+// rows of a short sequence count as such a window).  The scores cost 40 us
+// beside 108 at B 4 H 16 L 2048 window 256, 3 us at 300 tokens.
 inline bool few_keys(int window, int sink, int Lq) {
   return static_cast<int64_t>(window) + sink <= 64 || Lq <= 512;
 }

@@ -11,10 +11,10 @@
 // short cache, or a window), a cluster of CTAs takes each (sequence, head) unit,
 // cuts its tiles evenly and joins the results through distributed shared memory:
 // one launch and no workspace traffic, 6 us against 10 at the smallest sizes.
-// Beyond that lengths matter more: the tiles of 16 keys that some row sees, over all (sequence,
-// key/value head) units, form one line that is cut into equal
-// pieces, one per resident CTA: lengths may differ as they like and every CTA
-// reads the same amount.  A unit inside one piece is finished by its CTA; a
+// Beyond that lengths matter more: the tiles that some row sees, over all
+// (sequence, key/value head) units, form one line that is cut into equal pieces,
+// one per resident CTA: lengths may differ as they like and every CTA reads the
+// same amount.  A unit inside one piece is finished by its CTA; a
 // unit that pieces share leaves one normalised partial result and log-sum-exp
 // per piece in the workspace, and paged_merge_kernel joins them with weights
 // 2^(LSE_piece - LSE).  The cut depends on the lengths alone, so the result of
@@ -42,6 +42,15 @@
 // are exact in fp16; the products run in fp16 with fp32 sums.  The query row
 // is scaled to fp16's range by a power of two (undone in the score), P carries a
 // factor 2^7 so that weights down to 2^-31 of the largest survive in fp16.
+//
+// Measured (4 bits unless said; a copy reads and writes 6.8 TB/s): one sequence
+// of 701 tokens 5.9 us; 16 of 2048 to 8192, 8 heads of 64: 22 us; 12 of 9001 to
+// 32768, 8 heads of 128: 58 us, 4.6 TB/s; 8 of 1500 to 16001 with four new
+// tokens, 4 heads of 128 in bf16: 31 us, 3.1 TB/s; a window of 1024 with 4 sinks,
+// 32 sequences: 11 us.  Fixed: 1.3 us for the plan, 2 to the first tile, 5 for the
+// merge and its launch.  In between the longest case runs at the issue rate of
+// three CTAs an SM (0.56 of the slots; waits on fixed latencies and the ALU pipe
+// lead), the short ones at the latency of a few tiles per warp.
 #pragma once
 
 #include <cuda_bf16.h>
