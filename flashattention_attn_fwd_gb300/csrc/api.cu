@@ -417,7 +417,7 @@ fl_status fl_attn_schedule(const fl_attn_desc* desc, const int32_t* doc_offsets_
   const bool per_slot = d.dv <= 64;  // one MMA thread per slot: per-slot key ranges
   int64_t own = 0, all = 0;
   for (int u = 0; u < p.num_units; ++u) {
-    const fl::Unit U = fl::decode_unit<fl::KIND_ATTN>(p, u, per_slot, fl::sink_skip_ok(d.d, d.dv));
+    const fl::SinkUnit U = fl::decode_unit<fl::KIND_ATTN, fl::SinkUnit>(p, u, per_slot, fl::sink_skip_ok(d.d, d.dv));
     for (int s = 0; s < 2; ++s) {
       const int64_t n = fl::slot_len(U, s);
       all += n;

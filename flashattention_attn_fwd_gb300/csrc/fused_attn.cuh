@@ -50,6 +50,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -210,14 +211,19 @@ struct Unit {
   int lo[2], hi[2];  // key tiles each slot walks (inclusive, walked from hi down)
   int kv_lo, kv_hi;  // union of the slots' ranges: the tiles the load warp fetches
   int pb_b, pb_h;    // Evoformer: pair-bias tile coordinates
-  int nsink;         // window with sinks: tiles [0, nsink) follow the window's in
-                     // the ring (walked from nsink - 1 down)
-  int sk[2];         // those each slot walks: nsink, or 0 for a slot without rows
   int ks;            // key-split unit: both slots hold the same query rows,
                      // slot 0 the upper and slot 1 the lower half of the key
                      // range; their tiles alternate in the ring
 };
-static_assert(sizeof(Unit) <= 128, "unit ring entry");
+// Window with sinks.  Kernels of its own walk these units: in one kernel for
+// both, the tile loop's sink test cost the other calls 1 to 10 % (softcap, B 4,
+// H 16, L 2048, d 64: 123 us against 135).
+struct SinkUnit : Unit {
+  int nsink;         // tiles [0, nsink) follow the window's in the ring (walked
+                     // from nsink - 1 down)
+  int sk[2];         // those each slot walks: nsink, or 0 for a slot without rows
+};
+static_assert(sizeof(SinkUnit) <= 128, "unit ring entry");
 
 // Reads of the document offsets: through the read-only cache on the device,
 // plainly on the host (the host-side schedule query gets host offsets).
@@ -275,9 +281,13 @@ __device__ __forceinline__ Sched make_sched(const KParams& p) {
   return s;
 }
 
-// Tiles a unit fetches, and tiles slot s walks of them.
-__host__ __device__ __forceinline__ int ring_len(const Unit& U) { return U.kv_hi - U.kv_lo + 1 + U.nsink; }
-__host__ __device__ __forceinline__ int slot_len(const Unit& U, int s) { return U.hi[s] - U.lo[s] + 1 + U.sk[s]; }
+// Tiles a unit fetches, tiles slot s walks of them, and sinks' tiles among these.
+__host__ __device__ __forceinline__ int ring_len(const Unit& U) { return U.kv_hi - U.kv_lo + 1; }
+__host__ __device__ __forceinline__ int ring_len(const SinkUnit& U) { return U.kv_hi - U.kv_lo + 1 + U.nsink; }
+__host__ __device__ __forceinline__ int slot_len(const Unit& U, int s) { return U.hi[s] - U.lo[s] + 1; }
+__host__ __device__ __forceinline__ int slot_len(const SinkUnit& U, int s) { return U.hi[s] - U.lo[s] + 1 + U.sk[s]; }
+__host__ __device__ __forceinline__ int slot_sinks(const Unit&, int) { return 0; }
+__host__ __device__ __forceinline__ int slot_sinks(const SinkUnit& U, int s) { return U.sk[s]; }
 // Ring position of slot s's first own tile within a unit, and the distance
 // between its consecutive own tiles (past its window's last tile the slot also
 // skips the window tiles that only the other slot walks).
@@ -285,23 +295,27 @@ __host__ __device__ __forceinline__ int ring_first(const Unit& U, int s) { retur
 __host__ __device__ __forceinline__ int ring_stride(const Unit& U) { return U.ks ? 2 : 1; }
 // Key tile the load warp fetches at ring position i of a unit.
 __host__ __device__ __forceinline__ int ring_tile(const Unit& U, int i) {
-  if (U.ks) return U.hi[i & 1] - (i >> 1);
-  const int n = U.kv_hi - U.kv_lo + 1;
-  return i < n ? U.kv_hi - i : U.nsink - 1 - (i - n);
+  return U.ks ? U.hi[i & 1] - (i >> 1) : U.kv_hi - i;
 }
-// Does slot s walk the tile at ring position i?
-__host__ __device__ __forceinline__ bool ring_used(const Unit& U, int i, int s) {
-  if (U.ks) return s == (i & 1);
-  if (i > U.kv_hi - U.kv_lo) return U.sk[s] > 0;
-  const int t = U.kv_hi - i;
-  return t >= U.lo[s] && t <= U.hi[s];
+__host__ __device__ __forceinline__ int ring_tile(const SinkUnit& U, int i) {
+  const int n = U.kv_hi - U.kv_lo + 1;
+  return i < n ? ring_tile(static_cast<const Unit&>(U), i) : U.nsink - 1 - (i - n);
+}
+// Does slot s walk tile t, the one at ring position i?
+__host__ __device__ __forceinline__ bool ring_used(const Unit& U, int i, int t, int s) {
+  return U.ks ? s == (i & 1) : t >= U.lo[s] && t <= U.hi[s];
+}
+__host__ __device__ __forceinline__ bool ring_used(const SinkUnit& U, int i, int t, int s) {
+  return i > U.kv_hi - U.kv_lo ? U.sk[s] > 0 : ring_used(static_cast<const Unit&>(U), i, t, s);
 }
 
-template <int KIND>
-__host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bool per_slot, bool skip_ok) {
-  Unit U;
+// Unit u.  skip_ok (sinks): a slot may skip a tile that only the other walks.
+template <int KIND, class UnitT = Unit>
+__host__ __device__ __forceinline__ UnitT decode_base(const KParams& p, int u, bool per_slot, bool skip_ok) {
+  constexpr bool SINK = std::is_same<UnitT, SinkUnit>::value;
+  UnitT U;
   U.ks = 0;
-  U.nsink = U.sk[0] = U.sk[1] = 0;
+  if constexpr (SINK) U.nsink = U.sk[0] = U.sk[1] = 0;
   U.pb_b = 0;
   U.pb_h = 0;
   U.mbrow[0] = U.mbrow[1] = 0;
@@ -402,7 +416,7 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
     int lo, hi, lo2, hi2;
     row_bounds(p, U.b[s], U.row0[s], lo, hi);
     row_bounds(p, U.b[s], r1, lo2, hi2);
-    if (KIND == KIND_ATTN) sink_end = max(sink_end, min(p.sink, lo2));  // of the last row, whose window starts last
+    if (SINK) sink_end = max(sink_end, min(p.sink, lo2));  // of the last row, whose window starts last
     lo = min(lo, lo2);
     hi = max(hi, hi2);
     if (hi < lo) { lo = 0; hi = 0; }  // keep >= 1 tile
@@ -414,7 +428,7 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
   if (hi_max < 0) { lo_min = 0; hi_max = 0; }
   U.kv_lo = lo_min;
   U.kv_hi = hi_max;
-  if (KIND == KIND_ATTN) U.nsink = (sink_end + kBlockN - 1) / kBlockN;
+  if constexpr (SINK) U.nsink = (sink_end + kBlockN - 1) / kBlockN;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     // a slot with no rows of its own runs one tile (its results are dropped);
@@ -424,10 +438,10 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
     if (!per_slot) {
       U.lo[s] = lo_min;
       U.hi[s] = hi_max;
-      U.sk[s] = U.nsink;
+      if constexpr (SINK) U.sk[s] = U.nsink;
     } else if (U.hi[s] < U.lo[s]) {
       U.lo[s] = U.hi[s] = hi_max;
-    } else {
+    } else if constexpr (SINK) {
       U.sk[s] = U.nsink;
       if (U.nsink > 0 && !skip_ok) U.lo[s] = lo_min;
     }
@@ -441,12 +455,12 @@ __host__ __device__ __forceinline__ Unit decode_base(const KParams& p, int u, bo
 // epilogue merges the two partial (m, l, O) of every row.  A tile with a
 // single key tile (or a padding tile) is not split: it runs as a unit whose
 // second slot is a dropped copy of the first.
-template <int KIND>
-__host__ __device__ __forceinline__ Unit decode_unit(const KParams& p, int u, bool per_slot, bool skip_ok) {
+template <int KIND, class UnitT = Unit>
+__host__ __device__ __forceinline__ UnitT decode_unit(const KParams& p, int u, bool per_slot, bool skip_ok) {
   const int ks_first = p.num_units - p.ks_count;
-  if (KIND != KIND_ATTN || !per_slot || u < ks_first) return decode_base<KIND>(p, u, per_slot, skip_ok);
+  if (KIND != KIND_ATTN || !per_slot || u < ks_first) return decode_base<KIND, UnitT>(p, u, per_slot, skip_ok);
   const int j = u - ks_first;
-  Unit U = decode_base<KIND>(p, ks_first + (j >> 1), per_slot, skip_ok);
+  UnitT U = decode_base<KIND, UnitT>(p, ks_first + (j >> 1), per_slot, skip_ok);
   const bool s1 = (j & 1) != 0;
   // selects rather than a runtime index: U stays in registers
   const bool real = (s1 ? U.valid[1] : U.valid[0]) && (s1 ? U.row0[1] : U.row0[0]) < p.Lq &&
@@ -550,7 +564,7 @@ __device__ __forceinline__ float2 exp2_fma(float2 a) {
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, int DV, int KIND, int SCORE>
+template <int D, int DV, int KIND, int SCORE, bool SINK = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fused_attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ0, const __grid_constant__ CUtensorMap tmK0,
                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ1,
@@ -573,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kColO = kSepP ? 384u : 256u;
   // per-slot key ranges need one MMA thread per slot
   constexpr bool kPerSlot = kSepP;
-  static_assert(KIND != KIND_ATTN || !sink_skip_ok(D, DV) || S >= 3, "a skipped tile between two of a slot needs three ring stages");
+  using UnitT = std::conditional_t<SINK, SinkUnit, Unit>;
+  static_assert(!SINK || !sink_skip_ok(D, DV) || S >= 3, "a skipped tile between two of a slot needs three ring stages");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -602,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // arriving on the unit's q_full barriers (release); the MMA and softmax
   // threads read it after waiting on q_full (acquire).  A ring of 4 suffices:
   // the TMA thread runs at most two units ahead (two Q buffers).
-  auto unit_at = [&](uint32_t ucn) -> Unit& {
-    return *reinterpret_cast<Unit*>(smem + L::OFF_UNITS + (ucn & 3u) * L::UNIT_BYTES);
+  auto unit_at = [&](uint32_t ucn) -> UnitT& {
+    return *reinterpret_cast<UnitT*>(smem + L::OFF_UNITS + (ucn & 3u) * L::UNIT_BYTES);
   };
 
   const int warp = threadIdx.x >> 5;
@@ -689,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int st = 0; st < S; ++st) pb_tag[st] = -1;
       constexpr uint32_t kStageTx = L::NK * L::K_BYTES + L::NV * L::V_BYTES;
       for (int u = sch.first; u < sch.end; u += sch.step, ++uc) {
-        unit_at(uc) = decode_unit<KIND>(p, u, kPerSlot, sink_skip_ok(D, DV));
-        const Unit& U = unit_at(uc);  // fields are read back from shared memory
+        unit_at(uc) = decode_unit<KIND, UnitT>(p, u, kPerSlot, sink_skip_ok(D, DV));
+        const UnitT& U = unit_at(uc);  // fields are read back from shared memory
         const uint32_t qb = uc % L::QBUF, qph = (uc / L::QBUF) & 1u;
         bool ok = true;
 #pragma unroll
@@ -775,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // release the stage on behalf of a slot that does not use this tile
 #pragma unroll
           for (int s = 0; s < 2; ++s)
-            if (!ring_used(U, i, s)) ptx::mbar_arrive(&kv_empty[st]);
+            if (!ring_used(U, i, t, s)) ptx::mbar_arrive(&kv_empty[st]);
           kv_count = it + 1;
         }
         if (!ok) break;
@@ -867,11 +882,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool s_issued = false;  // first S of the current unit already issued
       while (ok && u < sch.end) {
         if (!wait_q(uc, s)) { ok = false; break; }
-        const Unit& Us = unit_at(uc);
+        const UnitT& Us = unit_at(uc);
         const int n = ring_len(Us);
         const int ns = slot_len(Us, s);
-        const int nw = ns - Us.sk[s];                      // window tiles, then sinks
-        const uint32_t gap = static_cast<uint32_t>(Us.lo[s] - Us.kv_lo);
+        const int nw = ns - slot_sinks(Us, s);             // window tiles, then sinks
+        const uint32_t gap = SINK ? static_cast<uint32_t>(Us.lo[s] - Us.kv_lo) : 0u;
         const uint32_t idx0 = first_idx(Us, it);
         if (!s_issued && !first_s(uc, idx0)) { ok = false; break; }
         s_issued = false;
@@ -879,8 +894,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int un = u + sch.step;
         const uint32_t stride = static_cast<uint32_t>(ring_stride(Us));
         for (int k = 0; k < ns && ok; ++k) {
-          const uint32_t idx = idx0 + k * stride + (k >= nw ? gap : 0u);
-          const uint32_t idn = idx + stride + (k + 1 == nw ? gap : 0u);
+          const uint32_t idx = idx0 + k * stride + (SINK && k >= nw ? gap : 0u);
+          const uint32_t idn = idx + stride + (SINK && k + 1 == nw ? gap : 0u);
           const int st = static_cast<int>(idx % S);
           FL_TR(s, idx, 0);
           if (k + 1 < ns) {
@@ -1315,9 +1330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       // this slot's fields of the unit, read straight from shared memory
-      const Unit& Us = unit_at(uc);
+      const UnitT& Us = unit_at(uc);
       const int u_hi = Us.hi[s], u_b = Us.b[s], u_hq = Us.hq[s], u_row0 = Us.row0[s];
-      const int ns = slot_len(Us, s), nw = ns - Us.sk[s];
+      const int ns = slot_len(Us, s), nw = ns - slot_sinks(Us, s);
       const bool turns = kPingPong && Us.lo[0] == Us.lo[1] && Us.hi[0] == Us.hi[1];
       const int n = ring_len(Us);
       // ring index of this slot's first tile (only the Evoformer kinds read
@@ -1329,7 +1344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       row_bounds(p, u_b, ic, lo, hi);
       // the tiles after the window's are the sinks': there the row sees [0, min(sink, lo))
       int sink_hi = 0;
-      if (KIND == KIND_ATTN) sink_hi = min(p.sink, lo) - 1;
+      if (SINK) sink_hi = min(p.sink, lo) - 1;
       float slope2 = 0.f;
       if (SCORE == SCORE_ALIBI) slope2 = __ldg(p.slopes + u_hq) * kLog2e;
       float m = -CUDART_INF_F, l = 0.f;
@@ -1349,7 +1364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int k = 0; k < ns; ++k, ++scnt) {
         int t = u_hi - k;
-        if (KIND == KIND_ATTN && k >= nw) {
+        if (SINK && k >= nw) {
           t = ns - 1 - k;
           lo = 0;
           hi = sink_hi;

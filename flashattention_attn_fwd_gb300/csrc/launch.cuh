@@ -6,9 +6,9 @@
 
 namespace fl {
 
-template <int D, int DV, int KIND, int SCORE>
+template <int D, int DV, int KIND, int SCORE, bool SINK = false>
 cudaError_t launch_fused(const CUtensorMap* maps, const KParams& p, int grid, cudaStream_t stream) {
-  auto kern = fused_attn_fwd_kernel<D, DV, KIND, SCORE>;
+  auto kern = fused_attn_fwd_kernel<D, DV, KIND, SCORE, SINK>;
   constexpr int smem = Layout<D, DV, KIND, SCORE>::SMEM_BYTES;
   // The register split (setmaxnreg) hands the control warpgroup's registers
   // to the softmax warpgroups; it needs exactly kLaunchRegs per thread at
@@ -26,15 +26,22 @@ cudaError_t launch_fused(const CUtensorMap* maps, const KParams& p, int grid, cu
   return cudaGetLastError();
 }
 
-template <int D, int DV>
+template <int D, int DV, bool SINK>
 cudaError_t launch_attn_by_score(int score_mod, const CUtensorMap* maps, const KParams& p, int grid,
                                  cudaStream_t s) {
   switch (score_mod) {
-    case SCORE_NONE: return launch_fused<D, DV, KIND_ATTN, SCORE_NONE>(maps, p, grid, s);
-    case SCORE_ALIBI: return launch_fused<D, DV, KIND_ATTN, SCORE_ALIBI>(maps, p, grid, s);
-    case SCORE_SOFTCAP: return launch_fused<D, DV, KIND_ATTN, SCORE_SOFTCAP>(maps, p, grid, s);
+    case SCORE_NONE: return launch_fused<D, DV, KIND_ATTN, SCORE_NONE, SINK>(maps, p, grid, s);
+    case SCORE_ALIBI: return launch_fused<D, DV, KIND_ATTN, SCORE_ALIBI, SINK>(maps, p, grid, s);
+    case SCORE_SOFTCAP: return launch_fused<D, DV, KIND_ATTN, SCORE_SOFTCAP, SINK>(maps, p, grid, s);
     default: return cudaErrorInvalidValue;
   }
+}
+
+template <int D, int DV>
+cudaError_t launch_attn_by_score(int score_mod, const CUtensorMap* maps, const KParams& p, int grid,
+                                 cudaStream_t s) {
+  return p.sink ? launch_attn_by_score<D, DV, true>(score_mod, maps, p, grid, s)
+                : launch_attn_by_score<D, DV, false>(score_mod, maps, p, grid, s);
 }
 
 }  // namespace fl
