@@ -238,10 +238,8 @@ __host__ __device__ __forceinline__ int32_t load_offset(const int32_t* x) {
 // Visible keys of query row i form one interval [lo, hi] for every mask kind
 // (with sinks, the window's; the row's sinks left of it, [0, min(sink, lo)),
 // are walked as tiles of their own, so that a tile keeps one interval per row:
-// B 4, H 16, L 2048, d 64, window 256: 36 us, with 4 sinks 42, the one tile more
-// of four; B 1, 32 heads over 8, L 16384, d 128, window 1024: 300 and 336.
-// Leaving out a tile's 32-key blocks that no row of a warp sees made those 47 and
-// 324, and unmasked and causal calls 8 to 17 % slower.)
+// B 4, H 16, L 2048, d 64, window 256: 35 us, with 4 sinks 44, the one tile more
+// of four; B 1, 32 heads over 8, L 16384, d 128, window 1024: 300 and 321.)
 __host__ __device__ __forceinline__ void row_bounds(const KParams& p, int b, int i, int& lo, int& hi) {
   switch (p.mask_kind) {
     case MASK_NONE: lo = 0; hi = p.Lk - 1; break;
@@ -1467,6 +1465,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < NBLK; ++b) cmax[b] = tm;
           row_done = true;
         }
+        // With sinks: blocks that no row of the warp sees, left out of the mask,
+        // the maximum and the exponentials.  Most of a sink tile is such blocks:
+        // 441 -> 410 us at B 4, 32 heads over 8, L 8192, d 64, window 1024, 337 ->
+        // 321 at d 128 (window 256, L 2048, d 64: 42 -> 44).  In the other calls'
+        // kernels the test in the exponentials' loop cost 8 to 17 %.
+        uint32_t dead = 0u;
         // Score transform and max, 32 columns at a time: the first block
         // while the others are still being read from TMEM.
 #pragma unroll
@@ -1480,6 +1484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s_free[s]);
+          }
+          if (SINK && tile_part && !__any_sync(0xffffffffu, j0 + c0 <= hi && j0 + c0 + 31 >= lo)) {
+            dead |= 1u << hf;
+            cmax[hf] = -CUDART_INF_F;
+            continue;
           }
           if (SCORE == SCORE_SOFTCAP) {
             // x = cap*log2(e) * tanh(s * scale / cap): an odd polynomial in
@@ -1608,6 +1617,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[kHalfCols / 2];
         // exponentials of 32-column block h: P packed to bf16 pairs, row sum
         auto expb = [&](int h) {
+          if (SINK && (dead >> h & 1u)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[h * 16 + e] = 0u;
+            return;
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 xv = make_float2(x[h * 32 + 2 * e], x[h * 32 + 2 * e + 1]);
