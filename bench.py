@@ -161,9 +161,9 @@ def make_calls(api, bufs, slopes):
 # another family uses, so a change to (say) the backward leaves the forward
 # kernels' counters valid.
 PAGED_SOURCES = ("paged", "kv_append.", "cvt4.")
-KERNEL_FAMILY_EXCLUDES = {"forward": ("bwd.", "bwd_dot.", "decode.", *PAGED_SOURCES),
+KERNEL_FAMILY_EXCLUDES = {"forward": ("bwd.", "bwd_dot.", "bwd_short.", "decode.", *PAGED_SOURCES),
                           "backward": ("decode.", *PAGED_SOURCES),
-                          "decode": ("bwd.", "bwd_dot.", *PAGED_SOURCES)}
+                          "decode": ("bwd.", "bwd_dot.", "bwd_short.", *PAGED_SOURCES)}
 TRAFFIC_FAMILY = {"decode": "decode", "backward": "backward", "backward_d128": "backward",
                   "diffattn_backward": "backward"}  # every other entry: forward
 

@@ -554,6 +554,9 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
   p.window = d.window; p.prefix = d.prefix_len; p.num_docs = d.num_docs;
   if (static_cast<int64_t>(d.B) * d.Hkv * (p.n_ktiles + static_cast<int64_t>(p.far_chunks) * p.sink_tiles) > 0x7fffffff)
     return FL_ERR_UNSUPPORTED;
+  if (d.sink && d.Lq <= fl::kShortRows && d.Lq == d.Lk && !dv_accumulate && dout_scale == 1.0f)
+    return launched("backward kernel launch",
+                    fl::launch_bwd_short(d.d, d.dv, d.score_mod, p, static_cast<cudaStream_t>(d.stream)));
   CUtensorMap maps[9];
   const int bw = box_width(d.d), bwv = box_width(d.dv);
   const int64_t sl = d.d, slv = d.dv;

@@ -93,6 +93,10 @@ inline bool few_keys(int window, int sink, int Lq) {
 // D, L2 and a zeroed dQ accumulator from the scores (sum P dP); (d, dv) as below.
 cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
 
+// With sinks, sequences of at most this many tokens: dQ, dK and dV in one launch.
+constexpr int kShortRows = 64;
+cudaError_t launch_bwd_short(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
+
 // (d, dv): (32, 32), (64, 64), (128, 128) or (64, 128)
 cudaError_t launch_bwd(int d, int dv, int score_mod, const CUtensorMap* maps, const BwdParams& p, cudaStream_t s);
 

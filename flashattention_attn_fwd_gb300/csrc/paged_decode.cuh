@@ -119,19 +119,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 template <int D>
 constexpr int kORow = D + 2;
 
-// All threads of the cluster's CTAs, with their shared memory made visible.
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// fp32 at shared address `a` of cluster rank `rank`
-__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
-  float v;
-  asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-               : "=f"(v)
-               : "r"(a), "r"(rank)
-               : "memory");
-  return v;
-}
 
 // Tiles of KT keys of one head of sequence b: `count` of them (at least one),
 // tile i at key KT * (i < sink ? i : i + skip).
@@ -871,7 +858,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
     }
     if (CL && p.cluster > 1) {
       // ---- the cluster's parts meet: every CTA joins a share of the outputs
-      cluster_barrier();
+      ptx::cluster_barrier();
       const uint32_t pa = ptx::smem_u32(part);
       const int rank = blockIdx.x % p.cluster;
       for (int e = rank + p.cluster * tid; e < p.M * CP; e += p.cluster * kPdThreads) {
@@ -881,8 +868,8 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < kClusterMax; ++c) {
           if (c < p.cluster) {
-            lse[c] = ld_cluster(pa + (p.M * D + rr) * 4, c);
-            ow[c] = make_float2(ld_cluster(pa + (rr * D + 2 * c2) * 4, c), ld_cluster(pa + (rr * D + 2 * c2) * 4 + 4, c));
+            lse[c] = ptx::ld_cluster(pa + (p.M * D + rr) * 4, c);
+            ow[c] = make_float2(ptx::ld_cluster(pa + (rr * D + 2 * c2) * 4, c), ptx::ld_cluster(pa + (rr * D + 2 * c2) * 4 + 4, c));
           }
         }
 #pragma unroll
@@ -906,7 +893,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
         if (c2 == 0 && p.lse)
           p.lse[(static_cast<int64_t>(b) * p.Hq + hq) * p.Lq + i] = tot == 0.f ? -CUDART_INF_F : (Ls + __log2f(tot)) * kPLn2;
       }
-      cluster_barrier();  // no CTA leaves while another reads its part
+      ptx::cluster_barrier();  // no CTA leaves while another reads its part
     }
     if (CL) return;
     cur = next;

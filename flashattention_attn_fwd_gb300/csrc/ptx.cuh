@@ -382,6 +382,20 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// All threads of the cluster's CTAs, with their shared memory made visible.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// fp32 at shared address `a` of cluster rank `rank`
+__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
+  float v;
+  asm volatile("{\n\t.reg .u32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
+               : "=f"(v)
+               : "r"(a), "r"(rank)
+               : "memory");
+  return v;
+}
+
 // The launch's queue: cancels the launch of a block that has not started and
 // writes which one it was (16 bytes, counted on the barrier); not to be asked
 // again once it has answered that none is left.

@@ -373,7 +373,8 @@ FL_API int32_t fl_kv_append_desc_size(void);
  * dv 128 (v, dv: [B, Hkv, Lk, dv]; out, dout: [B, Hq, Lq, dv]); Lq a
  * multiple of 4 (any Lq with sink > 0, whose workspace pads the per-row
  * vectors), strides zero.  Masks, ALiBi and softcap as in fl_attn_fwd.  dq is
- * summed with fp32 atomics in no fixed order; dk and dv in a fixed one.
+ * summed with fp32 atomics in no fixed order (but for at most 64 tokens with
+ * sinks, where it has one); dk and dv in a fixed one.
  */
 FL_API fl_status fl_attn_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout,
                              const float* lse, void* dq, void* dk, void* dv, void* workspace,

@@ -317,3 +317,79 @@ def test_schedule_walks_each_visible_block_once(L, window, sink, d, dv):
         assert tiles[0] == want
     else:
         assert want <= tiles[0] <= want + B * H * (nt * 2 + nt * -(-min(sink, L) // 128))
+
+
+@gpu
+@pytest.mark.parametrize("case", [
+    # (B, Hq, Hkv, L, d, dv, window, sink, score_mod)
+    (1, 1, 1, 15, 128, 128, 4, 4, "softcap"), (2, 16, 4, 12, 128, 128, 3, 200, "softcap"), (3, 4, 2, 1, 64, 64, 7, 2, "none"),
+    (2, 3, 3, 2, 64, 64, 1, 1, "none"), (1, 8, 1, 64, 64, 64, 5, 2, "none"), (2, 4, 2, 63, 128, 128, 20, 9, "alibi"),
+    (2, 6, 2, 17, 32, 32, 6, 1, "softcap"), (40, 8, 8, 33, 64, 64, 2 ** 31 - 1, 4, "none"), (2, 4, 2, 50, 64, 128, 16, 3, "none"),
+    (1, 2, 2, 64, 128, 128, 64, 64, "none"), (1, 2, 1, 48, 64, 64, 1, 1, "alibi"),
+    # clusters of 2, 4 and 8 that share a group's heads, and one block for all of them
+    (2, 6, 1, 31, 64, 64, 9, 2, "none"), (1, 16, 1, 64, 128, 128, 30, 4, "softcap"), (3, 12, 3, 40, 64, 128, 8, 3, "none"),
+    (90, 8, 2, 20, 32, 32, 5, 1, "none"),
+], ids=lambda c: "-".join(str(x) for x in c))
+def test_short_sequences_keep_their_gradients_to_the_rounding(case):
+    """Up to 64 tokens P and dS are not rounded to bf16 between the products: in
+    two bf16 parts they keep 2^-16 of their value.  With ds, eP and eD (D from the
+    scores) as above: eS = P (eD + eP) + (ds + 2^-16 + 2^-20) |dS| (+ 2^-20 P |dP
+    - D| for softcap's 1 - tanh^2); dQ and dK are scale sum eS |k|, scale sum eS
+    |q| off, dV sum (ds + 2^-16) P |dO|, and each is rounded once, 2^-8.  5 % for
+    products of errors and the products' fp32 sums."""
+    B, Hq, Hkv, L, d, dv, window, sink, mod = case
+    g = synth.generator(L * 31 + d + window % 97)
+    q, k = synth.randn_bf16((B, Hq, L, d), g), synth.randn_bf16((B, Hkv, L, d), g)
+    v, do = synth.randn_bf16((B, Hkv, L, dv), g), synth.randn_bf16((B, Hq, L, dv), g)
+    kw = dict(mask="window", window=window, sink=sink)
+    slopes, cap = None, None
+    if mod == "softcap":
+        cap = 30.0
+        kw.update(score_mod="softcap", softcap=cap)
+    if mod == "alibi":
+        slopes = 2.0 ** -torch.arange(1, Hq + 1, dtype=torch.float32)
+        kw.update(score_mod="alibi", alibi_slopes=slopes.to(DEV))
+    a = [t.to(DEV) for t in (q, k, v, do)]
+    out, lse = attn_fwd(*a[:3], **kw)
+    guard = [torch.full((t.numel() + 512,), 7.0, dtype=torch.bfloat16, device=DEV) for t in (q, k, v)]
+    grads = [x[256:-256].view(t.shape) for x, t in zip(guard, (q, k, v))]
+    got = attn_bwd(*a[:3], out, a[3], lse, dq=grads[0], dk=grads[1], dv=grads[2], **kw)
+    again = attn_bwd(*a[:3], out, a[3], lse, **kw)
+    sync_status()
+    for x, y in zip(got, again):
+        assert torch.equal(x, y)          # no atomics: the same every time
+    for x in guard:
+        assert (x[:256] == 7.0).all() and (x[-256:] == 7.0).all()
+    scale = 1.0 / np.sqrt(d)
+    vis = oracle.visibility("window", L, L, window=window, sink=sink)
+    Q, K, V, O = (t.double().numpy() for t in (q, k, v, do))
+    ref = {n: np.zeros(t.shape) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    err = {n: np.zeros(t.shape) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    for b in range(B):
+        for h in range(Hq):
+            j = h // (Hq // Hkv)
+            s = scale * (Q[b, h] @ K[b, j].T)
+            mag = np.where(vis, scale * (np.abs(Q[b, h]) @ np.abs(K[b, j]).T), 0).max(1)
+            t = oracle.apply_score_mod(s, mod, slope=None if slopes is None else float(slopes[h]), cap=cap)
+            if mod == "alibi":
+                mag = mag + abs(float(slopes[h])) * L
+            P, _ = oracle.attention.__globals__["softmax_rows"](np.where(vis, t, -np.inf))
+            ds = ((d + 8) * 2.0 ** -22 * mag + 2.0 ** -20 * (cap or 0.0) + 2.0 ** -18)[:, None]
+            dP = O[b, h] @ V[b, j].T
+            eP = 2.0 ** -22 * (dv + 8) * (np.abs(O[b, h]) @ np.abs(V[b, j]).T)
+            D = (P * dP).sum(1, keepdims=True)
+            eD = (P * (2 * ds * np.abs(dP) + eP)).sum(1, keepdims=True)
+            slope = 1 - np.tanh(s / cap) ** 2 if mod == "softcap" else 1.0
+            dS = P * (dP - D) * slope
+            eS = P * (eD + eP) + (ds + 2.0 ** -16 + 2.0 ** -20) * np.abs(dS)
+            if mod == "softcap":
+                eS = eS + 2.0 ** -20 * P * np.abs(dP - D)
+            dS[0] = eS[0] = 0
+            ref["dq"][b, h], err["dq"][b, h] = scale * dS @ K[b, j], scale * eS @ np.abs(K[b, j])
+            ref["dk"][b, j] += scale * dS.T @ Q[b, h]
+            err["dk"][b, j] += scale * eS.T @ np.abs(Q[b, h])
+            ref["dv"][b, j] += P.T @ O[b, h]
+            err["dv"][b, j] += ((ds + 2.0 ** -16) * P).T @ np.abs(O[b, h])
+    for n, x in zip(("dq", "dk", "dv"), got):
+        e = np.abs(x.double().cpu().numpy() - ref[n])
+        assert (e <= 1.05 * (err[n] + 2.0 ** -8 * np.abs(ref[n])) + 1e-30).all(), n
