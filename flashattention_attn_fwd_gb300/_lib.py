@@ -109,17 +109,28 @@ class KvAppendDesc(ctypes.Structure):
 _ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i 6i")
 _APPEND = struct.Struct("@4i 3P q 2P 4i 4P 12q P")
 _ZERO4 = (0, 0, 0, 0)
-APPEND_PACK = _APPEND.pack
-ATTN_PACK = _ATTN.pack
+
+
+def _packer(layout: struct.Struct):
+    def pack(*values):
+        try:
+            return layout.pack(*values)
+        except struct.error as e:
+            raise ValueError(f"argument out of the descriptor's range: {e}") from None
+    return pack
+
+
+APPEND_PACK = _packer(_APPEND)
+ATTN_PACK = _packer(_ATTN)
 
 
 def desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, *, scale=0.0, mask_kind=0, doc_causal=0, window=0, prefix=0, score_mod=0,
               softcap=0.0, slopes=0, doc_offsets=0, num_docs=0, q_strides=_ZERO4, k_strides=_ZERO4,
               v_strides=_ZERO4, o_strides=_ZERO4, stream=0, debug_flags=0, debug_arg=-1, wait_limit_ms=0, sink=0):
     """fl_attn_desc as bytes."""
-    return _ATTN.pack(B, Hq, Hkv, Lq, Lk, d, dv, scale, mask_kind, doc_causal, window, prefix, score_mod, softcap,
-                      slopes, doc_offsets, num_docs, *q_strides, *k_strides, *v_strides, *o_strides, stream,
-                      debug_flags, debug_arg, wait_limit_ms, sink, 0, 0, 0, 0, 0, 0)
+    return ATTN_PACK(B, Hq, Hkv, Lq, Lk, d, dv, scale, mask_kind, doc_causal, window, prefix, score_mod, softcap,
+                     slopes, doc_offsets, num_docs, *q_strides, *k_strides, *v_strides, *o_strides, stream,
+                     debug_flags, debug_arg, wait_limit_ms, sink, 0, 0, 0, 0, 0, 0)
 
 
 class FlattnError(RuntimeError):

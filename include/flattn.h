@@ -342,6 +342,9 @@ FL_API fl_status fl_kv_append(const void* k, const void* v, const fl_kv_cache* c
  * zero.  A visible key whose page is outside the pool is left out and the
  * call reports FL_ERR_DEVICE_BOUNDS through fl_sync_status.  Rows that see no
  * key get out = 0 and lse = -inf.  Results do not depend on where pages lie.
+ * Keys and values that no row of the call sees may hold anything; a value that
+ * is not finite and that one row sees reaches every row of its key/value head
+ * in that sequence (0 times it is a NaN).
  */
 FL_API fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, const int32_t* kv_len,
                                           const int32_t* block_table, int64_t table_stride, void* out, float* lse,

@@ -174,3 +174,14 @@ def test_python_layer_refuses_bad_tensors():
         PagedKVCache.allocate(4, 16, 2, 64, format="int4", device="cpu")
     with pytest.raises(TypeError):
         PagedKVCache(None, k)
+
+
+@pytest.mark.parametrize("kw", [dict(window=2 ** 31), dict(sink=2 ** 31), dict(Lk=-2 ** 31 - 1),
+                                dict(q_strides=(2 ** 63, 1, 1, 1))], ids=str)
+def test_values_past_the_descriptors_fields_are_refused(kw):
+    """Not cut to the field's width: a ValueError before any call."""
+    sizes = dict(B=1, Hq=1, Hkv=1, Lq=1, Lk=16, d=64, dv=64)
+    rest = {k: v for k, v in kw.items() if k not in sizes}
+    sizes.update({k: v for k, v in kw.items() if k in sizes})
+    with pytest.raises(ValueError, match="range"):
+        _lib.desc_pack(*sizes.values(), **rest)
