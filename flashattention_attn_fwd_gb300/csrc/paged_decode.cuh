@@ -924,17 +924,36 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   const int n = static_cast<int>(c1 - c0) + 1;
   const int64_t head = (c0 * 2 + (first <= c0 * per ? 0 : 1)) * p.M + m;
   auto part = [&](int i) { return i == 0 ? head : (c0 + i) * 2 * p.M + m; };
+  constexpr int PER = D / 32;
+  // the warp's first two pieces set out before the weights are known
+  constexpr int AHEAD = 2;
+  float first_o[AHEAD][PER], first_l[AHEAD];
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    const int i = warp + a * kMergeWarps;
+    const int64_t at = part(i < n ? i : 0);
+    const float* op = p.opart + at * D + lane * PER;
+    first_l[a] = i < n ? p.lpart[at] : -CUDART_INF_F;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) first_o[a][c] = op[c];
+  }
   float L = -CUDART_INF_F;
   for (int i = lane; i < n; i += 32) L = fmaxf(L, p.lpart[part(i)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, d));
   const float Ls = L == -CUDART_INF_F ? 0.f : L;
-  constexpr int PER = D / 32;
   float o[PER], ws = 0.f;
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
+#pragma unroll
+  for (int a = 0; a < AHEAD; ++a) {
+    const float w = ptx::ex2(first_l[a] - Ls);  // 0 where there is no piece
+    ws += w;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] = fmaf(w, first_o[a][c], o[c]);
+  }
 #pragma unroll 4
-  for (int i = warp; i < n; i += kMergeWarps) {
+  for (int i = warp + AHEAD * kMergeWarps; i < n; i += kMergeWarps) {
     const float w = ptx::ex2(p.lpart[part(i)] - Ls);
     const float* op = p.opart + part(i) * D + lane * PER;
     ws += w;
