@@ -120,6 +120,11 @@ template <int D>
 constexpr int kORow = D + 2;
 
 
+// a / b of non-negative values, in 32 bits where both fit (0.1 us less)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+}
+
 // Tiles of KT keys of one head of sequence b: `count` of them (at least one),
 // tile i at key KT * (i < sink ? i : i + skip).
 struct SeqTiles {
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       total += chunk;
     }
     const int64_t all = total * H;
-    const int64_t per = ((all + gridDim.x - 1) / gridDim.x + kPdWarps - 1) / kPdWarps * kPdWarps;
+    const int64_t per = (quotient(all + gridDim.x - 1, gridDim.x) + kPdWarps - 1) / kPdWarps * kPdWarps;
     begin = blockIdx.x * per;
     end = begin + per < all ? begin + per : all;
     int64_t carry = 0;  // tiles of one head before the chunk's sequences
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       }
       const int64_t local = cur - base;
       const int len = LEAD + sq.count;
-      hkv = static_cast<int>(local / len);
+      hkv = static_cast<int>(quotient(local, len));
       const int at = static_cast<int>(local - static_cast<int64_t>(hkv) * len);
       const int64_t room = at + (end - cur);
       const int to = room < len ? static_cast<int>(room) : len;
@@ -909,15 +914,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   __shared__ float osm[kMergeWarps][D];
   __shared__ float wsm[kMergeWarps];
   const int64_t H = p.c.Hkv;
-  const int64_t row = blockIdx.x;  // (sequence, key/value head, row of the group)
-  const int m = static_cast<int>(row % p.M);
-  const int hkv = static_cast<int>(row / p.M % p.c.Hkv);
-  const int b = static_cast<int>(row / p.M / p.c.Hkv);
+  // (sequence, key/value head, row of the group)
+  const uint32_t row = blockIdx.x, unit = row / static_cast<uint32_t>(p.M);
+  const int m = static_cast<int>(row - unit * p.M);
+  const int b = static_cast<int>(unit / static_cast<uint32_t>(p.c.Hkv));
+  const int hkv = static_cast<int>(unit - static_cast<uint32_t>(b) * p.c.Hkv);
   const int64_t per = p.plan[0];
   const int64_t before = p.plan[2 + b];
-  const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : p.plan[1] / H) - before;
+  const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : quotient(p.plan[1], H)) - before;
   const int64_t first = before * H + hkv * count;  // count: the unit's lead, then its tiles
-  const int64_t c0 = (first + lead) / per, c1 = (first + count - 1) / per;
+  const int64_t c0 = quotient(first + lead, per), c1 = quotient(first + count - 1, per);
   if (c0 == c1) return;  // finished by its CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // piece i: CTA c0 + i; the first CTA's piece is its second one unless it starts there
