@@ -44,10 +44,10 @@
 // factor 2^7 so that weights down to 2^-31 of the largest survive in fp16.
 //
 // Measured (4 bits unless said; a copy reads and writes 6.8 TB/s): one sequence
-// of 701 tokens 5.9 us; 16 of 2048 to 8192, 8 heads of 64: 22 us; 12 of 9001 to
-// 32768, 8 heads of 128: 58 us, 4.6 TB/s; 8 of 1500 to 16001 with four new
+// of 701 tokens 5.9 us; 16 of 2048 to 8192, 8 heads of 64: 21 us; 12 of 9001 to
+// 32768, 8 heads of 128: 57 us, 4.7 TB/s; 8 of 1500 to 16001 with four new
 // tokens, 4 heads of 128 in bf16: 31 us, 3.1 TB/s; a window of 1024 with 4 sinks,
-// 32 sequences: 11 us.  Fixed: 1.3 us for the plan, 2 to the first tile, 5 for the
+// 32 sequences: 11 us.  Fixed: 1.3 us for the plan, 2 to the first tile, 4 for the
 // merge and its launch.  In between the longest case runs at the issue rate of
 // three CTAs an SM (0.56 of the slots; waits on fixed latencies and the ALU pipe
 // lead), the short ones at the latency of a few tiles per warp.
@@ -1038,20 +1038,24 @@ cudaError_t launch_rows(const PagedDecodeParams& p, cudaStream_t s) {
 }
 
 // 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
-// (2, 2) and (2, 4)
+// (2, 2) and (2, 4), or with 64 channels, whose O leaves room, (4, 1) and (4, 2)
+// (8 sequences to 16001, 4 heads, 64 rows in 4 bits: 30 us against 62; 32 rows
+// the same)
+template <int D>
+constexpr int kWide = D == 64 ? 4 : 2;
 template <int FMT, int D, bool CL>
 int resident_ctas(int M) {
   return M <= 8    ? resident<FMT, D, 1, 1, CL>()
          : M <= 16 ? resident<FMT, D, 2, 1, CL>()
-         : M <= 32 ? resident<FMT, D, 2, 2, CL>()
-                   : resident<FMT, D, 2, 4, CL>();
+         : M <= 32 ? resident<FMT, D, kWide<D>, 4 / kWide<D>, CL>()
+                   : resident<FMT, D, kWide<D>, 8 / kWide<D>, CL>();
 }
 template <int FMT, int D>
 cudaError_t launch_paged(const PagedDecodeParams& p, cudaStream_t s) {
   return p.M <= 8    ? launch_rows<FMT, D, 1, 1>(p, s)
          : p.M <= 16 ? launch_rows<FMT, D, 2, 1>(p, s)
-         : p.M <= 32 ? launch_rows<FMT, D, 2, 2>(p, s)
-                     : launch_rows<FMT, D, 2, 4>(p, s);
+         : p.M <= 32 ? launch_rows<FMT, D, kWide<D>, 4 / kWide<D>>(p, s)
+                     : launch_rows<FMT, D, kWide<D>, 8 / kWide<D>>(p, s);
 }
 
 }  // namespace
