@@ -14,18 +14,21 @@ from ._lib import KV_FORMATS, MASKS, SCORE_MODS
 
 _SCALE_BLOCK = 16
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_Tensor = torch.Tensor
+# the current device's index (CUDA is up: a cache on a device exists)
+_device_index = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _check(t, name: str, ndim: int, dtype, index: int) -> None:
     """`t` is a tensor of this rank and type on CUDA device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != index:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != index:
         _need(t, name, ndim, dtype)
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
 def _current(index: int) -> None:
-    if torch.cuda.current_device() != index:
-        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+    if _device_index() != index:
+        raise ValueError(f"the cache is on cuda:{index}, the current device is cuda:{_device_index()}")
 
 
 class PagedKVCache:
@@ -96,7 +99,7 @@ def _need_table(cache, kv_len, block_table) -> tuple[int, int, int]:
     _check(kv_len, "kv_len", 1, _I32, cache.index)
     _check(block_table, "block_table", 2, _I32, cache.index)
     B, n = block_table.shape
-    if kv_len.shape[0] != B:
+    if kv_len.numel() != B:
         raise ValueError("block_table must have one row per sequence of kv_len")
     if not kv_len.is_contiguous():
         raise ValueError("kv_len must be contiguous")
@@ -108,9 +111,8 @@ def _need_table(cache, kv_len, block_table) -> tuple[int, int, int]:
 
 def _rows(t, name, T, H, d, index):
     """Checks a [T, H, d] bf16 row tensor; returns its (token, head) strides."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.shape != (T, H, d):
         _check(t, name, 3, _BF16, index)
-    if t.shape != (T, H, d):
         raise ValueError(f"{name} must be {[T, H, d]}, got {list(t.shape)}")
     st, sh, sc = t.stride()
     if sc != 1:
