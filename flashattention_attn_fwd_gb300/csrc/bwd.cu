@@ -16,8 +16,8 @@
 // <= 64, where shared memory holds K and V twice, a block that nears the end of
 // its walk takes over one that has not started (cluster launch control), so
 // that the next walk's loads and first products run under the last one's end:
-// B 4, H 16, L 2048, d 64: causal 173 -> 160 us, window of 256 104 -> 92, with
-// 4 sinks 126 -> 108.  All five
+// B 4, H 16, L 2048, d 64: causal 173 -> 158 us, window of 256 104 -> 90, with
+// 4 sinks 126 -> 107.  All five
 // products run on tcgen05 with accumulators in TMEM:
 //   S^T  = K Q^T   (A = K, B = Q smem)              TMEM [0,128)
 //   P^T  (bf16, written by the compute warps)        over S^T: [0,32), [64,96)
@@ -59,6 +59,7 @@
 
 #include "bwd.h"
 #include "fused_attn.cuh"
+#include "host.h"
 
 namespace fl {
 namespace {
@@ -1084,6 +1085,7 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
 // four channels per thread.
 template <int D, int DV>
 __global__ void __launch_bounds__(256) attn_bwd_post_kernel(const __grid_constant__ BwdParams p, int dq_blocks) {
+  ptx::wait_prerequisites();
   if (static_cast<int>(blockIdx.x) < dq_blocks) {
     const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
     if (e >= p.rows * D) return;
@@ -1141,8 +1143,9 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
   if (e != cudaSuccess) return e;
   const int pgrid = static_cast<int>((p.rows * D / 8 + 255) / 256);
   const int64_t quads = p.far_chunks ? static_cast<int64_t>(p.B) * p.Hkv * p.sink_tiles * 128 * ((D + DV) / 4) : 0;
-  attn_bwd_post_kernel<D, DV><<<pgrid + static_cast<int>((quads + 255) / 256), 256, 0, s>>>(p, pgrid);
-  return cudaGetLastError();
+  // chained: 2 to 3 us less on every backward.  The walks chained to the kernel
+  // before them gain 2 us with one launch per key tile's walk but lose 8 with sinks.
+  return launch_chained(attn_bwd_post_kernel<D, DV>, pgrid + static_cast<unsigned>((quads + 255) / 256), 256, 0, s, p, pgrid);
 }
 
 template <int D, int DV>

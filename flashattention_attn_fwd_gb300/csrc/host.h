@@ -27,4 +27,22 @@ fl_status device_info(int* sm_count, uint32_t** status);
 // FL_OK, or FL_ERR_CUDA with `where` and CUDA's message as the error detail.
 fl_status launch_result(const char* where, cudaError_t e);
 
+// Launches `kernel` behind the previous kernel of the stream, whose end it waits
+// for itself (ptx::wait_prerequisites), so that its set-up runs under that end.
+template <class... Params, class... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                           const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace fl

@@ -62,6 +62,7 @@
 #include <type_traits>
 
 #include "cvt4.cuh"
+#include "host.h"
 #include "paged.h"
 #include "ptx.cuh"
 
@@ -781,6 +782,7 @@ __global__ void __launch_bounds__(kPdThreads) paged_decode_kernel(const __grid_c
       ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
 
+    if (!CL && next >= end) ptx::launch_dependents();  // the merge may be set up
     // ---- the warps' states meet: weights 2^(m_w - m), found once a row.  Rows of
     // O lie kORow apart, which spreads a warp's stores over the banks.
     constexpr int OW = kORow<D>;
@@ -919,6 +921,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   const int m = static_cast<int>(row - unit * p.M);
   const int b = static_cast<int>(unit / static_cast<uint32_t>(p.c.Hkv));
   const int hkv = static_cast<int>(unit - static_cast<uint32_t>(b) * p.c.Hkv);
+  ptx::wait_prerequisites();
   const int64_t per = p.plan[0];
   const int64_t before = p.plan[2 + b];
   const int64_t count = (b + 1 < p.B ? p.plan[3 + b] : quotient(p.plan[1], H)) - before;
@@ -1033,8 +1036,9 @@ cudaError_t launch_rows(const PagedDecodeParams& p, cudaStream_t s) {
   paged_decode_kernel<FMT, D, NT, RW, false><<<p.grid, kPdThreads, decode_smem<FMT, D, NT, RW, false>(), s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  paged_merge_kernel<D><<<static_cast<unsigned>(p.B * p.c.Hkv * p.M), 32 * kMergeWarps, 0, s>>>(p, kLead<FMT, D>);
-  return cudaGetLastError();
+  // chained: 26.3 -> 22.9 us at B 16 in a stream (0.2 us less in a graph)
+  return launch_chained(paged_merge_kernel<D>, static_cast<unsigned>(p.B * p.c.Hkv * p.M), 32 * kMergeWarps, 0, s, p,
+                        kLead<FMT, D>);
 }
 
 // 8-row tiles per warp and warps per tile: (1, 1) to 8 rows, (2, 1) to 16, then
