@@ -32,7 +32,9 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+        # torch takes a null handle for none given and would wrap a stream of its pool
+        handle = _stream_ptr(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
