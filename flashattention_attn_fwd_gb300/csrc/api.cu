@@ -21,7 +21,6 @@ namespace {
 
 using fl::KParams;
 
-constexpr int kMaxDevices = 64;
 constexpr uint64_t kDefaultWaitNs = 2000ull * 1000ull * 1000ull;
 constexpr double kLog2e = 1.4426950408889634;
 
@@ -67,12 +66,12 @@ struct DeviceState {
 };
 
 std::mutex g_mutex;
-DeviceState g_dev[kMaxDevices];
+DeviceState g_dev[fl::kMaxDevices];
 
 fl_status device_state(DeviceState** out) {
   int dev = 0;
   const cudaError_t ge = cudaGetDevice(&dev);
-  if (ge != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cuda_fail("cudaGetDevice", ge);
+  if (ge != cudaSuccess || dev < 0 || dev >= fl::kMaxDevices) return cuda_fail("cudaGetDevice", ge);
   // make the device's primary context current on this thread (a thread that
   // has made no runtime call yet, e.g. an autograd worker, has none, and the
   // tensor-map encoder is a driver call)

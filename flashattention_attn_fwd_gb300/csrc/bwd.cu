@@ -1119,13 +1119,14 @@ template <int D, int DV, int SCORE>
 cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStream_t s) {
   auto kern = attn_bwd_kernel<D, DV, SCORE>;
   constexpr int smem = BwdLayout<D, DV>::SMEM;
-  static const cudaError_t checked = [&]() {
+  static OncePerDevice once;
+  const cudaError_t checked = on_this_device(once, [&]() {
     cudaFuncAttributes a{};
     cudaError_t e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kBwdLaunchRegs) return cudaErrorInvalidDeviceFunction;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  }();
+  });
   if (checked != cudaSuccess) return checked;
   cudaError_t e;
   if (p.sink && few_keys(p.window, p.sink, p.Lq)) {

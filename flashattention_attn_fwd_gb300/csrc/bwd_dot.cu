@@ -23,6 +23,7 @@
 #include <cstdint>
 
 #include "bwd.h"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace fl {
@@ -226,8 +227,10 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
 template <int D, int DV, int SCORE>
 cudaError_t launch_dot_ds(const BwdParams& p, cudaStream_t s) {
   constexpr int smem = 2 * kDotKeys * (D + DV) * 2;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_bwd_dot_kernel<D, DV, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static OncePerDevice once;
+  const cudaError_t attr = on_this_device(once, [] {
+    return cudaFuncSetAttribute(attn_bwd_dot_kernel<D, DV, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
   if (attr != cudaSuccess) return attr;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hq * ((p.Lq + kDotRows - 1) / kDotRows));
   attn_bwd_dot_kernel<D, DV, SCORE><<<grid, kDotThreads, smem, s>>>(p);

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "bwd.h"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace fl {
@@ -327,8 +328,10 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
 template <int D, int DV, int SCORE>
 cudaError_t launch_short_ds(const BwdParams& p, cudaStream_t s) {
   constexpr int smem = ShortLayout<D, DV>::BYTES;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(attn_bwd_short_kernel<D, DV, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static OncePerDevice once;
+  const cudaError_t attr = on_this_device(once, [] {
+    return cudaFuncSetAttribute(attn_bwd_short_kernel<D, DV, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
   if (attr != cudaSuccess) return attr;
   // a cluster per (batch, key/value head) while all of its blocks find a place,
   // two an SM: a power of two that divides the group, up to the portable 8

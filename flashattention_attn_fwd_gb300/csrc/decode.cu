@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "decode.h"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace fl {
@@ -620,9 +621,11 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const __grid_constant
 template <int D, int MR>
 cudaError_t launch_decode_dm(const CUtensorMap* maps, const DecodeParams& p, cudaStream_t stream) {
   const int smem = DecLayout<D>::smem_bytes(p.Hq / p.Hkv * p.Lq);
-  static const cudaError_t attr = cudaFuncSetAttribute(decode_split_kernel<D, MR>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       DecLayout<D>::smem_bytes(MR));
+  static OncePerDevice once;
+  const cudaError_t attr = on_this_device(once, [] {
+    return cudaFuncSetAttribute(decode_split_kernel<D, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                DecLayout<D>::smem_bytes(MR));
+  });
   if (attr != cudaSuccess) return attr;
   const int grid = p.B * p.Hkv * p.n_split;
   decode_split_kernel<D, MR><<<grid, kDecThreads, smem, stream>>>(maps[0], maps[1], p);
@@ -636,8 +639,10 @@ cudaError_t launch_decode_dm(const CUtensorMap* maps, const DecodeParams& p, cud
 template <int D>
 cudaError_t launch_decode_warp(const CUtensorMap* maps, const DecodeParams& p, cudaStream_t stream) {
   constexpr int smem = DwLayout<D>::SMEM;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(decode_warp_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static OncePerDevice once;
+  const cudaError_t attr = on_this_device(once, [] {
+    return cudaFuncSetAttribute(decode_warp_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
   if (attr != cudaSuccess) return attr;
   const int grid = p.B * p.Hkv * p.n_split;
   decode_warp_kernel<D><<<grid, kDwThreads, smem, stream>>>(maps[0], maps[1], p);

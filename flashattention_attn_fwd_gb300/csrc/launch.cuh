@@ -2,6 +2,7 @@
 #pragma once
 
 #include "fused_attn.cuh"
+#include "host.h"
 #include "kernels.h"
 
 namespace fl {
@@ -13,13 +14,14 @@ cudaError_t launch_fused(const CUtensorMap* maps, const KParams& p, int grid, cu
   // The register split (setmaxnreg) hands the control warpgroup's registers
   // to the softmax warpgroups; it needs exactly kLaunchRegs per thread at
   // launch, or the softmax warpgroups would wait for registers forever.
-  static const cudaError_t checked = [&]() {
+  static OncePerDevice once;
+  const cudaError_t checked = on_this_device(once, [&]() {
     cudaFuncAttributes a{};
     cudaError_t e = cudaFuncGetAttributes(&a, kern);
     if (e != cudaSuccess) return e;
     if (a.numRegs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  }();
+  });
   if (checked != cudaSuccess) return checked;
   kern<<<grid, kThreads, smem, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4], maps[5], maps[6], maps[7],
                                          p);

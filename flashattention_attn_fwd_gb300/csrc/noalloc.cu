@@ -28,7 +28,6 @@ namespace {
 constexpr int kScratchWords = 64;
 static __device__ __align__(256) uint32_t g_noalloc_scratch[kScratchWords];
 constexpr size_t kStatusBytes = 2 * sizeof(uint32_t);
-constexpr int kMaxDevices = 64;
 
 struct NoAllocDevice {
   bool ready = false;
@@ -37,14 +36,14 @@ struct NoAllocDevice {
 };
 
 std::mutex g_na_mutex;
-NoAllocDevice g_na_dev[kMaxDevices];
+NoAllocDevice g_na_dev[fl::kMaxDevices];
 
 // One-time set-up per device, with that device current: the SM count and
 // the device address of the scratch array (the array's name is only a host
 // stand-in, never a device pointer).
 fl_status na_setup(NoAllocDevice** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FL_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fl::kMaxDevices) return FL_ERR_CUDA;
   // the device's primary context current on this thread (the tensor-map
   // encoder is a driver call)
   if (cudaSetDevice(dev) != cudaSuccess) return FL_ERR_CUDA;

@@ -1001,20 +1001,21 @@ constexpr int decode_smem() {
   return merge > ring ? merge : ring;
 }
 
-// Resident CTAs per SM; sets the kernel's shared-memory limit (< 1 on a CUDA
-// error).
+// Resident CTAs per SM of the current device; sets the kernel's shared-memory
+// limit there (< 1 on a CUDA error).
 template <int FMT, int D, int NT, int RW, bool CL>
 int resident() {
-  static const int per_sm = [] {
+  static OncePerDevice once;
+  static int found[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
+  const cudaError_t e = once.run(dev, [dev] {
     constexpr int smem = decode_smem<FMT, D, NT, RW, CL>();
     auto* kernel = paged_decode_kernel<FMT, D, NT, RW, CL>;
-    int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kPdThreads, smem) != cudaSuccess)
-      return -1;
-    return n;
-  }();
-  return per_sm;
+    const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return r != cudaSuccess ? r : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&found[dev], kernel, kPdThreads, smem);
+  });
+  return e == cudaSuccess ? found[dev] : -1;
 }
 
 template <int FMT, int D, int NT, int RW>
