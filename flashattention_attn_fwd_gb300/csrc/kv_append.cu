@@ -27,8 +27,8 @@
 // A product and a sum are rounded separately (no fused multiply-add), so that
 // a value next to a rounding border of the 4-bit code falls to the side that
 // the definition says.  The code of u / s is decided on the correctly rounded
-// quotient: with r = 1 / s correctly rounded, q = u r and one residual step q +
-// r (u - q s) give it (Markstein, "Computation of elementary functions on the
+// quotient: with r = 1 / s correctly rounded, q = u r and one residual step q -
+// r (q s - u) give it (Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990), three operations where the general
 // division takes a dozen.
 #include <cuda_bf16.h>
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kAppThreads, 6) kv_append_kernel(const __grid_
       held = pack8(x);
       if (ok) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + slot * D + c0) = held;
     } else {
-      const float2 inv2 = make_float2(inv, inv);
+      // x becomes -u: see the residual step
+      const float2 inv2 = make_float2(-inv, -inv);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = ptx::mul2(x[e], inv2);
       float a = fmaxf(fabsf(x[0].x), fabsf(x[0].y));
@@ -215,12 +216,14 @@ __global__ void __launch_bounds__(kAppThreads, 6) kv_append_kernel(const __grid_
                              fminf(fmaxf(x[e].y, -2.f * kBlockMax), 2.f * kBlockMax));
       }
       const float rs = s > 0.f ? __frcp_rn(s) : 0.f;  // a zero scale: all codes zero
-      const float2 rs2 = make_float2(rs, rs), ns2 = make_float2(-s, -s);
+      // q - r (q s - u): with these signs a zero keeps its own, where q + r (u -
+      // q s) would make -0 of u a +0
+      const float2 nr2 = make_float2(-rs, -rs), s2 = make_float2(s, s);
       float z[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 q = ptx::mul2(x[e], rs2);
-        const float2 f = ptx::fma2(ptx::fma2(q, ns2, x[e]), rs2, q);
+        const float2 q = ptx::mul2(x[e], nr2);
+        const float2 f = ptx::fma2(ptx::fma2(q, s2, x[e]), nr2, q);
         z[2 * e] = s > 0.f ? f.x : 0.f;
         z[2 * e + 1] = s > 0.f ? f.y : 0.f;
       }
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kAppThreads, 6) kv_append_kernel(const __grid_
       if (out) {
         uint32_t hv[4];
         cvt4::from_e2m1x8(code, hv);
-        const float2 s2 = make_float2(s, s), g2 = make_float2(scale, scale);
+        const float2 g2 = make_float2(scale, scale);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = ptx::mul2(ptx::mul2(cvt4::unpack_f16x2(hv[e]), s2), g2);
         held = pack8(x);
