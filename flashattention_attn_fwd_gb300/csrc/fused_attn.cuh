@@ -284,6 +284,12 @@ __host__ __device__ __forceinline__ int ring_len(const Unit& U) { return U.kv_hi
 __host__ __device__ __forceinline__ int ring_len(const SinkUnit& U) { return U.kv_hi - U.kv_lo + 1 + U.nsink; }
 __host__ __device__ __forceinline__ int slot_len(const Unit& U, int s) { return U.hi[s] - U.lo[s] + 1; }
 __host__ __device__ __forceinline__ int slot_len(const SinkUnit& U, int s) { return U.hi[s] - U.lo[s] + 1 + U.sk[s]; }
+// Do both slots walk the same tiles?  (With sinks a slot without rows of its own
+// leaves these out.)
+__host__ __device__ __forceinline__ bool same_tiles(const Unit& U) { return U.lo[0] == U.lo[1] && U.hi[0] == U.hi[1]; }
+__host__ __device__ __forceinline__ bool same_tiles(const SinkUnit& U) {
+  return same_tiles(static_cast<const Unit&>(U)) && U.sk[0] == U.sk[1];
+}
 __host__ __device__ __forceinline__ int slot_sinks(const Unit&, int) { return 0; }
 __host__ __device__ __forceinline__ int slot_sinks(const SinkUnit& U, int s) { return U.sk[s]; }
 // Ring position of slot s's first own tile within a unit, and the distance
@@ -1331,7 +1337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const UnitT& Us = unit_at(uc);
       const int u_hi = Us.hi[s], u_b = Us.b[s], u_hq = Us.hq[s], u_row0 = Us.row0[s];
       const int ns = slot_len(Us, s), nw = ns - slot_sinks(Us, s);
-      const bool turns = kPingPong && Us.lo[0] == Us.lo[1] && Us.hi[0] == Us.hi[1];
+      const bool turns = kPingPong && same_tiles(Us);
       const int n = ring_len(Us);
       // ring index of this slot's first tile (only the Evoformer kinds read
       // the ring from here; their units are never key-split: stride 1)
