@@ -537,6 +537,7 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
     const fl::SinkSplit ss = fl::sink_split(d.B, d.Hkv, d.Lq, d.Lk, d.window, d.sink);
     p.sink = d.sink;
     p.sink_tiles = ss.tiles; p.far_chunks = ss.chunks; p.far_len = ss.len;
+    p.dot_rows = fl::score_rows(d.window, d.sink, d.Lq);
     p.part = p.dq_acc + (p.rows * d.d + 2 * vec + 3) / 4 * 4;
   }
   p.slopes = d.alibi_slopes; p.doc_offsets = d.doc_offsets;

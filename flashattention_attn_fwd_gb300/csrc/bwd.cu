@@ -1061,13 +1061,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // D_i = dout_scale * sum_c dO_ic O_ic, L2_i = LSE_i log2(e) (a row that saw
 // no key: +inf, so that its P is 0), and the dQ accumulator zeroed; DV / 8
 // lanes per row, 16 bytes of O and dO each, D / (DV / 8) accumulator values.
+// With sinks it runs beside the scores' kernel, which has the first p.dot_rows rows
+// of every head: it leaves these alone and its last block ends after that kernel, so
+// that what follows finds both done (every block waiting: 6 us more at B 2, 32 heads
+// over 8, L 2048, d 128).
 template <int D, int DV>
 __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant__ BwdParams p) {
   constexpr int LPR = DV / 8;
   constexpr int ZPL = D / LPR;  // accumulator floats zeroed per lane (4 or 8)
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / LPR) + threadIdx.x / LPR;
   const int sub = threadIdx.x % LPR;
-  const bool valid = row < p.rows;
+  bool valid = row < p.rows;
+  if (p.dot_rows) {
+    const int64_t i = row >> 32 ? row % p.Lq : static_cast<uint32_t>(row) % static_cast<uint32_t>(p.Lq);
+    valid = valid && i >= p.dot_rows;
+  }
   const int64_t off = (valid ? row : 0) * DV + sub * 8;
   const uint4 ov = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.out) + off));
   const uint4 gv = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.dout) + off));
@@ -1081,16 +1089,18 @@ __global__ void __launch_bounds__(256) attn_bwd_pre_kernel(const __grid_constant
   }
 #pragma unroll
   for (int w = LPR / 2; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-  if (!valid) return;
-  float4* acc = reinterpret_cast<float4*>(p.dq_acc + row * D + sub * ZPL);
+  if (valid) {
+    float4* acc = reinterpret_cast<float4*>(p.dq_acc + row * D + sub * ZPL);
 #pragma unroll
-  for (int i = 0; i < ZPL / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (sub == 0) {
-    const int64_t vrow = p.Lq_pad == p.Lq ? row : row / p.Lq * p.Lq_pad + row % p.Lq;
-    p.dvec[vrow] = s * p.dout_scale;
-    const float l = p.lse[row];
-    p.l2[vrow] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+    for (int i = 0; i < ZPL / 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sub == 0) {
+      const int64_t vrow = p.Lq_pad == p.Lq ? row : row / p.Lq * p.Lq_pad + row % p.Lq;
+      p.dvec[vrow] = s * p.dout_scale;
+      const float l = p.lse[row];
+      p.l2[vrow] = l == -CUDART_INF_F ? CUDART_INF_F : l * kLog2e;
+    }
   }
+  if (p.dot_rows && blockIdx.x == gridDim.x - 1) ptx::wait_prerequisites();
 }
 
 // dQ = scale * accumulator, rounded to bf16; eight elements per thread of the
@@ -1142,13 +1152,16 @@ cudaError_t launch_bwd_ds(const CUtensorMap* maps, const BwdParams& p, cudaStrea
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (checked != cudaSuccess) return checked;
-  cudaError_t e;
-  if (p.sink && few_keys(p.window, p.sink, p.Lq)) {
-    e = launch_bwd_dot(D, DV, SCORE, p, s);
-  } else {
+  cudaError_t e = cudaSuccess;
+  if (p.dot_rows) e = launch_bwd_dot(D, DV, SCORE, p, s);
+  if (e == cudaSuccess && p.dot_rows < p.Lq) {
     const int rgrid = static_cast<int>((p.rows + 256 / (DV / 8) - 1) / (256 / (DV / 8)));
-    attn_bwd_pre_kernel<D, DV><<<rgrid, 256, 0, s>>>(p);
-    e = cudaGetLastError();
+    if (p.dot_rows) {
+      e = launch_chained(attn_bwd_pre_kernel<D, DV>, rgrid, 256, 0, s, p);
+    } else {
+      attn_bwd_pre_kernel<D, DV><<<rgrid, 256, 0, s>>>(p);
+      e = cudaGetLastError();
+    }
   }
   if (e != cudaSuccess) return e;
   const int walks = p.B * p.Hkv * (p.n_ktiles + p.far_chunks * p.sink_tiles);

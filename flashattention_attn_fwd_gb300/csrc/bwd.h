@@ -48,6 +48,7 @@ struct BwdParams {
   // the tile's own leave fp32 partial dV and dK, [B * Hkv * sink_tiles][1 +
   // far_chunks][(DV + D) / 4][128][4], summed in order by a last kernel.  0: no split.
   int sink, sink_tiles, far_chunks, far_len;
+  int dot_rows;           // sinks: rows of every head whose D comes from the scores
 };
 
 // The split of the sink tiles' walks (see BwdParams), from sizes alone.
@@ -80,17 +81,22 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
   return s;
 }
 
-// With sinks: does D need the scores (launch_bwd_dot), or does dO . O do?  Where
-// rows see few keys the rounding of O shows: relative error of dQ against 64 bits
-// 2.4e-3 from the scores at any size; from O 4.6e-3 at 4 tokens, 3.0e-3 at 16,
-// 2.7e-3 at windows of 8, 2.5e-3 at windows of 64 and 2.4e-3 at 256 (the first
-// rows of a short sequence count as such a window).  The scores cost 40 us
-// beside 108 at B 4 H 16 L 2048 window 256, 3 us at 300 tokens.
-inline bool few_keys(int window, int sink, int Lq) {
-  return static_cast<int64_t>(window) + sink <= 64 || Lq <= 512;
+// With sinks: the first rows of every head whose D comes from the scores
+// (launch_bwd_dot); dO . O does for the others.  Where rows see few keys the
+// rounding of O shows: relative error of dQ against 64 bits 2.4e-3 from the scores
+// at any size; from O 4.6e-3 at 4 tokens, 3.0e-3 at 16, 2.7e-3 at windows of 8,
+// 2.5e-3 at windows of 64 and 2.4e-3 at 256.  So rows that see at most 64 keys:
+// all of them under a narrow window, else the first 64 of every sequence (a block
+// of that kernel).  The scores of all rows cost 40 us beside 108 at B 4 H 16 L
+// 2048 window 256, those of 64 rows a head 2 us there and 2.4 beside 14.4 at B 1 H 2
+// L 600; up to 512 tokens all rows' cost no more.
+constexpr int kDotRows = 64;
+inline int score_rows(int window, int sink, int Lq) {
+  return static_cast<int64_t>(window) + sink <= 64 || Lq <= 512 ? Lq : kDotRows;
 }
 
-// D, L2 and a zeroed dQ accumulator from the scores (sum P dP); (d, dv) as below.
+// D, L2 and a zeroed dQ accumulator of the first p.dot_rows rows of every head, from
+// the scores (sum P dP); (d, dv) as below.
 cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
 
 // With sinks, sequences of at most this many tokens: dQ, dK and dV in one launch.

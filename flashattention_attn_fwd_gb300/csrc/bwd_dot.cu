@@ -4,7 +4,7 @@
 // and D are then nearly equal.  D is otherwise taken as dO . O with the output
 // that the forward returned, whose bf16 rounding (2^-9 of |O|, and that of P
 // before it) then is the error of the difference; rows of a few keys, which
-// have little else to attend to, bring that out (few_keys in bwd.h has the
+// have little else to attend to, bring that out (score_rows in bwd.h has the
 // figures and the rule).  So this kernel forms S = Q K^T and dP = dO V^T once
 // more over the visible keys and sums P dP in 32 bits: P = 2^(t log2 e - L2) needs
 // no running maximum, as the log-sum-exp is known.
@@ -13,13 +13,16 @@
 // through a two-stage cp.async ring; both products are warp-level m16n8k16
 // tiles whose accumulators stay in registers.  Larger blocks read K and V less
 // often but leave fewer of them to hide each other's waits: 128 rows in 8 warps
-// and 32 rows per warp were 15 and 20 us slower at B 4 H 16 L 2048 d 64.  No
+// and 32 rows per warp were 15 and 20 us slower at B 4 H 16 L 2048 d 64, and for
+// the first rows alone 16 rows a block with the keys split over its warps: 3 us
+// there, for 0.7 us less at one sequence of 600 tokens.  No
 // accumulator outlives a tile, so there is nothing for TMEM to hold; bound by
 // the tensor core's warp-level rate and by the exponentials.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "bwd.h"
@@ -29,7 +32,7 @@
 namespace fl {
 namespace {
 
-constexpr int kDotRows = 64, kDotKeys = 64, kDotThreads = 128;
+constexpr int kDotKeys = 64, kDotThreads = 128;
 constexpr float kDotLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -65,7 +68,8 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
   extern __shared__ __align__(128) uint8_t dot_sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
-  const int n_rt = (p.Lq + kDotRows - 1) / kDotRows;
+  ptx::launch_dependents();  // the other rows' kernel shares nothing with this one
+  const int n_rt = (min(p.dot_rows, p.Lq) + kDotRows - 1) / kDotRows;
   const int rt = blockIdx.x % n_rt;
   const int bh = blockIdx.x / n_rt;  // (batch, query head)
   const int h = bh % p.Hq, b = bh / p.Hq;
@@ -232,7 +236,7 @@ cudaError_t launch_dot_ds(const BwdParams& p, cudaStream_t s) {
     return cudaFuncSetAttribute(attn_bwd_dot_kernel<D, DV, SCORE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (attr != cudaSuccess) return attr;
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hq * ((p.Lq + kDotRows - 1) / kDotRows));
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.Hq * ((std::min(p.dot_rows, p.Lq) + kDotRows - 1) / kDotRows));
   attn_bwd_dot_kernel<D, DV, SCORE><<<grid, kDotThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
