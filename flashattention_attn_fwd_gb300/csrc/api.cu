@@ -556,7 +556,7 @@ fl_status attn_bwd_run(const void* q, const void* k, const void* v, const void* 
     return FL_ERR_UNSUPPORTED;
   if (d.sink && d.Lq <= fl::kShortRows && d.Lq == d.Lk && !dv_accumulate && dout_scale == 1.0f)
     return launched("backward kernel launch",
-                    fl::launch_bwd_short(d.d, d.dv, d.score_mod, p, static_cast<cudaStream_t>(d.stream)));
+                    fl::launch_bwd_short(d.d, d.dv, d.score_mod, p, ds->sm_count, static_cast<cudaStream_t>(d.stream)));
   CUtensorMap maps[9];
   const int bw = box_width(d.d), bwv = box_width(d.dv);
   const int64_t sl = d.d, slv = d.dv;

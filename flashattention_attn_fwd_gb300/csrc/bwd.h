@@ -43,7 +43,7 @@ struct BwdParams {
   float dout_scale;
   int dv_accumulate;
   // Window with sinks: key tiles [0, sink_tiles) are seen by every later query,
-  // far more tiles than a window's.  The query tiles from far0(tile) on are
+  // far more tiles than a window's.  The query tiles from far_begin(tile) on are
   // cut into far_chunks runs of far_len tiles, one CTA each; those CTAs and
   // the tile's own leave fp32 partial dV and dK, [B * Hkv * sink_tiles][1 +
   // far_chunks][(DV + D) / 4][128][4], summed in order by a last kernel.  0: no split.
@@ -55,6 +55,10 @@ struct BwdParams {
 struct SinkSplit {
   int tiles, chunks, len;
 };
+// SMs that the split balances for: a tuning value, not a limit (the split is right
+// for any device), and fixed because the workspace's size, which depends on it, can
+// be asked for without a device.
+constexpr int kTunedSms = 152;
 // First query tile past key tile jt's window.
 #ifdef __CUDACC__
 __host__ __device__
@@ -73,7 +77,7 @@ inline SinkSplit sink_split(int B, int Hkv, int Lq, int Lk, int window, int sink
   // first), and no shorter than a window tile's walk.
   const int near = far_begin(0, window);
   const int64_t steps = static_cast<int64_t>(B) * Hkv * ((Lk + 127) / 128 * static_cast<int64_t>(near) + static_cast<int64_t>(far) * s.tiles);
-  const int64_t share = steps / (2 * 152);
+  const int64_t share = steps / (2 * kTunedSms);
   const int64_t most = share > near ? share : near;
   const int64_t want = (far + most - 1) / most;
   s.len = static_cast<int>((far + want - 1) / want);
@@ -101,7 +105,7 @@ cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cud
 
 // With sinks, sequences of at most this many tokens: dQ, dK and dV in one launch.
 constexpr int kShortRows = 64;
-cudaError_t launch_bwd_short(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);
+cudaError_t launch_bwd_short(int d, int dv, int score_mod, const BwdParams& p, int sm_count, cudaStream_t s);
 
 // (d, dv): (32, 32), (64, 64), (128, 128) or (64, 128)
 cudaError_t launch_bwd(int d, int dv, int score_mod, const CUtensorMap* maps, const BwdParams& p, cudaStream_t s);

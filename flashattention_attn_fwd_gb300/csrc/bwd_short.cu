@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
 }
 
 template <int D, int DV, int SCORE>
-cudaError_t launch_short_ds(const BwdParams& p, cudaStream_t s) {
+cudaError_t launch_short_ds(const BwdParams& p, int sm_count, cudaStream_t s) {
   constexpr int smem = ShortLayout<D, DV>::BYTES;
   static OncePerDevice once;
   const cudaError_t attr = on_this_device(once, [] {
@@ -338,7 +338,7 @@ cudaError_t launch_short_ds(const BwdParams& p, cudaStream_t s) {
   const int64_t units = static_cast<int64_t>(p.B) * p.Hkv;
   const int group = p.Hq / p.Hkv;
   int cl = 1;
-  while (cl < 8 && group % (2 * cl) == 0 && units * 2 * cl <= 2 * 152) cl *= 2;
+  while (cl < 8 && group % (2 * cl) == 0 && units * cl <= sm_count) cl *= 2;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * cl));
@@ -354,20 +354,20 @@ cudaError_t launch_short_ds(const BwdParams& p, cudaStream_t s) {
 }
 
 template <int D, int DV>
-cudaError_t launch_short_d(int score_mod, const BwdParams& p, cudaStream_t s) {
-  return score_mod == 0 ? launch_short_ds<D, DV, 0>(p, s)
-         : score_mod == 1 ? launch_short_ds<D, DV, 1>(p, s)
-                          : launch_short_ds<D, DV, 2>(p, s);
+cudaError_t launch_short_d(int score_mod, const BwdParams& p, int sm_count, cudaStream_t s) {
+  return score_mod == 0 ? launch_short_ds<D, DV, 0>(p, sm_count, s)
+         : score_mod == 1 ? launch_short_ds<D, DV, 1>(p, sm_count, s)
+                          : launch_short_ds<D, DV, 2>(p, sm_count, s);
 }
 
 }  // namespace
 
-cudaError_t launch_bwd_short(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s) {
-  if (dv != d) return launch_short_d<64, 128>(score_mod, p, s);
+cudaError_t launch_bwd_short(int d, int dv, int score_mod, const BwdParams& p, int sm_count, cudaStream_t s) {
+  if (dv != d) return launch_short_d<64, 128>(score_mod, p, sm_count, s);
   switch (d) {
-    case 32: return launch_short_d<32, 32>(score_mod, p, s);
-    case 64: return launch_short_d<64, 64>(score_mod, p, s);
-    default: return launch_short_d<128, 128>(score_mod, p, s);
+    case 32: return launch_short_d<32, 32>(score_mod, p, sm_count, s);
+    case 64: return launch_short_d<64, 64>(score_mod, p, sm_count, s);
+    default: return launch_short_d<128, 128>(score_mod, p, sm_count, s);
   }
 }
 
