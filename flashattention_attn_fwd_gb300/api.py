@@ -39,6 +39,11 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(stream, t: torch.Tensor) -> torch.Tensor:
+    """A tensor like the contiguous t, as ``_empty_on``."""
+    return _empty_on(stream, t.shape, t.dtype, t.device)
+
+
 def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim:
         return
@@ -127,12 +132,12 @@ def diffattn_fwd(q1, k1, q2, k2, v, lam: float, *, causal: bool = True, scale: f
     B, H, L, d = q1.shape
     dv = v.shape[-1]
     if out is None:
-        out = torch.empty((B, H, L, dv), device=q1.device, dtype=torch.bfloat16)
+        out = _empty_on(stream, (B, H, L, dv), torch.bfloat16, q1.device)
     _need(out, "out", 4)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     if lse is None and return_lse:
-        lse = torch.empty((2, B, H, L), device=q1.device, dtype=torch.float32)
+        lse = _empty_on(stream, (2, B, H, L), torch.float32, q1.device)
     desc = _lib.new_desc()
     desc.B, desc.Hq, desc.Hkv, desc.Lq, desc.Lk, desc.d, desc.dv = B, H, H, L, L, d, dv
     desc.scale = 0.0 if scale is None else float(scale)
@@ -154,11 +159,11 @@ def diffattn_bwd(q1, k1, q2, k2, v, dout, lam: float, *, causal: bool = True, sc
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
     B, H, L, d = q1.shape
-    dq1 = torch.empty_like(q1) if dq1 is None else dq1
-    dk1 = torch.empty_like(k1) if dk1 is None else dk1
-    dq2 = torch.empty_like(q2) if dq2 is None else dq2
-    dk2 = torch.empty_like(k2) if dk2 is None else dk2
-    dv = torch.empty_like(v) if dv is None else dv
+    dq1 = _like(stream, q1) if dq1 is None else dq1
+    dk1 = _like(stream, k1) if dk1 is None else dk1
+    dq2 = _like(stream, q2) if dq2 is None else dq2
+    dk2 = _like(stream, k2) if dk2 is None else dk2
+    dv = _like(stream, v) if dv is None else dv
     desc = _lib.new_desc()
     desc.B, desc.Hq, desc.Hkv, desc.Lq, desc.Lk, desc.d, desc.dv = B, H, H, L, L, d, v.shape[-1]
     desc.scale = 0.0 if scale is None else float(scale)
@@ -166,7 +171,7 @@ def diffattn_bwd(q1, k1, q2, k2, v, dout, lam: float, *, causal: bool = True, sc
     desc.stream = _stream_ptr(stream)
     need = int(_lib.lib().fl_diffattn_bwd_workspace_size(ctypes.byref(desc)))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), device=q1.device, dtype=torch.uint8)
+        workspace = _empty_on(stream, (max(need, 16),), torch.uint8, q1.device)
     st = _lib.lib().fl_diffattn_bwd(q1.data_ptr(), k1.data_ptr(), q2.data_ptr(), k2.data_ptr(), v.data_ptr(),
                                     dout.data_ptr(), ctypes.c_float(float(lam)), dq1.data_ptr(), dk1.data_ptr(),
                                     dq2.data_ptr(), dk2.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
@@ -195,10 +200,10 @@ def evoformer_gated_attn_fwd(q, k, v, pair_bias, mask_bias, gate, *, scale: floa
         if not mask_bias.is_contiguous() or tuple(mask_bias.shape) != (B, Ns, Nr):
             raise ValueError("mask_bias must be contiguous [B,N_seq,N_res]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(stream, q)
     _need(out, "out", 5)
     if lse is None and return_lse:
-        lse = torch.empty((B, Ns, H, Nr), device=q.device, dtype=torch.float32)
+        lse = _empty_on(stream, (B, Ns, H, Nr), torch.float32, q.device)
     st = _lib.lib().fl_evoformer_gated_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(),
         0 if pair_bias is None else pair_bias.data_ptr(),
@@ -225,10 +230,10 @@ def evoformer_col_gated_attn_fwd(q, k, v, mask_bias, gate, *, scale: float | Non
         if not mask_bias.is_contiguous() or tuple(mask_bias.shape) != (B, Nr, Ns):
             raise ValueError("mask_bias must be contiguous [B,N_res,N_seq]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(stream, q)
     _need(out, "out", 5)
     if lse is None and return_lse:
-        lse = torch.empty((B, H, Nr, Ns), device=q.device, dtype=torch.float32)
+        lse = _empty_on(stream, (B, H, Nr, Ns), torch.float32, q.device)
     st = _lib.lib().fl_evoformer_col_gated_attn_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(),
         0 if mask_bias is None else mask_bias.data_ptr(),
@@ -252,10 +257,10 @@ def attn_decode_fwd(q, k_cache, v_cache, kv_len=None, *, causal: bool = False, s
     B, Hq, Lq, d = q.shape
     _, Hkv, Lk, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _like(stream, q)
     _need(out, "out", 4)
     if lse is None and return_lse:
-        lse = torch.empty((B, Hq, Lq), device=q.device, dtype=torch.float32)
+        lse = _empty_on(stream, (B, Hq, Lq), torch.float32, q.device)
     if kv_len is not None:
         _need(kv_len, "kv_len", 1, torch.int32)
     desc = _lib.new_desc()
@@ -272,7 +277,7 @@ def attn_decode_fwd(q, k_cache, v_cache, kv_len=None, *, causal: bool = False, s
     desc.stream = _stream_ptr(stream)
     need = int(_lib.lib().fl_attn_decode_workspace_size(ctypes.byref(desc)))
     if need and workspace is None:
-        workspace = torch.empty(need, device=q.device, dtype=torch.uint8)
+        workspace = _empty_on(stream, (need,), torch.uint8, q.device)
     ws_ptr = 0 if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = _lib.lib().fl_attn_decode_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
@@ -296,10 +301,9 @@ def attn_bwd(q, k, v, out, dout, lse, *, mask: str = "none", window: int | None 
     _need(lse, "lse", 3, torch.float32)
     B, Hq, Lq, d = q.shape
     _, Hkv, Lk, _ = k.shape
-    like = torch.empty_like if stream is None else lambda t: _empty_on(stream, t.shape, t.dtype, t.device)
-    dq = like(q) if dq is None else dq
-    dk = like(k) if dk is None else dk
-    dv = like(v) if dv is None else dv
+    dq = _like(stream, q) if dq is None else dq
+    dk = _like(stream, k) if dk is None else dk
+    dv = _like(stream, v) if dv is None else dv
     desc = _variant_desc(B, Hq, Hkv, Lq, Lk, d, v.shape[-1], mask=mask, window=window, prefix=prefix,
                          doc_offsets=doc_offsets, doc_causal=doc_causal, score_mod=score_mod,
                          alibi_slopes=alibi_slopes, softcap=softcap, scale=scale, sink=sink,

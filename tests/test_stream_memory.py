@@ -73,3 +73,45 @@ def test_allocations_belong_to_the_named_stream():
             sync_status(stream)
             for a, b in zip(grads[1:], want[1:]):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_every_call_allocates_on_its_stream(monkeypatch):
+    """The calls with workspaces of their own: what they allocate, a workspace that
+    is let go when the call returns included, belongs to the stream they run on."""
+    from flashattention_attn_fwd_gb300 import (attn_decode_fwd, diffattn_bwd, diffattn_fwd, evoformer_col_gated_attn_fwd,
+                                               evoformer_gated_attn_fwd)
+    seen = []
+    real = api._empty_on
+
+    def spy(*args):
+        t = real(*args)
+        seen.append(_owner(t))
+        return t
+    q, k, v, kv_len = (t.to(DEV) for t in synth.decode_inputs(2, 8, 2, 1, 4096, 64, seed=1))
+    diff = [t.to(DEV) for t in synth.diff_inputs(1, 2, 256, seed=2)]
+    dout = torch.ones_like(diff[4])
+    row = [t.to(DEV) for t in synth.evo_inputs(1, 4, 64, 2, seed=3)]
+    col = [t.to(DEV) for t in synth.evo_col_inputs(1, 64, 4, 2, seed=4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    calls = {
+        "decode": (lambda s: attn_decode_fwd(q, k, v, kv_len, stream=s), 3),       # out, lse, workspace
+        "diff": (lambda s: diffattn_fwd(*diff, 0.5, stream=s), 2),
+        "diff backward": (lambda s: diffattn_bwd(*diff, dout, 0.5, stream=s), 6),  # five gradients, workspace
+        "row": (lambda s: evoformer_gated_attn_fwd(*row, stream=s), 2),
+        "column": (lambda s: evoformer_col_gated_attn_fwd(*col, stream=s), 2),
+    }
+    monkeypatch.setattr(api, "_empty_on", spy)
+    for name, (call, count) in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        for stream, handle in ((side, side.cuda_stream), (0, 0)):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                seen.clear()
+                got = call(stream)
+                assert seen == [handle] * count, name
+                sync_status(stream)
+            for i, (a, b) in enumerate(zip(got, want)):
+                # (dq1 and dq2 are sums in no fixed order)
+                assert torch.equal(a, b) or (name == "diff backward" and i in (0, 2)), (name, i)
