@@ -52,6 +52,7 @@ EncodeTiledFn encode_fn() {
 thread_local char g_detail[192] = "";
 
 fl_status cuda_fail(const char* where, cudaError_t e) {
+  cudaGetLastError();  // the runtime keeps it: a later launch would be blamed for it
   std::snprintf(g_detail, sizeof(g_detail), "%s: %s", where, e == cudaSuccess ? "failed" : cudaGetErrorString(e));
   return FL_ERR_CUDA;
 }

@@ -43,18 +43,23 @@ NoAllocDevice g_na_dev[fl::kMaxDevices];
 // stand-in, never a device pointer).
 fl_status na_setup(NoAllocDevice** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= fl::kMaxDevices) return FL_ERR_CUDA;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= fl::kMaxDevices)
+    return fl::launch_result("cudaGetDevice", e != cudaSuccess ? e : cudaErrorInvalidDevice);
   // the device's primary context current on this thread (the tensor-map
   // encoder is a driver call)
-  if (cudaSetDevice(dev) != cudaSuccess) return FL_ERR_CUDA;
+  if ((e = cudaSetDevice(dev)) != cudaSuccess) return fl::launch_result("cudaSetDevice", e);
   std::lock_guard<std::mutex> lock(g_na_mutex);
   NoAllocDevice& d = g_na_dev[dev];
   if (!d.ready) {
     int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
-      return FL_ERR_CUDA;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess || sms <= 0)
+      return fl::launch_result("cudaDeviceGetAttribute", e != cudaSuccess ? e : cudaErrorInvalidDevice);
     void* ptr = nullptr;
-    if (cudaGetSymbolAddress(&ptr, g_noalloc_scratch) != cudaSuccess || ptr == nullptr) return FL_ERR_CUDA;
+    e = cudaGetSymbolAddress(&ptr, g_noalloc_scratch);
+    if (e != cudaSuccess || ptr == nullptr)
+      return fl::launch_result("cudaGetSymbolAddress", e != cudaSuccess ? e : cudaErrorInvalidSymbol);
     d.sm_count = sms;
     d.scratch = static_cast<uint32_t*>(ptr);
     d.ready = true;
@@ -66,11 +71,14 @@ fl_status na_setup(NoAllocDevice** out) {
 // Status query: wait for the stream, then return and clear the scratch's
 // error bits.  No allocation: a synchronous copy into a host stack value.
 fl_status na_query(NoAllocDevice* nd, cudaStream_t stream) {
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return FL_ERR_CUDA;
+  cudaError_t e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess) return fl::launch_result("cudaStreamSynchronize", e);
   uint32_t h[2] = {0u, 0u};
-  if (cudaMemcpy(h, nd->scratch, kStatusBytes, cudaMemcpyDeviceToHost) != cudaSuccess) return FL_ERR_CUDA;
+  e = cudaMemcpy(h, nd->scratch, kStatusBytes, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return fl::launch_result("cudaMemcpy (status word)", e);
   if (h[0] == 0u) return FL_OK;
-  if (cudaMemset(nd->scratch, 0, kStatusBytes) != cudaSuccess) return FL_ERR_CUDA;
+  e = cudaMemset(nd->scratch, 0, kStatusBytes);
+  if (e != cudaSuccess) return fl::launch_result("cudaMemset (status word)", e);
   return (h[0] & 1u) ? FL_ERR_TIMEOUT : FL_ERR_DEVICE_BOUNDS;
 }
 

@@ -193,7 +193,11 @@ size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv
   if (fl::device_info(&sm_count, &status) != FL_OK) return 0;
   const int M = desc->Hq / desc->Hkv * desc->Lq;
   const int grid = fl::paged_resident(cache->format, cache->d, M, false) * sm_count;
-  return grid < 1 ? 0 : workspace_layout(*desc, M, grid).bytes;
+  if (grid < 1) {
+    fl::launch_result("paged decode occupancy", cudaErrorInvalidDeviceFunction);
+    return 0;
+  }
+  return workspace_layout(*desc, M, grid).bytes;
 }
 
 fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, const int32_t* kv_len,
