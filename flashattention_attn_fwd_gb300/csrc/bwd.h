@@ -99,6 +99,17 @@ inline int score_rows(int window, int sink, int Lq) {
   return static_cast<int64_t>(window) + sink <= 64 || Lq <= 512 ? Lq : kDotRows;
 }
 
+#ifdef __CUDACC__
+// Byte offset of 16-byte chunk c of row r in a shared tile of C bf16 channels (the
+// kernels with warp-level products): chunks permuted so that eight rows of one
+// chunk column meet all banks.
+template <int C>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  const int x = C >= 64 ? r & 7 : (r >> 1) & 3;
+  return static_cast<uint32_t>(r * C * 2 + ((c ^ x) << 4));
+}
+#endif
+
 // D, L2 and a zeroed dQ accumulator of the first p.dot_rows rows of every head, from
 // the scores (sum P dP); (d, dv) as below.
 cudaError_t launch_bwd_dot(int d, int dv, int score_mod, const BwdParams& p, cudaStream_t s);

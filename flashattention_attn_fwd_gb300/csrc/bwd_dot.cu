@@ -35,33 +35,6 @@ namespace {
 constexpr int kDotKeys = 64, kDotThreads = 128;
 constexpr float kDotLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  const uint32_t n = ok ? 16u : 0u;  // 0 bytes read: the chunk is zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte chunk c of row r in a tile of C channels: chunks
-// permuted so that eight rows of one chunk column meet all banks.
-template <int C>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  const int x = C >= 64 ? r & 7 : (r >> 1) & 3;
-  return static_cast<uint32_t>(r * C * 2 + ((c ^ x) << 4));
-}
-
 template <int D, int DV, int SCORE>
 __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_constant__ BwdParams p) {
   constexpr int STAGE = kDotKeys * (D + DV) * 2;
@@ -102,12 +75,12 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
     for (int c = tid; c < kDotKeys * (D / 8); c += kDotThreads) {
       const int r = c / (D / 8), cc = c % (D / 8);
       const bool ok = j0 + r < p.Lk;
-      cp16(st + chunk_at<D>(r, cc), k + static_cast<int64_t>(ok ? j0 + r : 0) * D + cc * 8, ok);
+      ptx::cp_async16(st + chunk_at<D>(r, cc), k + static_cast<int64_t>(ok ? j0 + r : 0) * D + cc * 8, ok);
     }
     for (int c = tid; c < kDotKeys * (DV / 8); c += kDotThreads) {
       const int r = c / (DV / 8), cc = c % (DV / 8);
       const bool ok = j0 + r < p.Lk;
-      cp16(st + kDotKeys * D * 2 + chunk_at<DV>(r, cc), v + static_cast<int64_t>(ok ? j0 + r : 0) * DV + cc * 8, ok);
+      ptx::cp_async16(st + kDotKeys * D * 2 + chunk_at<DV>(r, cc), v + static_cast<int64_t>(ok ? j0 + r : 0) * DV + cc * 8, ok);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -186,16 +159,16 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t r[4];
-        ldsm4(r, ks + chunk_at<D>(lr, 2 * kk + lc));
-        mma(s[0], qa[kk], r[0], r[1]);
-        mma(s[1], qa[kk], r[2], r[3]);
+        ptx::ldsm4(r, ks + chunk_at<D>(lr, 2 * kk + lc));
+        ptx::mma16816(s[0], qa[kk], r[0], r[1]);
+        ptx::mma16816(s[1], qa[kk], r[2], r[3]);
       }
 #pragma unroll
       for (int kk = 0; kk < DV / 16; ++kk) {
         uint32_t r[4];
-        ldsm4(r, vs + chunk_at<DV>(lr, 2 * kk + lc));
-        mma(dp[0], da[kk], r[0], r[1]);
-        mma(dp[1], da[kk], r[2], r[3]);
+        ptx::ldsm4(r, vs + chunk_at<DV>(lr, 2 * kk + lc));
+        ptx::mma16816(dp[0], da[kk], r[0], r[1]);
+        ptx::mma16816(dp[1], da[kk], r[2], r[3]);
       }
       if (jb >= lo_max && jb + 15 <= hi_min) {  // all of the warp's rows see all of it
 #pragma unroll

@@ -40,39 +40,8 @@ namespace {
 constexpr int kRows = kShortRows, kShortThreads = 128;
 constexpr float kShortLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-  const uint32_t n = ok ? 16u : 0u;  // 0 bytes read: the chunk is zeroed
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte chunk c of row r in a tile of C channels: chunks
-// permuted so that eight rows of one chunk column meet all banks.
-template <int C>
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  const int x = C >= 64 ? r & 7 : (r >> 1) & 3;
-  return static_cast<uint32_t>(r * C * 2 + ((c ^ x) << 4));
 }
 
 // x, y as bf16 pairs: the nearest, and what is left of each
@@ -112,7 +81,7 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
     for (int c = tid; c < nb * 16 * (C / 8); c += kShortThreads) {
       const int r = c / (C / 8), cc = c % (C / 8);
       const bool ok = r < n;
-      cp16(sm + dst + chunk_at<C>(r, cc), src + static_cast<int64_t>(ok ? r : 0) * C + cc * 8, ok);
+      ptx::cp_async16(sm + dst + chunk_at<C>(r, cc), src + static_cast<int64_t>(ok ? r : 0) * C + cc * 8, ok);
     }
   };
   load(std::integral_constant<int, D>{}, L::K, p.k, krow0);
@@ -155,14 +124,14 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
 #pragma unroll
         for (int kk = 0; kk < C / 16; ++kk) {
           uint32_t a[4];
-          ldsm4(a, sm + a_tile + chunk_at<C>(ar, 2 * kk + ac));
+          ptx::ldsm4(a, sm + a_tile + chunk_at<C>(ar, 2 * kk + ac));
 #pragma unroll
           for (int n2 = 0; n2 < kRows / 16; ++n2) {
             if (n2 >= nb) break;
             uint32_t r[4];
-            ldsm4(r, sm + b_tile + chunk_at<C>(n2 * 16 + br, 2 * kk + bc));
-            mma(acc[2 * n2], a, r[0], r[1]);
-            mma(acc[2 * n2 + 1], a, r[2], r[3]);
+            ptx::ldsm4(r, sm + b_tile + chunk_at<C>(n2 * 16 + br, 2 * kk + bc));
+            ptx::mma16816(acc[2 * n2], a, r[0], r[1]);
+            ptx::mma16816(acc[2 * n2 + 1], a, r[2], r[3]);
           }
         }
       };
@@ -230,12 +199,12 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
         for (int kk = 0; kk < kRows / 16; ++kk) {
           if (kk >= nb) break;
           uint32_t r[4];
-          ldsm4t(r, sm + L::K + chunk_at<D>(kk * 16 + (lane & 15), 2 * cc + (lane >> 4)));
+          ptx::ldsm4t(r, sm + L::K + chunk_at<D>(kk * 16 + (lane & 15), 2 * cc + (lane >> 4)));
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             const uint32_t a[4] = {dsa[part][2 * kk][0], dsa[part][2 * kk][1], dsa[part][2 * kk + 1][0], dsa[part][2 * kk + 1][1]};
-            mma(acc[0], a, r[0], r[1]);
-            mma(acc[1], a, r[2], r[3]);
+            ptx::mma16816(acc[0], a, r[0], r[1]);
+            ptx::mma16816(acc[1], a, r[2], r[3]);
           }
         }
 #pragma unroll
@@ -257,16 +226,16 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
         for (int kk = 0; kk < kRows / 16; ++kk) {
           if (kk >= nb) break;
           uint32_t a[2][4];
-          ldsm4t(a[0], sm + a_parts + chunk_at<kRows>(kk * 16 + tr, tc));
-          ldsm4t(a[1], sm + a_parts + L::PART + chunk_at<kRows>(kk * 16 + tr, tc));
+          ptx::ldsm4t(a[0], sm + a_parts + chunk_at<kRows>(kk * 16 + tr, tc));
+          ptx::ldsm4t(a[1], sm + a_parts + L::PART + chunk_at<kRows>(kk * 16 + tr, tc));
 #pragma unroll
           for (int cc = 0; cc < C / 16; ++cc) {
             uint32_t r[4];
-            ldsm4t(r, sm + b_tile + chunk_at<C>(kk * 16 + (lane & 15), 2 * cc + (lane >> 4)));
+            ptx::ldsm4t(r, sm + b_tile + chunk_at<C>(kk * 16 + (lane & 15), 2 * cc + (lane >> 4)));
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-              mma(acc[2 * cc], a[part], r[0], r[1]);
-              mma(acc[2 * cc + 1], a[part], r[2], r[3]);
+              ptx::mma16816(acc[2 * cc], a[part], r[0], r[1]);
+              ptx::mma16816(acc[2 * cc + 1], a[part], r[2], r[3]);
             }
           }
         }
