@@ -3,8 +3,8 @@
 //
 //   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin            (fp32)
 //   bf16: y rounded once
-//   e2m1: u = y / cache scale;  s = e4m3(max|u| over 16 channels / 6);
-//         code = e2m1(u / s)
+//   e2m1: u = y (1 / cache scale);  s = e4m3(max|u| over 16 channels (1/6));
+//         code = e2m1(u / s)                    (each step rounded once)
 //
 // The kernel moves bytes: every row is read and written once and a channel
 // costs a few operations.  One warp takes one token (its place in the cache
@@ -22,7 +22,9 @@
 // (6.1 TB/s).  Bound by memory in bf16; in 4 bits by loads that wait (half of
 // the warps' time) with the conversion's instructions in 57 % of the issue
 // slots: 80 registers for six blocks an SM were 54 -> 51 us, eight or two row
-// groups in flight instead of four slower.
+// groups in flight instead of four slower.  With that cap the 4-bit kernels spill
+// (half-split rotation 56 to 60 bytes, reloaded 164 to 176; in pairs 20 and 36; none
+// 4), which the residency outweighs.
 //
 // A product and a sum are rounded separately (no fused multiply-add), so that
 // a value next to a rounding border of the 4-bit code falls to the side that

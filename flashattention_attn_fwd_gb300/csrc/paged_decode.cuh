@@ -8,9 +8,12 @@
 // bytes in 4 bits, 4 d in bf16, against 4 d M operations.
 //
 // Work split.  With at most a few thousand keys to read per key/value head (a
-// short cache, or a window), a cluster of CTAs takes each (sequence, head) unit,
+// narrow table, or a window), a cluster of CTAs takes each (sequence, head) unit,
 // cuts its tiles evenly and joins the results through distributed shared memory:
-// one launch and no workspace traffic, 6 us against 10 at the smallest sizes.
+// one launch and no workspace traffic.  The choice is the host's, which knows the
+// table's width and not the lengths; a table wider than its sequences costs 0.8 us
+// at one sequence of 701 tokens (6.1 against 6.9), 2 at 16 (8.1, 9.8) and 4 at 64
+// (12.6, 16.7), 8 heads of 64 in 4 bits.
 // Beyond that lengths matter more: the tiles that some row sees, over all
 // (sequence, key/value head) units, form one line that is cut into equal pieces,
 // one per resident CTA: lengths may differ as they like and every CTA reads the
@@ -26,10 +29,13 @@
 // its own (one barrier per tile), so that a few stages per group, well above
 // the SM's share of bandwidth times latency, are always on the way.  Both
 // products are warp-level m16n8k16 tiles with the keys' side as the 16-row
-// operand, so that 8 query rows fill the tile:
+// operand, so that 8 query rows fill a tile:
 //   S^T (16 keys x 8 rows)      = K (16 keys x 16 channels) Q^T
 //   O^T (16 channels x 8 rows) += V^T (16 channels x 16 keys) P^T
-// (tcgen05's 64/128-row tiles would be mostly padding.)  The order of the
+// (tcgen05 could take the same turn, 128 keys or the channels on its M side, 8 to
+// 64 rows on N, O in TMEM.  That is not built: up to 8 rows these tiles read a bf16
+// cache at 0.76 to 1.0 of the copy rate; 16 to 64 rows pay for O in registers, up to
+// 255 a thread and two CTAs an SM.)  The order of the
 // channels inside S's contraction, of the channels among O's rows and of the
 // keys inside a tile is free, and is chosen so that a lane's fragments are
 // contiguous bytes of the cache: lane (g, t) = (lane / 4, lane % 4) takes a
@@ -41,13 +47,18 @@
 // 4-bit values times their block scale have at most six significant bits and
 // are exact in fp16; the products run in fp16 with fp32 sums.  The query row
 // is scaled to fp16's range by a power of two (undone in the score), P carries a
-// factor 2^7 so that weights down to 2^-31 of the largest survive in fp16.
+// factor 2^7 so that weights down to 2^-31 of the largest survive in fp16.  Over a
+// bf16 cache P is rounded to bf16, because a product's operands have one type and
+// V's exponents need bf16's: at most 2^-8 of a weight, as in the forward (2.3e-3
+// of the output in all; 1.7e-3, its own rounding, over a 4-bit cache).
 //
 // Measured (4 bits unless said; a copy reads and writes 6.8 TB/s): one sequence
-// of 701 tokens 5.9 us; 16 of 2048 to 8192, 8 heads of 64: 21 us; 12 of 9001 to
+// of 701 tokens 6.1 us; 16 of 2048 to 8192, 8 heads of 64: 21 us; 12 of 9001 to
 // 32768, 8 heads of 128: 57 us, 4.7 TB/s; 8 of 1500 to 16001 with four new
 // tokens, 4 heads of 128 in bf16: 31 us, 3.1 TB/s; a window of 1024 with 4 sinks,
-// 32 sequences: 11 us.  Fixed: 1.3 us for the plan, 2 to the first tile, 4 for the
+// 32 sequences: 11 us.  One new token over bf16, 8 heads: 16 of 2048 to 8192 31 us
+// at d 64 and 53 at d 128 (5.1 and 6.0 TB/s), 12 of 9001 to 32768 at d 128 141 us,
+// which is the copy rate.  Fixed: 1.3 us for the plan, 2 to the first tile, 4 for the
 // merge and its launch.  In between the longest case runs at the issue rate of
 // three CTAs an SM (0.56 of the slots; waits on fixed latencies and the ALU pipe
 // lead), the short ones at the latency of a few tiles per warp.
@@ -82,7 +93,12 @@ constexpr int kSteps = FMT == KV_BF16 && D == 128 ? 1 : 2;
 
 // Starting a unit (queries, pages, the first copies, the join at its end) costs
 // a CTA about as long as this many tiles; the line counts them before each
-// unit's own, so that a CTA that starts a second unit gets fewer tiles.
+// unit's own, so that a CTA that starts a second unit gets fewer tiles.  A balance
+// found by measuring 0, 8, 16, 28 and 48: in 4 bits 23.0, 21.6, 21.0, 22.2, 23.5 us
+// (16 sequences, d 64), 58.9, 58.1, 56.4, 57.7, 59.2 (12 long ones, d 128) and 37.4,
+// 34.5, 33.8, 36.6, 40.9 (64 of 500 to 4096, d 64); 64 rows of d 128 44.5, 45.1, 45.3,
+// 44.9, 50.0.  Over bf16, whose tiles take as long as their bytes, anything from 8
+// to 28 is within 1 % (d 64 and 128, one token and four), and 0 is 1 to 9 % worse.
 template <int FMT, int D>
 constexpr int kLead = FMT == KV_BF16 ? 28 : 16;
 

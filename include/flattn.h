@@ -339,9 +339,12 @@ FL_API fl_status fl_kv_append(const void* k, const void* v, const fl_kv_cache* c
  *                 calls that may overlap need one each
  * desc: B, Hq, Hkv, Lq, d == dv (the cache's Hkv and d), Lk = max_pages *
  * page_size, (Hq / Hkv) * Lq <= 64, any score_mod, k_strides and v_strides
- * zero.  A visible key whose page is outside the pool is left out and the
- * call reports FL_ERR_DEVICE_BOUNDS through fl_sync_status.  Rows that see no
- * key get out = 0 and lse = -inf.  Results do not depend on where pages lie.
+ * zero.  How the work is split follows these sizes and the window, not kv_len: a
+ * table much wider than its sequences may take two launches where a narrow one
+ * takes one (results then differ by rounding).  A visible key whose page is
+ * outside the pool is left out and the call reports FL_ERR_DEVICE_BOUNDS
+ * through fl_sync_status.  Rows that see no key get out = 0 and lse = -inf.
+ * Results do not depend on where pages lie.
  * Keys and values that no row of the call sees may hold anything; a value that
  * is not finite and that one row sees reaches every row of its key/value head
  * in that sequence (0 times it is a NaN).
