@@ -41,7 +41,7 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
 
 def _like(stream, t: torch.Tensor) -> torch.Tensor:
     """A tensor like the contiguous t, as ``_empty_on``."""
-    return _empty_on(stream, t.shape, t.dtype, t.device)
+    return torch.empty_like(t) if stream is None else _empty_on(stream, t.shape, t.dtype, t.device)
 
 
 def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):

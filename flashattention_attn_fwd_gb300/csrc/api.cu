@@ -78,6 +78,7 @@ fl_status device_state(DeviceState** out) {
   // tensor-map encoder is a driver call)
   const cudaError_t sd = cudaSetDevice(dev);
   if (sd != cudaSuccess) return cuda_fail("cudaSetDevice", sd);
+  fl::t_device = dev;
   std::lock_guard<std::mutex> lock(g_mutex);
   DeviceState& d = g_dev[dev];
   if (d.status == nullptr) {
@@ -270,6 +271,8 @@ void plan_key_split(const fl_attn_desc& d, int sm_count, KParams* p) {
 }  // namespace
 
 namespace fl {
+
+thread_local int t_device = 0;
 
 fl_status attn_fwd_check(const void* q, const void* k, const void* v, void* out, float* lse,
                          const fl_attn_desc* desc) {

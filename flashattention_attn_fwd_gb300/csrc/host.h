@@ -28,15 +28,15 @@ fl_status device_info(int* sm_count, uint32_t** status);
 // FL_OK, or FL_ERR_CUDA with `where` and CUDA's message as the error detail.
 fl_status launch_result(const char* where, cudaError_t e);
 
-// `step` once on the current device (a kernel's attributes and occupancy belong to
-// the device): its error until it succeeds there, then cudaSuccess.
+// The device of the call that this thread is in: below kMaxDevices, set by every
+// entry point before it launches (device_info, or the allocation-free call's set-up).
+extern thread_local int t_device;
+
+// `step` once on that device (a kernel's attributes and occupancy belong to the
+// device): its error until it succeeds there, then cudaSuccess.
 template <class Step>
 cudaError_t on_this_device(OncePerDevice& once, Step&& step) {
-  int dev = 0;
-  const cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  return once.run(dev, step);
+  return once.run(t_device, step);
 }
 
 // Launches `kernel` behind the previous kernel of the stream, whose end it waits

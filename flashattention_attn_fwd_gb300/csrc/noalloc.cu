@@ -49,6 +49,7 @@ fl_status na_setup(NoAllocDevice** out) {
   // the device's primary context current on this thread (the tensor-map
   // encoder is a driver call)
   if ((e = cudaSetDevice(dev)) != cudaSuccess) return fl::launch_result("cudaSetDevice", e);
+  fl::t_device = dev;
   std::lock_guard<std::mutex> lock(g_na_mutex);
   NoAllocDevice& d = g_na_dev[dev];
   if (!d.ready) {

@@ -1023,9 +1023,8 @@ template <int FMT, int D, int NT, int RW, bool CL>
 int resident() {
   static OncePerDevice once;
   static int found[kMaxDevices];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return -1;
-  const cudaError_t e = once.run(dev, [dev] {
+  const int dev = t_device;
+  const cudaError_t e = on_this_device(once, [dev] {
     constexpr int smem = decode_smem<FMT, D, NT, RW, CL>();
     auto* kernel = paged_decode_kernel<FMT, D, NT, RW, CL>;
     const cudaError_t r = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

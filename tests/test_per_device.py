@@ -66,5 +66,5 @@ def test_kernel_attributes_are_set_on_the_device_of_the_call():
         with open(os.path.join(CSRC, name)) as f:
             text = re.sub(r"//[^\n]*", "", f.read())
         uses = len(re.findall(r"\bcudaFuncSetAttribute\s*\(", text))
-        assert uses == 0 or len(re.findall(r"\bon_this_device\s*\(|\bonce\.run\s*\(dev,", text)) >= uses, name
+        assert uses == 0 or len(re.findall(r"\bon_this_device\s*\(", text)) >= uses, name
         assert not re.search(r"static const (cudaError_t|int) \w+ = (\[|cuda)", text), name
