@@ -676,7 +676,7 @@ fl_status fl_attn_decode_fwd(const void* q, const void* k_cache, const void* v_c
     p.lpart = p.opart + static_cast<int64_t>(p.n_split) * p.rows * d.d;
   }
   p.scale = d.scale > 0.f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.d));
-  p.softcap = d.softcap;
+  p.softcap = std::fmin(d.softcap, 1e38f);  // finite in log2 units too
   p.score_mod = d.score_mod;
   p.causal = d.mask_kind == FL_MASK_CAUSAL;
   p.status = ds->status;

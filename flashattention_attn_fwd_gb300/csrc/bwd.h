@@ -7,6 +7,10 @@
 
 #include <cstdint>
 
+#ifdef __CUDACC__
+#include "ptx.cuh"
+#endif
+
 namespace fl {
 
 struct BwdParams {
@@ -107,6 +111,40 @@ template <int C>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   const int x = C >= 64 ? r & 7 : (r >> 1) & 3;
   return static_cast<uint32_t>(r * C * 2 + ((c ^ x) << 4));
+}
+
+// Softcap's t = cap log2(e) tanh(s scale / cap) of N by 4 raw scores of every lane,
+// in place, and 1 - tanh^2: the forward's polynomial where all of the warp's scores are
+// in its range, else 1 - 2 d with d = 1 / (1 + e^(2 s scale / cap)), whose error is
+// one of cap and not of t (with a cap far above the scores it would be all of t).
+template <int N, bool SECH>
+__device__ __forceinline__ void softcap_log2(const BwdParams& p, float (&s)[N][4], float (&sech2)[SECH ? N : 1][4]) {
+  const float kcap = p.softcap * 1.4426950408889634f;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) top = fmaxf(top, fabsf(s[i / 4][i % 4]));
+  if (__all_sync(0xffffffffu, top <= p.sc_smax)) {
+    const float ikcap = 1.0f / kcap;
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) {
+      float& x = s[i / 4][i % 4];
+      const float z = x * x;
+      x *= fmaf(fmaf(fmaf(p.sc_q[3], z, p.sc_q[2]), z, p.sc_q[1]), z, p.sc_q[0]);
+      if (SECH) {
+        const float th = x * ikcap;
+        sech2[SECH ? i / 4 : 0][i % 4] = fmaf(-th, th, 1.0f);
+      }
+    }
+  } else {
+    const float zmul = 2.0f * p.scale * 1.4426950408889634f / p.softcap;
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) {
+      float& x = s[i / 4][i % 4];
+      const float d = ptx::rcp(1.0f + ptx::ex2(x * zmul));
+      x = fmaf(-2.0f * kcap, d, kcap);
+      if (SECH) sech2[SECH ? i / 4 : 0][i % 4] = 4.0f * d * (1.0f - d);
+    }
+  }
 }
 #endif
 

@@ -112,14 +112,13 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
     l2[e] = l == -CUDART_INF_F ? CUDART_INF_F : l * kDotLog2e;
   }
   const float sc = p.scale * kDotLog2e;
-  const float kcap = p.softcap * kDotLog2e, zmul = SCORE == 2 ? 2.0f * sc / p.softcap : 0.f;
   if (SCORE == 1) slope2 = __ldg(p.slopes + h) * kDotLog2e;
 
   // P = 2^(t log2 e - L2) of a raw score x, key j, row[w]
   float sum[2] = {0.f, 0.f};
   auto weight = [&](float x, int j, int w) {
     if (SCORE == 1) return ptx::ex2(fmaf(x, sc, fmaf(slope2, static_cast<float>(j - row[w]), -l2[w])));
-    if (SCORE == 2) return ptx::ex2(fmaf(-2.0f * kcap, ptx::rcp(1.0f + ptx::ex2(x * zmul)), kcap - l2[w]));
+    if (SCORE == 2) return ptx::ex2(x - l2[w]);  // x is t already
     return ptx::ex2(fmaf(x, sc, -l2[w]));
   };
   for (int i = 0; i < n_tiles; ++i) {
@@ -155,7 +154,7 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
       if (jb > hi_max || jb + 15 < lo_min) continue;
       // 16 keys: matrices (keys 0-7 | 8-15) x (channels 0-7 | 8-15) of a k-step
       const int lr = n2 * 16 + ((lane >> 4) << 3) + (lane & 7), lc = (lane >> 3) & 1;
-      float s[2][4] = {}, dp[2][4] = {};
+      float s[2][4] = {}, dp[2][4] = {}, none[1][4];
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         uint32_t r[4];
@@ -170,6 +169,7 @@ __global__ void __launch_bounds__(kDotThreads) attn_bwd_dot_kernel(const __grid_
         ptx::mma16816(dp[0], da[kk], r[0], r[1]);
         ptx::mma16816(dp[1], da[kk], r[2], r[3]);
       }
+      if constexpr (SCORE == 2) softcap_log2<2, false>(p, s, none);
       if (jb >= lo_max && jb + 15 <= hi_min) {  // all of the warp's rows see all of it
 #pragma unroll
         for (int n = 0; n < 2; ++n)

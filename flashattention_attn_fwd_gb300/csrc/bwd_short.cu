@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
   load(std::integral_constant<int, D>{}, L::K, p.k, krow0);
   load(std::integral_constant<int, DV>{}, L::V, p.v, krow0);
   const float sc = p.scale * kShortLog2e;
-  const float kcap = p.softcap * kShortLog2e, zmul = SCORE == 2 ? 2.0f * sc / p.softcap : 0.f;
 
   float dk[D / 8][4], dv[DV / 8][4];        // of this warp's 16 keys
 #pragma unroll
@@ -140,6 +139,7 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
       // ---- P, D and dS (row 0 sees one key: its softmax has no gradient)
       float dsum[2] = {0.f, 0.f};
       float sech[SCORE == 2 ? kRows / 8 : 1][4];
+      if constexpr (SCORE == 2) softcap_log2<kRows / 8, true>(p, s, sech);
 #pragma unroll
       for (int c = 0; c < kRows / 8; ++c)
 #pragma unroll
@@ -148,9 +148,7 @@ __global__ void __launch_bounds__(kShortThreads) attn_bwd_short_kernel(const __g
           const bool sees = i < n && j <= i && (j > i - p.window || j < p.sink);
           float t;
           if constexpr (SCORE == 2) {
-            const float d = ptx::rcp(1.0f + ptx::ex2(s[c][e] * zmul));
-            sech[c][e] = 4.0f * d * (1.0f - d);
-            t = fmaf(-2.0f * kcap, d, kcap - l2[w]);
+            t = s[c][e] - l2[w];  // capped already
           } else if constexpr (SCORE == 1) {
             t = fmaf(s[c][e], sc, fmaf(slope2, static_cast<float>(j - i), -l2[w]));
           } else {

@@ -235,7 +235,7 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   p.cap = d.Lk;
   const float scale = d.scale > 0.f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.d));
   p.scale_log2 = scale * static_cast<float>(kLog2e) * cache->k_scale;
-  p.softcap = d.softcap * static_cast<float>(kLog2e);
+  p.softcap = std::fmin(d.softcap, 1e38f) * static_cast<float>(kLog2e);  // finite in log2 units too
   p.score_mod = d.score_mod;
   p.causal = d.mask_kind != FL_MASK_NONE;
   if (d.mask_kind == FL_MASK_SLIDING_WINDOW) {
