@@ -31,8 +31,8 @@
 // overwrites the first 64 columns of S and O0, O1 start at column 256.
 //
 // Each slot walks only the key tiles its own rows can see (per-slot ranges,
-// DV <= 64); the load warp fetches the union and releases a stage on behalf
-// of a slot that skips it.
+// DV <= 64); the load warp fetches the union, and a slot passes the tiles
+// that only the other walks: it waits for each and releases it at once.
 //
 // The online softmax keeps (m, l) per row in the log2 domain.  The
 // reference max m is only raised when a new tile's max exceeds it by more
@@ -127,7 +127,7 @@ struct EmuPairs {
 #endif
 constexpr uint64_t kTurnWaitNs = 1500;
 
-template <int D, int DV, int KIND, int SCORE = SCORE_NONE>
+template <int D, int DV, int KIND, int SCORE = SCORE_NONE, bool SINK = false>
 struct Layout {
   static_assert(D == 32 || D == 64 || D == 128, "head dim");
   static_assert(DV == 32 || DV == 64 || DV == 128, "value head dim");
@@ -170,7 +170,10 @@ struct Layout {
   // that still leaves room for two stages.
   static constexpr int QBUF = (4 * Q_BYTES + 2 * STAGE_BYTES <= BUDGET) ? 2 : 1;
   static constexpr int STAGES_FIT = (BUDGET - 2 * QBUF * Q_BYTES) / STAGE_BYTES;
-  static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
+  static constexpr int STAGES_MAX = STAGES_FIT > 8 ? 8 : STAGES_FIT;
+  // key-split units: an even ring (see the MMA thread; at d 64 four stages instead
+  // of five: causal 60.4 -> 58.8 us, unmasked 75.5 -> 76.9, B 4, H 16, L 2048)
+  static constexpr int STAGES = KIND == KIND_ATTN && !SINK && key_split_ok(D, DV) ? STAGES_MAX & ~1 : STAGES_MAX;
   static_assert(STAGES >= 2, "ring too small");
   static constexpr int OFF_Q = 0;                        // Q[buffer][slot]
   static constexpr int OFF_K = 2 * QBUF * Q_BYTES;       // K[stage][NK]
@@ -304,13 +307,6 @@ __host__ __device__ __forceinline__ int ring_tile(const Unit& U, int i) {
 __host__ __device__ __forceinline__ int ring_tile(const SinkUnit& U, int i) {
   const int n = U.kv_hi - U.kv_lo + 1;
   return i < n ? ring_tile(static_cast<const Unit&>(U), i) : U.nsink - 1 - (i - n);
-}
-// Does slot s walk tile t, the one at ring position i?
-__host__ __device__ __forceinline__ bool ring_used(const Unit& U, int i, int t, int s) {
-  return U.ks ? s == (i & 1) : t >= U.lo[s] && t <= U.hi[s];
-}
-__host__ __device__ __forceinline__ bool ring_used(const SinkUnit& U, int i, int t, int s) {
-  return i > U.kv_hi - U.kv_lo ? U.sk[s] > 0 : ring_used(static_cast<const Unit&>(U), i, t, s);
 }
 
 // Unit u.  skip_ok (sinks): a slot may skip a tile that only the other walks.
@@ -575,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmO,
                           const __grid_constant__ CUtensorMap tmPB, const __grid_constant__ CUtensorMap tmMB,
                           const __grid_constant__ KParams p) {
-  using L = Layout<D, DV, KIND, SCORE>;
+  using L = Layout<D, DV, KIND, SCORE, SINK>;
   constexpr int S = L::STAGES;
   constexpr bool kEvo = KIND == KIND_EVO || KIND == KIND_EVO_COL;
   // TMEM columns: S0 [0,128) S1 [128,256); with DV <= 64 a separate P region
@@ -647,7 +643,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&drain[i], 1);
     }
     ptx::mbar_init(xch_full, kSoftmaxWarps);
-    ptx::mbar_init(stagger, kSoftmaxWarps / 2);
+    // Document masks: slot 0's first tile may lie behind tiles of slot 1 that the
+    // ring has to be rid of first, so slot 1 does not wait for it.  (The phase
+    // that it waits for is over from the start, and slot 0's warps, one phase
+    // each, leave the parity as it is.)
+    const bool apart = p.mask_kind == MASK_DOC && p.slot_mode == SLOT_ROWS;
+    static_assert(kSoftmaxWarps / 2 % 2 == 0, "an even number of phases");
+    ptx::mbar_init(stagger, apart ? 1 : kSoftmaxWarps / 2);
+    if (apart) ptx::mbar_arrive(stagger);
     ptx::mbar_init(&o_staged[0], kSoftmaxWarps / 2);
     ptx::mbar_init(&o_staged[1], kSoftmaxWarps / 2);
     for (int i = 0; i < 8; ++i) {
@@ -791,10 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tma_load_2d(smem + L::OFF_MB + st * L::MB_BYTES + s * kBlockN * 4, &tmMB, &kv_full[st],
                                t * kBlockN, U.mbrow[s], pol_reuse);
           }
-          // release the stage on behalf of a slot that does not use this tile
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (!ring_used(U, i, t, s)) ptx::mbar_arrive(&kv_empty[st]);
+          if (U.ks) ptx::mbar_arrive(&kv_empty[st]);  // on behalf of the slot whose tile it is not
           kv_count = it + 1;
         }
         if (!ok) break;
@@ -871,6 +871,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // as P is in TMEM (p_full).  The first S of the next unit is issued
       // during the last tile of the current one (two Q buffers) when the
       // ring distance allows it.
+      // A wait tells only the parity of a stage's phase, so a slot has to see
+      // every phase of every stage: it passes the tiles that only the other
+      // slot walks.  (Released for it, a stage could be two phases behind the
+      // one that it waits for, or past it.)  In a key-split unit, the last of
+      // a block, the slots' tiles alternate: with an even ring the tile before
+      // one's own in its stage is one's own too, and nothing need be passed.
       const int s = warp - 1;
       constexpr bool kCross = L::QBUF == 2;
       uint32_t it = 0, uc = 0, pc = 0;
@@ -879,8 +885,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto first_idx = [&](const Unit& V, uint32_t base) -> uint32_t {
         return base + static_cast<uint32_t>(ring_first(V, s));
       };
-      auto first_s = [&](uint32_t ucn, uint32_t idx) -> bool {
-        if (!wait_bar(&kv_full[idx % S], (idx / S) & 1u, ctl, 11)) return false;
+      auto pass = [&](uint32_t i, uint32_t to) -> bool {
+#pragma unroll 1
+        for (; i != to; ++i) {
+          if (!wait_bar(&kv_full[i % S], (i / S) & 1u, ctl, 17)) return false;
+          ptx::mbar_arrive(&kv_empty[i % S]);
+        }
+        return true;
+      };
+      auto first_s = [&](uint32_t ucn, uint32_t from, uint32_t idx) -> bool {
+        if (!pass(from, idx) || !wait_bar(&kv_full[idx % S], (idx / S) & 1u, ctl, 11)) return false;
         return issue_s(s, ucn % L::QBUF, static_cast<int>(idx % S));
       };
       bool s_issued = false;  // first S of the current unit already issued
@@ -892,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nw = ns - slot_sinks(Us, s);             // window tiles, then sinks
         const uint32_t gap = SINK ? static_cast<uint32_t>(Us.lo[s] - Us.kv_lo) : 0u;
         const uint32_t idx0 = first_idx(Us, it);
-        if (!s_issued && !first_s(uc, idx0)) { ok = false; break; }
+        if (!s_issued && !first_s(uc, Us.ks ? idx0 : it, idx0)) { ok = false; break; }
         s_issued = false;
         const uint32_t qb = uc % L::QBUF;
         const int un = u + sch.step;
@@ -903,6 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = static_cast<int>(idx % S);
           FL_TR(s, idx, 0);
           if (k + 1 < ns) {
+            if (SINK && idn != idx + 1 && !pass(idx + 1, idn)) { ok = false; break; }
             if (!wait_bar(&kv_full[idn % S], (idn / S) & 1u, ctl, 15)) { ok = false; break; }
             if (!issue_s(s, qb, static_cast<int>(idn % S))) { ok = false; break; }
           }
@@ -923,16 +938,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ptx::mma_commit(&pv_done[s]);
           ptx::mma_commit(&kv_empty[st]);
-          if (k + 1 == ns && kCross && un < sch.end) {
-            // next unit's first own tile, if its ring index is less than S
-            // ahead of this one (issued after the last P V, which the next
-            // unit's epilogue waits for)
-            if (!wait_q(uc + 1, s)) { ok = false; break; }
-            const uint32_t idxn = first_idx(unit_at(uc + 1), it + n);
-            if (idxn - idx < static_cast<uint32_t>(S)) {
-              if (!first_s(uc + 1, idxn)) { ok = false; break; }
-              s_issued = true;
-            }
+        }
+        const uint32_t idx = idx0 + (ns - 1) * stride + (SINK && ns > nw ? gap : 0u);  // the last own tile
+        if (!ok || (!Us.ks && !pass(idx + 1, it + n))) { ok = false; break; }
+        if (kCross && un < sch.end) {
+          // next unit's first own tile, if its ring index is less than S
+          // ahead of this one (issued after the last P V, which the next
+          // unit's epilogue waits for)
+          if (!wait_q(uc + 1, s)) { ok = false; break; }
+          const uint32_t idxn = first_idx(unit_at(uc + 1), it + n);
+          if (idxn - idx < static_cast<uint32_t>(S)) {
+            if (!first_s(uc + 1, unit_at(uc + 1).ks ? idxn : it + n, idxn)) { ok = false; break; }
+            s_issued = true;
           }
         }
         it += n;
