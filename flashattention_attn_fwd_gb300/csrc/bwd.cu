@@ -17,7 +17,7 @@
 // its walk takes over one that has not started (cluster launch control), so
 // that the next walk's loads and first products run under the last one's end:
 // B 4, H 16, L 2048, d 64: causal 173 -> 158 us, window of 256 104 -> 90, with
-// 4 sinks 126 -> 107.  All five
+// 4 sinks 126 -> 107 when that came; 152, 84 and 103 now.  All five
 // products run on tcgen05 with accumulators in TMEM:
 //   S^T  = K Q^T   (A = K, B = Q smem)              TMEM [0,128)
 //   P^T  (bf16, written by the compute warps)        over S^T: [0,32), [64,96)

@@ -241,8 +241,8 @@ __host__ __device__ __forceinline__ int32_t load_offset(const int32_t* x) {
 // Visible keys of query row i form one interval [lo, hi] for every mask kind
 // (with sinks, the window's; the row's sinks left of it, [0, min(sink, lo)),
 // are walked as tiles of their own, so that a tile keeps one interval per row:
-// B 4, H 16, L 2048, d 64, window 256: 35 us, with 4 sinks 44, the one tile more
-// of four; B 1, 32 heads over 8, L 16384, d 128, window 1024: 300 and 321.)
+// B 4, H 16, L 2048, d 64, window 256: 36 us, with 4 sinks 41, one tile more
+// beside three; B 1, 32 heads over 8, L 16384, d 128, window 1024: 298 and 320.)
 __host__ __device__ __forceinline__ void row_bounds(const KParams& p, int b, int i, int& lo, int& hi) {
   switch (p.mask_kind) {
     case MASK_NONE: lo = 0; hi = p.Lk - 1; break;
