@@ -112,7 +112,8 @@ typedef struct fl_attn_desc {
   void* stream;             /* cudaStream_t                                    */
   uint32_t debug_flags;     /* FL_DEBUG_*; 0 in normal use                     */
   int32_t debug_arg;
-  uint32_t wait_limit_ms;   /* device wait limit; 0 = default (2000 ms)        */
+  uint32_t wait_limit_ms;   /* limit of a device wait for one pipeline step;
+                               0 = default (2000 ms)                           */
   int32_t sink;             /* SLIDING_WINDOW: the first `sink` keys stay
                                visible to every later query; 0: none           */
   int32_t reserved[6];
@@ -303,12 +304,12 @@ typedef struct fl_kv_append_desc {
  * for each pair (x1, x2), cos and sin from row `position` of the tables; the
  * rest passes through.  A bf16 cache takes y rounded once.  An e2m1 cache
  * takes, per 16 channels of u = y * (1 / k_scale): block scale s = e4m3(max|u|
- * * (1/6)), codes e2m1(u / s), all rounded to nearest even and saturating; a
- * block whose scale rounds to 0 is stored as zeros; what a block with a NaN in
- * it holds is not specified (other blocks are not touched by it).  Values are
- * stored the same way without rotation.  k_out and v_out receive the stored values (for
- * the new tokens' own attention); q_out may be q, k_out k and v_out v (same
- * strides) to work in place.
+ * * (1/6)), codes e2m1(u / s), all rounded to nearest even and saturating (a
+ * zero keeps its sign); a block whose scale rounds to 0 is stored as zeros; what
+ * a block with a NaN in it holds is not specified (other blocks are not touched
+ * by it).  Values are stored the same way without rotation.  k_out and v_out
+ * receive the stored values (for the new tokens' own attention); q_out may be
+ * q, k_out k and v_out v (same strides) to work in place.
  * Left as they are: rows from seq_offsets[B] on, and rows whose position is
  * negative (kv_len[b] < n_b: a sequence that takes no part).  A row whose
  * position has no rotation, no block_table column or a page outside the pool
