@@ -160,7 +160,7 @@ def make_calls(api, bufs, slopes):
 # Each kernel family is built from every source file except the ones only
 # another family uses, so a change to (say) the backward leaves the forward
 # kernels' counters valid.
-PAGED_SOURCES = ("paged", "kv_append.", "cvt4.")
+PAGED_SOURCES = ("paged", "kv_append.", "cvt4.", "rope")
 KERNEL_FAMILY_EXCLUDES = {"forward": ("bwd.", "bwd_dot.", "bwd_short.", "decode.", *PAGED_SOURCES),
                           "backward": ("decode.", *PAGED_SOURCES),
                           "decode": ("bwd.", "bwd_dot.", "bwd_short.", *PAGED_SOURCES)}

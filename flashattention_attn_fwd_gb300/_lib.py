@@ -51,9 +51,19 @@ EXPORTS = (
     "fl_attn_paged_decode_workspace_size",
     "fl_kv_cache_size",
     "fl_kv_append_desc_size",
+    "fl_attn_paged_prefill_fwd",
+    "fl_attn_paged_prefill_workspace_size",
+    "fl_kv_read",
+    "fl_kv_read_desc_size",
+    "fl_rope_fwd",
+    "fl_rope_bwd",
+    "fl_rope_tables",
+    "fl_rope_desc_size",
+    "fl_rope_scaling_size",
 )
 
 KV_FORMATS = {"bf16": 0, "e2m1": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
 class AttnDesc(ctypes.Structure):
@@ -104,10 +114,45 @@ class KvAppendDesc(ctypes.Structure):
     ]
 
 
+class KvReadDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", ctypes.c_int32), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("reserved0", ctypes.c_int32),
+        ("seq_offsets", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+        ("k_out_strides", ctypes.c_int64 * 2), ("v_out_strides", ctypes.c_int64 * 2),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("L", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
+        ("d", ctypes.c_int32), ("rope_positions", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("rope_interleaved", ctypes.c_int32),
+        ("rope_cos", ctypes.c_void_p), ("rope_sin", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("positions_stride", ctypes.c_int64),
+        ("q_strides", ctypes.c_int64 * 3), ("k_strides", ctypes.c_int64 * 3),
+        ("q_out_strides", ctypes.c_int64 * 3), ("k_out_strides", ctypes.c_int64 * 3),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+        ("kind", ctypes.c_int32), ("original", ctypes.c_int32), ("amplitude", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
 # The structures as one packed bytes object (native alignment): a fraction of
 # the time of setting ctypes fields one by one.
 _ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i 6i")
 _APPEND = struct.Struct("@4i 3P q 2P 4i 4P 12q P")
+_READ = struct.Struct("@4i 3P q 4q P")
+_ROPE = struct.Struct("@8i 3P q 12q P")
+_SCALING = struct.Struct("@4d 2i f i")
 _ZERO4 = (0, 0, 0, 0)
 
 
@@ -122,6 +167,9 @@ def _packer(layout: struct.Struct):
 
 APPEND_PACK = _packer(_APPEND)
 ATTN_PACK = _packer(_ATTN)
+READ_PACK = _packer(_READ)
+ROPE_PACK = _packer(_ROPE)
+SCALING_PACK = _packer(_SCALING)
 
 
 def desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, *, scale=0.0, mask_kind=0, doc_causal=0, window=0, prefix=0, score_mod=0,
@@ -202,6 +250,21 @@ def lib() -> ctypes.CDLL:
         L.fl_kv_cache_size.restype = i32
         L.fl_kv_append_desc_size.argtypes = []
         L.fl_kv_append_desc_size.restype = i32
+        L.fl_attn_paged_prefill_fwd.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int64, vp, vp, vp, ctypes.c_size_t, vp]
+        L.fl_attn_paged_prefill_fwd.restype = i32
+        L.fl_attn_paged_prefill_workspace_size.argtypes = [vp, vp]
+        L.fl_attn_paged_prefill_workspace_size.restype = ctypes.c_size_t
+        L.fl_kv_read.argtypes = [vp, vp, vp, vp]
+        L.fl_kv_read.restype = i32
+        L.fl_rope_fwd.argtypes = [vp, vp, vp, vp, vp]
+        L.fl_rope_fwd.restype = i32
+        L.fl_rope_bwd.argtypes = [vp, vp, vp, vp, vp]
+        L.fl_rope_bwd.restype = i32
+        L.fl_rope_tables.argtypes = [vp, vp, i32, i32, vp, vp]
+        L.fl_rope_tables.restype = i32
+        for name in ("fl_kv_read_desc_size", "fl_rope_desc_size", "fl_rope_scaling_size"):
+            getattr(L, name).argtypes = []
+            getattr(L, name).restype = i32
         L.fl_attn_desc_size.argtypes = []
         L.fl_attn_desc_size.restype = i32
         if L.fl_attn_desc_size() != ctypes.sizeof(AttnDesc) or ctypes.sizeof(AttnDesc) != _ATTN.size:
@@ -210,6 +273,11 @@ def lib() -> ctypes.CDLL:
                 L.fl_kv_append_desc_size() != ctypes.sizeof(KvAppendDesc) or \
                 ctypes.sizeof(KvAppendDesc) != _APPEND.size:
             raise RuntimeError("paged cache layout mismatch between flattn.h and the binding")
+        for size, struct_, packed in ((L.fl_kv_read_desc_size(), KvReadDesc, _READ),
+                                      (L.fl_rope_desc_size(), RopeDesc, _ROPE),
+                                      (L.fl_rope_scaling_size(), RopeScaling, _SCALING)):
+            if not size == ctypes.sizeof(struct_) == packed.size:
+                raise RuntimeError(f"{struct_.__name__} layout mismatch between flattn.h and the binding")
         _lib = L
     return _lib
 

@@ -39,6 +39,18 @@ def _empty_on(stream, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _zeros_on(stream, shape, dtype, device) -> torch.Tensor:
+    """As ``_empty_on``, zeroed on that stream."""
+    if stream is None:
+        return torch.zeros(shape, dtype=dtype, device=device)
+    t = _empty_on(stream, shape, dtype, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_ptr(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return t.zero_()
+
+
 def _like(stream, t: torch.Tensor) -> torch.Tensor:
     """A tensor like the contiguous t, as ``_empty_on``."""
     return torch.empty_like(t) if stream is None else _empty_on(stream, t.shape, t.dtype, t.device)

@@ -2,6 +2,7 @@
 // append kernel and the decode kernels (internal header).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstddef>
@@ -107,5 +108,68 @@ inline cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParam
   if (format == KV_BF16) return d == 64 ? launch_paged_bf16_d64(p, s) : launch_paged_bf16_d128(p, s);
   return d == 64 ? launch_paged_e2m1_d64(p, s) : launch_paged_e2m1_d128(p, s);
 }
+
+// ---- attention of chunks of new tokens over the cache (paged_prefill.cuh)
+
+// Query rows of a unit: two slots of 128 rows, a row for every (token, head of
+// the group); a slot holds 128 / G tokens.
+constexpr int kPrefillTile = 128;
+// Head groups (Hq / Hkv) that a slot takes.
+constexpr int kPrefillMaxGroup = 128;
+
+struct PrefillParams {
+  PagedCache c;
+  const void* q;
+  void* out;
+  float* lse;                  // [T, Hq], or null
+  int64_t q_t, q_h, o_t, o_h;  // (token, head) strides, elements
+  const int32_t* seq_offsets;  // [B + 1]; null: one token a sequence
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t table_stride;
+  const float* slopes;
+  int B, T, Hq, G, RT;         // RT = 128 / G tokens a slot
+  int max_pages, cap;          // cap = max_pages * page_size
+  float scale_log2;            // scale * log2(e) * k_scale
+  float softcap;               // in log2 units (cap * log2(e))
+  float cap_arg;               // softcap: 2 y log2(e) of y = score / cap is raw score * cap_arg
+  float sc_q[4], sc_smax;      // softcap's polynomial (as the forward's)
+  int causal, window, sink;    // window 0: none
+  // workspace: for every block how the unit that it starts inside of is cut,
+  // and two partial results for every block
+  int32_t* rec;                // [grid][8]
+  float* opart;                // [grid][2][slot 2][d / 4][128][4], normalised
+  float* lpart;                // [grid][2][slot 2][128], log2
+  int grid;
+  uint32_t* status;
+  uint64_t timeout_ns;
+  int dbg_skip_tile;           // < 0: off
+};
+
+// One launch per format, head dim and score_mod; maps: q, k, v (bf16 cache only).
+#define FL_DECLARE_PREFILL(NAME) \
+  cudaError_t launch_prefill_##NAME(int score_mod, const CUtensorMap* maps, const PrefillParams& p, cudaStream_t s);
+FL_DECLARE_PREFILL(bf16_d64)
+FL_DECLARE_PREFILL(bf16_d128)
+FL_DECLARE_PREFILL(e2m1_d64)
+FL_DECLARE_PREFILL(e2m1_d128)
+#undef FL_DECLARE_PREFILL
+
+// ---- reading the cache back (kv_read.cu)
+
+struct ReadParams {
+  PagedCache c;
+  void* k_out;
+  void* v_out;
+  int64_t ko_t, ko_h, vo_t, vo_h;  // (token, head) strides, elements
+  const int32_t* seq_offsets;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int64_t table_stride;
+  int T, B, max_pages;
+  uint32_t* status;
+};
+
+cudaError_t launch_kv_read(int format, int d, const ReadParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace fl

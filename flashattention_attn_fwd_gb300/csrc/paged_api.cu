@@ -1,9 +1,11 @@
 // C ABI of the paged key/value cache: argument checks, parameters and
 // launches of the append and of the decode attention.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "flattn.h"
 #include "host.h"
@@ -148,6 +150,91 @@ WorkspaceLayout workspace_layout(const fl_attn_desc& d, int M, int grid) {
   return w;
 }
 
+// ---- chunks of new tokens
+
+// tanh(y) ~= y (p0 + p1 y^2 + p2 y^4 + p3 y^6) for |y| <= kTanhRange: the
+// forward's polynomial (csrc/fit_poly.py)
+constexpr double kTanhRange = 0.5;
+constexpr float kTanhP[4] = {0.999999464f, -0.333263218f, 0.13190335f, -0.0444031134f};
+constexpr uint64_t kDefaultWaitNs = 2000ull * 1000ull * 1000ull;
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tokens of a call: positions stay within 32 bits
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// 4-D bf16 map with boxes of 64 channels, box[1] x box[2] x box[3], 128-byte swizzle
+// (strides of dimensions 1 to 3 in elements); reads outside are zeros.
+bool encode_rows(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const int64_t (&strides)[3],
+                 const uint32_t (&rows)[3]) {
+  static EncodeTiled fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(ptr);
+  });
+  if (!fn) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t s[3] = {static_cast<cuuint64_t>(strides[0]) * 2, static_cast<cuuint64_t>(strides[1]) * 2,
+                           static_cast<cuuint64_t>(strides[2]) * 2};
+  const cuuint32_t b[4] = {64u, rows[0], rows[1], rows[2]}, e[4] = {1u, 1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, s, b, e, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+fl_status prefill_desc_check(const fl_kv_cache* cache, const fl_attn_desc* desc) {
+  if (!desc) return FL_ERR_INVALID_ARG;
+  const fl_status cs = cache_check(cache);
+  if (cs != FL_OK) return cs;
+  const fl_attn_desc& d = *desc;
+  if (d.B < 1 || d.Hq < 1 || d.Hkv < 1 || d.Lq < 1 || d.Lk < 1 || d.Hq % d.Hkv != 0) return FL_ERR_INVALID_ARG;
+  if (d.Hkv != cache->Hkv || d.d != cache->d || d.dv != cache->d || d.Lk % cache->page_size) return FL_ERR_INVALID_ARG;
+  if (d.Lk > kMaxTokens || d.Lq > kMaxRows || d.B > kMaxRows) return FL_ERR_UNSUPPORTED;
+  if (d.Hq / d.Hkv > fl::kPrefillMaxGroup) return FL_ERR_UNSUPPORTED;
+  if (!std::isfinite(d.scale)) return FL_ERR_INVALID_ARG;
+  if (d.mask_kind < FL_MASK_NONE || d.mask_kind > FL_MASK_DOCUMENT) return FL_ERR_INVALID_ARG;
+  if (d.mask_kind > FL_MASK_SLIDING_WINDOW) return FL_ERR_UNSUPPORTED;
+  if (d.mask_kind == FL_MASK_SLIDING_WINDOW && d.window < 1) return FL_ERR_INVALID_ARG;
+  if (d.sink < 0 || (d.sink && d.mask_kind != FL_MASK_SLIDING_WINDOW)) return FL_ERR_INVALID_ARG;
+  if (d.score_mod < FL_SCORE_NONE || d.score_mod > FL_SCORE_SOFTCAP) return FL_ERR_INVALID_ARG;
+  if (d.score_mod == FL_SCORE_ALIBI && !d.alibi_slopes) return FL_ERR_INVALID_ARG;
+  if (d.score_mod == FL_SCORE_SOFTCAP && !(d.softcap > 0.f && std::isfinite(d.softcap))) return FL_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (d.k_strides[i] || d.v_strides[i]) return FL_ERR_UNSUPPORTED;
+  return FL_OK;
+}
+
+// (token, head) strides of the packed q or out; all zero: contiguous [T, Hq, d]
+fl_status packed_strides(const int64_t s[4], int64_t H, int64_t d, int64_t* t, int64_t* h) {
+  if (s[0] == 0 && s[1] == 0 && s[2] == 0 && s[3] == 0) {
+    *h = d;
+    *t = H * d;
+    return FL_OK;
+  }
+  if (s[0] != 0 || s[3] != 1 || s[1] < d || s[2] < d) return FL_ERR_INVALID_ARG;
+  *h = s[1];
+  *t = s[2];
+  return (s[1] % 8 || s[2] % 8) ? FL_ERR_ALIGNMENT : FL_OK;
+}
+
+// Workspace: a record for every block, two partial results of 256 rows and
+// their log-sum-exps.
+struct PrefillWorkspace {
+  size_t opart, lpart, bytes;
+};
+PrefillWorkspace prefill_workspace(int d, int grid) {
+  PrefillWorkspace w;
+  const size_t rows = static_cast<size_t>(grid) * 4 * fl::kPrefillTile;
+  w.opart = static_cast<size_t>(grid) * 8 * sizeof(int32_t);
+  w.lpart = w.opart + rows * d * sizeof(float);
+  w.bytes = w.lpart + rows * sizeof(float);
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -184,6 +271,38 @@ fl_status fl_kv_append(const void* k, const void* v, const fl_kv_cache* cache, c
   }
   return fl::launch_result("cache append launch",
                            fl::launch_kv_append(cache->format, cache->d, p, sm_count, static_cast<cudaStream_t>(a.stream)));
+}
+
+int32_t fl_kv_read_desc_size(void) { return static_cast<int32_t>(sizeof(fl_kv_read_desc)); }
+
+fl_status fl_kv_read(const fl_kv_cache* cache, void* k_out, void* v_out, const fl_kv_read_desc* desc) {
+  if (!k_out || !v_out || !desc) return FL_ERR_INVALID_ARG;
+  const fl_status cs = cache_check(cache);
+  if (cs != FL_OK) return cs;
+  const fl_kv_read_desc& a = *desc;
+  if (a.T < 1 || a.B < 1 || a.max_pages < 1 || a.reserved0) return FL_ERR_INVALID_ARG;
+  if (!a.kv_len || !a.block_table || a.table_stride < a.max_pages) return FL_ERR_INVALID_ARG;
+  if (!a.seq_offsets && a.T != a.B) return FL_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(a.max_pages) * cache->page_size > kMaxTokens) return FL_ERR_UNSUPPORTED;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(a.seq_offsets, 4) || !aligned(a.kv_len, 4) ||
+      !aligned(a.block_table, 4))
+    return FL_ERR_ALIGNMENT;
+  fl_status st = rows_check(a.k_out_strides, cache->d);
+  if (st == FL_OK) st = rows_check(a.v_out_strides, cache->d);
+  if (st != FL_OK) return st;
+  fl::ReadParams p{};
+  int sm_count = 0;
+  st = fl::device_info(&sm_count, &p.status);
+  if (st != FL_OK) return st;
+  p.c = cache_params(*cache);
+  p.k_out = k_out; p.v_out = v_out;
+  p.ko_t = a.k_out_strides[0]; p.ko_h = a.k_out_strides[1];
+  p.vo_t = a.v_out_strides[0]; p.vo_h = a.v_out_strides[1];
+  p.seq_offsets = a.seq_offsets; p.kv_len = a.kv_len;
+  p.table = a.block_table; p.table_stride = a.table_stride;
+  p.T = a.T; p.B = a.B; p.max_pages = a.max_pages;
+  return fl::launch_result("cache read launch",
+                           fl::launch_kv_read(cache->format, cache->d, p, sm_count, static_cast<cudaStream_t>(a.stream)));
 }
 
 size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv_cache* cache) {
@@ -257,6 +376,91 @@ fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cache, cons
   p.lpart = reinterpret_cast<float*>(ws + w.lpart);
   return fl::launch_result("paged decode launch", fl::launch_paged_decode(cache->format, cache->d, p,
                                                                          static_cast<cudaStream_t>(d.stream)));
+}
+
+size_t fl_attn_paged_prefill_workspace_size(const fl_attn_desc* desc, const fl_kv_cache* cache) {
+  if (prefill_desc_check(cache, desc) != FL_OK) return 0;
+  int sm_count = 0;
+  uint32_t* status = nullptr;
+  if (fl::device_info(&sm_count, &status) != FL_OK) return 0;
+  return prefill_workspace(desc->d, sm_count).bytes;
+}
+
+fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, const int32_t* seq_offsets,
+                                    const int32_t* kv_len, const int32_t* block_table, int64_t table_stride, void* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, const fl_attn_desc* desc) {
+  if (!q || !out || !kv_len || !block_table) return FL_ERR_INVALID_ARG;
+  const fl_status chk = prefill_desc_check(cache, desc);
+  if (chk != FL_OK) return chk;
+  const fl_attn_desc& d = *desc;
+  if (!seq_offsets && d.Lq != d.B) return FL_ERR_INVALID_ARG;
+  fl::PrefillParams p{};
+  p.max_pages = d.Lk / cache->page_size;
+  if (table_stride < p.max_pages) return FL_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(seq_offsets, 4) || !aligned(kv_len, 4) ||
+      !aligned(block_table, 4) || !aligned(d.alibi_slopes, 4))
+    return FL_ERR_ALIGNMENT;
+  fl_status st = packed_strides(d.q_strides, d.Hq, d.d, &p.q_t, &p.q_h);
+  if (st == FL_OK) st = packed_strides(d.o_strides, d.Hq, d.d, &p.o_t, &p.o_h);
+  if (st != FL_OK) return st;
+  if (!workspace) return FL_ERR_INVALID_ARG;
+  if (!aligned(workspace, 16)) return FL_ERR_ALIGNMENT;
+  int sm_count = 0;
+  st = fl::device_info(&sm_count, &p.status);
+  if (st != FL_OK) return st;
+  p.grid = sm_count;
+  const PrefillWorkspace w = prefill_workspace(d.d, p.grid);
+  if (workspace_bytes < w.bytes) return FL_ERR_INVALID_ARG;
+  p.c = cache_params(*cache);
+  p.q = q; p.out = out; p.lse = lse;
+  p.seq_offsets = seq_offsets; p.kv_len = kv_len;
+  p.table = block_table; p.table_stride = table_stride;
+  p.slopes = d.alibi_slopes;
+  p.B = d.B; p.T = d.Lq; p.Hq = d.Hq; p.G = d.Hq / d.Hkv;
+  p.RT = fl::kPrefillTile / p.G;
+  p.cap = d.Lk;
+  const float scale = (d.scale > 0.f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.d))) * cache->k_scale;
+  p.scale_log2 = scale * static_cast<float>(kLog2e);
+  if (d.score_mod == FL_SCORE_SOFTCAP) {
+    const double cap = std::fmin(d.softcap, 1e38f);  // finite in log2 units too
+    const double y = static_cast<double>(scale) / cap;
+    double power = y * cap * kLog2e;
+    for (int i = 0; i < 4; ++i, power *= y * y) p.sc_q[i] = static_cast<float>(kTanhP[i] * power);
+    p.sc_smax = static_cast<float>(kTanhRange / y);
+    p.softcap = static_cast<float>(cap * kLog2e);
+    p.cap_arg = static_cast<float>(2.0 * kLog2e * y);
+  }
+  p.causal = d.mask_kind != FL_MASK_NONE;
+  if (d.mask_kind == FL_MASK_SLIDING_WINDOW) {
+    p.window = d.window < kMaxTokens ? d.window : static_cast<int>(kMaxTokens);
+    p.sink = d.sink < kMaxTokens ? d.sink : static_cast<int>(kMaxTokens);
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.rec = reinterpret_cast<int32_t*>(ws);
+  p.opart = reinterpret_cast<float*>(ws + w.opart);
+  p.lpart = reinterpret_cast<float*>(ws + w.lpart);
+  p.timeout_ns = d.wait_limit_ms ? static_cast<uint64_t>(d.wait_limit_ms) * 1000ull * 1000ull : kDefaultWaitNs;
+  p.dbg_skip_tile = (d.debug_flags & FL_DEBUG_SKIP_KV_LOAD) ? d.debug_arg : -1;
+  CUtensorMap maps[3] = {};
+  if (cache->format == FL_KV_BF16) {
+    const uint64_t D = d.d, G = p.G, Hkv = d.Hkv, page = cache->page_size;
+    const uint64_t qd[4] = {D, G, Hkv, static_cast<uint64_t>(p.T)};
+    const int64_t qs[3] = {p.q_h, p.q_h * p.G, p.q_t};
+    const uint32_t qb[3] = {static_cast<uint32_t>(G), 1u, static_cast<uint32_t>(p.RT)};
+    const uint64_t kd[4] = {D, page, Hkv, static_cast<uint64_t>(cache->num_pages)};
+    const int64_t ks[3] = {cache->d, static_cast<int64_t>(page) * cache->d, static_cast<int64_t>(Hkv * page) * cache->d};
+    const uint32_t kb[3] = {static_cast<uint32_t>(page < 128 ? page : 128), 1u, 1u};
+    if (!encode_rows(&maps[0], q, qd, qs, qb) || !encode_rows(&maps[1], cache->k, kd, ks, kb) ||
+        !encode_rows(&maps[2], cache->v, kd, ks, kb))
+      return fl::launch_result("paged prefill tensor map", cudaErrorInvalidValue);
+  }
+  const cudaStream_t s = static_cast<cudaStream_t>(d.stream);
+  const bool bf16 = cache->format == FL_KV_BF16;
+  const cudaError_t e = d.d == 64 ? (bf16 ? fl::launch_prefill_bf16_d64(d.score_mod, maps, p, s)
+                                          : fl::launch_prefill_e2m1_d64(d.score_mod, maps, p, s))
+                                  : (bf16 ? fl::launch_prefill_bf16_d128(d.score_mod, maps, p, s)
+                                          : fl::launch_prefill_e2m1_d128(d.score_mod, maps, p, s));
+  return fl::launch_result("paged prefill launch", e);
 }
 
 }  // extern "C"

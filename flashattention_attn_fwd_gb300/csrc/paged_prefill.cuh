@@ -1,0 +1,1002 @@
+// Attention of chunks of new tokens over a paged key/value cache in bf16 or in
+// 4 bits, for packed sequences that bring anything from no to many tokens.
+//
+//   t = mod(scale q K^T),  out = softmax(t) V,  lse = log sum exp t
+//
+// with an online softmax in 32 bits.  4 d operations per visible (query, key)
+// and head; the cache's rows are read once per head and unit of 256 query rows.
+//
+// Rows.  The G query heads of a group times 128 / G consecutive tokens make the
+// 128 rows of a slot (row r: token r / G, head r % G), so that a few new tokens of
+// grouped heads already fill a tile and a diagonal tile is one of few tokens.  A
+// unit is two slots, next to each other in one sequence, and one key/value head:
+// both slots use each key tile that is brought in.
+//
+// Work split.  The host knows neither lengths nor offsets.  The key tiles of all
+// (unit, head) pairs form one line that is cut into equal pieces, a block each
+// (one per SM), so that any mix of long and short sequences keeps all SMs busy
+// to the end.  Every block finds its piece by itself: unit u of the batch takes
+// the place floor(seq_offsets[b] / R) + b + (its number in sequence b), R tokens
+// a unit, which needs no sum over the sequences before it; a scan of the units'
+// tile counts gives the line.  A unit that pieces share leaves one normalised
+// partial result and log-sum-exp per piece in the workspace, joined by
+// paged_prefill_merge_kernel in piece order, so that a call's result is the same
+// every time.
+//
+// Roles of a block (bf16 384 threads, 4 bits 512):
+//   warp 0      bf16: Q, K and V by TMA, a box per page and 64 channels
+//   warps 1, 2  one thread each issues tcgen05.mma of slot 0, of slot 1
+//   warp 3      bf16: zeroes V's rows that no row of the unit sees
+//   warps 4-11  softmax, a warpgroup per slot and a thread per row
+//   warps 12-15 4 bits: load codes and scales into registers a tile ahead, write
+//               K and V as fp16 into the swizzled tiles; scale Q to fp16
+// K and V tiles alternate in one ring, so that at d 128 five 32 KB places hold
+// two and a half tiles beside Q.
+//
+// 4 bits: code times block scale has at most six significant bits and is exact
+// in fp16; the row of Q is scaled by a power of two into fp16's range (undone in
+// the score), and P carries 2^7 so that weights down to 2^-31 of the largest
+// survive in fp16.  bf16: P is rounded to bf16, V's type.
+//
+// TMEM (512 columns): S of slot s at 128 s; d 64: P at 256 + 64 s, O at 384 + 64 s,
+// and the next tile's S is issued as soon as this one is in registers; d 128: P
+// over the first half of S, O at 256 + 128 s.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <cstdint>
+
+#include "cvt4.cuh"
+#include "fused_attn.cuh"
+#include "host.h"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fl {
+namespace {
+
+constexpr int kPfLead = 2;       // tiles that starting and ending a unit costs a block
+constexpr uint32_t kPfLift = 7;  // 4 bits: P carries 2^kPfLift
+
+template <int FMT, int D>
+struct PfLayout {
+  static constexpr bool Q4 = FMT == KV_E2M1;
+  static constexpr int THREADS = Q4 ? 512 : 384;
+  // registers per thread: at launch, then of the control, softmax and loading warpgroups
+  static constexpr int LAUNCH_REGS = Q4 ? 128 : 168;
+  static constexpr int CTL_REGS = Q4 ? 48 : 56;
+  static constexpr int SOFT_REGS = Q4 ? 192 : 224;
+  static constexpr int LOAD_REGS = Q4 ? 80 : 0;
+  static_assert(CTL_REGS + 2 * SOFT_REGS + LOAD_REGS <= (THREADS / 128) * LAUNCH_REGS, "register split");
+  static constexpr int HALVES = D / 64;                // 64-channel halves of a row (128 bytes each)
+  static constexpr int HALF = 128 * 128;               // bytes of one half of a tile
+  static constexpr int TILE = HALVES * HALF;           // bytes of a K, V or Q tile
+  static constexpr int FIXED = 1024;                   // barriers and small arrays
+  static constexpr int QF = Q4 ? 2 * 128 * 4 : 0;      // 4 bits: the rows' factors
+  static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - QF;
+  static constexpr int SLOTS_FIT = (BUDGET - 2 * TILE) / TILE;
+  static constexpr int NS = SLOTS_FIT > 8 ? 8 : SLOTS_FIT;  // ring places
+  static_assert(NS >= 4, "ring too small");
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_QF = OFF_RING + NS * TILE;
+  static constexpr int OFF_FIXED = OFF_QF + QF;
+  // at least 117 KB, so that one block (which owns TMEM) is resident per SM
+  static constexpr int END = OFF_FIXED + FIXED + 1024;
+  static constexpr int SMEM = END > 120 * 1024 ? END : 120 * 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// Barriers and small arrays in the fixed area.
+template <int NS>
+struct PfShared {
+  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_lo[2], p_hi[2], pv_done[2], o_empty[2], drain[2];
+  uint64_t v_land[8];       // V tiles with rows to be zeroed: landed
+  int64_t scan[16];
+  int64_t found_base;
+  int found_b, found_qt, found_h;
+  uint32_t tmem, abort;
+  uint32_t bad[16];         // by tile: bits of 16-key groups whose page is not in the pool
+  uint32_t issued[NS];      // last load of each place: (barrier << 1 | parity) + 1, 0: none
+};
+
+// One (unit, head): tokens, keys, tiles.
+struct PfUnit {
+  int b, qt, h;
+  int tok0, ntok;     // first token (row of q) and tokens of the unit
+  int p0, n;          // position of the first token; keys of the sequence
+  int vis_lo, vis_end;  // some row sees keys [vis_lo, vis_end) and, below vis_end, [0, sink)
+  int sinkt, skip, count;  // tile i is that of key 128 (i < sinkt ? i : i + skip)
+  int64_t base;       // line position of tile 0
+};
+
+struct PfSeqs {
+  const PrefillParams& p;
+  int R;  // tokens per unit
+  __device__ __forceinline__ int offset(int b) const {
+    if (!p.seq_offsets) return b;
+    return min(max(__ldg(p.seq_offsets + b), 0), p.T);
+  }
+  // tiles of unit qt of sequence b (offsets o to e), with its fields
+  __device__ __forceinline__ void fill(PfUnit& u, int b, int qt, int o, int e) const {
+    u.b = b;
+    u.qt = qt;
+    u.tok0 = o + qt * R;
+    u.ntok = min(R, e - u.tok0);
+    u.n = min(max(__ldg(p.kv_len + b), 0), p.cap);
+    u.p0 = u.n - (e - o) + qt * R;
+    tiles(u);
+  }
+  __device__ __forceinline__ void tiles(PfUnit& u) const {
+    u.vis_end = p.causal ? max(u.p0 + u.ntok, 0) : u.n;
+    u.vis_lo = p.window ? max(u.p0 - p.window + 1, 0) : 0;
+    const int first = u.vis_lo >> 7;
+    u.sinkt = p.window ? min((p.sink + 127) >> 7, first) : 0;
+    u.skip = first - u.sinkt;
+    u.count = max(((u.vis_end + 127) >> 7) - u.skip, 1);
+  }
+  // the next (unit, head) of the line; false behind the last
+  __device__ __forceinline__ bool next(PfUnit& u) const {
+    u.base += kPfLead + u.count;
+    if (++u.h < p.c.Hkv) return true;
+    u.h = 0;
+    int o = offset(u.b), e = max(offset(u.b + 1), o);
+    if (u.tok0 + R < e) {
+      fill(u, u.b, u.qt + 1, o, e);
+      return true;
+    }
+    for (int b = u.b + 1; b < p.B; ++b) {
+      o = offset(b);
+      e = max(offset(b + 1), o);
+      if (e > o) {
+        fill(u, b, 0, o, e);
+        return true;
+      }
+    }
+    return false;
+  }
+};
+__device__ __forceinline__ int pf_key(const PfUnit& u, int i) { return 128 * (i < u.sinkt ? i : i + u.skip); }
+__device__ __forceinline__ bool pf_seen(const PrefillParams& p, const PfUnit& u, int j) {
+  return j < u.vis_end && (j >= u.vis_lo || j < p.sink);
+}
+// does every key of [j, j + len) meet some row of the unit, does any
+__device__ __forceinline__ bool pf_all_seen(const PrefillParams& p, const PfUnit& u, int j, int len) {
+  return j + len <= u.vis_end && (j >= u.vis_lo || j + len <= p.sink);
+}
+__device__ __forceinline__ bool pf_any_seen(const PrefillParams& p, const PfUnit& u, int j, int len) {
+  return j < u.vis_end && (j + len > u.vis_lo || j < p.sink);
+}
+
+// the lowest n bits (n <= 0: none, n >= 32: all)
+__device__ __forceinline__ uint32_t pf_low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ uint32_t pf_pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void st_shared128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+template <int FMT, int D, int SCORE>
+__global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
+    paged_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PrefillParams p) {
+  using L = PfLayout<FMT, D>;
+  constexpr bool Q4 = L::Q4;
+  constexpr int NS = L::NS;
+  constexpr bool kSepP = D == 64;
+  constexpr uint32_t kColP = kSepP ? 256u : 0u, kStrP = kSepP ? 64u : 128u;
+  constexpr uint32_t kColO = kSepP ? 384u : 256u;
+  extern __shared__ uint8_t pf_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~uintptr_t(1023));
+  using Shared = PfShared<NS>;
+  static_assert(sizeof(Shared) <= L::FIXED, "fixed area");
+  Shared& sh = *reinterpret_cast<Shared*>(smem + L::OFF_FIXED);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const PfSeqs seqs{p, 2 * p.RT};
+  const int64_t H = p.c.Hkv;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      ptx::mbar_init(&sh.kv_full[i], Q4 ? 4 : 1);
+      ptx::mbar_init(&sh.kv_empty[i], 2);
+      sh.issued[i] = 0u;
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh.q_full[i], Q4 ? 4 : 1);
+      ptx::mbar_init(&sh.q_empty[i], Q4 ? 5 : 1);
+      ptx::mbar_init(&sh.s_full[i], 1);
+      ptx::mbar_init(&sh.s_free[i], 4);
+      ptx::mbar_init(&sh.p_lo[i], 4);
+      ptx::mbar_init(&sh.p_hi[i], 4);
+      ptx::mbar_init(&sh.pv_done[i], 1);
+      ptx::mbar_init(&sh.o_empty[i], 4);
+      ptx::mbar_init(&sh.drain[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) ptx::mbar_init(&sh.v_land[i], 1);
+    sh.abort = 0u;
+    sh.found_b = -1;
+    ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (tid < 16) sh.bad[tid] = 0u;
+  if (warp == 1) {
+    ptx::tmem_alloc(&sh.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0 && !Q4) {
+    ptx::prefetch_tensormap(&tmQ);
+    ptx::prefetch_tensormap(&tmK);
+    ptx::prefetch_tensormap(&tmV);
+  }
+  if (!Q4 && p.RT * p.G < 128) {
+    // rows behind the last token's heads are never loaded: zeros
+    uint4* q = reinterpret_cast<uint4*>(smem + L::OFF_Q);
+    for (int i = tid; i < 2 * L::TILE / 16; i += L::THREADS) q[i] = make_uint4(0u, 0u, 0u, 0u);
+    ptx::fence_proxy_async_smem();
+  }
+
+  // ---- this block's piece of the line
+  const int R = seqs.R;
+  const int places = p.T / R + p.B;
+  int64_t per, begin, end;
+  {
+    const int chunk = (places + L::THREADS - 1) / L::THREADS;
+    const int u0 = tid * chunk, u1 = min(u0 + chunk, places);
+    // the last sequence whose units start at or before place u0
+    auto start = [&](int b) { return seqs.offset(b) / R + b; };
+    int b0 = 0;
+    if (u0 < u1) {
+      int hi = p.B - 1;
+      while (b0 < hi) {
+        const int mid = (b0 + hi + 1) >> 1;
+        if (start(mid) <= u0) b0 = mid; else hi = mid - 1;
+      }
+    }
+    auto walk = [&](auto&& f) {
+      int b = b0;
+      int o = 0, e = 0, s = 0, s1 = 0;
+      if (u0 < u1) {
+        o = seqs.offset(b);
+        e = max(seqs.offset(b + 1), o);
+        s = o / R + b;
+        s1 = b + 1 < p.B ? start(b + 1) : places;
+      }
+      for (int u = u0; u < u1; ++u) {
+        while (u >= s1 && b + 1 < p.B) {
+          ++b;
+          o = seqs.offset(b);
+          e = max(seqs.offset(b + 1), o);
+          s = o / R + b;
+          s1 = b + 1 < p.B ? start(b + 1) : places;
+        }
+        if (u < s || static_cast<int64_t>(u - s) * R >= e - o) continue;
+        PfUnit un;
+        seqs.fill(un, b, u - s, o, e);
+        f(un);
+      }
+    };
+    int64_t mine = 0;
+    walk([&](const PfUnit& un) { mine += kPfLead + un.count; });
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+    for (int w = 0; w < L::THREADS / 32; ++w) {
+      if (w < warp) before += sh.scan[w];
+      total += sh.scan[w];
+    }
+    total *= H;
+    per = (total + gridDim.x - 1) / gridDim.x;
+    begin = per * blockIdx.x;
+    end = min(begin + per, total);
+    if (begin < end && before * H <= begin && begin < (before + mine) * H) {
+      int64_t at = before * H;
+      walk([&](const PfUnit& un) {
+        const int64_t c = kPfLead + un.count;
+        if (at <= begin && begin < at + c * H) {
+          const int h = static_cast<int>((begin - at) / c);
+          sh.found_b = un.b;
+          sh.found_qt = un.qt;
+          sh.found_h = h;
+          sh.found_base = at + h * c;
+        }
+        at += c * H;
+      });
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const Ctl ctl{reinterpret_cast<volatile uint32_t*>(&sh.abort), p.status, p.timeout_ns};
+  const uint64_t drain_ns = 50ull * 1000ull * 1000ull;
+  ptx::launch_dependents();
+
+  PfUnit first;
+  const bool any = sh.found_b >= 0;
+  if (any) {
+    const int o = seqs.offset(sh.found_b);
+    seqs.fill(first, sh.found_b, sh.found_qt, o, max(seqs.offset(sh.found_b + 1), o));
+    first.h = sh.found_h;
+    first.base = sh.found_base;
+  }
+  if (blockIdx.x > 0 && tid == 0) {
+    // is this block's border inside of a unit, and which pieces share that one
+    int32_t* r = p.rec + static_cast<int64_t>(blockIdx.x) * 8;
+    const int64_t t = any ? begin - first.base : 0;
+    const bool cut = any && t > 0 && t < first.count;
+    r[0] = cut ? 1 : 0;
+    if (cut) {
+      r[1] = first.tok0;
+      r[2] = first.ntok;
+      r[3] = first.h;
+      r[4] = static_cast<int>(first.base / per);
+      r[5] = static_cast<int>((first.base + first.count - 1) / per);
+    }
+  }
+  // calls f(unit, first tile, tile behind the last) for every unit of the piece
+  // that has tiles in it, until f fails
+  auto each_unit = [&](auto&& f) {
+    if (!any) return;
+    PfUnit u = first;
+    while (u.base < end) {
+      const int64_t t0 = begin - u.base, t1 = end - u.base;
+      const int a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(u.count))) : 0;
+      const int z = t1 < u.count ? static_cast<int>(t1) : u.count;
+      if (a < z && !f(u, a, z)) return;
+      if (!seqs.next(u)) return;
+    }
+  };
+  const int shift = p.c.page_shift;
+  const int page_mask = (1 << shift) - 1;
+
+  if (warp < 4) {
+    ptx::setmaxnreg_dec<L::CTL_REGS>();
+    if (warp == 0 && !Q4) {
+      // ---------------------------------------------------------------- loads
+      const uint64_t pol_q = ptx::policy_evict_first(), pol_kv = ptx::policy_evict_last();
+      const int nsub = shift >= 7 ? 1 : 128 >> shift;  // pages of a tile
+      const int sub_len = 128 / nsub;
+      const int box = lane & 15;                       // lanes 0-15 K, 16-31 V
+      const bool mine = box < nsub * L::HALVES;
+      const int sub = mine ? box % nsub : 0, half = mine ? box / nsub : 0;
+      uint32_t e = 0, tile = 0, part = 0, qc[2] = {0u, 0u};
+      int q_phase[2] = {-1, -1};
+      bool skipped = false;
+      each_unit([&](const PfUnit& u, int a, int z) {
+        // page of this lane's keys of tile i: num_pages (read as zeros) when no
+        // row sees them, or (reported) when it is not in the pool
+        auto lookup = [&](int i) -> int {
+          const int j = pf_key(u, i) + sub * sub_len;
+          if (i >= z || !mine || !pf_any_seen(p, u, j, sub_len)) return p.c.num_pages;
+          return __ldg(p.table + u.b * p.table_stride + (j >> shift));
+        };
+        int next = lookup(a);
+        for (int s = 0; s < 2; ++s) {
+          if (u.ntok <= s * p.RT) continue;
+          if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(&sh.q_full[s], p.RT * p.G * D * 2);
+            for (int x = 0; x < L::HALVES; ++x)
+              ptx::tma_load_4d(smem + L::OFF_Q + s * L::TILE + x * L::HALF, &tmQ, &sh.q_full[s], 64 * x, 0, u.h,
+                               u.tok0 + s * p.RT, pol_q);
+          }
+          q_phase[s] = static_cast<int>(qc[s] & 1u);
+          ++qc[s];
+        }
+        for (int i = a; i < z; ++i, ++tile, e += 2) {
+          const int j0 = pf_key(u, i);
+          int page = next;
+          next = lookup(i + 1);
+          const bool out_of_pool = page != p.c.num_pages && (page < 0 || page > p.c.num_pages);
+          const bool at_end = page == p.c.num_pages && mine && pf_any_seen(p, u, j0 + sub * sub_len, sub_len);
+          const bool bad = out_of_pool || at_end;
+          if (bad) page = p.c.num_pages;
+          const uint32_t badl = __ballot_sync(0xffffffffu, bad && box < nsub && lane < 16);
+          if (lane == 0) {
+            uint32_t w = 0u;
+            if (badl) {
+              atomicOr(p.status, 2u);
+              for (int g = 0; g < 8; ++g)
+                if (badl >> (g * 16 / sub_len) & 1u) w |= 1u << (8 * (g >> 1) + (g & 1));
+            }
+            sh.bad[tile & 15u] = w;
+          }
+          const int row = j0 & page_mask;  // of a page of 128 keys and more
+          const bool whole = pf_all_seen(p, u, j0, 128);
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t ev = e + v;
+            const int st = static_cast<int>(ev % NS);
+            if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[st], ((ev / NS) & 1u) ^ 1u, ctl, 2))) return false;
+            const bool land = v == 1 && !whole;
+            uint64_t* bar = land ? &sh.v_land[part & 7u] : &sh.kv_full[st];
+            const bool skip = v == 0 && p.dbg_skip_tile >= 0 && blockIdx.x == 0 &&
+                              static_cast<int>(tile) == p.dbg_skip_tile;
+            if (lane == 0) {
+              const uint32_t ph = land ? (part >> 3) & 1u : (ev / NS) & 1u;
+              const uint32_t which = land ? NS + (part & 7u) : st;
+              sh.issued[st] = skip ? 0u : (which << 1 | ph) + 1u;
+              ptx::mbar_arrive_expect_tx(bar, L::TILE);
+            }
+            __syncwarp();
+            if (mine && (lane >= 16) == (v == 1) && !skip)
+              ptx::tma_load_4d(smem + L::OFF_RING + st * L::TILE + half * L::HALF + sub * sub_len * 128, v ? &tmV : &tmK, bar,
+                               64 * half, nsub == 1 ? row : 0, u.h, page, pol_kv);
+            skipped |= skip;
+            if (land) ++part;
+          }
+        }
+        return true;
+      });
+      if (lane == 0 && *ctl.abort) {
+        // let every copy land before the block exits
+        for (int st = 0; st < NS; ++st) {
+          const uint32_t w = sh.issued[st];
+          if (!w) continue;
+          const uint32_t which = (w - 1u) >> 1;
+          wait_drain(which < NS ? &sh.kv_full[which] : &sh.v_land[which - NS], (w - 1u) & 1u, drain_ns);
+        }
+        for (int s = 0; s < 2; ++s)
+          if (q_phase[s] >= 0) wait_drain(&sh.q_full[s], static_cast<uint32_t>(q_phase[s]), drain_ns);
+      }
+      __syncwarp();
+    } else if (warp == 3 && !Q4) {
+      // ------------------------- V's rows that no row of the unit sees: zeros
+      // (P is 0 there, and 0 times whatever the pool holds has to be 0)
+      uint32_t e = 0, part = 0;
+      Ctl later = ctl;  // the limit once per tile that is passed
+      each_unit([&](const PfUnit& u, int a, int z) {
+        for (int i = a; i < z; ++i, e += 2) {
+          const int j0 = pf_key(u, i);
+          later.timeout_ns += ctl.timeout_ns;
+          if (pf_all_seen(p, u, j0, 128)) continue;
+          const int st = static_cast<int>((e + 1) % NS);
+          if (!__all_sync(0xffffffffu, wait_bar(&sh.v_land[part & 7u], (part >> 3) & 1u, later, 3))) return false;
+          later.timeout_ns = ctl.timeout_ns;
+          ++part;
+          const uint32_t base = ptx::smem_u32(smem + L::OFF_RING + st * L::TILE);
+          for (int x = lane; x < 128 * L::HALVES * 8; x += 32) {
+            const int r = (x >> 3) & 127;
+            if (!pf_seen(p, u, j0 + r)) st_shared128(base + x * 16, 0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.kv_full[st]);
+        }
+        return true;
+      });
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
+      // ------------------------------------------------------------ MMA issue
+      const int s = warp - 1;
+      constexpr uint32_t kTypes = Q4 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 operands
+      constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false) & kTypes;
+      constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(128, D, true) & kTypes;
+      const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
+      const uint64_t qd = ptx::smem_desc(ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE, 16, 1024, 2u);
+      uint32_t e = 0, qc = 0, sc = 0, pc = 0;
+      auto full = [&](uint32_t ev, int where) { return wait_bar(&sh.kv_full[ev % NS], (ev / NS) & 1u, ctl, where); };
+      auto issue_s = [&](uint32_t ev, bool last) -> bool {
+        if (!full(ev, 11)) return false;
+        if (kSepP && !wait_bar(&sh.s_free[s], (sc & 1u) ^ 1u, ctl, 12)) return false;
+        ptx::tc_fence_after();
+        const uint64_t kd = ptx::smem_desc(ring + (ev % NS) * L::TILE, 16, 1024, 2u);
+#pragma unroll
+        for (int kb = 0; kb < D / 16; ++kb) {
+          const uint32_t off = ((kb / 4) * L::HALF + (kb % 4) * 32) >> 4;
+          ptx::mma_ss(tmem + s * 128, qd + off, kd + off, IDESC_S, kb > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(&sh.s_full[s]);
+        ptx::mma_commit(&sh.kv_empty[ev % NS]);
+        if (last) ptx::mma_commit(&sh.q_empty[s]);
+        ++sc;
+        return true;
+      };
+      auto issue_pv = [&](uint32_t ev, bool acc, int kb0, int kb1) {
+        const uint64_t vd = ptx::smem_desc(ring + (ev % NS) * L::TILE, L::HALF, 1024, 2u);
+#pragma unroll
+        for (int kb = kb0; kb < kb1; ++kb)
+          ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 16 * 128) >> 4), IDESC_O,
+                      (acc || kb > 0) ? 1u : 0u);
+      };
+      each_unit([&](const PfUnit& u, int a, int z) {
+        const int n = z - a;
+        if (u.ntok <= s * p.RT) {
+          // no rows in this slot: pass the unit's tiles
+          for (int i = 0; i < 2 * n; ++i, ++e) {
+            if (!full(e, 17)) return false;
+            ptx::mbar_arrive(&sh.kv_empty[e % NS]);
+          }
+          return true;
+        }
+        if (!wait_bar(&sh.q_full[s], qc & 1u, ctl, 10)) return false;
+        if (!issue_s(e, n == 1)) return false;
+        for (int i = 0; i < n; ++i, e += 2) {
+          if (kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
+          if (i == 0 && !wait_bar(&sh.o_empty[s], (qc & 1u) ^ 1u, ctl, 13)) return false;
+          if (!full(e + 1, 16)) return false;
+          if (!wait_bar(&sh.p_lo[s], pc & 1u, ctl, 14)) return false;
+          ptx::tc_fence_after();
+          issue_pv(e + 1, i > 0, 0, 4);
+          if (!wait_bar(&sh.p_hi[s], pc & 1u, ctl, 15)) return false;
+          ptx::tc_fence_after();
+          issue_pv(e + 1, true, 4, 8);
+          ++pc;
+          ptx::mma_commit(&sh.pv_done[s]);
+          ptx::mma_commit(&sh.kv_empty[(e + 1) % NS]);
+          if (!kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
+        }
+        ++qc;
+        return true;
+      });
+      // every MMA this thread issued must finish before TMEM is released
+      ptx::mma_commit(&sh.drain[s]);
+      wait_drain(&sh.drain[s], 0u, drain_ns);
+    }
+    __syncwarp();
+  } else if (warp < 12) {
+    // -------------------------------------------------------------- softmax
+    ptx::setmaxnreg_inc<L::SOFT_REGS>();
+    const int sw = warp - 4, s = sw >> 2, quad = sw & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tS = tl + s * 128, tP = tl + kColP + s * kStrP, tO = tl + kColO + s * D;
+    const int rtok = r / p.G, rg = r - rtok * p.G;
+    const bool row_used = rtok < p.RT;
+    uint32_t qc = 0, sc = 0, tile = 0;
+    Ctl later = ctl;  // the limit once per tile of the other slot that is passed
+    each_unit([&](const PfUnit& u, int a, int z) {
+      const int n_tiles = z - a;
+      if (u.ntok <= s * p.RT) {
+        tile += n_tiles;
+        later.timeout_ns += ctl.timeout_ns * n_tiles;
+        return true;
+      }
+      // rows without a token take the last one's bounds (their results are dropped)
+      const int tok = s * p.RT + rtok;
+      const int pos = u.p0 + min(tok, u.ntok - 1);
+      const int hi = p.causal ? min(pos, u.n - 1) : u.n - 1;
+      const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
+      const int hq = u.h * p.G + rg;
+      float xmul = p.scale_log2, rf = 1.f;
+      if (Q4) {
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.q_full[s], qc & 1u, later, 27))) return false;
+        rf = reinterpret_cast<const float*>(smem + L::OFF_QF)[s * 128 + r];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.q_empty[s]);
+        xmul *= rf;
+      }
+      if (SCORE != SCORE_NONE) xmul = 1.f;
+      const float slope2 = SCORE == SCORE_ALIBI ? __ldg(p.slopes + (row_used ? hq : 0)) * kLog2e : 0.f;
+      float m = -CUDART_INF_F, l = 0.f;
+      for (int i = a; i < z; ++i, ++sc, ++tile) {
+        const int j0 = pf_key(u, i);
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], sc & 1u, later, 20 + s))) return false;
+        later.timeout_ns = ctl.timeout_ns;
+        ptx::tc_fence_after();
+        float x[128];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) ptx::tmem_ld32f(tS + 32 * b, &x[32 * b]);
+        const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sh.bad[tile & 15u]);
+        const bool part = j0 + 127 > hi || (j0 < lo && j0 + 127 >= p.sink) || bad != 0u;
+        const bool any_part = __any_sync(0xffffffffu, part);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int b = 0; b < 4; ++b) ptx::reg_fence32f(&x[32 * b]);
+        if (kSepP) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.s_free[s]);
+        }
+        if (SCORE == SCORE_SOFTCAP) {
+          // x = cap log2(e) tanh(s scale / cap): a polynomial while every |s| of the
+          // warp is in its range, else 1 - 2 / (1 + e^2y)
+          float am[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 128; c += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) am[q] = ptx::max3(am[q], fabsf(x[c + q]), fabsf(x[c + 4 + q]));
+          const float amax = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])) * rf;
+          if (__all_sync(0xffffffffu, amax <= p.sc_smax)) {
+            const float2 sq0 = make_float2(p.sc_q[0], p.sc_q[0]), sq1 = make_float2(p.sc_q[1], p.sc_q[1]);
+            const float2 sq2 = make_float2(p.sc_q[2], p.sc_q[2]), sq3 = make_float2(p.sc_q[3], p.sc_q[3]);
+            const float2 rf2 = make_float2(rf, rf);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              float2 sv = make_float2(x[c], x[c + 1]);
+              if (Q4) sv = ptx::mul2(sv, rf2);
+              const float2 y = ptx::mul2(sv, sv);
+              float2 q = ptx::fma2(sq3, y, sq2);
+              q = ptx::fma2(q, y, sq1);
+              q = ptx::fma2(q, y, sq0);
+              const float2 v = ptx::mul2(sv, q);
+              x[c] = v.x;
+              x[c + 1] = v.y;
+            }
+          } else {
+            const float arg = p.cap_arg * rf;
+#pragma unroll
+            for (int c = 0; c < 128; ++c) {
+              const float ez = ptx::ex2(x[c] * arg);
+              x[c] = fmaf(-2.0f * p.softcap, ptx::rcp(1.0f + ez), p.softcap);
+            }
+          }
+        } else if (SCORE == SCORE_ALIBI) {
+          // x = scale s + slope (j - pos), in log2 units
+          const float2 sc2 = make_float2(p.scale_log2 * rf, p.scale_log2 * rf), sl2 = make_float2(slope2, slope2);
+          const float off = slope2 * static_cast<float>(j0 - pos);
+          const float2 off2 = make_float2(off, off);
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) {
+            const float2 t = ptx::fma2(make_float2(static_cast<float>(c), static_cast<float>(c + 1)), sl2, off2);
+            const float2 v = ptx::fma2(make_float2(x[c], x[c + 1]), sc2, t);
+            x[c] = v.x;
+            x[c + 1] = v.y;
+          }
+        }
+        if (any_part) {
+          // 32 keys at a time as a word of bits: below hi, and from lo on or a sink
+          const int chi = hi - j0, clo = lo - j0, csk = (p.window ? p.sink : 0) - j0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t w = pf_low_bits(chi + 1 - 32 * b) & (~pf_low_bits(clo - 32 * b) | pf_low_bits(csk - 32 * b));
+            if (bad) w &= ~(((bad >> (8 * b) & 1u) ? 0xffffu : 0u) | ((bad >> (8 * b) & 2u) ? 0xffff0000u : 0u));
+            if (!__any_sync(0xffffffffu, w != 0xffffffffu)) continue;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[32 * b + c] = w & (1u << c) ? x[32 * b + c] : -CUDART_INF_F;
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(x[q], x[4 + q]);
+#pragma unroll
+        for (int c = 8; c < 128; c += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], x[c + q], x[c + 4 + q]);
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * xmul;
+        // the reference maximum is raised only by more than 8 (in log2 units)
+        const float m_new = fmaxf(m, tmax);
+        const bool raise = m_new > m + kRescaleThreshold || (m == -CUDART_INF_F && m_new != -CUDART_INF_F);
+        const bool any_raise = __any_sync(0xffffffffu, raise);
+        float alpha = 1.f;
+        if (any_raise) {
+          alpha = raise ? ptx::ex2(m - m_new) : 1.f;
+          m = raise ? m_new : m;
+          l *= alpha;
+        }
+        const float sub = (Q4 ? static_cast<float>(kPfLift) : 0.f) - (m == -CUDART_INF_F ? 0.f : m);
+        const float2 negm = make_float2(sub, sub), xm2 = make_float2(xmul, xmul);
+        // P and O may change once the previous P V is done (d 128: it was, before this S)
+        if (kSepP && sc > 0 && !__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s))) return false;
+        ptx::tc_fence_after();
+        if (i > a && any_raise) {
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + c, o);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            ptx::tmem_st32(tO + c, o);
+          }
+        }
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float2 arg = ptx::fma2(make_float2(x[b * 32 + 2 * q], x[b * 32 + 2 * q + 1]), xm2, negm);
+            const float2 pv = make_float2(ptx::ex2(arg.x), ptx::ex2(arg.y));
+            ls[q & 1] = ptx::add2(ls[q & 1], pv);
+            pk[q] = Q4 ? pf_pack_f16(pv.x, pv.y) : ptx::pack_bf16x2(pv.x, pv.y);
+          }
+          ptx::tmem_st16(tP + b * 16, pk);
+          if (b & 1) {
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(b == 1 ? &sh.p_lo[s] : &sh.p_hi[s]);
+          }
+        }
+        const float2 lsum = ptx::add2(ls[0], ls[1]);
+        l += lsum.x + lsum.y;
+      }
+      // ---- the unit's end
+      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 30 + s))) return false;
+      ptx::tc_fence_after();
+      const bool live = row_used && tok < u.ntok;
+      const float lse2 = l > 0.f ? m + __log2f(l) - (Q4 ? static_cast<float>(kPfLift) : 0.f) : (l == l ? -CUDART_INF_F : l);
+      const float inv = l > 0.f || l != l ? (Q4 ? p.c.v_scale : 1.f) / l : 0.f;
+      if (n_tiles == u.count) {
+        const int64_t row = static_cast<int64_t>(u.tok0 + tok);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.o_t + hq * p.o_h;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + c, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = ptx::pack_bf16x2(__uint_as_float(o[q + 2 * k]) * inv, __uint_as_float(o[q + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + c + q) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (live && p.lse) p.lse[row * p.Hq + hq] = lse2 * kLn2;
+      } else {
+        // a partial result: of a unit that an earlier block began (0), or that a later one ends (1)
+        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (a > 0 ? 0 : 1)) * 2 + s;
+        float4* op = reinterpret_cast<float4*>(p.opart) + at * (D / 4) * 128 + r;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + c, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            op[(c / 4 + q) * 128] =
+                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                            __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        }
+        p.lpart[at * 128 + r] = lse2;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
+      ++qc;
+      return true;
+    });
+  } else if constexpr (Q4) {
+    // -------------------------------------- 4 bits: Q, K and V tiles in fp16
+    ptx::setmaxnreg_dec<L::LOAD_REGS>();
+    const int r = tid - 384;  // key row of the tile, query row of the slot
+    const int rtok = r / p.G, rg = r - rtok * p.G;
+    const int row_off = r * 128;
+    constexpr int W = D / 32;   // 16-byte words of a row's codes
+    uint32_t e = 0, tile = 0, qc[2] = {0u, 0u};
+    const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
+    each_unit([&](const PfUnit& u, int a, int z) {
+      uint4 kc[W], vc[W];
+      uint32_t ks[D / 64], vs[D / 64];
+      bool bad = false;
+      // this row's place in the pool for tile i: token index times heads, or -1
+      auto lookup = [&](int i) -> int {
+        const int j = pf_key(u, i) + r;
+        return i < z && pf_seen(p, u, j) ? __ldg(p.table + u.b * p.table_stride + (j >> shift)) : -2;
+      };
+      auto in_pool = [&](int page) { return page >= 0 && page < p.c.num_pages; };
+      auto load_k = [&](int i, int page) {
+        if (in_pool(page)) {
+          const int64_t slot = ((static_cast<int64_t>(page) * p.c.Hkv + u.h) << shift) + ((pf_key(u, i) + r) & page_mask);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.c.k) + slot * (D / 2));
+#pragma unroll
+          for (int q = 0; q < W; ++q) kc[q] = __ldg(src + q);
+          const uint32_t* sc = reinterpret_cast<const uint32_t*>(p.c.ks + slot * (D / 16));
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) ks[q] = __ldg(sc + q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < W; ++q) kc[q] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) ks[q] = 0u;
+        }
+      };
+      auto load_v = [&](int i, int page) {
+        if (in_pool(page)) {
+          const int64_t run = (static_cast<int64_t>(page) * p.c.Hkv + u.h) << shift;
+          const int at = (pf_key(u, i) + r) & page_mask;
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.c.v) + (run + at) * (D / 2));
+#pragma unroll
+          for (int q = 0; q < W; ++q) vc[q] = __ldg(src + q);
+          const uint8_t* sc = p.c.vs + run * (D / 16) + at;
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) {
+            uint32_t w = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w |= static_cast<uint32_t>(__ldg(sc + (static_cast<int64_t>(4 * q + k) << shift))) << (8 * k);
+            vs[q] = w;
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < W; ++q) vc[q] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int q = 0; q < D / 64; ++q) vs[q] = 0u;
+        }
+      };
+      // row r of a tile: 16 bytes (8 channels) at a time to their swizzled places
+      auto put = [&](int st, const uint4 (&c)[W], const uint32_t (&s8)[D / 64]) {
+        const uint32_t base = ring + st * L::TILE + row_off;
+#pragma unroll
+        for (int q = 0; q < W; ++q) {
+          const uint32_t w[4] = {c[q].x, c[q].y, c[q].z, c[q].w};
+          // channels 32 q ..: two blocks of 16
+          const uint32_t two = cvt4::from_e4m3x2((s8[q / 2] >> (16 * (q & 1))) & 0xffffu);
+          const uint32_t s0 = __byte_perm(two, 0u, 0x1010), s1 = __byte_perm(two, 0u, 0x3232);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t hv[4];
+            cvt4::from_e2m1x8(w[k], hv);
+            const uint32_t sc = k < 2 ? s0 : s1;
+            const int piece = (q * 4 + k) & 7, half = (q * 4 + k) >> 3;
+            st_shared128(base + half * L::HALF + ((piece ^ (r & 7)) << 4), cvt4::hmul2(hv[0], sc), cvt4::hmul2(hv[1], sc),
+                         cvt4::hmul2(hv[2], sc), cvt4::hmul2(hv[3], sc));
+          }
+        }
+      };
+      int page = lookup(a), page1 = lookup(a + 1);
+      load_k(a, page);
+      load_v(a, page);
+      for (int s = 0; s < 2; ++s) {
+        if (u.ntok <= s * p.RT) continue;
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
+        ++qc[s];
+        // the row scaled by a power of two that takes its largest channel to 2^14
+        const bool ok = rtok < p.RT && s * p.RT + rtok < u.ntok;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                          static_cast<int64_t>(u.tok0 + (ok ? s * p.RT + rtok : 0)) * p.q_t +
+                                                          static_cast<int64_t>(u.h * p.G + (ok ? rg : 0)) * p.q_h);
+        uint32_t mx = 0u;  // bf16 magnitudes order as integers
+#pragma unroll 4
+        for (int q = 0; q < D / 8; ++q) {
+          const uint4 w = ok ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+        const int ex = static_cast<int>((max(mx & 0xffffu, mx >> 16) >> 7) & 0xffu);  // biased exponent
+        // zeros, and rows whose largest is not finite, as they are; tiny ones by 2^110 at most
+        const int up = ex == 0 || ex == 255 ? 0 : min(14 - (ex - 127), 110);
+        const float f = __int_as_float((up + 127) << 23);
+        const uint32_t base = ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE + row_off;
+#pragma unroll 4
+        for (int q = 0; q < D / 8; ++q) {
+          const uint4 w = ok ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pf_pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+          st_shared128(base + (q >> 3) * L::HALF + (((q & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        reinterpret_cast<float*>(smem + L::OFF_QF)[s * 128 + r] = __int_as_float((127 - up) << 23);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.q_full[s]);
+      }
+      for (int i = a; i < z; ++i, ++tile, e += 2) {
+        // page: this tile's; page1: the next one's
+        const int page2 = lookup(i + 2);
+        bad = page != -2 && !in_pool(page);
+        const uint32_t bb = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) {
+          if (bb) atomicOr(p.status, 2u);
+          reinterpret_cast<uint8_t*>(&sh.bad[tile & 15u])[warp - 12] =
+              static_cast<uint8_t>(((bb & 0xffffu) ? 1u : 0u) | ((bb >> 16) ? 2u : 0u));
+        }
+        const int sk = static_cast<int>(e % NS), sv = static_cast<int>((e + 1) % NS);
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[sk], ((e / NS) & 1u) ^ 1u, ctl, 2))) return false;
+        put(sk, kc, ks);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        const bool skip = p.dbg_skip_tile >= 0 && blockIdx.x == 0 && static_cast<int>(tile) == p.dbg_skip_tile;
+        if (lane == 0 && !skip) ptx::mbar_arrive(&sh.kv_full[sk]);
+        if (i + 1 < z) load_k(i + 1, page1);
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[sv], (((e + 1) / NS) & 1u) ^ 1u, ctl, 2))) return false;
+        put(sv, vc, vs);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.kv_full[sv]);
+        if (i + 1 < z) load_v(i + 1, page1);
+        page = page1;
+        page1 = page2;
+      }
+      return true;
+    });
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the partial results of the units that pieces share: 8 blocks of 32 rows
+// for every border between pieces; the first border inside of a unit does it.
+template <int D>
+__global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  ptx::wait_prerequisites();
+  const int border = 1 + blockIdx.x / 8, part = blockIdx.x % 8;
+  const int32_t* rec = p.rec + static_cast<int64_t>(border) * 8;
+  if (!rec[0] || rec[4] != border - 1) return;
+  const int s = part >> 2, r = (part & 3) * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  const int rtok = r / p.G, tok = s * p.RT + rtok;
+  if (rtok >= p.RT || tok >= rec[2]) return;
+  const int hq = rec[3] * p.G + r - rtok * p.G;
+  const int last = rec[5];
+  auto at = [&](int piece) { return (static_cast<int64_t>(piece) * 2 + (piece == border - 1 ? 1 : 0)) * 2 + s; };
+  float m = -CUDART_INF_F;
+  for (int i = border - 1; i <= last; ++i) m = fmaxf(m, p.lpart[at(i) * 128 + r]);
+  const float ref = m == -CUDART_INF_F ? 0.f : m;
+  constexpr int C = D / 16;  // float4 of this thread
+  float4 o[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  for (int i = border - 1; i <= last; ++i) {
+    const float wt = ptx::ex2(p.lpart[at(i) * 128 + r] - ref);
+    const float4* src = reinterpret_cast<const float4*>(p.opart) + (at(i) * (D / 4) + w * C) * 128 + r;
+    sum += wt;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float4 v = src[c * 128];
+      o[c].x = fmaf(v.x, wt, o[c].x);
+      o[c].y = fmaf(v.y, wt, o[c].y);
+      o[c].z = fmaf(v.z, wt, o[c].z);
+      o[c].w = fmaf(v.w, wt, o[c].w);
+    }
+  }
+  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+  const int64_t row = static_cast<int64_t>(rec[1] + tok);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.o_t + hq * p.o_h + w * (D / 4);
+#pragma unroll
+  for (int c = 0; c < C; c += 2)
+    *reinterpret_cast<uint4*>(out + 4 * c) =
+        make_uint4(ptx::pack_bf16x2(o[c].x * inv, o[c].y * inv), ptx::pack_bf16x2(o[c].z * inv, o[c].w * inv),
+                   ptx::pack_bf16x2(o[c + 1].x * inv, o[c + 1].y * inv), ptx::pack_bf16x2(o[c + 1].z * inv, o[c + 1].w * inv));
+  if (w == 0 && p.lse) p.lse[row * p.Hq + hq] = (sum > 0.f || sum != sum ? m + __log2f(sum) : -CUDART_INF_F) * kLn2;
+}
+
+template <int FMT, int D, int SCORE>
+cudaError_t launch_prefill_score(const CUtensorMap* maps, const PrefillParams& p, cudaStream_t s) {
+  using L = PfLayout<FMT, D>;
+  auto kern = paged_prefill_kernel<FMT, D, SCORE>;
+  static OncePerDevice once;
+  const cudaError_t checked = on_this_device(once, [&]() {
+    cudaFuncAttributes a{};
+    cudaError_t e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    // the register split needs these at launch
+    if (a.numRegs != L::LAUNCH_REGS) return cudaErrorInvalidDeviceFunction;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  });
+  if (checked != cudaSuccess) return checked;
+  kern<<<p.grid, L::THREADS, L::SMEM, s>>>(maps[0], maps[1], maps[2], p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || p.grid < 2) return e;
+  return launch_chained(paged_prefill_merge_kernel<D>, static_cast<unsigned>(p.grid - 1) * 8u, 128u, 0, s, p);
+}
+
+template <int FMT, int D>
+cudaError_t launch_prefill(int score_mod, const CUtensorMap* maps, const PrefillParams& p, cudaStream_t s) {
+  switch (score_mod) {
+    case SCORE_NONE: return launch_prefill_score<FMT, D, SCORE_NONE>(maps, p, s);
+    case SCORE_ALIBI: return launch_prefill_score<FMT, D, SCORE_ALIBI>(maps, p, s);
+    case SCORE_SOFTCAP: return launch_prefill_score<FMT, D, SCORE_SOFTCAP>(maps, p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+}  // namespace fl

@@ -1,0 +1,193 @@
+// Rotation of queries and keys by their positions, forward and backward, and the
+// tables that it reads.
+//
+//   y1 = x1 cos - x2 sin,  y2 = x2 cos + x1 sin   (fp32, every product and sum
+//   rounded once, then y to bf16), pairs (c, c + rope_dim / 2) or (2c, 2c + 1)
+//
+// The gradient is the turn the other way: the same with -sin.  Bound by memory:
+// every row is read and written once.  One warp takes one token: its position
+// and rotation are then warp-uniform, and a lane keeps the cos and sin of its
+// eight channels in registers for all heads, d / 8 lanes a row; the partner
+// channel of the half-split pairing comes by shuffle.  Strides are free, so that
+// the projection's token-major output becomes the [B, H, L, d] that the backward
+// pass of attention takes, in the same pass.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "paged_rows.cuh"
+#include "ptx.cuh"
+#include "rope.h"
+
+namespace fl {
+namespace {
+
+constexpr int kRopeThreads = 128;
+
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int LPR = D / 8;        // lanes per row
+  constexpr int RPS = 32 / LPR;     // rows a warp handles at once
+  constexpr int NB = 4;             // row groups in flight per warp
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
+  const int64_t token = w / p.splits;
+  const int part = static_cast<int>(w % p.splits);
+  if (token >= static_cast<int64_t>(p.B) * p.L) return;
+  const int b = static_cast<int>(token / p.L), l = static_cast<int>(token % p.L);
+  const int pos = p.positions ? __ldg(p.positions + b * p.pos_b + l) : l;
+  if (pos < 0 || pos >= p.table_rows) {
+    if (lane == 0 && part == 0) atomicOr(p.status, 2u);
+    return;
+  }
+  const int sub = lane / LPR, c8 = lane % LPR, c0 = 8 * c8;
+  const bool turn = c0 < p.rope_dim;
+  const int half = p.rope_dim >> 1;
+  const bool second = !PAIRS && c0 >= half;
+  const int partner = turn && !PAIRS ? sub * LPR + (second ? c0 - half : c0 + half) / 8 : lane;
+  // y = x cos + partner * sn; the first channel of a pair takes its partner with -sin
+  float2 cs[4], sn[4];
+  if (turn) {
+    const int64_t row = static_cast<int64_t>(pos) * half;
+    if (PAIRS) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(p.cos + row + c0 / 2));
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(p.sin + row + c0 / 2));
+      const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        cs[e] = make_float2(cc[e], cc[e]);
+        sn[e] = make_float2(-p.sign * ss[e], p.sign * ss[e]);
+      }
+    } else {
+      const int at = second ? c0 - half : c0;
+      const float4* cp = reinterpret_cast<const float4*>(p.cos + row + at);
+      const float4* sp = reinterpret_cast<const float4*>(p.sin + row + at);
+      const float4 ca = __ldg(cp), cb = __ldg(cp + 1), sa = __ldg(sp), sb = __ldg(sp + 1);
+      const float f = second ? p.sign : -p.sign;
+      cs[0] = make_float2(ca.x, ca.y); cs[1] = make_float2(ca.z, ca.w);
+      cs[2] = make_float2(cb.x, cb.y); cs[3] = make_float2(cb.z, cb.w);
+      sn[0] = make_float2(f * sa.x, f * sa.y); sn[1] = make_float2(f * sa.z, f * sa.w);
+      sn[2] = make_float2(f * sb.x, f * sb.y); sn[3] = make_float2(f * sb.z, f * sb.w);
+    }
+  }
+  int first = 0;  // row groups before this tensor's
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const RopeRows& t = p.t[k];
+    const int groups = (t.heads + RPS - 1) / RPS;
+    int g = (part - first) % p.splits;
+    if (g < 0) g += p.splits;
+    first += groups;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(t.x) + b * t.x_b + l * t.x_l + c0;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(t.y) + b * t.y_b + l * t.y_l + c0;
+    for (; g < groups; g += NB * p.splits) {
+      uint4 raw[NB];
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        const int r = (g + u * p.splits) * RPS + sub;
+        raw[u] = r < t.heads ? *reinterpret_cast<const uint4*>(src + r * t.x_h) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        if (g + u * p.splits >= groups) break;
+        const int r = (g + u * p.splits) * RPS + sub;
+        float2 x[4], y[4];
+        unpack8(raw[u], x);
+        if (PAIRS) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = make_float2(x[e].y, x[e].x);
+        } else {
+          unpack8(make_uint4(__shfl_sync(0xffffffffu, raw[u].x, partner), __shfl_sync(0xffffffffu, raw[u].y, partner),
+                             __shfl_sync(0xffffffffu, raw[u].z, partner), __shfl_sync(0xffffffffu, raw[u].w, partner)),
+                  y);
+        }
+        if (turn) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // products and sums rounded one by one, as the cache's append does
+            x[e].x = __fadd_rn(__fmul_rn(x[e].x, cs[e].x), __fmul_rn(y[e].x, sn[e].x));
+            x[e].y = __fadd_rn(__fmul_rn(x[e].y, cs[e].y), __fmul_rn(y[e].y, sn[e].y));
+          }
+        }
+        if (r < t.heads) *reinterpret_cast<uint4*>(dst + r * t.y_h) = turn ? pack8(x) : raw[u];
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_rope_d(RopeParams& p, int sm_count, cudaStream_t s) {
+  constexpr int RPS = 32 / (D / 8);
+  const int64_t tokens = static_cast<int64_t>(p.B) * p.L;
+  const int groups = (p.t[0].heads + RPS - 1) / RPS + (p.t[1].heads + RPS - 1) / RPS;
+  // spread a token's rows over more warps while that leaves fewer than 32 warps an SM
+  int64_t splits = (static_cast<int64_t>(sm_count) * 32 + tokens - 1) / tokens;
+  splits = splits > groups ? groups : splits;
+  p.splits = static_cast<int>(splits);
+  const int64_t blocks = (tokens * splits + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  if (p.interleaved) rope_kernel<D, true><<<static_cast<unsigned>(blocks), kRopeThreads, 0, s>>>(p);
+  else rope_kernel<D, false><<<static_cast<unsigned>(blocks), kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Tables: cos and sin of position * angle step.  The angle is a 64-bit fraction
+// of a turn, so that position times step wraps where a turn ends and nothing is
+// lost at far positions (error 2^-64 turns times the position, with integer
+// products where fp64's would be slow).  Its quarter turns pick the function and the sign, the
+// rest, at most an eighth of a turn either way, is an fp32 argument.
+constexpr int kTabThreads = 256;
+constexpr int kTabRows = 8;  // positions of a thread
+
+__global__ void __launch_bounds__(kTabThreads) rope_tables_kernel(const __grid_constant__ RopeTableParams p) {
+  const int lanes = p.half / 4;              // threads of a position, four pairs each
+  const int rows = kTabThreads / lanes;      // positions at once
+  const int c = threadIdx.x % lanes, r = threadIdx.x / lanes;
+  if (r >= rows) return;
+  uint64_t step[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) step[e] = p.turn[4 * c + e];
+  const int64_t pos0 = static_cast<int64_t>(blockIdx.x) * rows * kTabRows + r;
+#pragma unroll 2
+  for (int k = 0; k < kTabRows; ++k) {
+    const int64_t pos = pos0 + static_cast<int64_t>(k) * rows;
+    if (pos >= p.positions) return;
+    float co[4], si[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t a = step[e] * static_cast<uint64_t>(pos) + (uint64_t(1) << 61);  // an eighth of a turn further
+      const uint32_t hi = static_cast<uint32_t>(a >> 32);
+      const int quarter = static_cast<int>(hi >> 30);
+      // the rest in half turns, [-1/4, 1/4)
+      const float x = static_cast<float>(static_cast<int>(hi & 0x3fffffffu) - (1 << 29)) * 0x1p-31f;
+      float s, q;
+      sincospif(x, &s, &q);
+      const float u = quarter & 1 ? s : q, v = quarter & 1 ? q : s;
+      co[e] = (quarter == 1 || quarter == 2 ? -u : u) * p.amplitude;
+      si[e] = (quarter & 2 ? -v : v) * p.amplitude;
+    }
+    const int64_t at = pos * p.half + 4 * c;
+    *reinterpret_cast<float4*>(p.cos + at) = make_float4(co[0], co[1], co[2], co[3]);
+    *reinterpret_cast<float4*>(p.sin + at) = make_float4(si[0], si[1], si[2], si[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int d, RopeParams& p, int sm_count, cudaStream_t s) {
+  switch (d) {
+    case 32: return launch_rope_d<32>(p, sm_count, s);
+    case 64: return launch_rope_d<64>(p, sm_count, s);
+    case 128: return launch_rope_d<128>(p, sm_count, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_rope_tables(const RopeTableParams& p, cudaStream_t s) {
+  const int rows = kTabThreads / (p.half / 4) * kTabRows;
+  rope_tables_kernel<<<static_cast<unsigned>((static_cast<int64_t>(p.positions) + rows - 1) / rows), kTabThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fl

@@ -9,7 +9,7 @@ import ctypes
 import torch
 
 from . import _lib
-from .api import _empty_on, _need, _raw_stream, _stream_ptr
+from .api import _empty_on, _need, _raw_stream, _stream_ptr, _zeros_on
 from ._lib import KV_FORMATS, MASKS, SCORE_MODS
 
 _SCALE_BLOCK = 16
@@ -260,4 +260,110 @@ def attn_paged_decode_fwd(q, cache: PagedKVCache, kv_len, block_table, *, mask: 
                                     workspace.numel() * workspace.element_size(), desc)
     if st:
         _lib.check(st, "fl_attn_paged_decode_fwd")
+    return out, lse
+
+
+def _offsets_ptr(seq_offsets, B, T, index) -> int:
+    """Checks the packed rows' offsets; returns their address (0: one row a sequence)."""
+    if seq_offsets is None:
+        if T != B:
+            raise ValueError("without seq_offsets every sequence has one row")
+        return 0
+    _check(seq_offsets, "seq_offsets", 1, _I32, index)
+    if seq_offsets.shape[0] != B + 1 or not seq_offsets.is_contiguous():
+        raise ValueError("seq_offsets must be contiguous [B + 1]")
+    return seq_offsets.data_ptr()
+
+
+def kv_read(cache: PagedKVCache, kv_len, block_table, T: int, *, seq_offsets=None, k_out=None, v_out=None, stream=None):
+    """fl_kv_read: what the cache holds for T packed rows, the last n_b =
+    seq_offsets[b + 1] - seq_offsets[b] of the first kv_len[b] tokens of every
+    sequence (seq_offsets None: the last one).  Returns (k_out, v_out), bf16
+    [T, Hkv, d], allocated (zeroed, since rows may be left) when not given."""
+    index = cache.index
+    _current(index)
+    B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
+    T = int(T)
+    offsets = _offsets_ptr(seq_offsets, B, T, index)
+    shape = (T, cache.Hkv, cache.d)
+    if k_out is None:
+        k_out = _zeros_on(stream, shape, _BF16, cache.device)
+    if v_out is None:
+        v_out = _zeros_on(stream, shape, _BF16, cache.device)
+    kos, vos = _rows(k_out, "k_out", *shape, index), _rows(v_out, "v_out", *shape, index)
+    desc = _lib.READ_PACK(T, B, max_pages, 0, offsets, kv_len.data_ptr(), block_table.data_ptr(), table_stride, *kos, *vos,
+                          _raw_stream(index) if stream is None else _stream_ptr(stream))
+    st = _lib.lib().fl_kv_read(cache._ref, k_out.data_ptr(), v_out.data_ptr(), desc)
+    if st:
+        _lib.check(st, "fl_kv_read")
+    return k_out, v_out
+
+
+def _prefill_desc(q, cache, B, columns, **kw):
+    T, Hq, d = q.shape
+    return _lib.desc_pack(B, Hq, cache.Hkv, T, columns * cache.page_size, d, d, **kw)
+
+
+def attn_paged_prefill_workspace_size(q, cache: PagedKVCache, block_table) -> int:
+    """fl_attn_paged_prefill_workspace_size: bytes of workspace that a call
+    with these arguments needs."""
+    _check(q, "q", 3, _BF16, cache.index)
+    _check(block_table, "block_table", 2, _I32, cache.index)
+    _current(cache.index)
+    return int(_lib.lib().fl_attn_paged_prefill_workspace_size(_prefill_desc(q, cache, *block_table.shape), cache._ref))
+
+
+def attn_paged_prefill_fwd(q, cache: PagedKVCache, kv_len, block_table, *, seq_offsets=None, mask: str = "causal",
+                           window: int | None = None, sink: int | None = None, score_mod: str = "none",
+                           alibi_slopes=None, softcap: float | None = None, scale: float | None = None, out=None,
+                           lse=None, return_lse: bool = True, workspace=None, stream=None, debug_flags: int = 0,
+                           debug_arg: int = -1, wait_limit_ms: int = 0):
+    """fl_attn_paged_prefill_fwd: the packed new tokens q [T, Hq, d] bf16 (any
+    token and head strides that are multiples of 8) of B sequences, rows
+    seq_offsets[b] to seq_offsets[b + 1] at the last positions of the first
+    kv_len[b] cached tokens (seq_offsets None: one row per sequence); mask
+    "causal", "none" or "window" (with ``window`` and ``sink``).  The workspace
+    is allocated with torch when not given.  Returns (out [T, Hq, d] bf16, lse
+    [T, Hq] fp32 or None)."""
+    index = cache.index
+    _current(index)
+    B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
+    _check(q, "q", 3, _BF16, index)
+    T, Hq, d = shape = q.shape
+    offsets = _offsets_ptr(seq_offsets, B, T, index)
+    if mask not in MASKS:
+        raise ValueError(f"unknown mask {mask!r}")
+    if score_mod not in SCORE_MODS:
+        raise ValueError(f"unknown score_mod {score_mod!r}")
+    slopes = 0
+    if alibi_slopes is not None:
+        _check(alibi_slopes, "alibi_slopes", 1, _F32, index)
+        if alibi_slopes.shape[0] != Hq or not alibi_slopes.is_contiguous():
+            raise ValueError("alibi_slopes must be contiguous [Hq]")
+        slopes = alibi_slopes.data_ptr()
+    if out is None:
+        out = _empty_on(stream, shape, _BF16, cache.device)
+    if lse is None and return_lse:
+        lse = _empty_on(stream, shape[:2], _F32, cache.device)
+    elif lse is not None:
+        _check(lse, "lse", 2, _F32, index)
+        if lse.shape != shape[:2] or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous [T, Hq]")
+    qs, os_ = _rows(q, "q", T, Hq, d, index), _rows(out, "out", T, Hq, d, index)
+    desc = _prefill_desc(q, cache, B, max_pages, scale=scale or 0.0, mask_kind=MASKS[mask], window=window or 0,
+                         sink=sink or 0, score_mod=SCORE_MODS[score_mod], softcap=softcap or 0.0, slopes=slopes,
+                         q_strides=(0, qs[1], qs[0], 1), o_strides=(0, os_[1], os_[0], 1),
+                         stream=_raw_stream(index) if stream is None else _stream_ptr(stream),
+                         debug_flags=debug_flags, debug_arg=debug_arg, wait_limit_ms=wait_limit_ms)
+    L = _lib.lib()
+    if workspace is None:
+        n = int(L.fl_attn_paged_prefill_workspace_size(desc, cache._ref))
+        workspace = _empty_on(stream, (max(n, 16),), torch.uint8, cache.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
+    st = L.fl_attn_paged_prefill_fwd(q.data_ptr(), cache._ref, offsets, kv_len.data_ptr(), block_table.data_ptr(),
+                                     table_stride, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel() * workspace.element_size(), desc)
+    if st:
+        _lib.check(st, "fl_attn_paged_prefill_fwd")
     return out, lse

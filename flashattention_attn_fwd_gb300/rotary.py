@@ -1,0 +1,149 @@
+"""Python binding of the rotary positions (include/flattn.h): rotation of queries
+and keys with its gradient, and the tables that it and ``kv_append`` read.  As in
+``api`` only arguments are marshalled here; the library's kernels do the work.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .api import _empty_on, _need, _stream_ptr
+from ._lib import ROPE_SCALINGS
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _strides(t, name):
+    """(b, h, l) strides; those of axes of length 1 are never used to step."""
+    sb, sh, sl, sc = t.stride()
+    if sc != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have a contiguous head dimension")
+    B, H, L, d = t.shape
+    return sb if B > 1 else H * L * d, sh if H > 1 else L * d, sl if L > 1 else d
+
+
+def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, q_out, k_out, stream):
+    _need(q, names[0], 4)
+    B, Hq, L, d = q.shape
+    index = q.get_device()
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"{names[0]} is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
+
+    def on_device(t, name):
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
+        _need(t, name, 2, _F32)
+        on_device(t, name)
+        if t.shape != rope_cos.shape or not t.is_contiguous():
+            raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
+    Hk = 0
+    if k is not None:
+        _need(k, names[1], 4)
+        on_device(k, names[1])
+        Hk = k.shape[1]
+        if k.shape[0] != B or k.shape[2] != L or k.shape[3] != d:
+            raise ValueError(f"{names[1]} must be [{B}, heads, {L}, {d}], got {list(k.shape)}")
+    elif k_out is not None:
+        raise ValueError(f"{names[3]} needs {names[1]}")
+    pos = pos_stride = 0
+    if positions is not None:
+        _need(positions, "positions", positions.dim() if isinstance(positions, torch.Tensor) else 2, _I32)
+        on_device(positions, "positions")
+        if tuple(positions.shape) not in ((B, L), (L,)):
+            raise ValueError(f"positions must be [{B}, {L}] or [{L}], got {list(positions.shape)}")
+        if L > 1 and positions.stride(-1) != 1:
+            raise ValueError("positions must have contiguous rows")
+        pos = positions.data_ptr()
+        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+    q_out = _empty_on(stream, q.shape, _BF16, q.device) if q_out is None else q_out
+    k_out = _empty_on(stream, k.shape, _BF16, k.device) if k is not None and k_out is None else k_out
+    for name, t, x in ((names[2], q_out, q), (names[3], k_out, k)):
+        if t is not None:
+            _need(t, name, 4)
+            on_device(t, name)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must be {list(x.shape)}, got {list(t.shape)}")
+    none = (0, 0, 0)
+    desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rope_cos.shape[0], 2 * rope_cos.shape[1], 1 if rope_interleaved else 0,
+                          rope_cos.data_ptr(), rope_sin.data_ptr(), pos, pos_stride, *_strides(q, names[0]),
+                          *(none if k is None else _strides(k, names[1])), *_strides(q_out, names[2]),
+                          *(none if k is None else _strides(k_out, names[3])), _stream_ptr(stream))
+    st = getattr(_lib.lib(), call)(q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
+                                   0 if k is None else k_out.data_ptr(), desc)
+    if st:
+        _lib.check(st, call)
+    return q_out, k_out
+
+
+def rope_fwd(q, k, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool = False, q_out=None, k_out=None,
+             stream=None):
+    """fl_rope_fwd: rotate q [B, Hq, L, d] and k [B, Hk, L, d] (or None), bf16
+    with any strides that are multiples of 8, by positions (int32 [B, L] or [L];
+    None: row l has position l); rope_cos, rope_sin fp32 [positions, rope_dim /
+    2].  Returns (q_out, k_out), contiguous when not given."""
+    return _rotate("fl_rope_fwd", ("q", "k", "q_out", "k_out"), q, k, rope_cos, rope_sin, positions, rope_interleaved,
+                   q_out, k_out, stream)
+
+
+def rope_bwd(dq_out, dk_out, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool = False, dq=None, dk=None,
+             stream=None):
+    """fl_rope_bwd: gradients (dq, dk) of rope_fwd's q and k for those of its
+    outputs, dq_out and dk_out (or None); the other arguments are the forward's."""
+    return _rotate("fl_rope_bwd", ("dq_out", "dk_out", "dq", "dk"), dq_out, dk_out, rope_cos, rope_sin, positions,
+                   rope_interleaved, dq, dk, stream)
+
+
+def _dense(t):
+    """A gradient with strides that the kernel takes (an expanded one has zeros)."""
+    if t is None or (t.stride(3) == 1 and all(s > 0 and s % 8 == 0 for s in t.stride()[:3]) and t.data_ptr() % 16 == 0):
+        return t
+    return t.contiguous()
+
+
+class _Rope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, rope_cos, rope_sin, positions, interleaved):
+        ctx.save_for_backward(rope_cos, rope_sin, positions)
+        ctx.interleaved = interleaved
+        return rope_fwd(q, k, rope_cos, rope_sin, positions=positions, rope_interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        rope_cos, rope_sin, positions = ctx.saved_tensors
+        dq, dk = rope_bwd(_dense(dq_out), _dense(dk_out), rope_cos, rope_sin, positions=positions, rope_interleaved=ctx.interleaved)
+        return dq, dk, None, None, None, None
+
+
+def rope(q, k, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool = False):
+    """Differentiable rotation of q and k: rope_fwd in the forward, rope_bwd in
+    the backward.  Returns contiguous (q, k) as ``attention`` takes them."""
+    return _Rope.apply(q, k, rope_cos, rope_sin, positions, rope_interleaved)
+
+
+def rope_tables(positions: int, rope_dim: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                original: int = 0, low_turns: float = 1.0, high_turns: float = 32.0, amplitude: float = 1.0, cos=None,
+                sin=None, device="cuda", stream=None):
+    """fl_rope_tables: (cos, sin) fp32 [positions, rope_dim / 2] of position times
+    base^(-2i / rope_dim), times amplitude.  For contexts longer than the model
+    was trained on, scaling "linear" (positions / factor), "ntk" (a larger base)
+    or "by_parts" (pairs that turn at least high_turns times in the ``original``
+    positions stay, those below low_turns are interpolated by factor)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    shape = (int(positions), int(rope_dim) // 2)
+    if cos is None:
+        cos = _empty_on(stream, shape, _F32, torch.device(device) if sin is None else sin.device)
+    if sin is None:
+        sin = _empty_on(stream, shape, _F32, cos.device)
+    for name, t in (("cos", cos), ("sin", sin)):
+        _need(t, name, 2, _F32)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    spec = _lib.SCALING_PACK(base, factor, low_turns, high_turns, ROPE_SCALINGS[scaling], original, amplitude, 0)
+    st = _lib.lib().fl_rope_tables(cos.data_ptr(), sin.data_ptr(), int(positions), int(rope_dim), spec, _stream_ptr(stream))
+    if st:
+        _lib.check(st, "fl_rope_tables")
+    return cos, sin

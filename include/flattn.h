@@ -358,9 +358,162 @@ FL_API fl_status fl_attn_paged_decode_fwd(const void* q, const fl_kv_cache* cach
    current device (0 on an invalid descriptor or without a device). */
 FL_API size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, const fl_kv_cache* cache);
 
-/* sizeof(fl_kv_cache) and sizeof(fl_kv_append_desc) as compiled (binding check). */
+/*
+ * Attention of chunks of new tokens over a paged cache (bf16 or 4-bit): prompts,
+ * whole or in pieces, drafts, and single tokens, packed in one call.  The Lq rows
+ * of B sequences are packed: sequence b owns rows [seq_offsets[b],
+ * seq_offsets[b + 1]), n_b of them (none is fine).  Its row i sits at position
+ * p = kv_len[b] - n_b + i, so that the new tokens' keys and values are in the
+ * cache already (fl_kv_append with the same seq_offsets and kv_len).  Keys are
+ * visible as in fl_attn_paged_decode_fwd; pages that hold no visible key may be
+ * missing from the table.
+ *   q, out      : bf16 [Lq, Hq, d]; desc->q_strides / o_strides (zero: contiguous,
+ *                 else element 0 is 0, then head and token strides of at least d,
+ *                 multiples of 8, and 1)
+ *   lse         : fp32 [Lq, Hq] contiguous, or NULL
+ *   seq_offsets : device int32 [B + 1], non-decreasing from 0; NULL: Lq == B, one
+ *                 row per sequence
+ *   kv_len      : device int32 [B], clamped to [0, max_pages * page_size]
+ *   block_table : device int32 [B, max_pages], rows table_stride apart
+ *   workspace   : caller-owned device buffer of at least
+ *                 fl_attn_paged_prefill_workspace_size() bytes, 16-byte aligned;
+ *                 calls that may overlap need one each
+ * desc: B, Hq, Hkv, Lq (all rows of the call, at most 2^30), d == dv (the cache's
+ * Hkv and d), Lk = max_pages * page_size, Hq / Hkv at most 128, mask NONE, CAUSAL
+ * or SLIDING_WINDOW, any score_mod, k_strides and v_strides zero.
+ * Left as they are: rows from seq_offsets[B] on.  A visible key whose page is
+ * outside the pool is left out and the call reports FL_ERR_DEVICE_BOUNDS through
+ * fl_sync_status.  Rows that see no key get out = 0 and lse = -inf (with CAUSAL and
+ * SLIDING_WINDOW those at negative positions, kv_len[b] < n_b, among them).  The
+ * work is cut by the lengths alone: a call's result is the same every time.
+ * Keys and values that no row of the call sees may hold anything.  A value that is
+ * not finite and that one row sees may reach rows of the same key/value head and
+ * sequence near that one (0 times it is a NaN).
+ */
+FL_API fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, const int32_t* seq_offsets,
+                                           const int32_t* kv_len, const int32_t* block_table, int64_t table_stride,
+                                           void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                           const fl_attn_desc* desc);
+
+/* Workspace bytes fl_attn_paged_prefill_fwd needs for `desc` and `cache` on the
+   current device (0 on an invalid descriptor or without a device). */
+FL_API size_t fl_attn_paged_prefill_workspace_size(const fl_attn_desc* desc, const fl_kv_cache* cache);
+
+/*
+ * Rows to read back from a paged cache, packed as fl_kv_append_desc's: row
+ * seq_offsets[b] + i is position kv_len[b] - n_b + i of sequence b.  Row strides are
+ * in elements, (token, head), multiples of 8; channels are contiguous.
+ */
+typedef struct fl_kv_read_desc {
+  int32_t T, B;
+  int32_t max_pages;            /* columns of block_table                      */
+  int32_t reserved0;
+  const int32_t* seq_offsets;   /* device int32 [B + 1], non-decreasing from 0;
+                                   NULL: T == B, one row per sequence          */
+  const int32_t* kv_len;        /* device int32 [B]                            */
+  const int32_t* block_table;   /* device int32 [B, max_pages]                 */
+  int64_t table_stride;         /* elements between rows of block_table        */
+  int64_t k_out_strides[2], v_out_strides[2];
+  void* stream;
+} fl_kv_read_desc;
+
+/*
+ * Read a paged cache back: the keys and values that it holds for the rows of
+ * `desc`, as bf16 (a sequence that leaves the pool, or whose cache is checked or
+ * goes to another kernel).
+ *   k_out, v_out : bf16 [T, Hkv, d]
+ * A bf16 cache's rows come as they are, a 4-bit one's as code * block scale *
+ * k_scale (v_scale), the last product rounded to fp32 and then to bf16: bit for
+ * bit what fl_kv_append gave as k_out and v_out.
+ * Left as they are: rows from seq_offsets[B] on, and rows whose position is
+ * negative.  A row whose position has no block_table column or a page outside the
+ * pool is left too, and the call reports FL_ERR_DEVICE_BOUNDS through
+ * fl_sync_status.
+ */
+FL_API fl_status fl_kv_read(const fl_kv_cache* cache, void* k_out, void* v_out, const fl_kv_read_desc* desc);
+
+/* sizeof(fl_kv_cache), sizeof(fl_kv_append_desc) and sizeof(fl_kv_read_desc) as
+   compiled (binding check). */
 FL_API int32_t fl_kv_cache_size(void);
 FL_API int32_t fl_kv_append_desc_size(void);
+FL_API int32_t fl_kv_read_desc_size(void);
+
+/*
+ * Rotary positions of queries and keys, for models that train (fl_kv_append
+ * rotates what it stores by itself, with the same formula and tables).
+ *   q [B, Hq, L, d], k [B, Hk, L, d], bf16; d in {32, 64, 128}
+ * The first rope_dim channels (a multiple of 16, at most d) are rotated in fp32,
+ * each product and sum rounded once, and rounded to bf16:
+ *   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin
+ * for each pair (x1, x2), cos and sin from row `position` of the tables; the rest
+ * passes through.  Row l of batch entry b takes positions[b][l], or l.
+ */
+typedef struct fl_rope_desc {
+  int32_t B, L, Hq, Hk, d;      /* Hk 0: no keys                               */
+  int32_t rope_positions, rope_dim;
+  int32_t rope_interleaved;     /* 0: channel c pairs with c + rope_dim / 2;
+                                   1: channel 2c with 2c + 1                   */
+  const float* rope_cos;        /* device fp32 [rope_positions, rope_dim / 2]  */
+  const float* rope_sin;
+  const int32_t* positions;     /* device int32, [b][l] at b * positions_stride
+                                   + l, or NULL: row l has position l          */
+  int64_t positions_stride;     /* 0: the same for every batch entry           */
+  int64_t q_strides[3], k_strides[3];          /* (b, h, l), elements,         */
+  int64_t q_out_strides[3], k_out_strides[3];  /* multiples of 8; zeros:
+                                                  contiguous                   */
+  void* stream;
+} fl_rope_desc;
+
+/*
+ * q_out and k_out: the rotated q and k (in place is fine with the same strides).
+ * A row whose position is not in the tables is left as it is, and the call
+ * reports FL_ERR_DEVICE_BOUNDS through fl_sync_status (with positions NULL, L is
+ * at most rope_positions).
+ */
+FL_API fl_status fl_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const fl_rope_desc* desc);
+
+/*
+ * The gradients dq, dk of fl_rope_fwd's q and k for the gradients dq_out, dk_out of
+ * its outputs: the rotation the other way, rounded as above.  desc: q_strides and
+ * k_strides are those of dq_out and dk_out, q_out_strides and k_out_strides those of
+ * dq and dk.
+ */
+FL_API fl_status fl_rope_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk, const fl_rope_desc* desc);
+
+/*
+ * How the angle inv_i that pair i of r = rope_dim channels turns by at every
+ * position is scaled for contexts longer than the model was trained on:
+ *   PLAIN     inv_i = base^(-2i / r)
+ *   LINEAR    inv_i / factor
+ *   NTK       that of the base  base * factor^(r / (r - 2))
+ *   BY_PARTS  inv_i (g + (1 - g) / factor),  g = (original inv_i / 2 pi - low_turns) /
+ *             (high_turns - low_turns) within [0, 1]: pairs that turn often within the
+ *             original context keep their angle, slow ones are interpolated
+ */
+typedef enum { FL_ROPE_PLAIN = 0, FL_ROPE_LINEAR = 1, FL_ROPE_NTK = 2, FL_ROPE_BY_PARTS = 3 } fl_rope_kind;
+
+typedef struct fl_rope_scaling {
+  double base;                   /* > 1                                         */
+  double factor;                 /* >= 1; not read by PLAIN                     */
+  double low_turns, high_turns;  /* BY_PARTS: 0 <= low_turns < high_turns       */
+  int32_t kind;                  /* fl_rope_kind                                */
+  int32_t original;              /* BY_PARTS: positions of the original context */
+  float amplitude;               /* > 0: factor of cos and sin                  */
+  int32_t reserved;              /* zero                                        */
+} fl_rope_scaling;
+
+/*
+ * The tables that fl_rope_fwd and fl_kv_append read: rope_cos[p][i] = amplitude
+ * cos(p inv_i), rope_sin the same, device fp32 [positions, rope_dim / 2], 16-byte
+ * aligned; rope_dim a multiple of 16, at most 128.  inv_i in fp64, angles as
+ * 64-bit fractions of a turn: at any position within a few roundings of fp32.
+ */
+FL_API fl_status fl_rope_tables(float* rope_cos, float* rope_sin, int32_t positions, int32_t rope_dim,
+                                const fl_rope_scaling* scaling, void* stream);
+
+/* sizeof(fl_rope_desc) and sizeof(fl_rope_scaling) as compiled (binding check). */
+FL_API int32_t fl_rope_desc_size(void);
+FL_API int32_t fl_rope_scaling_size(void);
 
 /*
  * Backward pass of fl_attn_fwd (the Flashlight wiki summary lists the
