@@ -27,9 +27,10 @@
 //   warp 0      bf16: Q, K and V by TMA, a box per page and 64 channels
 //   warps 1, 2  one thread each issues tcgen05.mma of slot 0, of slot 1
 //   warp 3      bf16: zeroes V's rows that no row of the unit sees
-//   warps 4-11  softmax, a warpgroup per slot and a thread per row
+//   warps 4-11  softmax, a warpgroup per slot and a thread per row; 4 bits: its
+//               row of Q, scaled, in fp16
 //   warps 12-15 4 bits: load codes and scales into registers a tile ahead, write
-//               K and V as fp16 into the swizzled tiles; scale Q to fp16
+//               K and V as fp16 into the swizzled tiles
 // K and V tiles alternate in one ring, so that at d 128 five 32 KB places hold
 // two and a half tiles beside Q.
 //
@@ -61,6 +62,7 @@ namespace fl {
 namespace {
 
 constexpr int kPfLead = 2;       // tiles that starting and ending a unit costs a block
+constexpr uint64_t kPfTurnNs = 4000;
 constexpr uint32_t kPfLift = 7;  // 4 bits: P carries 2^kPfLift
 
 template <int FMT, int D>
@@ -76,34 +78,18 @@ struct PfLayout {
   static constexpr int HALVES = D / 64;                // 64-channel halves of a row (128 bytes each)
   static constexpr int HALF = 128 * 128;               // bytes of one half of a tile
   static constexpr int TILE = HALVES * HALF;           // bytes of a K, V or Q tile
-  static constexpr int FIXED = 1024;                   // barriers and small arrays
-  static constexpr int QF = Q4 ? 2 * 128 * 4 : 0;      // 4 bits: the rows' factors
-  static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED - QF;
+  static constexpr int FIXED = 2048;                   // barriers and small arrays
+  static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED;
   static constexpr int SLOTS_FIT = (BUDGET - 2 * TILE) / TILE;
   static constexpr int NS = SLOTS_FIT > 8 ? 8 : SLOTS_FIT;  // ring places
   static_assert(NS >= 4, "ring too small");
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_QF = OFF_RING + NS * TILE;
-  static constexpr int OFF_FIXED = OFF_QF + QF;
+  static constexpr int OFF_FIXED = OFF_RING + NS * TILE;
   // at least 117 KB, so that one block (which owns TMEM) is resident per SM
   static constexpr int END = OFF_FIXED + FIXED + 1024;
   static constexpr int SMEM = END > 120 * 1024 ? END : 120 * 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-};
-
-// Barriers and small arrays in the fixed area.
-template <int NS>
-struct PfShared {
-  uint64_t kv_full[NS], kv_empty[NS];
-  uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_lo[2], p_hi[2], pv_done[2], o_empty[2], drain[2];
-  uint64_t v_land[8];       // V tiles with rows to be zeroed: landed
-  int64_t scan[16];
-  int64_t found_base;
-  int found_b, found_qt, found_h;
-  uint32_t tmem, abort;
-  uint32_t bad[16];         // by tile: bits of 16-key groups whose page is not in the pool
-  uint32_t issued[NS];      // last load of each place: (barrier << 1 | parity) + 1, 0: none
 };
 
 // One (unit, head): tokens, keys, tiles.
@@ -114,6 +100,22 @@ struct PfUnit {
   int vis_lo, vis_end;  // some row sees keys [vis_lo, vis_end) and, below vis_end, [0, sink)
   int sinkt, skip, count;  // tile i is that of key 128 (i < sinkt ? i : i + skip)
   int64_t base;       // line position of tile 0
+};
+
+// Barriers and small arrays in the fixed area.
+template <int NS>
+struct PfShared {
+  uint64_t kv_full[NS], kv_empty[NS];
+  uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_lo[2], p_hi[2], pv_done[2], o_empty[2], drain[2];
+  uint64_t v_land[8];       // V tiles with rows to be zeroed: landed
+  int64_t scan[16];
+  PfUnit found;             // the piece's first unit; b < 0: none
+  uint32_t tmem, abort;
+  uint32_t bad[16];         // by tile: bits of 16-key groups whose page is not in the pool
+  uint32_t issued[NS];      // last load of each place: (barrier << 1 | parity) + 1, 0: none
+  uint32_t turn;            // tiles of which slot 0's products have been issued
+  int64_t per, begin, end;  // positions of the line per block; this block's
+  PfUnit unit[16];          // of every warp: where it is (in registers they would be spilled)
 };
 
 struct PfSeqs {
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&sh.q_full[i], Q4 ? 4 : 1);
-      ptx::mbar_init(&sh.q_empty[i], Q4 ? 5 : 1);
+      ptx::mbar_init(&sh.q_empty[i], 1);
       ptx::mbar_init(&sh.s_full[i], 1);
       ptx::mbar_init(&sh.s_free[i], 4);
       ptx::mbar_init(&sh.p_lo[i], 4);
@@ -225,7 +227,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     }
     for (int i = 0; i < 8; ++i) ptx::mbar_init(&sh.v_land[i], 1);
     sh.abort = 0u;
-    sh.found_b = -1;
+    sh.found.b = -1;
+    sh.turn = 0u;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
@@ -311,10 +314,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const int64_t c = kPfLead + un.count;
         if (at <= begin && begin < at + c * H) {
           const int h = static_cast<int>((begin - at) / c);
-          sh.found_b = un.b;
-          sh.found_qt = un.qt;
-          sh.found_h = h;
-          sh.found_base = at + h * c;
+          PfUnit f = un;
+          f.h = h;
+          f.base = at + h * c;
+          sh.found = f;
         }
         at += c * H;
       });
@@ -328,38 +331,45 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   const uint64_t drain_ns = 50ull * 1000ull * 1000ull;
   ptx::launch_dependents();
 
-  PfUnit first;
-  const bool any = sh.found_b >= 0;
-  if (any) {
-    const int o = seqs.offset(sh.found_b);
-    seqs.fill(first, sh.found_b, sh.found_qt, o, max(seqs.offset(sh.found_b + 1), o));
-    first.h = sh.found_h;
-    first.base = sh.found_base;
-  }
-  if (blockIdx.x > 0 && tid == 0) {
-    // is this block's border inside of a unit, and which pieces share that one
-    int32_t* r = p.rec + static_cast<int64_t>(blockIdx.x) * 8;
-    const int64_t t = any ? begin - first.base : 0;
-    const bool cut = any && t > 0 && t < first.count;
-    r[0] = cut ? 1 : 0;
-    if (cut) {
-      r[1] = first.tok0;
-      r[2] = first.ntok;
-      r[3] = first.h;
-      r[4] = static_cast<int>(first.base / per);
-      r[5] = static_cast<int>((first.base + first.count - 1) / per);
+  if (tid == 0) {
+    sh.per = per;
+    sh.begin = begin;
+    sh.end = end;
+    if (blockIdx.x > 0) {
+      // is this block's border inside of a unit, and which pieces share that one
+      const PfUnit f = sh.found;
+      int32_t* r = p.rec + static_cast<int64_t>(blockIdx.x) * 8;
+      const int64_t t = f.b >= 0 ? begin - f.base : 0;
+      const bool cut = t > 0 && t < f.count;
+      r[0] = cut ? 1 : 0;
+      if (cut) {
+        r[1] = f.tok0;
+        r[2] = f.ntok;
+        r[3] = f.h;
+        r[4] = static_cast<int>(f.base / per);
+        r[5] = static_cast<int>((f.base + f.count - 1) / per);
+      }
     }
   }
+  __syncthreads();
   // calls f(unit, first tile, tile behind the last) for every unit of the piece
-  // that has tiles in it, until f fails
-  auto each_unit = [&](auto&& f) {
-    if (!any) return;
-    PfUnit u = first;
-    while (u.base < end) {
-      const int64_t t0 = begin - u.base, t1 = end - u.base;
-      const int a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(u.count))) : 0;
-      const int z = t1 < u.count ? static_cast<int>(t1) : u.count;
-      if (a < z && !f(u, a, z)) return;
+  // that has tiles in it, until f fails; by a whole warp, or by one lane of it
+  auto each_unit = [&](auto&& f, bool one_lane = false) {
+    PfUnit& at = sh.unit[warp];
+    PfUnit u = sh.found;
+    if (u.b < 0) return;
+    while (true) {
+      at = u;
+      if (!one_lane) __syncwarp();
+      const int64_t base = at.base;
+      const int count = at.count;
+      const int64_t t0 = sh.begin - base, t1 = sh.end - base;
+      if (t1 <= 0) return;
+      const int a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(count))) : 0;
+      const int z = t1 < count ? static_cast<int>(t1) : count;
+      if (a < z && !f(static_cast<const PfUnit&>(at), a, z)) return;
+      u = at;
+      if (!one_lane) __syncwarp();
       if (!seqs.next(u)) return;
     }
   };
@@ -378,7 +388,6 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const int sub = mine ? box % nsub : 0, half = mine ? box / nsub : 0;
       uint32_t e = 0, tile = 0, part = 0, qc[2] = {0u, 0u};
       int q_phase[2] = {-1, -1};
-      bool skipped = false;
       each_unit([&](const PfUnit& u, int a, int z) {
         // page of this lane's keys of tile i: num_pages (read as zeros) when no
         // row sees them, or (reported) when it is not in the pool
@@ -388,18 +397,6 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           return __ldg(p.table + u.b * p.table_stride + (j >> shift));
         };
         int next = lookup(a);
-        for (int s = 0; s < 2; ++s) {
-          if (u.ntok <= s * p.RT) continue;
-          if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
-          if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(&sh.q_full[s], p.RT * p.G * D * 2);
-            for (int x = 0; x < L::HALVES; ++x)
-              ptx::tma_load_4d(smem + L::OFF_Q + s * L::TILE + x * L::HALF, &tmQ, &sh.q_full[s], 64 * x, 0, u.h,
-                               u.tok0 + s * p.RT, pol_q);
-          }
-          q_phase[s] = static_cast<int>(qc[s] & 1u);
-          ++qc[s];
-        }
         for (int i = a; i < z; ++i, ++tile, e += 2) {
           const int j0 = pf_key(u, i);
           int page = next;
@@ -438,8 +435,21 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             if (mine && (lane >= 16) == (v == 1) && !skip)
               ptx::tma_load_4d(smem + L::OFF_RING + st * L::TILE + half * L::HALF + sub * sub_len * 128, v ? &tmV : &tmK, bar,
                                64 * half, nsub == 1 ? row : 0, u.h, page, pol_kv);
-            skipped |= skip;
             if (land) ++part;
+            if (i > a || v) continue;
+            // Q behind the first K, which need not wait for the last unit's end
+            for (int s = 0; s < 2; ++s) {
+              if (u.ntok <= s * p.RT) continue;
+              if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
+              if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(&sh.q_full[s], p.RT * p.G * D * 2);
+                for (int x = 0; x < L::HALVES; ++x)
+                  ptx::tma_load_4d(smem + L::OFF_Q + s * L::TILE + x * L::HALF, &tmQ, &sh.q_full[s], 64 * x, 0, u.h,
+                                   u.tok0 + s * p.RT, pol_q);
+              }
+              q_phase[s] = static_cast<int>(qc[s] & 1u);
+              ++qc[s];
+            }
           }
         }
         return true;
@@ -514,6 +524,16 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 16 * 128) >> 4), IDESC_O,
                       (acc || kb > 0) ? 1u : 0u);
       };
+      // Slot 1's products of a tile follow slot 0's, so that one slot's softmax runs
+      // under the other's products; left alone, the slots fall into step and then
+      // wait for the tensor core and for the softmax in turn.  Only an order:
+      // giving up is fine.
+      auto await_turn = [&](uint32_t tile) {
+        if (static_cast<int32_t>(*reinterpret_cast<volatile uint32_t*>(&sh.turn) - tile) > 0) return;
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (static_cast<int32_t>(*reinterpret_cast<volatile uint32_t*>(&sh.turn) - tile) <= 0)
+          if (ptx::globaltimer_ns() - t0 > kPfTurnNs) return;
+      };
       each_unit([&](const PfUnit& u, int a, int z) {
         const int n = z - a;
         if (u.ntok <= s * p.RT) {
@@ -531,6 +551,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           if (i == 0 && !wait_bar(&sh.o_empty[s], (qc & 1u) ^ 1u, ctl, 13)) return false;
           if (!full(e + 1, 16)) return false;
           if (!wait_bar(&sh.p_lo[s], pc & 1u, ctl, 14)) return false;
+          if (s == 1) await_turn(e >> 1);
           ptx::tc_fence_after();
           issue_pv(e + 1, i > 0, 0, 4);
           if (!wait_bar(&sh.p_hi[s], pc & 1u, ctl, 15)) return false;
@@ -540,10 +561,11 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ptx::mma_commit(&sh.pv_done[s]);
           ptx::mma_commit(&sh.kv_empty[(e + 1) % NS]);
           if (!kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
+          if (s == 0) *reinterpret_cast<volatile uint32_t*>(&sh.turn) = (e >> 1) + 1;
         }
         ++qc;
         return true;
-      });
+      }, true);
       // every MMA this thread issued must finish before TMEM is released
       ptx::mma_commit(&sh.drain[s]);
       wait_drain(&sh.drain[s], 0u, drain_ns);
@@ -558,13 +580,86 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     const uint32_t tS = tl + s * 128, tP = tl + kColP + s * kStrP, tO = tl + kColO + s * D;
     const int rtok = r / p.G, rg = r - rtok * p.G;
     const bool row_used = rtok < p.RT;
-    uint32_t qc = 0, sc = 0, tile = 0;
-    Ctl later = ctl;  // the limit once per tile of the other slot that is passed
+    uint32_t sc = 0, tile = 0;
+    int idle = 1;  // tiles of the other slot that were passed, in limits of a wait
+    // What is left to do for a unit when its tiles are done: that runs once the
+    // next unit's queries are on their way.
+    struct Rest {
+      float m, l;
+      int64_t row;   // of out and lse, or of the partial results
+      int h;
+      bool live, whole;
+    } rest{};
+    bool have_rest = false;
+    auto finish = [&]() -> bool {
+      have_rest = false;
+      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 30 + s))) return false;
+      ptx::tc_fence_after();
+      const float l = rest.l, lift = Q4 ? static_cast<float>(kPfLift) : 0.f;
+      const float lse2 = l > 0.f ? rest.m + __log2f(l) - lift : (l == l ? -CUDART_INF_F : l);
+      const float inv = l > 0.f || l != l ? (Q4 ? p.c.v_scale : 1.f) / l : 0.f;
+      if (rest.whole) {
+        // Four lanes exchange 16-byte pieces so that each stores its piece of four
+        // rows and the four together 64 bytes of a row: a thread's own row in
+        // 16-byte stores took five times as long (32 lines an instruction).
+        const int64_t at = rest.live ? rest.row * p.o_t + rest.h * p.o_h : -1;
+        if (rest.live && p.lse) p.lse[rest.row * p.Hq + rest.h] = lse2 * kLn2;
+        int64_t row[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32], w[4][4];
+          ptx::tmem_ld32(tO + c, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            w[q >> 2][q & 3] = ptx::pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+#pragma unroll
+          for (int st = 1; st < 4; st *= 2) {
+            const bool up = lane & st;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (q & st) continue;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[q][k] : w[q + st][k], st);
+                if (up) w[q][k] = t;
+                else w[q + st][k] = t;
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (row[k] >= 0) *reinterpret_cast<uint4*>(out + row[k] + c) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+        }
+      } else {
+        float4* op = reinterpret_cast<float4*>(p.opart) + rest.row * (D / 4) * 128 + r;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + c, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            op[(c / 4 + q) * 128] =
+                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                            __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        }
+        p.lpart[rest.row * 128 + r] = lse2;
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
+      return true;
+    };
     each_unit([&](const PfUnit& u, int a, int z) {
-      const int n_tiles = z - a;
       if (u.ntok <= s * p.RT) {
-        tile += n_tiles;
-        later.timeout_ns += ctl.timeout_ns * n_tiles;
+        tile += z - a;
+        idle += z - a;
         return true;
       }
       // rows without a token take the last one's bounds (their results are dropped)
@@ -573,21 +668,49 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const int hi = p.causal ? min(pos, u.n - 1) : u.n - 1;
       const int lo = p.window ? max(pos - p.window + 1, 0) : 0;
       const int hq = u.h * p.G + rg;
-      float xmul = p.scale_log2, rf = 1.f;
-      if (Q4) {
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.q_full[s], qc & 1u, later, 27))) return false;
-        rf = reinterpret_cast<const float*>(smem + L::OFF_QF)[s * 128 + r];
+      const bool live = row_used && tok < u.ntok;
+      float rf = 1.f;
+      if constexpr (Q4) {
+        // The row of Q to fp16, scaled by a power of two that takes its largest channel
+        // to 2^14.  The last unit's Q is free: its last S is done (this warp has it).
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                          static_cast<int64_t>(u.tok0 + tok) * p.q_t + hq * p.q_h);
+        uint4 w[D / 8];
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) w[q] = live ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t mx = 0u;  // bf16 magnitudes order as integers
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q)
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[q].x & 0x7fff7fffu, w[q].y & 0x7fff7fffu),
+                                     __vmaxu2(w[q].z & 0x7fff7fffu, w[q].w & 0x7fff7fffu)));
+        const int ex = static_cast<int>((max(mx & 0xffffu, mx >> 16) >> 7) & 0xffu);  // biased exponent
+        // zeros, and rows whose largest is not finite, as they are; tiny ones by 2^110 at most
+        const int up = ex == 0 || ex == 255 ? 0 : min(14 - (ex - 127), 110);
+        const float f = __int_as_float((up + 127) << 23);
+        const uint32_t base = ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE + r * 128;
+#pragma unroll
+        for (int q = 0; q < D / 8; ++q) {
+          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[k] = pf_pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+          st_shared128(base + (q >> 3) * L::HALF + (((q & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+        rf = __int_as_float((127 - up) << 23);
+        ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.q_empty[s]);
-        xmul *= rf;
+        if (lane == 0) ptx::mbar_arrive(&sh.q_full[s]);
       }
-      if (SCORE != SCORE_NONE) xmul = 1.f;
+      if (have_rest && !finish()) return false;
+      const float xmul = SCORE == SCORE_NONE ? p.scale_log2 * rf : 1.f;
       const float slope2 = SCORE == SCORE_ALIBI ? __ldg(p.slopes + (row_used ? hq : 0)) * kLog2e : 0.f;
       float m = -CUDART_INF_F, l = 0.f;
       for (int i = a; i < z; ++i, ++sc, ++tile) {
         const int j0 = pf_key(u, i);
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], sc & 1u, later, 20 + s))) return false;
-        later.timeout_ns = ctl.timeout_ns;
+        if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], sc & 1u, Ctl{ctl.abort, p.status, p.timeout_ns * idle}, 20 + s)))
+          return false;
+        idle = 1;
         ptx::tc_fence_after();
         float x[128];
 #pragma unroll
@@ -685,15 +808,16 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         if (kSepP && sc > 0 && !__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s))) return false;
         ptx::tc_fence_after();
         if (i > a && any_raise) {
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            ptx::tmem_ld32(tO + c, o);
+          // a few columns at a time: the row's scores hold most registers
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld16(tO + c, o);
             ptx::tmem_ld_wait();
-            ptx::reg_fence32(o);
+            ptx::reg_fence16(o);
 #pragma unroll
-            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-            ptx::tmem_st32(tO + c, o);
+            for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            ptx::tmem_st16(tO + c, o);
           }
         }
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -718,65 +842,22 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const float2 lsum = ptx::add2(ls[0], ls[1]);
         l += lsum.x + lsum.y;
       }
-      // ---- the unit's end
-      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 30 + s))) return false;
-      ptx::tc_fence_after();
-      const bool live = row_used && tok < u.ntok;
-      const float lse2 = l > 0.f ? m + __log2f(l) - (Q4 ? static_cast<float>(kPfLift) : 0.f) : (l == l ? -CUDART_INF_F : l);
-      const float inv = l > 0.f || l != l ? (Q4 ? p.c.v_scale : 1.f) / l : 0.f;
-      if (n_tiles == u.count) {
-        const int64_t row = static_cast<int64_t>(u.tok0 + tok);
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * p.o_t + hq * p.o_h;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + c, o);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(o);
-          if (live) {
-#pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                w[k] = ptx::pack_bf16x2(__uint_as_float(o[q + 2 * k]) * inv, __uint_as_float(o[q + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + c + q) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        if (live && p.lse) p.lse[row * p.Hq + hq] = lse2 * kLn2;
-      } else {
-        // a partial result: of a unit that an earlier block began (0), or that a later one ends (1)
-        const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + (a > 0 ? 0 : 1)) * 2 + s;
-        float4* op = reinterpret_cast<float4*>(p.opart) + at * (D / 4) * 128 + r;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + c, o);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(o);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            op[(c / 4 + q) * 128] =
-                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                            __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-        }
-        p.lpart[at * 128 + r] = lse2;
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
-      ++qc;
+      // a partial result: of a unit that an earlier block began (0), or that a later one ends (1)
+      const bool whole = a == 0 && z == u.count;
+      rest = Rest{m, l, whole ? static_cast<int64_t>(u.tok0 + tok)
+                              : (static_cast<int64_t>(blockIdx.x) * 2 + (a > 0 ? 0 : 1)) * 2 + s,
+                  hq, live, whole};
+      have_rest = true;
       return true;
     });
+    if (have_rest && !*ctl.abort) finish();
   } else if constexpr (Q4) {
     // -------------------------------------- 4 bits: Q, K and V tiles in fp16
     ptx::setmaxnreg_dec<L::LOAD_REGS>();
-    const int r = tid - 384;  // key row of the tile, query row of the slot
-    const int rtok = r / p.G, rg = r - rtok * p.G;
+    const int r = tid - 384;  // key row of the tile
     const int row_off = r * 128;
     constexpr int W = D / 32;   // 16-byte words of a row's codes
-    uint32_t e = 0, tile = 0, qc[2] = {0u, 0u};
+    uint32_t e = 0, tile = 0;
     const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
     each_unit([&](const PfUnit& u, int a, int z) {
       uint4 kc[W], vc[W];
@@ -849,41 +930,6 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       int page = lookup(a), page1 = lookup(a + 1);
       load_k(a, page);
       load_v(a, page);
-      for (int s = 0; s < 2; ++s) {
-        if (u.ntok <= s * p.RT) continue;
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
-        ++qc[s];
-        // the row scaled by a power of two that takes its largest channel to 2^14
-        const bool ok = rtok < p.RT && s * p.RT + rtok < u.ntok;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                          static_cast<int64_t>(u.tok0 + (ok ? s * p.RT + rtok : 0)) * p.q_t +
-                                                          static_cast<int64_t>(u.h * p.G + (ok ? rg : 0)) * p.q_h);
-        uint32_t mx = 0u;  // bf16 magnitudes order as integers
-#pragma unroll 4
-        for (int q = 0; q < D / 8; ++q) {
-          const uint4 w = ok ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-        }
-        const int ex = static_cast<int>((max(mx & 0xffffu, mx >> 16) >> 7) & 0xffu);  // biased exponent
-        // zeros, and rows whose largest is not finite, as they are; tiny ones by 2^110 at most
-        const int up = ex == 0 || ex == 255 ? 0 : min(14 - (ex - 127), 110);
-        const float f = __int_as_float((up + 127) << 23);
-        const uint32_t base = ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE + row_off;
-#pragma unroll 4
-        for (int q = 0; q < D / 8; ++q) {
-          const uint4 w = ok ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = pf_pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
-          st_shared128(base + (q >> 3) * L::HALF + (((q & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-        }
-        reinterpret_cast<float*>(smem + L::OFF_QF)[s * 128 + r] = __int_as_float((127 - up) << 23);
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.q_full[s]);
-      }
       for (int i = a; i < z; ++i, ++tile, e += 2) {
         // page: this tile's; page1: the next one's
         const int page2 = lookup(i + 2);
