@@ -113,7 +113,7 @@ struct PfShared {
   uint32_t tmem, abort;
   uint32_t bad[16];         // by tile: bits of 16-key groups whose page is not in the pool
   uint32_t issued[NS];      // last load of each place: (barrier << 1 | parity) + 1, 0: none
-  uint32_t turn;            // tiles of which slot 0's products have been issued
+  uint32_t turn[2];         // tiles of which a slot's products have been issued
   int64_t per, begin, end;  // positions of the line per block; this block's
   PfUnit unit[16];          // of every warp: where it is (in registers they would be spilled)
 };
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     for (int i = 0; i < 8; ++i) ptx::mbar_init(&sh.v_land[i], 1);
     sh.abort = 0u;
     sh.found.b = -1;
-    sh.turn = 0u;
+    sh.turn[0] = sh.turn[1] = 0u;
     ptx::fence_mbar_init();
     ptx::fence_proxy_async_smem();
   }
@@ -524,16 +524,18 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 16 * 128) >> 4), IDESC_O,
                       (acc || kb > 0) ? 1u : 0u);
       };
-      // Slot 1's products of a tile follow slot 0's, so that one slot's softmax runs
-      // under the other's products; left alone, the slots fall into step and then
-      // wait for the tensor core and for the softmax in turn.  Only an order:
-      // giving up is fine.
-      auto await_turn = [&](uint32_t tile) {
-        if (static_cast<int32_t>(*reinterpret_cast<volatile uint32_t*>(&sh.turn) - tile) > 0) return;
+      // The slots take turns: slot 1's products of a tile follow slot 0's, and slot
+      // 0's of the next tile those, so that one slot's softmax runs under the other's
+      // products; left alone, the slots fall into step and then wait for the tensor
+      // core and for the softmax in turn.  Only an order: giving up is fine.
+      auto await_turn = [&](uint32_t tiles) {  // of the other slot
+        volatile uint32_t* t = &sh.turn[s ^ 1];
+        if (static_cast<int32_t>(*t - tiles) >= 0) return;
         const uint64_t t0 = ptx::globaltimer_ns();
-        while (static_cast<int32_t>(*reinterpret_cast<volatile uint32_t*>(&sh.turn) - tile) <= 0)
+        while (static_cast<int32_t>(*t - tiles) < 0)
           if (ptx::globaltimer_ns() - t0 > kPfTurnNs) return;
       };
+      auto my_turn_over = [&](uint32_t tiles) { *const_cast<volatile uint32_t*>(&sh.turn[s]) = tiles; };
       each_unit([&](const PfUnit& u, int a, int z) {
         const int n = z - a;
         if (u.ntok <= s * p.RT) {
@@ -541,6 +543,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           for (int i = 0; i < 2 * n; ++i, ++e) {
             if (!full(e, 17)) return false;
             ptx::mbar_arrive(&sh.kv_empty[e % NS]);
+            my_turn_over((e >> 1) + 1);
           }
           return true;
         }
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           if (i == 0 && !wait_bar(&sh.o_empty[s], (qc & 1u) ^ 1u, ctl, 13)) return false;
           if (!full(e + 1, 16)) return false;
           if (!wait_bar(&sh.p_lo[s], pc & 1u, ctl, 14)) return false;
-          if (s == 1) await_turn(e >> 1);
+          await_turn((e >> 1) + s);
           ptx::tc_fence_after();
           issue_pv(e + 1, i > 0, 0, 4);
           if (!wait_bar(&sh.p_hi[s], pc & 1u, ctl, 15)) return false;
@@ -561,7 +564,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ptx::mma_commit(&sh.pv_done[s]);
           ptx::mma_commit(&sh.kv_empty[(e + 1) % NS]);
           if (!kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
-          if (s == 0) *reinterpret_cast<volatile uint32_t*>(&sh.turn) = (e >> 1) + 1;
+          my_turn_over((e >> 1) + 1);
         }
         ++qc;
         return true;
