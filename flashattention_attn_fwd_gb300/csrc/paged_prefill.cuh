@@ -25,7 +25,7 @@
 //
 // Roles of a block (bf16 384 threads, 4 bits 512):
 //   warp 0      bf16: Q, K and V by TMA, a box per page and 64 channels
-//   warps 1, 2  one thread each issues tcgen05.mma of slot 0, of slot 1
+//   warps 1, 2  issue tcgen05.mma: d 64 one warp a slot, d 128 warp 1 for both
 //   warp 3      bf16: zeroes V's rows that no row of the unit sees
 //   warps 4-11  softmax, a warpgroup per slot and a thread per row; 4 bits: its
 //               row of Q, scaled, in fp16
@@ -71,8 +71,8 @@ struct PfLayout {
   static constexpr int THREADS = Q4 ? 512 : 384;
   // registers per thread: at launch, then of the control, softmax and loading warpgroups
   static constexpr int LAUNCH_REGS = Q4 ? 128 : 168;
-  static constexpr int CTL_REGS = Q4 ? 48 : 56;
-  static constexpr int SOFT_REGS = Q4 ? 192 : 224;
+  static constexpr int CTL_REGS = Q4 ? 64 : 72;
+  static constexpr int SOFT_REGS = Q4 ? 184 : 216;
   static constexpr int LOAD_REGS = Q4 ? 80 : 0;
   static_assert(CTL_REGS + 2 * SOFT_REGS + LOAD_REGS <= (THREADS / 128) * LAUNCH_REGS, "register split");
   static constexpr int HALVES = D / 64;                // 64-channel halves of a row (128 bytes each)
@@ -187,6 +187,16 @@ __device__ __forceinline__ uint32_t pf_pack_f16(float lo, float hi) {
 }
 __device__ __forceinline__ void st_shared128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// One lane of the converged warp.  The warps that issue tcgen05.mma stay converged
+// and wait with all lanes: a lane that went its own way had 200 cycles between a
+// wait and its next product, time in which the tensor core runs dry (it is fed a
+// product or two ahead).
+__device__ __forceinline__ bool pf_elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0u;
 }
 
 template <int FMT, int D, int SCORE>
@@ -353,14 +363,14 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   }
   __syncthreads();
   // calls f(unit, first tile, tile behind the last) for every unit of the piece
-  // that has tiles in it, until f fails; by a whole warp, or by one lane of it
-  auto each_unit = [&](auto&& f, bool one_lane = false) {
+  // that has tiles in it, until f fails; by a whole warp
+  auto each_unit = [&](auto&& f) {
     PfUnit& at = sh.unit[warp];
     PfUnit u = sh.found;
     if (u.b < 0) return;
     while (true) {
       at = u;
-      if (!one_lane) __syncwarp();
+      __syncwarp();
       const int64_t base = at.base;
       const int count = at.count;
       const int64_t t0 = sh.begin - base, t1 = sh.end - base;
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const int z = t1 < count ? static_cast<int>(t1) : count;
       if (a < z && !f(static_cast<const PfUnit&>(at), a, z)) return;
       u = at;
-      if (!one_lane) __syncwarp();
+      __syncwarp();
       if (!seqs.next(u)) return;
     }
   };
@@ -491,20 +501,25 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         }
         return true;
       });
-    } else if ((warp == 1 || warp == 2) && lane == 0) {
+    } else if (warp == 1 || (kSepP && warp == 2)) {
       // ------------------------------------------------------------ MMA issue
-      const int s = warp - 1;
+      // A commit, too, costs the tensor core its lead (60 cycles where two follow
+      // one another), so that there is one for S and one where P V has to be known
+      // as done; the places of K and V are given back by the softmax warps, which
+      // wait for those anyway.
       constexpr uint32_t kTypes = Q4 ? ~((1u << 7) | (1u << 10)) : ~0u;  // fp16 operands
       constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(128, 128, false) & kTypes;
       constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(128, D, true) & kTypes;
       const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
-      const uint64_t qd = ptx::smem_desc(ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE, 16, 1024, 2u);
-      uint32_t e = 0, qc = 0, sc = 0, pc = 0;
-      auto full = [&](uint32_t ev, int where) { return wait_bar(&sh.kv_full[ev % NS], (ev / NS) & 1u, ctl, where); };
-      auto issue_s = [&](uint32_t ev, bool last) -> bool {
-        if (!full(ev, 11)) return false;
-        if (kSepP && !wait_bar(&sh.s_free[s], (sc & 1u) ^ 1u, ctl, 12)) return false;
-        ptx::tc_fence_after();
+      const uint32_t qa = ptx::smem_u32(smem + L::OFF_Q);
+      auto wait = [&](uint64_t* bar, uint32_t parity, int where) { return wait_bar(bar, parity & 1u, ctl, where); };
+      auto full = [&](uint32_t ev, int where) { return wait(&sh.kv_full[ev % NS], ev / NS, where); };
+      auto free_place = [&](uint32_t ev) {
+        if (lane == 0) ptx::mbar_arrive(&sh.kv_empty[ev % NS]);
+      };
+      // by the elected lane
+      auto issue_s = [&](int s, uint32_t ev) {
+        const uint64_t qd = ptx::smem_desc(qa + s * L::TILE, 16, 1024, 2u);
         const uint64_t kd = ptx::smem_desc(ring + (ev % NS) * L::TILE, 16, 1024, 2u);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
@@ -512,66 +527,121 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ptx::mma_ss(tmem + s * 128, qd + off, kd + off, IDESC_S, kb > 0 ? 1u : 0u);
         }
         ptx::mma_commit(&sh.s_full[s]);
-        ptx::mma_commit(&sh.kv_empty[ev % NS]);
-        if (last) ptx::mma_commit(&sh.q_empty[s]);
-        ++sc;
-        return true;
       };
-      auto issue_pv = [&](uint32_t ev, bool acc, int kb0, int kb1) {
+      auto issue_pv = [&](int s, uint32_t ev, bool acc, int kb0) {
         const uint64_t vd = ptx::smem_desc(ring + (ev % NS) * L::TILE, L::HALF, 1024, 2u);
 #pragma unroll
-        for (int kb = kb0; kb < kb1; ++kb)
+        for (int k = 0; k < 4; ++k) {
+          const int kb = kb0 + k;
           ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 16 * 128) >> 4), IDESC_O,
                       (acc || kb > 0) ? 1u : 0u);
+        }
       };
-      // The slots take turns: slot 1's products of a tile follow slot 0's, and slot
-      // 0's of the next tile those, so that one slot's softmax runs under the other's
-      // products; left alone, the slots fall into step and then wait for the tensor
-      // core and for the softmax in turn.  Only an order: giving up is fine.
-      auto await_turn = [&](uint32_t tiles) {  // of the other slot
-        volatile uint32_t* t = &sh.turn[s ^ 1];
-        if (static_cast<int32_t>(*t - tiles) >= 0) return;
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (static_cast<int32_t>(*t - tiles) < 0)
-          if (ptx::globaltimer_ns() - t0 > kPfTurnNs) return;
-      };
-      auto my_turn_over = [&](uint32_t tiles) { *const_cast<volatile uint32_t*>(&sh.turn[s]) = tiles; };
-      each_unit([&](const PfUnit& u, int a, int z) {
-        const int n = z - a;
-        if (u.ntok <= s * p.RT) {
-          // no rows in this slot: pass the unit's tiles
-          for (int i = 0; i < 2 * n; ++i, ++e) {
-            if (!full(e, 17)) return false;
-            ptx::mbar_arrive(&sh.kv_empty[e % NS]);
+      uint32_t e = 0;
+      if constexpr (!kSepP) {
+        // d 128, P over S: P V and then the next S of one slot, then of the other,
+        // so that one slot's softmax runs under the other's products
+        uint32_t qc = 0u, pc = 0u;  // bit s: the phase of slot s
+        each_unit([&](const PfUnit& u, int a, int z) {
+          const int n = z - a;
+          const int slots = u.ntok > p.RT ? 2 : 1;  // with rows
+          if (!full(e, 11)) return false;
+#pragma unroll 1
+          for (int s = 0; s < slots; ++s) {
+            if (!wait(&sh.q_full[s], qc >> s, 10)) return false;
+            ptx::tc_fence_after();
+            if (pf_elect()) issue_s(s, e);
+          }
+          if (slots < 2) free_place(e);
+          for (int i = 0; i < n; ++i, e += 2) {
+            const bool more = i + 1 < n;
+            if (!full(e + 1, 16) || (more && !full(e + 2, 11))) return false;
+            if (slots < 2) {
+              free_place(e + 1);
+              if (more) free_place(e + 2);
+            }
+#pragma unroll 1
+            for (int s = 0; s < slots; ++s) {
+              if (i == 0 && !wait(&sh.o_empty[s], (qc >> s) + 1u, 13)) return false;
+              if (!wait(&sh.p_lo[s], pc >> s, 14)) return false;
+              ptx::tc_fence_after();
+              if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
+              if (!wait(&sh.p_hi[s], pc >> s, 15)) return false;
+              ptx::tc_fence_after();
+              if (pf_elect()) {
+                issue_pv(s, e + 1, true, 4);
+                if (more) issue_s(s, e + 2);
+                else ptx::mma_commit(&sh.pv_done[s]);
+              }
+              pc ^= 1u << s;
+            }
+          }
+          qc ^= slots < 2 ? 1u : 3u;
+          return true;
+        });
+      } else {
+        // d 64, P beside S: a warp a slot; the next S as soon as this one is in
+        // registers.  The slots' P V take turns: slot 1's of a tile follows slot 0's,
+        // and slot 0's of the next tile that one; left alone, the slots fall into step.
+        // Only an order: giving up is fine.
+        const int s = warp - 1;
+        uint32_t qc = 0, sc = 0, pc = 0;
+        auto await_turn = [&](uint32_t tiles) {  // of the other slot
+          volatile uint32_t* t = &sh.turn[s ^ 1];
+          if (static_cast<int32_t>(*t - tiles) >= 0) return;
+          const uint64_t t0 = ptx::globaltimer_ns();
+          while (static_cast<int32_t>(*t - tiles) < 0)
+            if (ptx::globaltimer_ns() - t0 > kPfTurnNs) return;
+        };
+        auto my_turn_over = [&](uint32_t tiles) {
+          if (lane == 0) *const_cast<volatile uint32_t*>(&sh.turn[s]) = tiles;
+        };
+        auto next_s = [&](uint32_t ev) {
+          if (!full(ev, 11) || !wait(&sh.s_free[s], sc + 1u, 12)) return false;
+          ptx::tc_fence_after();
+          if (pf_elect()) issue_s(s, ev);
+          ++sc;
+          return true;
+        };
+        each_unit([&](const PfUnit& u, int a, int z) {
+          const int n = z - a;
+          if (u.ntok <= s * p.RT) {
+            // no rows in this slot: pass the unit's tiles
+            for (int i = 0; i < 2 * n; ++i, ++e) {
+              if (!full(e, 17)) return false;
+              free_place(e);
+              my_turn_over((e >> 1) + 1);
+            }
+            return true;
+          }
+          if (!wait(&sh.q_full[s], qc, 10) || !next_s(e)) return false;
+          for (int i = 0; i < n; ++i, e += 2) {
+            if (i + 1 < n && !next_s(e + 2)) return false;
+            if (i == 0 && !wait(&sh.o_empty[s], qc + 1u, 13)) return false;
+            if (!full(e + 1, 16)) return false;
+            await_turn((e >> 1) + s);
+            if (!wait(&sh.p_lo[s], pc, 14)) return false;
+            ptx::tc_fence_after();
+            if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
+            if (!wait(&sh.p_hi[s], pc, 15)) return false;
+            ptx::tc_fence_after();
+            if (pf_elect()) {
+              issue_pv(s, e + 1, true, 4);
+              ptx::mma_commit(&sh.pv_done[s]);
+            }
+            ++pc;
             my_turn_over((e >> 1) + 1);
           }
+          ++qc;
           return true;
-        }
-        if (!wait_bar(&sh.q_full[s], qc & 1u, ctl, 10)) return false;
-        if (!issue_s(e, n == 1)) return false;
-        for (int i = 0; i < n; ++i, e += 2) {
-          if (kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
-          if (i == 0 && !wait_bar(&sh.o_empty[s], (qc & 1u) ^ 1u, ctl, 13)) return false;
-          if (!full(e + 1, 16)) return false;
-          if (!wait_bar(&sh.p_lo[s], pc & 1u, ctl, 14)) return false;
-          await_turn((e >> 1) + s);
-          ptx::tc_fence_after();
-          issue_pv(e + 1, i > 0, 0, 4);
-          if (!wait_bar(&sh.p_hi[s], pc & 1u, ctl, 15)) return false;
-          ptx::tc_fence_after();
-          issue_pv(e + 1, true, 4, 8);
-          ++pc;
-          ptx::mma_commit(&sh.pv_done[s]);
-          ptx::mma_commit(&sh.kv_empty[(e + 1) % NS]);
-          if (!kSepP && i + 1 < n && !issue_s(e + 2, i + 2 == n)) return false;
-          my_turn_over((e >> 1) + 1);
-        }
-        ++qc;
-        return true;
-      }, true);
-      // every MMA this thread issued must finish before TMEM is released
-      ptx::mma_commit(&sh.drain[s]);
-      wait_drain(&sh.drain[s], 0u, drain_ns);
+        });
+      }
+      // every MMA that was issued must finish before TMEM is released
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mma_commit(&sh.drain[warp - 1]);
+        wait_drain(&sh.drain[warp - 1], 0u, drain_ns);
+      }
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -590,13 +660,21 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     struct Rest {
       float m, l;
       int64_t row;   // of out and lse, or of the partial results
+      uint32_t tile; // the last one
       int h;
       bool live, whole;
     } rest{};
     bool have_rest = false;
+    // the place of the ring that entry ev (2 tile: K, 2 tile + 1: V) had, for this slot
+    auto free_place = [&](uint32_t ev) {
+      if (lane == 0 && quad == 0) ptx::mbar_arrive(&sh.kv_empty[ev % NS]);
+    };
+    uint32_t units = 0;  // of this slot
     auto finish = [&]() -> bool {
       have_rest = false;
-      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 30 + s))) return false;
+      const uint32_t done = kSepP ? sc - 1 : units - 1;  // phases: a tile each, or (d 128) a unit each
+      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], done & 1u, ctl, 30 + s))) return false;
+      free_place(2 * rest.tile + 1);
       ptx::tc_fence_after();
       const float l = rest.l, lift = Q4 ? static_cast<float>(kPfLift) : 0.f;
       const float lse2 = l > 0.f ? rest.m + __log2f(l) - lift : (l == l ? -CUDART_INF_F : l);
@@ -714,6 +792,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], sc & 1u, Ctl{ctl.abort, p.status, p.timeout_ns * idle}, 20 + s)))
           return false;
         idle = 1;
+        free_place(2 * tile);
+        // d 128: that S was issued behind the last tile's P V
+        if (!kSepP && i > a) free_place(2 * tile - 1);
+        if (!Q4 && i + 1 == z && lane == 0 && quad == 0) ptx::mbar_arrive(&sh.q_empty[s]);
         ptx::tc_fence_after();
         float x[128];
 #pragma unroll
@@ -808,7 +890,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const float sub = (Q4 ? static_cast<float>(kPfLift) : 0.f) - (m == -CUDART_INF_F ? 0.f : m);
         const float2 negm = make_float2(sub, sub), xm2 = make_float2(xmul, xmul);
         // P and O may change once the previous P V is done (d 128: it was, before this S)
-        if (kSepP && sc > 0 && !__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s))) return false;
+        if (kSepP && i > a) {
+          if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s))) return false;
+          free_place(2 * tile - 1);
+        }
         ptx::tc_fence_after();
         if (i > a && any_raise) {
           // a few columns at a time: the row's scores hold most registers
@@ -849,8 +934,9 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const bool whole = a == 0 && z == u.count;
       rest = Rest{m, l, whole ? static_cast<int64_t>(u.tok0 + tok)
                               : (static_cast<int64_t>(blockIdx.x) * 2 + (a > 0 ? 0 : 1)) * 2 + s,
-                  hq, live, whole};
+                  tile - 1, hq, live, whole};
       have_rest = true;
+      ++units;
       return true;
     });
     if (have_rest && !*ctl.abort) finish();
