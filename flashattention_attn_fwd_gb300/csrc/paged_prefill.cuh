@@ -491,10 +491,12 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           later.timeout_ns = ctl.timeout_ns;
           ++part;
           const uint32_t base = ptx::smem_u32(smem + L::OFF_RING + st * L::TILE);
-          for (int x = lane; x < 128 * L::HALVES * 8; x += 32) {
-            const int r = (x >> 3) & 127;
-            if (!pf_seen(p, u, j0 + r)) st_shared128(base + x * 16, 0u, 0u, 0u, 0u);
-          }
+          const int end = u.vis_end - j0, from = u.vis_lo - j0, sinks = p.sink - j0;
+#pragma unroll 4
+          for (int r = lane >> 3; r < 128; r += 4)
+            if (r >= end || (r < from && r >= sinks))
+#pragma unroll
+              for (int h = 0; h < L::HALVES; ++h) st_shared128(base + h * L::HALF + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.kv_full[st]);
@@ -537,6 +539,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
                       (acc || kb > 0) ? 1u : 0u);
         }
       };
+      const bool leader = pf_elect();
       uint32_t e = 0;
       if constexpr (!kSepP) {
         // d 128, P over S: P V and then the next S of one slot, then of the other,
@@ -550,30 +553,39 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           for (int s = 0; s < slots; ++s) {
             if (!wait(&sh.q_full[s], qc >> s, 10)) return false;
             ptx::tc_fence_after();
-            if (pf_elect()) issue_s(s, e);
+            if (leader) issue_s(s, e);
           }
           if (slots < 2) free_place(e);
           for (int i = 0; i < n; ++i, e += 2) {
             const bool more = i + 1 < n;
-            if (!full(e + 1, 16) || (more && !full(e + 2, 11))) return false;
-            if (slots < 2) {
-              free_place(e + 1);
-              if (more) free_place(e + 2);
-            }
 #pragma unroll 1
             for (int s = 0; s < slots; ++s) {
-              if (i == 0 && !wait(&sh.o_empty[s], (qc >> s) + 1u, 13)) return false;
-              if (!wait(&sh.p_lo[s], pc >> s, 14)) return false;
+              // all at once first: one wait's latency, not four
+              uint64_t* v_bar = &sh.kv_full[(e + 1) % NS];
+              uint64_t* k_bar = &sh.kv_full[(e + 2) % NS];
+              const uint32_t v_ph = ((e + 1) / NS) & 1u, k_ph = ((e + 2) / NS) & 1u;
+              const bool v_ok = ptx::mbar_test_wait(v_bar, v_ph), k_ok = ptx::mbar_test_wait(k_bar, k_ph);
+              const bool o_ok = ptx::mbar_test_wait(&sh.o_empty[s], ((qc >> s) + 1u) & 1u);
+              const bool p_ok = ptx::mbar_test_wait(&sh.p_lo[s], (pc >> s) & 1u);
+              if (!(v_ok & (k_ok | !more) & (o_ok | (i > 0)) & p_ok)) {
+                if (!wait_bar(v_bar, v_ph, ctl, 16) || (more && !wait_bar(k_bar, k_ph, ctl, 11))) return false;
+                if (i == 0 && !wait(&sh.o_empty[s], (qc >> s) + 1u, 13)) return false;
+                if (!wait(&sh.p_lo[s], pc >> s, 14)) return false;
+              }
               ptx::tc_fence_after();
-              if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
+              if (leader) issue_pv(s, e + 1, i > 0, 0);
               if (!wait(&sh.p_hi[s], pc >> s, 15)) return false;
               ptx::tc_fence_after();
-              if (pf_elect()) {
+              if (leader) {
                 issue_pv(s, e + 1, true, 4);
                 if (more) issue_s(s, e + 2);
                 else ptx::mma_commit(&sh.pv_done[s]);
               }
               pc ^= 1u << s;
+            }
+            if (slots < 2) {
+              free_place(e + 1);
+              if (more) free_place(e + 2);
             }
           }
           qc ^= slots < 2 ? 1u : 3u;
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         auto next_s = [&](uint32_t ev) {
           if (!full(ev, 11) || !wait(&sh.s_free[s], sc + 1u, 12)) return false;
           ptx::tc_fence_after();
-          if (pf_elect()) issue_s(s, ev);
+          if (leader) issue_s(s, ev);
           ++sc;
           return true;
         };
@@ -622,10 +634,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             await_turn((e >> 1) + s);
             if (!wait(&sh.p_lo[s], pc, 14)) return false;
             ptx::tc_fence_after();
-            if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
+            if (leader) issue_pv(s, e + 1, i > 0, 0);
             if (!wait(&sh.p_hi[s], pc, 15)) return false;
             ptx::tc_fence_after();
-            if (pf_elect()) {
+            if (leader) {
               issue_pv(s, e + 1, true, 4);
               ptx::mma_commit(&sh.pv_done[s]);
             }
@@ -689,12 +701,15 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
+        uint32_t ob[2][32];
+        ptx::tmem_ld32(tO, ob[0]);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
-          uint32_t o[32], w[4][4];
-          ptx::tmem_ld32(tO + c, o);
+          uint32_t (&o)[32] = ob[c / 32 & 1];
+          uint32_t w[4][4];
           ptx::tmem_ld_wait();
           ptx::reg_fence32(o);
+          if (c + 32 < D) ptx::tmem_ld32(tO + c + 32, ob[(c / 32 + 1) & 1]);
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             w[q >> 2][q & 3] = ptx::pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
