@@ -71,8 +71,8 @@ struct PfLayout {
   static constexpr int THREADS = Q4 ? 512 : 384;
   // registers per thread: at launch, then of the control, softmax and loading warpgroups
   static constexpr int LAUNCH_REGS = Q4 ? 128 : 168;
-  static constexpr int CTL_REGS = Q4 ? 64 : 72;
-  static constexpr int SOFT_REGS = Q4 ? 184 : 216;
+  static constexpr int CTL_REGS = Q4 ? 64 : D == 128 ? 104 : 72;
+  static constexpr int SOFT_REGS = Q4 ? 184 : D == 128 ? 200 : 216;
   static constexpr int LOAD_REGS = Q4 ? 80 : 0;
   static_assert(CTL_REGS + 2 * SOFT_REGS + LOAD_REGS <= (THREADS / 128) * LAUNCH_REGS, "register split");
   static constexpr int HALVES = D / 64;                // 64-channel halves of a row (128 bytes each)
@@ -539,7 +539,6 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
                       (acc || kb > 0) ? 1u : 0u);
         }
       };
-      const bool leader = pf_elect();
       uint32_t e = 0;
       if constexpr (!kSepP) {
         // d 128, P over S: P V and then the next S of one slot, then of the other,
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           for (int s = 0; s < slots; ++s) {
             if (!wait(&sh.q_full[s], qc >> s, 10)) return false;
             ptx::tc_fence_after();
-            if (leader) issue_s(s, e);
+            if (pf_elect()) issue_s(s, e);
           }
           if (slots < 2) free_place(e);
           for (int i = 0; i < n; ++i, e += 2) {
@@ -573,10 +572,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
                 if (!wait(&sh.p_lo[s], pc >> s, 14)) return false;
               }
               ptx::tc_fence_after();
-              if (leader) issue_pv(s, e + 1, i > 0, 0);
+              if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
               if (!wait(&sh.p_hi[s], pc >> s, 15)) return false;
               ptx::tc_fence_after();
-              if (leader) {
+              if (pf_elect()) {
                 issue_pv(s, e + 1, true, 4);
                 if (more) issue_s(s, e + 2);
                 else ptx::mma_commit(&sh.pv_done[s]);
@@ -611,7 +610,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         auto next_s = [&](uint32_t ev) {
           if (!full(ev, 11) || !wait(&sh.s_free[s], sc + 1u, 12)) return false;
           ptx::tc_fence_after();
-          if (leader) issue_s(s, ev);
+          if (pf_elect()) issue_s(s, ev);
           ++sc;
           return true;
         };
@@ -634,10 +633,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             await_turn((e >> 1) + s);
             if (!wait(&sh.p_lo[s], pc, 14)) return false;
             ptx::tc_fence_after();
-            if (leader) issue_pv(s, e + 1, i > 0, 0);
+            if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
             if (!wait(&sh.p_hi[s], pc, 15)) return false;
             ptx::tc_fence_after();
-            if (leader) {
+            if (pf_elect()) {
               issue_pv(s, e + 1, true, 4);
               ptx::mma_commit(&sh.pv_done[s]);
             }
@@ -767,33 +766,47 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const bool live = row_used && tok < u.ntok;
       float rf = 1.f;
       if constexpr (Q4) {
-        // The row of Q to fp16, scaled by a power of two that takes its largest channel
-        // to 2^14.  The last unit's Q is free: its last S is done (this warp has it).
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                          static_cast<int64_t>(u.tok0 + tok) * p.q_t + hq * p.q_h);
-        uint4 w[D / 8];
+        // Q to fp16, each row scaled by a power of two that takes its largest channel to
+        // 2^14.  The last unit's Q is free: its last S is done (this warp has it).  Four
+        // lanes read 64 bytes of a row together, four rows in turn (a thread's own row in
+        // 16-byte loads took three times as long: 32 lines an instruction).
+        const int64_t at = live ? static_cast<int64_t>(u.tok0 + tok) * p.q_t + hq * p.q_h : -1;
+        const int r4 = lane & ~3, j4 = lane & 3;
+        uint4 w[4][D / 32];
 #pragma unroll
-        for (int q = 0; q < D / 8; ++q) w[q] = live ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t mx = 0u;  // bf16 magnitudes order as integers
+        for (int k = 0; k < 4; ++k) {
+          const int64_t row = __shfl_sync(0xffffffffu, at, r4 + k);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + row) + j4;
 #pragma unroll
-        for (int q = 0; q < D / 8; ++q)
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[q].x & 0x7fff7fffu, w[q].y & 0x7fff7fffu),
-                                     __vmaxu2(w[q].z & 0x7fff7fffu, w[q].w & 0x7fff7fffu)));
-        const int ex = static_cast<int>((max(mx & 0xffffu, mx >> 16) >> 7) & 0xffu);  // biased exponent
-        // zeros, and rows whose largest is not finite, as they are; tiny ones by 2^110 at most
-        const int up = ex == 0 || ex == 255 ? 0 : min(14 - (ex - 127), 110);
-        const float f = __int_as_float((up + 127) << 23);
-        const uint32_t base = ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE + r * 128;
-#pragma unroll
-        for (int q = 0; q < D / 8; ++q) {
-          const uint32_t x[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-          uint32_t y[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[k] = pf_pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
-          st_shared128(base + (q >> 3) * L::HALF + (((q & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+          for (int c = 0; c < D / 32; ++c) w[k][c] = row >= 0 ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
         }
-        rf = __int_as_float((127 - up) << 23);
+        const uint32_t base = ptx::smem_u32(smem + L::OFF_Q) + s * L::TILE + (quad * 32 + r4) * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t mx = 0u;  // bf16 magnitudes order as integers
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w[k][c].x & 0x7fff7fffu, w[k][c].y & 0x7fff7fffu),
+                                       __vmaxu2(w[k][c].z & 0x7fff7fffu, w[k][c].w & 0x7fff7fffu)));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int ex = static_cast<int>((max(mx & 0xffffu, mx >> 16) >> 7) & 0xffu);  // biased exponent
+          // zeros, and rows whose largest is not finite, as they are; tiny ones by 2^110 at most
+          const int up = ex == 0 || ex == 255 ? 0 : min(14 - (ex - 127), 110);
+          const float f = __int_as_float((up + 127) << 23);
+          if (k == j4) rf = __int_as_float((127 - up) << 23);
+          const int rx = (r4 + k) & 7;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int piece = 4 * c + j4;
+            const uint32_t x[4] = {w[k][c].x, w[k][c].y, w[k][c].z, w[k][c].w};
+            uint32_t y[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              y[q] = pf_pack_f16(__uint_as_float(x[q] << 16) * f, __uint_as_float(x[q] & 0xffff0000u) * f);
+            st_shared128(base + k * 128 + (piece >> 3) * L::HALF + (((piece & 7) ^ rx) << 4), y[0], y[1], y[2], y[3]);
+          }
+        }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.q_full[s]);

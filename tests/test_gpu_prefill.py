@@ -386,3 +386,46 @@ def test_chunks_tables_append_decode_and_read_together(fmt):
     for b in range(2):
         diff = torch.cat(got[b]).float() - full[b].transpose(0, 1).float()
         assert diff.abs().max() <= 2e-2 and diff.norm() <= 1e-2 * full[b].float().norm()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_grow_from_tile_to_tile(fmt, d):
+    """Keys whose scores rise by small and by large steps (up to hundreds, past
+    what a 32-bit exponential takes) in either half of a tile, for some rows and
+    not for others, and fall again: the running reference has to follow."""
+    Hq, Hkv, page, n = 2, 1, 64, 1500
+    lens, new = [n], [130]
+    pages = -(-n // page)
+    parts, K, V = pool(fmt, pages, Hkv, page, d, seed=21)
+    table = table_for(lens, page, pages, seed=22)
+    rng = np.random.default_rng(23)
+    level = np.zeros(n)
+    for at, to in ((40, 1.0), (100, 3.0), (130, 9.0), (250, 2.0), (300, 20.0), (460, 21.0), (600, 60.0), (1000, 5.0),
+                   (1100, 61.0), (1215, 300.0), (1300, 0.0)):
+        level[at:] = to
+    # every row's score of key j is about level[j] times the row's factor
+    factor = np.where(np.arange(130)[:, None] % 3 == 0, 0.0, 1.0) * np.array([1.0, -0.5])[None]
+    u = np.ones(d)
+    q = torch.from_numpy(factor[..., None] * u * np.sqrt(d) / 8 + 0.02 * rng.normal(size=(130, Hq, d))).bfloat16()
+    parts = [t.clone() if t is not None else None for t in parts]
+    for j in range(n):
+        pg, at = table[0, j // page], j % page
+        row = level[j] * 8.0 / d * u + 0.05 * rng.normal(size=d)
+        if fmt == "bf16":
+            parts[0][pg, 0, at] = torch.from_numpy(row).bfloat16()
+        else:
+            c, s8 = oracle.quantise(row, 1.0)
+            parts[0][pg, 0, at] = torch.from_numpy((c[0::2] | (c[1::2] << 4)).astype(np.uint8))
+            parts[2][pg, 0, at] = torch.from_numpy(s8.astype(np.uint8))
+    if fmt == "bf16":
+        K = parts[0].double().numpy()
+    else:
+        b = parts[0].numpy()
+        K = oracle.dequantise(np.stack((b & 15, b >> 4), -1).reshape(pages, Hkv, page, d), parts[2].numpy(), 1.0)
+    for kw in (dict(mask="causal"), dict(mask="window", window=400, sink=110)):
+        ref = reference(q, K, V, lens, new, table, **kw)
+        out, lse = attn_paged_prefill_fwd(q.to(DEV), make_cache(parts), dev(lens, torch.int32), dev(table),
+                                          seq_offsets=dev([0, 130], torch.int32), **kw)
+        sync_status()
+        check(out, lse, ref, fmt, d)
