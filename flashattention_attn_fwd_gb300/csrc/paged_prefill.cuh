@@ -362,26 +362,30 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     }
   }
   __syncthreads();
-  // calls f(unit, first tile, tile behind the last) for every unit of the piece
-  // that has tiles in it, until f fails; by a whole warp
-  auto each_unit = [&](auto&& f) {
+  // The warp's next unit that has tiles in this piece, into sh.unit[warp], and its
+  // tiles [a, z) there; not to be asked again once there is none.
+  bool begun = false;
+  auto next_unit = [&](int& a, int& z) -> bool {
     PfUnit& at = sh.unit[warp];
-    PfUnit u = sh.found;
-    if (u.b < 0) return;
     while (true) {
+      PfUnit u = begun ? at : sh.found;
+      __syncwarp();
+      if (begun ? !seqs.next(u) : u.b < 0) return false;
+      begun = true;
       at = u;
       __syncwarp();
-      const int64_t base = at.base;
-      const int count = at.count;
-      const int64_t t0 = sh.begin - base, t1 = sh.end - base;
-      if (t1 <= 0) return;
-      const int a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(count))) : 0;
-      const int z = t1 < count ? static_cast<int>(t1) : count;
-      if (a < z && !f(static_cast<const PfUnit&>(at), a, z)) return;
-      u = at;
-      __syncwarp();
-      if (!seqs.next(u)) return;
+      const int64_t t0 = sh.begin - u.base, t1 = sh.end - u.base;
+      if (t1 <= 0) return false;
+      a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(u.count))) : 0;
+      z = t1 < u.count ? static_cast<int>(t1) : u.count;
+      if (a < z) return true;
     }
+  };
+  // f(unit, a, z) for each of them, until f fails
+  auto each_unit = [&](auto&& f) {
+    int a, z;
+    while (next_unit(a, z))
+      if (!f(static_cast<const PfUnit&>(sh.unit[warp]), a, z)) return;
   };
   const int shift = p.c.page_shift;
   const int page_mask = (1 << shift) - 1;
@@ -542,20 +546,37 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       uint32_t e = 0;
       if constexpr (!kSepP) {
         // d 128, P over S: P V and then the next S of one slot, then of the other,
-        // so that one slot's softmax runs under the other's products
-        uint32_t qc = 0u, pc = 0u;  // bit s: the phase of slot s
-        each_unit([&](const PfUnit& u, int a, int z) {
-          const int n = z - a;
-          const int slots = u.ntok > p.RT ? 2 : 1;  // with rows
-          if (!full(e, 11)) return false;
-#pragma unroll 1
-          for (int s = 0; s < slots; ++s) {
-            if (!wait(&sh.q_full[s], qc >> s, 10)) return false;
-            ptx::tc_fence_after();
-            if (pf_elect()) issue_s(s, e);
+        // so that one slot's softmax runs under the other's products.  A unit's last P V
+        // is followed by the next unit's first S (4 bits: once both slots are through,
+        // since their queries come late).
+        constexpr bool kAhead = !Q4;
+        uint32_t qc = 0u, oc = 0u, pc = 0u;  // bit s: slot s's phases of Q, O and P
+        auto next_piece = [&](int& n, int& slots) {
+          int a, z;
+          if (!next_unit(a, z)) return false;
+          n = z - a;
+          slots = sh.unit[warp].ntok > p.RT ? 2 : 1;  // with rows
+          return true;
+        };
+        // a unit's first S of slot s, its K at ev
+        auto first_s = [&](int s, uint32_t ev) {
+          if (!full(ev, 11) || !wait(&sh.q_full[s], qc >> s, 10)) return false;
+          ptx::tc_fence_after();
+          if (pf_elect()) issue_s(s, ev);
+          qc ^= 1u << s;
+          return true;
+        };
+        int n = 0, slots = 0;
+        bool go = next_piece(n, slots);
+        bool ahead = false;  // the unit's first S is issued
+        while (go) {
+          if (!ahead) {
+            if (!first_s(0, e) || (slots > 1 && !first_s(1, e))) break;
+            if (slots < 2) free_place(e);
           }
-          if (slots < 2) free_place(e);
-          for (int i = 0; i < n; ++i, e += 2) {
+          int n1 = 0, slots1 = 0;
+          const bool go1 = next_piece(n1, slots1);
+          for (int i = 0; i < n && go; ++i, e += 2) {
             const bool more = i + 1 < n;
 #pragma unroll 1
             for (int s = 0; s < slots; ++s) {
@@ -564,16 +585,17 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
               uint64_t* k_bar = &sh.kv_full[(e + 2) % NS];
               const uint32_t v_ph = ((e + 1) / NS) & 1u, k_ph = ((e + 2) / NS) & 1u;
               const bool v_ok = ptx::mbar_test_wait(v_bar, v_ph), k_ok = ptx::mbar_test_wait(k_bar, k_ph);
-              const bool o_ok = ptx::mbar_test_wait(&sh.o_empty[s], ((qc >> s) + 1u) & 1u);
+              const bool o_ok = ptx::mbar_test_wait(&sh.o_empty[s], ((oc >> s) + 1u) & 1u);
               const bool p_ok = ptx::mbar_test_wait(&sh.p_lo[s], (pc >> s) & 1u);
               if (!(v_ok & (k_ok | !more) & (o_ok | (i > 0)) & p_ok)) {
-                if (!wait_bar(v_bar, v_ph, ctl, 16) || (more && !wait_bar(k_bar, k_ph, ctl, 11))) return false;
-                if (i == 0 && !wait(&sh.o_empty[s], (qc >> s) + 1u, 13)) return false;
-                if (!wait(&sh.p_lo[s], pc >> s, 14)) return false;
+                go = wait_bar(v_bar, v_ph, ctl, 16) && (!more || wait_bar(k_bar, k_ph, ctl, 11)) &&
+                     (i > 0 || wait(&sh.o_empty[s], (oc >> s) + 1u, 13)) && wait(&sh.p_lo[s], pc >> s, 14);
+                if (!go) break;
               }
               ptx::tc_fence_after();
               if (pf_elect()) issue_pv(s, e + 1, i > 0, 0);
-              if (!wait(&sh.p_hi[s], pc >> s, 15)) return false;
+              go = wait(&sh.p_hi[s], pc >> s, 15);
+              if (!go) break;
               ptx::tc_fence_after();
               if (pf_elect()) {
                 issue_pv(s, e + 1, true, 4);
@@ -581,15 +603,27 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
                 else ptx::mma_commit(&sh.pv_done[s]);
               }
               pc ^= 1u << s;
+              if (kAhead && !more && s < slots1) {
+                go = first_s(s, e + 2);
+                if (!go) break;
+              }
             }
             if (slots < 2) {
               free_place(e + 1);
               if (more) free_place(e + 2);
             }
           }
-          qc ^= slots < 2 ? 1u : 3u;
-          return true;
-        });
+          if (!go) break;
+          oc ^= slots < 2 ? 1u : 3u;
+          ahead = kAhead && go1;
+          if (ahead) {
+            if (slots1 < 2) free_place(e);
+            else if (slots < 2 && !first_s(1, e)) break;
+          }
+          n = n1;
+          slots = slots1;
+          go = go1;
+        }
       } else {
         // d 64, P beside S: a warp a slot; the next S as soon as this one is in
         // registers.  The slots' P V take turns: slot 1's of a tile follows slot 0's,
@@ -690,65 +724,68 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const float l = rest.l, lift = Q4 ? static_cast<float>(kPfLift) : 0.f;
       const float lse2 = l > 0.f ? rest.m + __log2f(l) - lift : (l == l ? -CUDART_INF_F : l);
       const float inv = l > 0.f || l != l ? (Q4 ? p.c.v_scale : 1.f) / l : 0.f;
+      // Four lanes exchange 16-byte pieces so that each stores its piece of four rows
+      // and the four together 64 bytes of a row: a thread's own row in 16-byte stores
+      // took five times as long (32 lines an instruction).  Partial results lie with
+      // the rows innermost, a lane each.
+      int64_t row[4];
+      float4* op = reinterpret_cast<float4*>(p.opart) + rest.row * (D / 4) * 128 + r;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
       if (rest.whole) {
-        // Four lanes exchange 16-byte pieces so that each stores its piece of four
-        // rows and the four together 64 bytes of a row: a thread's own row in
-        // 16-byte stores took five times as long (32 lines an instruction).
         const int64_t at = rest.live ? rest.row * p.o_t + rest.h * p.o_h : -1;
-        if (rest.live && p.lse) p.lse[rest.row * p.Hq + rest.h] = lse2 * kLn2;
-        int64_t row[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
-        uint32_t ob[2][32];
-        ptx::tmem_ld32(tO, ob[0]);
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t (&o)[32] = ob[c / 32 & 1];
-          uint32_t w[4][4];
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(o);
-          if (c + 32 < D) ptx::tmem_ld32(tO + c + 32, ob[(c / 32 + 1) & 1]);
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            w[q >> 2][q & 3] = ptx::pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
-#pragma unroll
-          for (int st = 1; st < 4; st *= 2) {
-            const bool up = lane & st;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q & st) continue;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[q][k] : w[q + st][k], st);
-                if (up) w[q][k] = t;
-                else w[q + st][k] = t;
-              }
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (row[k] >= 0) *reinterpret_cast<uint4*>(out + row[k] + c) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-        }
+        if (rest.live && p.lse) p.lse[rest.row * p.Hq + rest.h] = lse2 * kLn2;
       } else {
-        float4* op = reinterpret_cast<float4*>(p.opart) + rest.row * (D / 4) * 128 + r;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          ptx::tmem_ld32(tO + c, o);
-          ptx::tmem_ld_wait();
-          ptx::reg_fence32(o);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            op[(c / 4 + q) * 128] =
-                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                            __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-        }
         p.lpart[rest.row * 128 + r] = lse2;
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
+      constexpr int CH = Q4 ? 64 : D;  // columns at once: what the registers hold
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += CH) {
+        float o[CH];
+#pragma unroll
+        for (int c = 0; c < CH; c += 32) ptx::tmem_ld32f(tO + c0 + c, &o[c]);
+        ptx::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < CH; c += 32) ptx::reg_fence32f(&o[c]);
+        if (c0 + CH == D) {
+          // O is in registers: the next unit's P V may begin
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
+        }
+        if (rest.whole) {
+#pragma unroll
+          for (int c = 0; c < CH; c += 32) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int q = 0; q < 16; ++q)
+              w[q >> 2][q & 3] = ptx::pack_bf16x2(o[c + 2 * q] * inv, o[c + 2 * q + 1] * inv);
+#pragma unroll
+            for (int st = 1; st < 4; st *= 2) {
+              const bool up = lane & st;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (q & st) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[q][k] : w[q + st][k], st);
+                  if (up) w[q][k] = t;
+                  else w[q + st][k] = t;
+                }
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (row[k] >= 0)
+                *reinterpret_cast<uint4*>(out + row[k] + c0 + c) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < CH / 4; ++q)
+            op[(c0 / 4 + q) * 128] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
+        }
+      }
       return true;
     };
     each_unit([&](const PfUnit& u, int a, int z) {
