@@ -1136,25 +1136,47 @@ __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const __grid_c
   const int hq = rec[3] * p.G + r - rtok * p.G;
   const int last = rec[5];
   auto at = [&](int piece) { return (static_cast<int64_t>(piece) * 2 + (piece == border - 1 ? 1 : 0)) * 2 + s; };
-  float m = -CUDART_INF_F;
-  for (int i = border - 1; i <= last; ++i) m = fmaxf(m, p.lpart[at(i) * 128 + r]);
-  const float ref = m == -CUDART_INF_F ? 0.f : m;
-  constexpr int C = D / 16;  // float4 of this thread
+  // one pass with a running maximum, so that a piece's log-sum-exp and output come
+  // in one trip to memory; kJoin pieces at once
+  constexpr int C = D / 16;                // float4 of this thread
+  constexpr int kJoin = D == 64 ? 4 : 2;
   float4 o[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  for (int i = border - 1; i <= last; ++i) {
-    const float wt = ptx::ex2(p.lpart[at(i) * 128 + r] - ref);
-    const float4* src = reinterpret_cast<const float4*>(p.opart) + (at(i) * (D / 4) + w * C) * 128 + r;
-    sum += wt;
+  float m = -CUDART_INF_F, sum = 0.f;
+  for (int i0 = border - 1; i0 <= last; i0 += kJoin) {
+    float l[kJoin];
+    float4 v[kJoin][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const float4 v = src[c * 128];
-      o[c].x = fmaf(v.x, wt, o[c].x);
-      o[c].y = fmaf(v.y, wt, o[c].y);
-      o[c].z = fmaf(v.z, wt, o[c].z);
-      o[c].w = fmaf(v.w, wt, o[c].w);
+    for (int k = 0; k < kJoin; ++k) {
+      const bool ok = i0 + k <= last;
+      const int64_t piece = at(ok ? i0 + k : last);
+      l[k] = p.lpart[piece * 128 + r];
+      const float4* src = reinterpret_cast<const float4*>(p.opart) + (piece * (D / 4) + w * C) * 128 + r;
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[k][c] = src[c * 128];
+      if (!ok) l[k] = -CUDART_INF_F;
+    }
+    float m_new = m;
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) m_new = fmaxf(m_new, l[k]);
+    const float ref = m_new == -CUDART_INF_F ? 0.f : m_new;
+    const float old = ptx::ex2(m - ref);  // of nothing yet: 0
+    m = m_new;
+    sum *= old;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[c] = make_float4(o[c].x * old, o[c].y * old, o[c].z * old, o[c].w * old);
+#pragma unroll
+    for (int k = 0; k < kJoin; ++k) {
+      const float wt = ptx::ex2(l[k] - ref);
+      sum += wt;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        o[c].x = fmaf(v[k][c].x, wt, o[c].x);
+        o[c].y = fmaf(v[k][c].y, wt, o[c].y);
+        o[c].z = fmaf(v[k][c].z, wt, o[c].z);
+        o[c].w = fmaf(v[k][c].w, wt, o[c].w);
+      }
     }
   }
   const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;

@@ -7,70 +7,84 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _empty_on, _need, _stream_ptr
+from .api import _empty_on, _need, _raw_stream, _stream_ptr
 from ._lib import ROPE_SCALINGS
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _strides(t, name):
+_Tensor = torch.Tensor
+_device_index = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_NONE = (0, 0, 0)
+
+
+def _check(t, name: str, ndim: int, dtype, index: int) -> None:
+    """`t` is a tensor of this rank and type on CUDA device `index`."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != ndim or t.get_device() != index:
+        _need(t, name, ndim, dtype)
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+
+
+def _strides(t, name, B, H, L, d):
     """(b, h, l) strides; those of axes of length 1 are never used to step."""
     sb, sh, sl, sc = t.stride()
-    if sc != 1 and t.shape[3] > 1:
+    if sc != 1:
         raise ValueError(f"{name} must have a contiguous head dimension")
-    B, H, L, d = t.shape
     return sb if B > 1 else H * L * d, sh if H > 1 else L * d, sl if L > 1 else d
 
 
 def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, q_out, k_out, stream):
     _need(q, names[0], 4)
-    B, Hq, L, d = q.shape
+    B, Hq, L, d = shape = q.shape
     index = q.get_device()
-    if torch.cuda.current_device() != index:
-        raise ValueError(f"{names[0]} is on cuda:{index}, the current device is cuda:{torch.cuda.current_device()}")
-
-    def on_device(t, name):
-        if t.get_device() != index:
-            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    for name, t in (("rope_cos", rope_cos), ("rope_sin", rope_sin)):
-        _need(t, name, 2, _F32)
-        on_device(t, name)
-        if t.shape != rope_cos.shape or not t.is_contiguous():
-            raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
-    Hk = 0
+    if _device_index() != index:
+        raise ValueError(f"{names[0]} is on cuda:{index}, the current device is cuda:{_device_index()}")
+    _check(rope_cos, "rope_cos", 2, _F32, index)
+    _check(rope_sin, "rope_sin", 2, _F32, index)
+    rows, half = rope_cos.shape
+    if rope_sin.shape != rope_cos.shape or not rope_cos.is_contiguous() or not rope_sin.is_contiguous():
+        raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
+    if q_out is None:
+        q_out = _empty_on(stream, shape, _BF16, q.device)
+        qos = _NONE
+    else:
+        _check(q_out, names[2], 4, _BF16, index)
+        if q_out.shape != shape:
+            raise ValueError(f"{names[2]} must be {list(shape)}, got {list(q_out.shape)}")
+        qos = _strides(q_out, names[2], B, Hq, L, d)
+    Hk = kp = kop = 0
+    ks = kos = _NONE
     if k is not None:
-        _need(k, names[1], 4)
-        on_device(k, names[1])
-        Hk = k.shape[1]
-        if k.shape[0] != B or k.shape[2] != L or k.shape[3] != d:
-            raise ValueError(f"{names[1]} must be [{B}, heads, {L}, {d}], got {list(k.shape)}")
+        _check(k, names[1], 4, _BF16, index)
+        kshape = k.shape
+        Hk = kshape[1]
+        if kshape[0] != B or kshape[2] != L or kshape[3] != d:
+            raise ValueError(f"{names[1]} must be [{B}, heads, {L}, {d}], got {list(kshape)}")
+        ks = _strides(k, names[1], B, Hk, L, d)
+        if k_out is None:
+            k_out = _empty_on(stream, kshape, _BF16, q.device)
+        else:
+            _check(k_out, names[3], 4, _BF16, index)
+            if k_out.shape != kshape:
+                raise ValueError(f"{names[3]} must be {list(kshape)}, got {list(k_out.shape)}")
+            kos = _strides(k_out, names[3], B, Hk, L, d)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError(f"{names[3]} needs {names[1]}")
     pos = pos_stride = 0
     if positions is not None:
-        _need(positions, "positions", positions.dim() if isinstance(positions, torch.Tensor) else 2, _I32)
-        on_device(positions, "positions")
-        if tuple(positions.shape) not in ((B, L), (L,)):
+        n = positions.dim() if isinstance(positions, _Tensor) else 2
+        _check(positions, "positions", n, _I32, index)
+        if tuple(positions.shape) != ((B, L) if n == 2 else (L,)):
             raise ValueError(f"positions must be [{B}, {L}] or [{L}], got {list(positions.shape)}")
         if L > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must have contiguous rows")
         pos = positions.data_ptr()
-        pos_stride = positions.stride(0) if positions.dim() == 2 and B > 1 else 0
-    q_out = _empty_on(stream, q.shape, _BF16, q.device) if q_out is None else q_out
-    k_out = _empty_on(stream, k.shape, _BF16, k.device) if k is not None and k_out is None else k_out
-    for name, t, x in ((names[2], q_out, q), (names[3], k_out, k)):
-        if t is not None:
-            _need(t, name, 4)
-            on_device(t, name)
-            if t.shape != x.shape:
-                raise ValueError(f"{name} must be {list(x.shape)}, got {list(t.shape)}")
-    none = (0, 0, 0)
-    desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rope_cos.shape[0], 2 * rope_cos.shape[1], 1 if rope_interleaved else 0,
-                          rope_cos.data_ptr(), rope_sin.data_ptr(), pos, pos_stride, *_strides(q, names[0]),
-                          *(none if k is None else _strides(k, names[1])), *_strides(q_out, names[2]),
-                          *(none if k is None else _strides(k_out, names[3])), _stream_ptr(stream))
-    st = getattr(_lib.lib(), call)(q.data_ptr(), 0 if k is None else k.data_ptr(), q_out.data_ptr(),
-                                   0 if k is None else k_out.data_ptr(), desc)
+        pos_stride = positions.stride(0) if n == 2 and B > 1 else 0
+    desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rows, 2 * half, 1 if rope_interleaved else 0, rope_cos.data_ptr(),
+                          rope_sin.data_ptr(), pos, pos_stride, *_strides(q, names[0], B, Hq, L, d), *ks, *qos, *kos,
+                          _raw_stream(index) if stream is None else _stream_ptr(stream))
+    st = getattr(_lib.lib(), call)(q.data_ptr(), kp, q_out.data_ptr(), kop, desc)
     if st:
         _lib.check(st, call)
     return q_out, k_out
@@ -131,19 +145,22 @@ def rope_tables(positions: int, rope_dim: int, *, base: float = 10000.0, scaling
     positions stay, those below low_turns are interpolated by factor)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"unknown scaling {scaling!r}")
-    shape = (int(positions), int(rope_dim) // 2)
+    positions, rope_dim = int(positions), int(rope_dim)
+    shape = (positions, rope_dim // 2)
     if cos is None:
         cos = _empty_on(stream, shape, _F32, torch.device(device) if sin is None else sin.device)
     if sin is None:
         sin = _empty_on(stream, shape, _F32, cos.device)
-    for name, t in (("cos", cos), ("sin", sin)):
-        _need(t, name, 2, _F32)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
-        if t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    _need(cos, "cos", 2, _F32)
+    index = cos.get_device()
+    _check(sin, "sin", 2, _F32, index)
+    if _device_index() != index:
+        raise ValueError(f"cos is on cuda:{index}, the current device is cuda:{_device_index()}")
+    if cos.shape != shape or sin.shape != shape or not cos.is_contiguous() or not sin.is_contiguous():
+        raise ValueError(f"cos and sin must be contiguous {list(shape)}, got {list(cos.shape)} and {list(sin.shape)}")
     spec = _lib.SCALING_PACK(base, factor, low_turns, high_turns, ROPE_SCALINGS[scaling], original, amplitude, 0)
-    st = _lib.lib().fl_rope_tables(cos.data_ptr(), sin.data_ptr(), int(positions), int(rope_dim), spec, _stream_ptr(stream))
+    st = _lib.lib().fl_rope_tables(cos.data_ptr(), sin.data_ptr(), positions, rope_dim, spec,
+                                   _raw_stream(index) if stream is None else _stream_ptr(stream))
     if st:
         _lib.check(st, "fl_rope_tables")
     return cos, sin
