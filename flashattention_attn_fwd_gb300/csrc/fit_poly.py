@@ -1,4 +1,4 @@
-"""Fits the two polynomials the attention kernels evaluate on the FMA pipe.
+"""Fits the polynomials the kernels evaluate on the FMA pipe.
 
   tanh   tanh(y) ~= y * P(y^2) on |y| <= T, P of degree n in y^2
          (softcap score modification; default T = 0.5, n = 3)
@@ -6,14 +6,17 @@
          (the share of the softmax exponentials computed without the MUFU
          unit, after the Cody-Waite split x = j + f, j = floor(x);
          default n = 3)
+  turn   sin(pi x) ~= x S(x^2), cos(pi x) ~= C(x^2) on |x| <= 1/4, of degrees
+         3 and 4 in x^2 (the rotary tables, whose argument is in half turns)
 
-Both are fitted for minimum maximum relative error by Lawson's iteratively
+They are fitted for minimum maximum relative error by Lawson's iteratively
 reweighted least squares on Chebyshev nodes (float64), then the float32-
 rounded coefficients are checked in float32 Horner arithmetic.  The kernel
 header holds the coefficients this script prints with its defaults.
 
     python fit_poly.py tanh [T] [n]
     python fit_poly.py exp2 [n]
+    python fit_poly.py turn
 """
 import sys
 
@@ -67,6 +70,18 @@ def fit_exp2(n: int):
     return c32, rel
 
 
+def fit_turn():
+    x = cheb_nodes(0.0, 0.25)
+    x = x[x > 1e-6]
+    s = np.float32(lawson(np.stack([x ** (2 * j) for j in range(4)], axis=1), np.sin(np.pi * x) / x))
+    c = np.float32(lawson(np.stack([x ** (2 * j) for j in range(5)], axis=1), np.cos(np.pi * x)))
+    xs = np.linspace(-0.25, 0.25, 400001).astype(np.float32)
+    z = (xs * xs).astype(np.float32)
+    es = float(np.max(np.abs((xs * horner_f32(s, z)).astype(np.float64) - np.sin(np.pi * xs.astype(np.float64)))))
+    ec = float(np.max(np.abs(horner_f32(c, z) - np.cos(np.pi * xs.astype(np.float64)))))
+    return s, c, es, ec
+
+
 if __name__ == "__main__":
     what = sys.argv[1] if len(sys.argv) > 1 else "tanh"
     if what == "tanh":
@@ -82,5 +97,11 @@ if __name__ == "__main__":
         print(f"2^f on [0, 1), degree {n}: float32 max rel err {rel:.3e}")
         for j, cj in enumerate(c):
             print(f"  e{j} = {float(cj):.9g}f  // f^{j}")
+    elif what == "turn":
+        s, c, es, ec = fit_turn()
+        print(f"sin(pi x), cos(pi x) on |x| <= 1/4: float32 max abs err {es:.3e}, {ec:.3e}")
+        for name, k in (("s", s), ("c", c)):
+            for j, cj in enumerate(k):
+                print(f"  {name}{j} = {float(cj):.9g}f")
     else:
-        raise SystemExit("usage: fit_poly.py tanh [T] [n] | exp2 [n]")
+        raise SystemExit("usage: fit_poly.py tanh [T] [n] | exp2 [n] | turn")

@@ -61,7 +61,12 @@
 namespace fl {
 namespace {
 
-constexpr int kPfLead = 2;       // tiles that starting and ending a unit costs a block
+// Tiles that starting and ending a unit costs a block, found by measuring 1, 2, 3, 4 and 6
+// on packed prompts of 901 to 2999 tokens, 32 heads over 8: bf16 d 128 184, 163, 161, 166
+// and 178 us, d 64 145, 131, 135, 140 and 152; 4 bits d 128 278, 229, 210, 204 and 206,
+// d 64 194, 156, 152, 157 and 186.
+template <int FMT, int D>
+constexpr int kPfLead = FMT == KV_BF16 ? 2 : D == 64 ? 3 : 4;
 constexpr uint64_t kPfTurnNs = 4000;
 constexpr uint32_t kPfLift = 7;  // 4 bits: P carries 2^kPfLift
 
@@ -118,6 +123,7 @@ struct PfShared {
   PfUnit unit[16];          // of every warp: where it is (in registers they would be spilled)
 };
 
+template <int LEAD>
 struct PfSeqs {
   const PrefillParams& p;
   int R;  // tokens per unit
@@ -145,7 +151,7 @@ struct PfSeqs {
   }
   // the next (unit, head) of the line; false behind the last
   __device__ __forceinline__ bool next(PfUnit& u) const {
-    u.base += kPfLead + u.count;
+    u.base += LEAD + u.count;
     if (++u.h < p.c.Hkv) return true;
     u.h = 0;
     int o = offset(u.b), e = max(offset(u.b + 1), o);
@@ -215,7 +221,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   static_assert(sizeof(Shared) <= L::FIXED, "fixed area");
   Shared& sh = *reinterpret_cast<Shared*>(smem + L::OFF_FIXED);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const PfSeqs seqs{p, 2 * p.RT};
+  constexpr int LEAD = kPfLead<FMT, D>;
+  const PfSeqs<LEAD> seqs{p, 2 * p.RT};
   const int64_t H = p.c.Hkv;
 
   if (tid == 0) {
@@ -300,7 +307,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       }
     };
     int64_t mine = 0;
-    walk([&](const PfUnit& un) { mine += kPfLead + un.count; });
+    walk([&](const PfUnit& un) { mine += LEAD + un.count; });
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     if (begin < end && before * H <= begin && begin < (before + mine) * H) {
       int64_t at = before * H;
       walk([&](const PfUnit& un) {
-        const int64_t c = kPfLead + un.count;
+        const int64_t c = LEAD + un.count;
         if (at <= begin && begin < at + c * H) {
           const int h = static_cast<int>((begin - at) / c);
           PfUnit f = un;
@@ -724,68 +731,65 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       const float l = rest.l, lift = Q4 ? static_cast<float>(kPfLift) : 0.f;
       const float lse2 = l > 0.f ? rest.m + __log2f(l) - lift : (l == l ? -CUDART_INF_F : l);
       const float inv = l > 0.f || l != l ? (Q4 ? p.c.v_scale : 1.f) / l : 0.f;
-      // Four lanes exchange 16-byte pieces so that each stores its piece of four rows
-      // and the four together 64 bytes of a row: a thread's own row in 16-byte stores
-      // took five times as long (32 lines an instruction).  Partial results lie with
-      // the rows innermost, a lane each.
-      int64_t row[4];
-      float4* op = reinterpret_cast<float4*>(p.opart) + rest.row * (D / 4) * 128 + r;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
       if (rest.whole) {
+        // Four lanes exchange 16-byte pieces so that each stores its piece of four
+        // rows and the four together 64 bytes of a row: a thread's own row in
+        // 16-byte stores took five times as long (32 lines an instruction).
         const int64_t at = rest.live ? rest.row * p.o_t + rest.h * p.o_h : -1;
+        if (rest.live && p.lse) p.lse[rest.row * p.Hq + rest.h] = lse2 * kLn2;
+        int64_t row[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) row[k] = __shfl_sync(0xffffffffu, at, (lane & ~3) + k);
-        if (rest.live && p.lse) p.lse[rest.row * p.Hq + rest.h] = lse2 * kLn2;
-      } else {
-        p.lpart[rest.row * 128 + r] = lse2;
-      }
-      constexpr int CH = Q4 ? 64 : D;  // columns at once: what the registers hold
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + 8 * (lane & 3);
+        uint32_t ob[2][32];
+        ptx::tmem_ld32(tO, ob[0]);
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += CH) {
-        float o[CH];
+        for (int c = 0; c < D; c += 32) {
+          uint32_t (&o)[32] = ob[c / 32 & 1];
+          uint32_t w[4][4];
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+          if (c + 32 < D) ptx::tmem_ld32(tO + c + 32, ob[(c / 32 + 1) & 1]);
 #pragma unroll
-        for (int c = 0; c < CH; c += 32) ptx::tmem_ld32f(tO + c0 + c, &o[c]);
-        ptx::tmem_ld_wait();
+          for (int q = 0; q < 16; ++q)
+            w[q >> 2][q & 3] = ptx::pack_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
 #pragma unroll
-        for (int c = 0; c < CH; c += 32) ptx::reg_fence32f(&o[c]);
-        if (c0 + CH == D) {
-          // O is in registers: the next unit's P V may begin
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
-        }
-        if (rest.whole) {
+          for (int st = 1; st < 4; st *= 2) {
+            const bool up = lane & st;
 #pragma unroll
-          for (int c = 0; c < CH; c += 32) {
-            uint32_t w[4][4];
+            for (int q = 0; q < 4; ++q) {
+              if (q & st) continue;
 #pragma unroll
-            for (int q = 0; q < 16; ++q)
-              w[q >> 2][q & 3] = ptx::pack_bf16x2(o[c + 2 * q] * inv, o[c + 2 * q + 1] * inv);
-#pragma unroll
-            for (int st = 1; st < 4; st *= 2) {
-              const bool up = lane & st;
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                if (q & st) continue;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[q][k] : w[q + st][k], st);
-                  if (up) w[q][k] = t;
-                  else w[q + st][k] = t;
-                }
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t t = __shfl_xor_sync(0xffffffffu, up ? w[q][k] : w[q + st][k], st);
+                if (up) w[q][k] = t;
+                else w[q + st][k] = t;
               }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (row[k] >= 0)
-                *reinterpret_cast<uint4*>(out + row[k] + c0 + c) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
           }
-        } else {
 #pragma unroll
-          for (int q = 0; q < CH / 4; ++q)
-            op[(c0 / 4 + q) * 128] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
+          for (int k = 0; k < 4; ++k)
+            if (row[k] >= 0) *reinterpret_cast<uint4*>(out + row[k] + c) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
         }
+      } else {
+        float4* op = reinterpret_cast<float4*>(p.opart) + rest.row * (D / 4) * 128 + r;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          ptx::tmem_ld32(tO + c, o);
+          ptx::tmem_ld_wait();
+          ptx::reg_fence32(o);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            op[(c / 4 + q) * 128] =
+                make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                            __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+        }
+        p.lpart[rest.row * 128 + r] = lse2;
       }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
       return true;
     };
     each_unit([&](const PfUnit& u, int a, int z) {

@@ -11,6 +11,13 @@
 // channel of the half-split pairing comes by shuffle.  Strides are free, so that
 // the projection's token-major output becomes the [B, H, L, d] that the backward
 // pass of attention takes, in the same pass.
+//
+// Measured: 2 x 8192 tokens of 32 + 8 heads of 128, half of the channels in pairs, 57 us
+// (5.9 TB/s, 88 % of the copy rate); 4 x 2048 tokens of 2 x 16 heads of 64, 15 us a
+// direction (4.4 TB/s: two waves of blocks and the launch); 64 tokens 6 us, the launch
+// and three loads one after another.  Two or eight row groups in flight instead of
+// four, more warps a token, registers for more blocks an SM: 20 to 40 % slower in the
+// second case, whose blocks then make a third, ragged wave.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -135,41 +142,74 @@ cudaError_t launch_rope_d(RopeParams& p, int sm_count, cudaStream_t s) {
 // Tables: cos and sin of position * angle step.  The angle is a 64-bit fraction
 // of a turn, so that position times step wraps where a turn ends and nothing is
 // lost at far positions (error 2^-64 turns times the position, with integer
-// products where fp64's would be slow).  Its quarter turns pick the function and the sign, the
-// rest, at most an eighth of a turn either way, is an fp32 argument.
+// sums where fp64's rate is low).  Its quarter turns pick the function and the sign;
+// the rest x, in half turns at most 1/4 either way, goes through
+//   sin(pi x) = x S(x^2),  cos(pi x) = C(x^2)
+// (fit_poly.py turn: within 9e-8, two channels an instruction).  A thread takes
+// four neighbouring pairs at several positions.  131072 positions of 64 pairs: 14 us
+// (4.7 TB/s of writes; with sincospif 18), 4096 of 32 pairs 4.7 (the launch).
 constexpr int kTabThreads = 256;
-constexpr int kTabRows = 8;  // positions of a thread
+constexpr int kTabRowsMax = 8;  // positions of a thread
 
-__global__ void __launch_bounds__(kTabThreads) rope_tables_kernel(const __grid_constant__ RopeTableParams p) {
-  const int lanes = p.half / 4;              // threads of a position, four pairs each
-  const int rows = kTabThreads / lanes;      // positions at once
+struct TableLaunch {
+  RopeTableParams t;
+  int rows;  // positions of a thread
+};
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+__global__ void __launch_bounds__(kTabThreads) rope_tables_kernel(const __grid_constant__ TableLaunch a) {
+  constexpr float kTurnS[4] = {3.14159274f, -5.16770792f, 2.54976106f, -0.589013278f};
+  constexpr float kTurnC[5] = {1.f, -4.93480206f, 4.05870676f, -1.33503592f, 0.231261194f};
+  const RopeTableParams& p = a.t;
+  const int lanes = p.half / 4;              // threads of a position
+  const int wide = kTabThreads / lanes;      // positions at once
   const int c = threadIdx.x % lanes, r = threadIdx.x / lanes;
-  if (r >= rows) return;
-  uint64_t step[4];
+  if (r >= wide) return;
+  int64_t pos = static_cast<int64_t>(blockIdx.x) * wide * a.rows + r;
+  uint64_t turn[4], step[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) step[e] = p.turn[4 * c + e];
-  const int64_t pos0 = static_cast<int64_t>(blockIdx.x) * rows * kTabRows + r;
-#pragma unroll 2
-  for (int k = 0; k < kTabRows; ++k) {
-    const int64_t pos = pos0 + static_cast<int64_t>(k) * rows;
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t t = p.turn[4 * c + e];
+    turn[e] = t * static_cast<uint64_t>(pos) + (uint64_t(1) << 61);  // an eighth of a turn further
+    step[e] = t * static_cast<uint64_t>(wide);
+  }
+  for (int k = 0; k < a.rows; ++k, pos += wide) {
     if (pos >= p.positions) return;
-    float co[4], si[4];
+    float2 co[2], si[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint64_t a = step[e] * static_cast<uint64_t>(pos) + (uint64_t(1) << 61);  // an eighth of a turn further
-      const uint32_t hi = static_cast<uint32_t>(a >> 32);
-      const int quarter = static_cast<int>(hi >> 30);
-      // the rest in half turns, [-1/4, 1/4)
-      const float x = static_cast<float>(static_cast<int>(hi & 0x3fffffffu) - (1 << 29)) * 0x1p-31f;
-      float s, q;
-      sincospif(x, &s, &q);
-      const float u = quarter & 1 ? s : q, v = quarter & 1 ? q : s;
-      co[e] = (quarter == 1 || quarter == 2 ? -u : u) * p.amplitude;
-      si[e] = (quarter & 2 ? -v : v) * p.amplitude;
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t h0 = static_cast<uint32_t>(turn[2 * e] >> 32), h1 = static_cast<uint32_t>(turn[2 * e + 1] >> 32);
+      turn[2 * e] += step[2 * e];
+      turn[2 * e + 1] += step[2 * e + 1];
+      // what is left of the quarter turn, in half turns
+      const float2 x = ptx::mul2(make_float2(static_cast<float>(static_cast<int>(h0 & 0x3fffffffu) - (1 << 29)),
+                                             static_cast<float>(static_cast<int>(h1 & 0x3fffffffu) - (1 << 29))),
+                                 both(0x1p-31f));
+      const float2 z = ptx::mul2(x, x);
+      float2 s = ptx::fma2(both(kTurnS[3]), z, both(kTurnS[2]));
+      s = ptx::fma2(s, z, both(kTurnS[1]));
+      s = ptx::fma2(s, z, both(kTurnS[0]));
+      s = ptx::mul2(s, x);
+      float2 q = ptx::fma2(both(kTurnC[4]), z, both(kTurnC[3]));
+      q = ptx::fma2(q, z, both(kTurnC[2]));
+      q = ptx::fma2(q, z, both(kTurnC[1]));
+      q = ptx::fma2(q, z, both(kTurnC[0]));
+      s = ptx::mul2(s, both(p.amplitude));
+      q = ptx::mul2(q, both(p.amplitude));
+      // quarter 0: (q, s), 1: (-s, q), 2: (-q, -s), 3: (s, -q)
+      auto place = [](uint32_t h, float s1, float q1, float& cosine, float& sine) {
+        const bool odd = h & 0x40000000u;
+        const uint32_t cs = (h ^ (h << 1)) & 0x80000000u, ss = h & 0x80000000u;
+        cosine = __uint_as_float(__float_as_uint(odd ? s1 : q1) ^ cs);
+        sine = __uint_as_float(__float_as_uint(odd ? q1 : s1) ^ ss);
+      };
+      place(h0, s.x, q.x, co[e].x, si[e].x);
+      place(h1, s.y, q.y, co[e].y, si[e].y);
     }
     const int64_t at = pos * p.half + 4 * c;
-    *reinterpret_cast<float4*>(p.cos + at) = make_float4(co[0], co[1], co[2], co[3]);
-    *reinterpret_cast<float4*>(p.sin + at) = make_float4(si[0], si[1], si[2], si[3]);
+    *reinterpret_cast<float4*>(p.cos + at) = make_float4(co[0].x, co[0].y, co[1].x, co[1].y);
+    *reinterpret_cast<float4*>(p.sin + at) = make_float4(si[0].x, si[0].y, si[1].x, si[1].y);
   }
 }
 
@@ -184,9 +224,13 @@ cudaError_t launch_rope(int d, RopeParams& p, int sm_count, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_rope_tables(const RopeTableParams& p, cudaStream_t s) {
-  const int rows = kTabThreads / (p.half / 4) * kTabRows;
-  rope_tables_kernel<<<static_cast<unsigned>((static_cast<int64_t>(p.positions) + rows - 1) / rows), kTabThreads, 0, s>>>(p);
+cudaError_t launch_rope_tables(const RopeTableParams& p, int sm_count, cudaStream_t s) {
+  // several positions a thread once every SM has eight blocks
+  const int wide = kTabThreads / (p.half / 4);
+  const int64_t rows = static_cast<int64_t>(p.positions) / (static_cast<int64_t>(sm_count) * 8 * wide);
+  const TableLaunch a{p, static_cast<int>(rows < 1 ? 1 : rows > kTabRowsMax ? kTabRowsMax : rows)};
+  const int64_t per = static_cast<int64_t>(wide) * a.rows;
+  rope_tables_kernel<<<static_cast<unsigned>((p.positions + per - 1) / per), kTabThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 

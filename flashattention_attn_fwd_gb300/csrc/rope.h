@@ -37,6 +37,6 @@ struct RopeTableParams {
   float amplitude;
   uint64_t turn[kRopeMaxDim / 2];  // of a position step: its fraction of a turn in units of 2^-64
 };
-cudaError_t launch_rope_tables(const RopeTableParams& p, cudaStream_t s);
+cudaError_t launch_rope_tables(const RopeTableParams& p, int sm_count, cudaStream_t s);
 
 }  // namespace fl

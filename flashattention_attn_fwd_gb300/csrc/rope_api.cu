@@ -120,7 +120,7 @@ fl_status fl_rope_tables(float* rope_cos, float* rope_sin, int32_t positions, in
   uint32_t* status = nullptr;
   const fl_status st = fl::device_info(&sm_count, &status);
   if (st != FL_OK) return st;
-  return fl::launch_result("rope tables launch", fl::launch_rope_tables(p, static_cast<cudaStream_t>(stream)));
+  return fl::launch_result("rope tables launch", fl::launch_rope_tables(p, sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

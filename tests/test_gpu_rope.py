@@ -6,8 +6,9 @@ Tables' bound.  The angle's rest, at most a quarter of a half turn, is rounded t
 fp32 (2^-27 half turns) after its fraction of a turn was cut to 32 bits (2^-32
 turns): pi 2^-27 + 2 pi 2^-32 < 2.5e-8.  The step's fp64 value carries at most 4
 roundings of 2^-53 (power, products, quotient), times the angle, which is at most the
-position: 2^-51 pos; cut at 2^-64 turns it adds 2 pi 2^-64 pos.  sinpi and cospi are
-within two units of 2^-24, the amplitude's product rounds by 2^-24: 3 x 2^-24."""
+position: 2^-51 pos; cut at 2^-64 turns it adds 2 pi 2^-64 pos.  The two
+polynomials are within 9e-8, less than two units of 2^-24 (tests/test_turn_poly.py;
+fused steps round less), the amplitude's product rounds by 2^-24: 3 x 2^-24."""
 import math
 
 import numpy as np
