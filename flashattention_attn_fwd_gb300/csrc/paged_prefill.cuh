@@ -123,6 +123,12 @@ struct PfShared {
   PfUnit unit[16];          // of every warp: where it is (in registers they would be spilled)
 };
 
+// As wait_bar, its slow path out of the way.
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, const Ctl& c, int where) {
+  if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
+  return wait_slow(bar, parity, c, where);
+}
+
 template <int LEAD>
 struct PfSeqs {
   const PrefillParams& p;
@@ -441,7 +447,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           for (int v = 0; v < 2; ++v) {
             const uint32_t ev = e + v;
             const int st = static_cast<int>(ev % NS);
-            if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[st], ((ev / NS) & 1u) ^ 1u, ctl, 2))) return false;
+            if (!__all_sync(0xffffffffu, pf_wait(&sh.kv_empty[st], ((ev / NS) & 1u) ^ 1u, ctl, 2))) return false;
             const bool land = v == 1 && !whole;
             uint64_t* bar = land ? &sh.v_land[part & 7u] : &sh.kv_full[st];
             const bool skip = v == 0 && p.dbg_skip_tile >= 0 && blockIdx.x == 0 &&
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             // Q behind the first K, which need not wait for the last unit's end
             for (int s = 0; s < 2; ++s) {
               if (u.ntok <= s * p.RT) continue;
-              if (!__all_sync(0xffffffffu, wait_bar(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
+              if (!__all_sync(0xffffffffu, pf_wait(&sh.q_empty[s], (qc[s] & 1u) ^ 1u, ctl, 1))) return false;
               if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(&sh.q_full[s], p.RT * p.G * D * 2);
                 for (int x = 0; x < L::HALVES; ++x)
@@ -498,7 +504,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           later.timeout_ns += ctl.timeout_ns;
           if (pf_all_seen(p, u, j0, 128)) continue;
           const int st = static_cast<int>((e + 1) % NS);
-          if (!__all_sync(0xffffffffu, wait_bar(&sh.v_land[part & 7u], (part >> 3) & 1u, later, 3))) return false;
+          if (!__all_sync(0xffffffffu, pf_wait(&sh.v_land[part & 7u], (part >> 3) & 1u, later, 3))) return false;
           later.timeout_ns = ctl.timeout_ns;
           ++part;
           const uint32_t base = ptx::smem_u32(smem + L::OFF_RING + st * L::TILE);
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(128, D, true) & kTypes;
       const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
       const uint32_t qa = ptx::smem_u32(smem + L::OFF_Q);
-      auto wait = [&](uint64_t* bar, uint32_t parity, int where) { return wait_bar(bar, parity & 1u, ctl, where); };
+      auto wait = [&](uint64_t* bar, uint32_t parity, int where) { return pf_wait(bar, parity & 1u, ctl, where); };
       auto full = [&](uint32_t ev, int where) { return wait(&sh.kv_full[ev % NS], ev / NS, where); };
       auto free_place = [&](uint32_t ev) {
         if (lane == 0) ptx::mbar_arrive(&sh.kv_empty[ev % NS]);
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
               const bool o_ok = ptx::mbar_test_wait(&sh.o_empty[s], ((oc >> s) + 1u) & 1u);
               const bool p_ok = ptx::mbar_test_wait(&sh.p_lo[s], (pc >> s) & 1u);
               if (!(v_ok & (k_ok | !more) & (o_ok | (i > 0)) & p_ok)) {
-                go = wait_bar(v_bar, v_ph, ctl, 16) && (!more || wait_bar(k_bar, k_ph, ctl, 11)) &&
+                go = pf_wait(v_bar, v_ph, ctl, 16) && (!more || pf_wait(k_bar, k_ph, ctl, 11)) &&
                      (i > 0 || wait(&sh.o_empty[s], (oc >> s) + 1u, 13)) && wait(&sh.p_lo[s], pc >> s, 14);
                 if (!go) break;
               }
@@ -725,7 +731,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     auto finish = [&]() -> bool {
       have_rest = false;
       const uint32_t done = kSepP ? sc - 1 : units - 1;  // phases: a tile each, or (d 128) a unit each
-      if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], done & 1u, ctl, 30 + s))) return false;
+      if (!__all_sync(0xffffffffu, pf_wait(&sh.pv_done[s], done & 1u, ctl, 30 + s))) return false;
       free_place(2 * rest.tile + 1);
       ptx::tc_fence_after();
       const float l = rest.l, lift = Q4 ? static_cast<float>(kPfLift) : 0.f;
@@ -792,11 +798,19 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       if (lane == 0) ptx::mbar_arrive(&sh.o_empty[s]);
       return true;
     };
-    each_unit([&](const PfUnit& u, int a, int z) {
-      if (u.ntok <= s * p.RT) {
+    // one copy of each part in the code: the tile loop shares the instruction cache
+    // with the other roles
+    while (true) {
+      int a = 0, z = 0;
+      bool more;
+      const PfUnit& u = sh.unit[warp];
+      while ((more = next_unit(a, z)) && u.ntok <= s * p.RT) {
         tile += z - a;
         idle += z - a;
-        return true;
+      }
+      if (!more) {
+        if (have_rest) finish();
+        break;
       }
       // rows without a token take the last one's bounds (their results are dropped)
       const int tok = s * p.RT + rtok;
@@ -852,14 +866,15 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.q_full[s]);
       }
-      if (have_rest && !finish()) return false;
+      if (have_rest && !finish()) break;
       const float xmul = SCORE == SCORE_NONE ? p.scale_log2 * rf : 1.f;
       const float slope2 = SCORE == SCORE_ALIBI ? __ldg(p.slopes + (row_used ? hq : 0)) * kLog2e : 0.f;
       float m = -CUDART_INF_F, l = 0.f;
+      bool ok = true;
       for (int i = a; i < z; ++i, ++sc, ++tile) {
         const int j0 = pf_key(u, i);
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.s_full[s], sc & 1u, Ctl{ctl.abort, p.status, p.timeout_ns * idle}, 20 + s)))
-          return false;
+        ok = __all_sync(0xffffffffu, pf_wait(&sh.s_full[s], sc & 1u, Ctl{ctl.abort, p.status, p.timeout_ns * idle}, 20 + s));
+        if (!ok) break;
         idle = 1;
         free_place(2 * tile);
         // d 128: that S was issued behind the last tile's P V
@@ -926,7 +941,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             x[c + 1] = v.y;
           }
         }
-        if (any_part) {
+        if (__builtin_expect(any_part, 0)) {
           // 32 keys at a time as a word of bits: below hi, and from lo on or a sink
           const int chi = hi - j0, clo = lo - j0, csk = (p.window ? p.sink : 0) - j0;
 #pragma unroll
@@ -951,7 +966,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const bool raise = m_new > m + kRescaleThreshold || (m == -CUDART_INF_F && m_new != -CUDART_INF_F);
         const bool any_raise = __any_sync(0xffffffffu, raise);
         float alpha = 1.f;
-        if (any_raise) {
+        if (__builtin_expect(any_raise, 0)) {
           alpha = raise ? ptx::ex2(m - m_new) : 1.f;
           m = raise ? m_new : m;
           l *= alpha;
@@ -960,11 +975,12 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const float2 negm = make_float2(sub, sub), xm2 = make_float2(xmul, xmul);
         // P and O may change once the previous P V is done (d 128: it was, before this S)
         if (kSepP && i > a) {
-          if (!__all_sync(0xffffffffu, wait_bar(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s))) return false;
+          ok = __all_sync(0xffffffffu, pf_wait(&sh.pv_done[s], (sc - 1) & 1u, ctl, 24 + s));
+          if (!ok) break;
           free_place(2 * tile - 1);
         }
         ptx::tc_fence_after();
-        if (i > a && any_raise) {
+        if (__builtin_expect(i > a && any_raise, 0)) {
           // a few columns at a time: the row's scores hold most registers
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
@@ -999,6 +1015,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
         const float2 lsum = ptx::add2(ls[0], ls[1]);
         l += lsum.x + lsum.y;
       }
+      if (!ok) break;
       // a partial result: of a unit that an earlier block began (0), or that a later one ends (1)
       const bool whole = a == 0 && z == u.count;
       rest = Rest{m, l, whole ? static_cast<int64_t>(u.tok0 + tok)
@@ -1006,9 +1023,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
                   tile - 1, hq, live, whole};
       have_rest = true;
       ++units;
-      return true;
-    });
-    if (have_rest && !*ctl.abort) finish();
+    }
   } else if constexpr (Q4) {
     // -------------------------------------- 4 bits: Q, K and V tiles in fp16
     ptx::setmaxnreg_dec<L::LOAD_REGS>();
@@ -1099,14 +1114,14 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
               static_cast<uint8_t>(((bb & 0xffffu) ? 1u : 0u) | ((bb >> 16) ? 2u : 0u));
         }
         const int sk = static_cast<int>(e % NS), sv = static_cast<int>((e + 1) % NS);
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[sk], ((e / NS) & 1u) ^ 1u, ctl, 2))) return false;
+        if (!__all_sync(0xffffffffu, pf_wait(&sh.kv_empty[sk], ((e / NS) & 1u) ^ 1u, ctl, 2))) return false;
         put(sk, kc, ks);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         const bool skip = p.dbg_skip_tile >= 0 && blockIdx.x == 0 && static_cast<int>(tile) == p.dbg_skip_tile;
         if (lane == 0 && !skip) ptx::mbar_arrive(&sh.kv_full[sk]);
         if (i + 1 < z) load_k(i + 1, page1);
-        if (!__all_sync(0xffffffffu, wait_bar(&sh.kv_empty[sv], (((e + 1) / NS) & 1u) ^ 1u, ctl, 2))) return false;
+        if (!__all_sync(0xffffffffu, pf_wait(&sh.kv_empty[sv], (((e + 1) / NS) & 1u) ^ 1u, ctl, 2))) return false;
         put(sv, vc, vs);
         ptx::fence_proxy_async_smem();
         __syncwarp();
