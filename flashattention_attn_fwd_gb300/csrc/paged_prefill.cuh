@@ -21,7 +21,7 @@
 // tile counts gives the line.  A unit that pieces share leaves one normalised
 // partial result and log-sum-exp per piece in the workspace, joined by
 // paged_prefill_merge_kernel in piece order, so that a call's result is the same
-// every time.
+// every time.  Where whole units are spread evenly enough none is cut.
 //
 // Roles of a block (bf16 384 threads, 4 bits 512):
 //   warp 0      bf16: Q, K and V by TMA, a box per page and 64 channels
@@ -67,6 +67,8 @@ namespace {
 // d 64 194, 156, 152, 157 and 186.
 template <int FMT, int D>
 constexpr int kPfLead = FMT == KV_BF16 ? 2 : D == 64 ? 3 : 4;
+// Tiles that leaving partial results and joining them costs.
+constexpr int kPfJoin = 4;
 constexpr uint64_t kPfTurnNs = 4000;
 constexpr uint32_t kPfLift = 7;  // 4 bits: P carries 2^kPfLift
 
@@ -104,7 +106,7 @@ struct PfUnit {
   int p0, n;          // position of the first token; keys of the sequence
   int vis_lo, vis_end;  // some row sees keys [vis_lo, vis_end) and, below vis_end, [0, sink)
   int sinkt, skip, count;  // tile i is that of key 128 (i < sinkt ? i : i + skip)
-  int64_t base;       // line position of tile 0
+  int64_t base;       // line position of tile 0 (whole units: the unit's)
 };
 
 // Barriers and small arrays in the fixed area.
@@ -114,12 +116,14 @@ struct PfShared {
   uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_lo[2], p_hi[2], pv_done[2], o_empty[2], drain[2];
   uint64_t v_land[8];       // V tiles with rows to be zeroed: landed
   int64_t scan[16];
+  int scan_units[16], largest[16];
   PfUnit found;             // the piece's first unit; b < 0: none
   uint32_t tmem, abort;
   uint32_t bad[16];         // by tile: bits of 16-key groups whose page is not in the pool
   uint32_t issued[NS];      // last load of each place: (barrier << 1 | parity) + 1, 0: none
   uint32_t turn[2];         // tiles of which a slot's products have been issued
-  int64_t per, begin, end;  // positions of the line per block; this block's
+  int64_t begin, end;       // this block's piece of the line
+  int whole;                // the line counts units: none is cut
   PfUnit unit[16];          // of every warp: where it is (in registers they would be spilled)
 };
 
@@ -156,8 +160,8 @@ struct PfSeqs {
     u.count = max(((u.vis_end + 127) >> 7) - u.skip, 1);
   }
   // the next (unit, head) of the line; false behind the last
-  __device__ __forceinline__ bool next(PfUnit& u) const {
-    u.base += LEAD + u.count;
+  __device__ __forceinline__ bool next(PfUnit& u, bool whole) const {
+    u.base += whole ? 1 : LEAD + u.count;
     if (++u.h < p.c.Hkv) return true;
     u.h = 0;
     int o = offset(u.b), e = max(offset(u.b + 1), o);
@@ -231,6 +235,11 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   const PfSeqs<LEAD> seqs{p, 2 * p.RT};
   const int64_t H = p.c.Hkv;
 
+  // the plan's first reads, on their way during the set-up
+  if (32 * tid <= p.B) {
+    if (p.seq_offsets) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.seq_offsets + 32 * tid));
+    if (32 * tid < p.B) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.kv_len + 32 * tid));
+  }
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       ptx::mbar_init(&sh.kv_full[i], Q4 ? 4 : 1);
@@ -276,6 +285,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   const int R = seqs.R;
   const int places = p.T / R + p.B;
   int64_t per, begin, end;
+  bool whole;
   {
     const int chunk = (places + L::THREADS - 1) / L::THREADS;
     const int u0 = tid * chunk, u1 = min(u0 + chunk, places);
@@ -313,28 +323,64 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       }
     };
     int64_t mine = 0;
-    walk([&](const PfUnit& un) { mine += LEAD + un.count; });
+    int units = 0, largest = 0;
+    walk([&](const PfUnit& un) {
+      mine += LEAD + un.count;
+      ++units;
+      largest = max(largest, LEAD + un.count);
+    });
     int64_t incl = mine;
+    int incl_units = units;  // places fit 32 bits
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int w = __shfl_up_sync(0xffffffffu, incl_units, o);
+      if (lane >= o) {
+        incl += v;
+        incl_units += w;
+      }
     }
-    if (lane == 31) sh.scan[warp] = incl;
+    largest = __reduce_max_sync(0xffffffffu, largest);
+    if (lane == 31) {
+      sh.scan[warp] = incl;
+      sh.scan_units[warp] = incl_units;
+      sh.largest[warp] = largest;
+    }
     __syncthreads();
     int64_t before = incl - mine, total = 0;
+    int before_units = incl_units - units, total_units = 0;
     for (int w = 0; w < L::THREADS / 32; ++w) {
-      if (w < warp) before += sh.scan[w];
+      if (w < warp) {
+        before += sh.scan[w];
+        before_units += sh.scan_units[w];
+      }
       total += sh.scan[w];
+      total_units += sh.scan_units[w];
+      largest = max(largest, sh.largest[w]);
+    }
+    per = (total * H + gridDim.x - 1) / gridDim.x;
+    // as many whole units a block where the longest such piece costs no more than a cut
+    // one with a unit's start and the joining of partial results more
+    const int64_t each = (total_units * H + gridDim.x - 1) / gridDim.x;
+    whole = each * largest <= per + LEAD + kPfJoin;
+    if (whole) {
+      per = each;
+      total = total_units;
+      mine = units;
+      before = before_units;
     }
     total *= H;
-    per = (total + gridDim.x - 1) / gridDim.x;
     begin = per * blockIdx.x;
     end = min(begin + per, total);
+    if (tid == 0) {
+      sh.begin = begin;
+      sh.end = end;
+      sh.whole = whole;
+    }
     if (begin < end && before * H <= begin && begin < (before + mine) * H) {
       int64_t at = before * H;
       walk([&](const PfUnit& un) {
-        const int64_t c = LEAD + un.count;
+        const int64_t c = whole ? 1 : LEAD + un.count;
         if (at <= begin && begin < at + c * H) {
           const int h = static_cast<int>((begin - at) / c);
           PfUnit f = un;
@@ -354,27 +400,21 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   const uint64_t drain_ns = 50ull * 1000ull * 1000ull;
   ptx::launch_dependents();
 
-  if (tid == 0) {
-    sh.per = per;
-    sh.begin = begin;
-    sh.end = end;
-    if (blockIdx.x > 0) {
-      // is this block's border inside of a unit, and which pieces share that one
-      const PfUnit f = sh.found;
-      int32_t* r = p.rec + static_cast<int64_t>(blockIdx.x) * 8;
-      const int64_t t = f.b >= 0 ? begin - f.base : 0;
-      const bool cut = t > 0 && t < f.count;
-      r[0] = cut ? 1 : 0;
-      if (cut) {
-        r[1] = f.tok0;
-        r[2] = f.ntok;
-        r[3] = f.h;
-        r[4] = static_cast<int>(f.base / per);
-        r[5] = static_cast<int>((f.base + f.count - 1) / per);
-      }
+  if (blockIdx.x > 0 && tid == 0) {
+    // is this block's border inside of a unit, and which pieces share that one
+    const PfUnit f = sh.found;
+    int32_t* r = p.rec + static_cast<int64_t>(blockIdx.x) * 8;
+    const int64_t t = f.b >= 0 ? begin - f.base : 0;
+    const bool cut = !whole && t > 0 && t < f.count;
+    r[0] = cut ? 1 : 0;
+    if (cut) {
+      r[1] = f.tok0;
+      r[2] = f.ntok;
+      r[3] = f.h;
+      r[4] = static_cast<int>(f.base / per);
+      r[5] = static_cast<int>((f.base + f.count - 1) / per);
     }
   }
-  __syncthreads();
   // The warp's next unit that has tiles in this piece, into sh.unit[warp], and its
   // tiles [a, z) there; not to be asked again once there is none.
   bool begun = false;
@@ -383,12 +423,17 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     while (true) {
       PfUnit u = begun ? at : sh.found;
       __syncwarp();
-      if (begun ? !seqs.next(u) : u.b < 0) return false;
+      if (begun ? !seqs.next(u, sh.whole) : u.b < 0) return false;
       begun = true;
       at = u;
       __syncwarp();
       const int64_t t0 = sh.begin - u.base, t1 = sh.end - u.base;
       if (t1 <= 0) return false;
+      if (sh.whole) {
+        a = 0;
+        z = u.count;
+        return true;
+      }
       a = t0 > 0 ? static_cast<int>(min(t0, static_cast<int64_t>(u.count))) : 0;
       z = t1 < u.count ? static_cast<int>(t1) : u.count;
       if (a < z) return true;
