@@ -129,6 +129,8 @@ struct PrefillParams {
   int64_t table_stride;
   const float* slopes;
   int B, T, Hq, G, RT;         // RT = 128 / G tokens a slot
+  uint32_t div_m;              // t / (2 RT) is the high word of t * div_m, shifted by div_s,
+  int div_s;                   // for t < 2^31
   int max_pages, cap;          // cap = max_pages * page_size
   float scale_log2;            // scale * log2(e) * k_scale
   float softcap;               // in log2 units (cap * log2(e))

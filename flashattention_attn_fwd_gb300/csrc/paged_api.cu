@@ -418,6 +418,8 @@ fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, con
   p.slopes = d.alibi_slopes;
   p.B = d.B; p.T = d.Lq; p.Hq = d.Hq; p.G = d.Hq / d.Hkv;
   p.RT = fl::kPrefillTile / p.G;
+  while ((2 << p.div_s) < 2 * p.RT) ++p.div_s;
+  p.div_m = static_cast<uint32_t>((uint64_t(1) << (32 + p.div_s)) / (2 * p.RT)) + 1u;
   p.cap = d.Lk;
   const float scale = (d.scale > 0.f ? d.scale : 1.0f / std::sqrt(static_cast<float>(d.d))) * cache->k_scale;
   p.scale_log2 = scale * static_cast<float>(kLog2e);

@@ -141,6 +141,10 @@ struct PfSeqs {
     if (!p.seq_offsets) return b;
     return min(max(__ldg(p.seq_offsets + b), 0), p.T);
   }
+  // units in t tokens, rounded down
+  __device__ __forceinline__ int units(int t) const {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(t), p.div_m) >> p.div_s);
+  }
   // tiles of unit qt of sequence b (offsets o to e), with its fields
   __device__ __forceinline__ void fill(PfUnit& u, int b, int qt, int o, int e) const {
     u.b = b;
@@ -190,6 +194,11 @@ __device__ __forceinline__ bool pf_all_seen(const PrefillParams& p, const PfUnit
 }
 __device__ __forceinline__ bool pf_any_seen(const PrefillParams& p, const PfUnit& u, int j, int len) {
   return j < u.vis_end && (j + len > u.vis_lo || j < p.sink);
+}
+
+// a / b of non-negative values, in 32 bits where both fit
+__device__ __forceinline__ int64_t pf_quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 // the lowest n bits (n <= 0: none, n >= 32: all)
@@ -283,14 +292,14 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
 
   // ---- this block's piece of the line
   const int R = seqs.R;
-  const int places = p.T / R + p.B;
+  const int places = seqs.units(p.T) + p.B;
   int64_t per, begin, end;
   bool whole;
   {
     const int chunk = (places + L::THREADS - 1) / L::THREADS;
     const int u0 = tid * chunk, u1 = min(u0 + chunk, places);
     // the last sequence whose units start at or before place u0
-    auto start = [&](int b) { return seqs.offset(b) / R + b; };
+    auto start = [&](int b) { return seqs.units(seqs.offset(b)) + b; };
     int b0 = 0;
     if (u0 < u1) {
       int hi = p.B - 1;
@@ -305,7 +314,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       if (u0 < u1) {
         o = seqs.offset(b);
         e = max(seqs.offset(b + 1), o);
-        s = o / R + b;
+        s = seqs.units(o) + b;
         s1 = b + 1 < p.B ? start(b + 1) : places;
       }
       for (int u = u0; u < u1; ++u) {
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           ++b;
           o = seqs.offset(b);
           e = max(seqs.offset(b + 1), o);
-          s = o / R + b;
+          s = seqs.units(o) + b;
           s1 = b + 1 < p.B ? start(b + 1) : places;
         }
         if (u < s || static_cast<int64_t>(u - s) * R >= e - o) continue;
@@ -358,10 +367,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       total_units += sh.scan_units[w];
       largest = max(largest, sh.largest[w]);
     }
-    per = (total * H + gridDim.x - 1) / gridDim.x;
+    per = pf_quotient(total * H + gridDim.x - 1, gridDim.x);
     // as many whole units a block where the longest such piece costs no more than a cut
     // one with a unit's start and the joining of partial results more
-    const int64_t each = (total_units * H + gridDim.x - 1) / gridDim.x;
+    const int64_t each = pf_quotient(total_units * H + gridDim.x - 1, gridDim.x);
     whole = each * largest <= per + LEAD + kPfJoin;
     if (whole) {
       per = each;
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       walk([&](const PfUnit& un) {
         const int64_t c = whole ? 1 : LEAD + un.count;
         if (at <= begin && begin < at + c * H) {
-          const int h = static_cast<int>((begin - at) / c);
+          const int h = static_cast<int>(pf_quotient(begin - at, c));
           PfUnit f = un;
           f.h = h;
           f.base = at + h * c;
@@ -411,8 +420,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       r[1] = f.tok0;
       r[2] = f.ntok;
       r[3] = f.h;
-      r[4] = static_cast<int>(f.base / per);
-      r[5] = static_cast<int>((f.base + f.count - 1) / per);
+      r[4] = static_cast<int>(pf_quotient(f.base, per));
+      r[5] = static_cast<int>(pf_quotient(f.base + f.count - 1, per));
     }
   }
   // The warp's next unit that has tiles in this piece, into sh.unit[warp], and its
