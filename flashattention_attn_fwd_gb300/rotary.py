@@ -25,49 +25,51 @@ def _check(t, name: str, ndim: int, dtype, index: int) -> None:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
-def _strides(t, name, B, H, L, d):
-    """(b, h, l) strides; those of axes of length 1 are never used to step."""
+def _rows(t, name, shape, index):
+    """Checks a [B, H, L, d] bf16 tensor; returns its (b, h, l) strides (those of
+    axes of length 1 are never used to step)."""
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != index or t.shape != shape:
+        _check(t, name, 4, _BF16, index)
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     sb, sh, sl, sc = t.stride()
     if sc != 1:
         raise ValueError(f"{name} must have a contiguous head dimension")
+    B, H, L, d = shape
     return sb if B > 1 else H * L * d, sh if H > 1 else L * d, sl if L > 1 else d
 
 
 def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, q_out, k_out, stream):
     _need(q, names[0], 4)
-    B, Hq, L, d = shape = q.shape
+    shape = q.shape
+    B, Hq, L, d = shape
     index = q.get_device()
     if _device_index() != index:
         raise ValueError(f"{names[0]} is on cuda:{index}, the current device is cuda:{_device_index()}")
+    qs = _rows(q, names[0], shape, index)
     _check(rope_cos, "rope_cos", 2, _F32, index)
     _check(rope_sin, "rope_sin", 2, _F32, index)
-    rows, half = rope_cos.shape
-    if rope_sin.shape != rope_cos.shape or not rope_cos.is_contiguous() or not rope_sin.is_contiguous():
+    tables = rope_cos.shape
+    if rope_sin.shape != tables or not rope_cos.is_contiguous() or not rope_sin.is_contiguous():
         raise ValueError("rope_cos and rope_sin must be contiguous and of one shape")
-    if q_out is None:
-        q_out = _empty_on(stream, shape, _BF16, q.device)
-        qos = _NONE
-    else:
-        _check(q_out, names[2], 4, _BF16, index)
-        if q_out.shape != shape:
-            raise ValueError(f"{names[2]} must be {list(shape)}, got {list(q_out.shape)}")
-        qos = _strides(q_out, names[2], B, Hq, L, d)
+    rows, half = tables
+    device = q.device
+    qos = kos = ks = _NONE
     Hk = kp = kop = 0
-    ks = kos = _NONE
+    if q_out is None:
+        q_out = _empty_on(stream, shape, _BF16, device)
+    else:
+        qos = _rows(q_out, names[2], shape, index)
     if k is not None:
         _check(k, names[1], 4, _BF16, index)
         kshape = k.shape
         Hk = kshape[1]
         if kshape[0] != B or kshape[2] != L or kshape[3] != d:
             raise ValueError(f"{names[1]} must be [{B}, heads, {L}, {d}], got {list(kshape)}")
-        ks = _strides(k, names[1], B, Hk, L, d)
+        ks = _rows(k, names[1], kshape, index)
         if k_out is None:
-            k_out = _empty_on(stream, kshape, _BF16, q.device)
+            k_out = _empty_on(stream, kshape, _BF16, device)
         else:
-            _check(k_out, names[3], 4, _BF16, index)
-            if k_out.shape != kshape:
-                raise ValueError(f"{names[3]} must be {list(kshape)}, got {list(k_out.shape)}")
-            kos = _strides(k_out, names[3], B, Hk, L, d)
+            kos = _rows(k_out, names[3], kshape, index)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError(f"{names[3]} needs {names[1]}")
@@ -75,16 +77,18 @@ def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, 
     if positions is not None:
         n = positions.dim() if isinstance(positions, _Tensor) else 2
         _check(positions, "positions", n, _I32, index)
-        if tuple(positions.shape) != ((B, L) if n == 2 else (L,)):
+        if positions.shape != ((B, L) if n == 2 else (L,)):
             raise ValueError(f"positions must be [{B}, {L}] or [{L}], got {list(positions.shape)}")
-        if L > 1 and positions.stride(-1) != 1:
+        steps = positions.stride()
+        if L > 1 and steps[-1] != 1:
             raise ValueError("positions must have contiguous rows")
         pos = positions.data_ptr()
-        pos_stride = positions.stride(0) if n == 2 and B > 1 else 0
+        pos_stride = steps[0] if n == 2 and B > 1 else 0
     desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rows, 2 * half, 1 if rope_interleaved else 0, rope_cos.data_ptr(),
-                          rope_sin.data_ptr(), pos, pos_stride, *_strides(q, names[0], B, Hq, L, d), *ks, *qos, *kos,
+                          rope_sin.data_ptr(), pos, pos_stride, *qs, *ks, *qos, *kos,
                           _raw_stream(index) if stream is None else _stream_ptr(stream))
-    st = getattr(_lib.lib(), call)(q.data_ptr(), kp, q_out.data_ptr(), kop, desc)
+    L_ = _lib.lib()
+    st = (L_.fl_rope_bwd if call == "fl_rope_bwd" else L_.fl_rope_fwd)(q.data_ptr(), kp, q_out.data_ptr(), kop, desc)
     if st:
         _lib.check(st, call)
     return q_out, k_out
