@@ -1090,10 +1090,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       uint4 kc[W], vc[W];
       uint32_t ks[D / 64], vs[D / 64];
       bool bad = false;
-      // this row's place in the pool for tile i: token index times heads, or -1
+      // this row's page for tile i; -1: negative in the table, -2: no row of the unit sees it
       auto lookup = [&](int i) -> int {
         const int j = pf_key(u, i) + r;
-        return i < z && pf_seen(p, u, j) ? __ldg(p.table + u.b * p.table_stride + (j >> shift)) : -2;
+        return i < z && pf_seen(p, u, j) ? max(__ldg(p.table + u.b * p.table_stride + (j >> shift)), -1) : -2;
       };
       auto in_pool = [&](int page) { return page >= 0 && page < p.c.num_pages; };
       auto load_k = [&](int i, int page) {

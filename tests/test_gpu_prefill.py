@@ -207,6 +207,24 @@ def test_a_bad_page_is_left_out_and_reported(fmt, page):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
+def test_every_number_outside_the_pool_is_a_bad_page(fmt):
+    """-2 and others next to the pool's limits are left out and reported alike."""
+    past, new = [96], [16]
+    parts, scales, K, V, table, q, lens, off = setup(fmt, 4, 2, 64, 16, past, new, seed=14)
+    cache, n, o = make_cache(parts, **scales), dev(lens, torch.int32), dev(off)
+    pages = parts[0].shape[0]
+    rest = reference(q, K, V, [lens[0] - 16], new, np.delete(table, 2, axis=1), mask="causal")
+    for bad in (-2, -3, -2 ** 31 + 1, pages, pages + 1):
+        t2 = table.copy()
+        t2[0, 2] = bad
+        out, lse = attn_paged_prefill_fwd(q.to(DEV), cache, n, dev(t2), seq_offsets=o)
+        with pytest.raises(FlattnError) as e:
+            sync_status()
+        assert e.value.status == 6
+        check(out, lse, rest, fmt, 64)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e2m1"])
 def test_lengths_and_offsets_at_their_limits(fmt):
     """Lengths past the table are clamped, below zero nothing is seen; more new
     rows than tokens: those at negative positions see nothing; rows behind the
