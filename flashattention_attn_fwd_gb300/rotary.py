@@ -35,6 +35,9 @@ def _rows(t, name, shape, index):
     if sc != 1:
         raise ValueError(f"{name} must have a contiguous head dimension")
     B, H, L, d = shape
+    # (all zeros would read as contiguous)
+    if (B > 1 and sb == 0) or (H > 1 and sh == 0) or (L > 1 and sl == 0):
+        raise ValueError(f"{name} must not be expanded")
     return sb if B > 1 else H * L * d, sh if H > 1 else L * d, sl if L > 1 else d
 
 

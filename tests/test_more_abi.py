@@ -205,3 +205,15 @@ def test_python_checks():
         rope_fwd(x, None, torch.zeros(4, 32), torch.zeros(4, 32))
     with pytest.raises(ValueError):
         rope_tables(8, 64, scaling="square", device="cpu")
+
+
+@pytest.mark.parametrize("axes", [(0, 1, 2), (0,), (1,), (2,), (1, 2)])
+def test_rope_refuses_expanded_tensors(axes):
+    """Three zero strides are the ABI's sign for contiguous: an expanded tensor
+    must not get there."""
+    from flashattention_attn_fwd_gb300 import rotary
+    shape = (2, 3, 4, 64)
+    x = torch.zeros([1 if i in axes else n for i, n in enumerate(shape)], dtype=torch.bfloat16).expand(shape)
+    with pytest.raises(ValueError, match="expanded"):
+        rotary._rows(x, "q", x.shape, x.get_device())
+    assert rotary._rows(x.contiguous(), "q", x.shape, x.get_device()) == (768, 256, 64)
