@@ -5,6 +5,7 @@ and keys with its gradient, and the tables that it and ``kv_append`` read.  As i
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .api import _empty_on, _need, _raw_stream, _stream_ptr
@@ -130,15 +131,20 @@ class _Rope(torch.autograd.Function):
         return rope_fwd(q, k, rope_cos, rope_sin, positions=positions, rope_interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         rope_cos, rope_sin, positions = ctx.saved_tensors
-        dq, dk = rope_bwd(_dense(dq_out), _dense(dk_out), rope_cos, rope_sin, positions=positions, rope_interleaved=ctx.interleaved)
+        dq, dk = rope_bwd(_dense(dq_out), _dense(dk_out), rope_cos, rope_sin, positions=positions,
+                          rope_interleaved=ctx.interleaved)
         return dq, dk, None, None, None, None
 
 
 def rope(q, k, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool = False):
-    """Differentiable rotation of q and k: rope_fwd in the forward, rope_bwd in
-    the backward.  Returns contiguous (q, k) as ``attention`` takes them."""
+    """Differentiable rotation of q and k (once; the tables have no gradient):
+    rope_fwd in the forward, rope_bwd in the backward.  Returns contiguous (q, k)
+    as ``attention`` takes them."""
+    if rope_cos.requires_grad or rope_sin.requires_grad:
+        raise ValueError("rope_cos and rope_sin have no gradient: detach them")
     return _Rope.apply(q, k, rope_cos, rope_sin, positions, rope_interleaved)
 
 

@@ -187,3 +187,38 @@ def test_tables(positions, scaling, rot):
     c2, s2 = torch.zeros_like(cos), torch.zeros_like(sin)
     rope_tables(positions, rot, cos=c2, sin=s2, **kw)
     assert torch.equal(c2, cos) and torch.equal(s2, sin)
+
+
+def test_autograd_captured_and_replayed_and_only_once():
+    """Forward and backward captured on one stream and replayed over other
+    values; a second derivative is refused, not zero."""
+    B, H, L, d = 2, 3, 40, 64
+    g = synth.generator(6)
+    cos, sin = (t.to(DEV) for t in host_tables(L, d))
+    q, k, dy, dz = (torch.zeros((B, H, L, d), device=DEV, dtype=torch.bfloat16) for _ in range(4))
+    q.requires_grad_()
+    k.requires_grad_()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        return torch.autograd.grad(rope(q, k, cos, sin, rope_interleaved=True), (q, k), (dy, dz))
+
+    with torch.cuda.stream(st):
+        step()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        dq, dk = step()
+    values = [synth.randn_bf16((B, H, L, d), g) for _ in range(2)]
+    dy.copy_(values[0])
+    dz.copy_(values[1])
+    graph.replay()
+    sync_status()
+    at = torch.arange(L).expand(B, L)
+    for got, x in zip((dq, dk), values):
+        assert torch.equal(got.cpu(), turned(x, cos.cpu(), sin.cpu(), at, True, -1.0))
+    y, _ = rope(q, k, cos, sin)
+    first, = torch.autograd.grad((y * y).sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        first.sum().backward()

@@ -217,3 +217,11 @@ def test_rope_refuses_expanded_tensors(axes):
     with pytest.raises(ValueError, match="expanded"):
         rotary._rows(x, "q", x.shape, x.get_device())
     assert rotary._rows(x.contiguous(), "q", x.shape, x.get_device()) == (768, 256, 64)
+
+
+def test_rope_refuses_tables_that_want_a_gradient():
+    from flashattention_attn_fwd_gb300 import rope
+    x, t = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16), torch.zeros(4, 32, requires_grad=True)
+    for cos, sin in ((t, t.detach()), (t.detach(), t)):
+        with pytest.raises(ValueError, match="gradient"):
+            rope(x, x, cos, sin)
