@@ -114,6 +114,9 @@ inline cudaError_t launch_paged_decode(int format, int d, const PagedDecodeParam
 // Query rows of a unit: two slots of 128 rows, a row for every (token, head of
 // the group); a slot holds 128 / G tokens.
 constexpr int kPrefillTile = 128;
+// Rows of a page (at most) that a TMA box of a bf16 cache takes (2048 over 32768 tokens
+// at d 64: 495 us with 64 or 128, 502 with 32, 564 with 16).
+constexpr int kPrefillBox = 64;
 // Head groups (Hq / Hkv) that a slot takes.
 constexpr int kPrefillMaxGroup = 128;
 

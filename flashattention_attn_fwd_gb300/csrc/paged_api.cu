@@ -449,9 +449,14 @@ fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, con
     const uint64_t qd[4] = {D, G, Hkv, static_cast<uint64_t>(p.T)};
     const int64_t qs[3] = {p.q_h, p.q_h * p.G, p.q_t};
     const uint32_t qb[3] = {static_cast<uint32_t>(G), 1u, static_cast<uint32_t>(p.RT)};
-    const uint64_t kd[4] = {D, page, Hkv, static_cast<uint64_t>(cache->num_pages)};
-    const int64_t ks[3] = {cache->d, static_cast<int64_t>(page) * cache->d, static_cast<int64_t>(Hkv * page) * cache->d};
-    const uint32_t kb[3] = {static_cast<uint32_t>(page < 128 ? page : 128), 1u, 1u};
+    // the pool as groups of 8 rows: 64 channels, rows, halves of a row, groups (that fit 31
+    // bits in any memory of less than 2 TB)
+    const uint64_t groups = static_cast<uint64_t>(cache->num_pages) * Hkv * (page / 8);
+    if (groups + Hkv * (page / 8) > 0x7fffffffu) return FL_ERR_UNSUPPORTED;
+    const uint64_t kd[4] = {64u, 8u, D / 64, groups};
+    const int64_t ks[3] = {cache->d, 64, 8 * static_cast<int64_t>(cache->d)};
+    const uint32_t kb[3] = {8u, static_cast<uint32_t>(D / 64),
+                            static_cast<uint32_t>(page < fl::kPrefillBox ? page : fl::kPrefillBox) / 8u};
     if (!encode_rows(&maps[0], q, qd, qs, qb) || !encode_rows(&maps[1], cache->k, kd, ks, kb) ||
         !encode_rows(&maps[2], cache->v, kd, ks, kb))
       return fl::launch_result("paged prefill tensor map", cudaErrorInvalidValue);

@@ -24,7 +24,7 @@
 // every time.  Where whole units are spread evenly enough none is cut.
 //
 // Roles of a block (bf16 384 threads, 4 bits 512):
-//   warp 0      bf16: Q, K and V by TMA, a box per page and 64 channels
+//   warp 0      bf16: Q, K and V by TMA, a box per page (of up to 64 rows)
 //   warps 1, 2  issue tcgen05.mma: d 64 one warp a slot, d 128 warp 1 for both
 //   warp 3      bf16: zeroes V's rows that no row of the unit sees
 //   warps 4-11  softmax, a warpgroup per slot and a thread per row; 4 bits: its
@@ -85,6 +85,10 @@ struct PfLayout {
   static constexpr int HALVES = D / 64;                // 64-channel halves of a row (128 bytes each)
   static constexpr int HALF = 128 * 128;               // bytes of one half of a tile
   static constexpr int TILE = HALVES * HALF;           // bytes of a K, V or Q tile
+  // Q: one half after the other.  K and V: groups of 8 rows, in a group 8 rows of one half
+  // before 8 of the other, so that one box of a page holds both halves (with a box for each,
+  // pages of 16 at d 128 took 869 us for 2048 over 32768 tokens, 32 boxes of 2 KB a tile; 695).
+  static constexpr int GROUP = HALVES * 1024;
   static constexpr int FIXED = 2048;                   // barriers and small arrays
   static constexpr int BUDGET = 227 * 1024 - 1024 - FIXED;
   static constexpr int SLOTS_FIT = (BUDGET - 2 * TILE) / TILE;
@@ -462,11 +466,10 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     if (warp == 0 && !Q4) {
       // ---------------------------------------------------------------- loads
       const uint64_t pol_q = ptx::policy_evict_first(), pol_kv = ptx::policy_evict_last();
-      const int nsub = shift >= 7 ? 1 : 128 >> shift;  // pages of a tile
-      const int sub_len = 128 / nsub;
-      const int box = lane & 15;                       // lanes 0-15 K, 16-31 V
-      const bool mine = box < nsub * L::HALVES;
-      const int sub = mine ? box % nsub : 0, half = mine ? box / nsub : 0;
+      const int sub_len = min(1 << shift, kPrefillBox), nsub = 128 / sub_len;  // boxes of a tile
+      const int sub = lane & 15;                       // lanes 0-15 K, 16-31 V
+      const bool mine = sub < nsub;
+      const int groups = 1 << (shift - 3);             // of 8 rows, in a page and head
       uint32_t e = 0, tile = 0, part = 0, qc[2] = {0u, 0u};
       int q_phase[2] = {-1, -1};
       each_unit([&](const PfUnit& u, int a, int z) {
@@ -486,7 +489,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           const bool at_end = page == p.c.num_pages && mine && pf_any_seen(p, u, j0 + sub * sub_len, sub_len);
           const bool bad = out_of_pool || at_end;
           if (bad) page = p.c.num_pages;
-          const uint32_t badl = __ballot_sync(0xffffffffu, bad && box < nsub && lane < 16);
+          const uint32_t badl = __ballot_sync(0xffffffffu, bad && mine && lane < 16);
           if (lane == 0) {
             uint32_t w = 0u;
             if (badl) {
@@ -496,7 +499,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             }
             sh.bad[tile & 15u] = w;
           }
-          const int row = j0 & page_mask;  // of a page of 128 keys and more
+          const int group = (page * p.c.Hkv + u.h) * groups + (((j0 + sub * sub_len) & page_mask) >> 3);
           const bool whole = pf_all_seen(p, u, j0, 128);
           for (int v = 0; v < 2; ++v) {
             const uint32_t ev = e + v;
@@ -514,8 +517,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             }
             __syncwarp();
             if (mine && (lane >= 16) == (v == 1) && !skip)
-              ptx::tma_load_4d(smem + L::OFF_RING + st * L::TILE + half * L::HALF + sub * sub_len * 128, v ? &tmV : &tmK, bar,
-                               64 * half, nsub == 1 ? row : 0, u.h, page, pol_kv);
+              ptx::tma_load_4d(smem + L::OFF_RING + st * L::TILE + sub * (sub_len / 8) * L::GROUP, v ? &tmV : &tmK, bar, 0, 0,
+                               0, group, pol_kv);
             if (land) ++part;
             if (i > a || v) continue;
             // Q behind the first K, which need not wait for the last unit's end
@@ -567,7 +570,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
           for (int r = lane >> 3; r < 128; r += 4)
             if (r >= end || (r < from && r >= sinks))
 #pragma unroll
-              for (int h = 0; h < L::HALVES; ++h) st_shared128(base + h * L::HALF + r * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
+              for (int h = 0; h < L::HALVES; ++h)
+                st_shared128(base + (r >> 3) * L::GROUP + h * 1024 + (r & 7) * 128 + (lane & 7) * 16, 0u, 0u, 0u, 0u);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.kv_full[st]);
@@ -593,20 +597,21 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       // by the elected lane
       auto issue_s = [&](int s, uint32_t ev) {
         const uint64_t qd = ptx::smem_desc(qa + s * L::TILE, 16, 1024, 2u);
-        const uint64_t kd = ptx::smem_desc(ring + (ev % NS) * L::TILE, 16, 1024, 2u);
+        const uint64_t kd = ptx::smem_desc(ring + (ev % NS) * L::TILE, 16, L::GROUP, 2u);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
-          const uint32_t off = ((kb / 4) * L::HALF + (kb % 4) * 32) >> 4;
-          ptx::mma_ss(tmem + s * 128, qd + off, kd + off, IDESC_S, kb > 0 ? 1u : 0u);
+          const uint32_t c = (kb % 4) * 32;
+          ptx::mma_ss(tmem + s * 128, qd + (((kb / 4) * L::HALF + c) >> 4), kd + (((kb / 4) * 1024 + c) >> 4), IDESC_S,
+                      kb > 0 ? 1u : 0u);
         }
         ptx::mma_commit(&sh.s_full[s]);
       };
       auto issue_pv = [&](int s, uint32_t ev, bool acc, int kb0) {
-        const uint64_t vd = ptx::smem_desc(ring + (ev % NS) * L::TILE, L::HALF, 1024, 2u);
+        const uint64_t vd = ptx::smem_desc(ring + (ev % NS) * L::TILE, 1024, L::GROUP, 2u);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int kb = kb0 + k;
-          ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 16 * 128) >> 4), IDESC_O,
+          ptx::mma_ts(tmem + kColO + s * D, tmem + kColP + s * kStrP + kb * 8, vd + ((kb * 2 * L::GROUP) >> 4), IDESC_O,
                       (acc || kb > 0) ? 1u : 0u);
         }
       };
@@ -1082,7 +1087,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
     // -------------------------------------- 4 bits: Q, K and V tiles in fp16
     ptx::setmaxnreg_dec<L::LOAD_REGS>();
     const int r = tid - 384;  // key row of the tile
-    const int row_off = r * 128;
+    const int row_off = (r >> 3) * L::GROUP + (r & 7) * 128;
     constexpr int W = D / 32;   // 16-byte words of a row's codes
     uint32_t e = 0, tile = 0;
     const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
@@ -1149,7 +1154,7 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
             cvt4::from_e2m1x8(w[k], hv);
             const uint32_t sc = k < 2 ? s0 : s1;
             const int piece = (q * 4 + k) & 7, half = (q * 4 + k) >> 3;
-            st_shared128(base + half * L::HALF + ((piece ^ (r & 7)) << 4), cvt4::hmul2(hv[0], sc), cvt4::hmul2(hv[1], sc),
+            st_shared128(base + half * 1024 + ((piece ^ (r & 7)) << 4), cvt4::hmul2(hv[0], sc), cvt4::hmul2(hv[1], sc),
                          cvt4::hmul2(hv[2], sc), cvt4::hmul2(hv[3], sc));
           }
         }
