@@ -39,6 +39,14 @@
 // the score), and P carries 2^7 so that weights down to 2^-31 of the largest
 // survive in fp16.  bf16: P is rounded to bf16, V's type.
 //
+// Measured: 2048 tokens over 32768, 32 heads over 8: bf16 d 128 680 us (1.57 PFLOP/s; 725
+// to 750 once the power cap has brought the clock down), d 64 505 (1.05), 4 bits d 128 774
+// (1.38), d 64 605 (0.88).  bf16 d 128 is bound by the feeding of the tensor core: a P V and
+// S pair takes 1034 cycles, one after another 1245, the waits for P between them.  The
+// others are bound by the softmax warps, two a scheduler: 2400 cycles a tile in which each
+// waits for S, loads it (300), looks for the maximum (450), writes P (1100).  A change of
+// units costs a slot 4000 cycles beside its tiles (output 1800 to 2700, next unit 1200).
+//
 // TMEM (512 columns): S of slot s at 128 s; d 64: P at 256 + 64 s, O at 384 + 64 s,
 // and the next tile's S is issued as soon as this one is in registers; d 128: P
 // over the first half of S, O at 256 + 128 s.
@@ -62,11 +70,11 @@ namespace fl {
 namespace {
 
 // Tiles that starting and ending a unit costs a block, found by measuring 1, 2, 3, 4 and 6
-// on packed prompts of 901 to 2999 tokens, 32 heads over 8: bf16 d 128 184, 163, 161, 166
-// and 178 us, d 64 145, 131, 135, 140 and 152; 4 bits d 128 278, 229, 210, 204 and 206,
-// d 64 194, 156, 152, 157 and 186.
+// on packed prompts of 901 to 2999 tokens, 32 heads over 8: bf16 d 128 166, 155, 159, 166
+// and 176 us, d 64 144, 127, 125, 129 and 138; 4 bits d 128 258, 209, 197, 198 and 207,
+// d 64 200, 161, 150, 153 and 166.
 template <int FMT, int D>
-constexpr int kPfLead = FMT == KV_BF16 ? 2 : D == 64 ? 3 : 4;
+constexpr int kPfLead = FMT == KV_BF16 && D == 128 ? 2 : 3;
 // Tiles that leaving partial results and joining them costs.
 constexpr int kPfJoin = 4;
 constexpr uint64_t kPfTurnNs = 4000;
