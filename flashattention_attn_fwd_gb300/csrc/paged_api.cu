@@ -195,6 +195,11 @@ fl_status prefill_desc_check(const fl_kv_cache* cache, const fl_attn_desc* desc)
   if (d.Hkv != cache->Hkv || d.d != cache->d || d.dv != cache->d || d.Lk % cache->page_size) return FL_ERR_INVALID_ARG;
   if (d.Lk > kMaxTokens || d.Lq > kMaxRows || d.B > kMaxRows) return FL_ERR_UNSUPPORTED;
   if (d.Hq / d.Hkv > fl::kPrefillMaxGroup) return FL_ERR_UNSUPPORTED;
+  // a bf16 pool's groups of 8 rows, one page more for what is outside, are counted in 31
+  // bits (two terabytes of keys at d 64)
+  if (cache->format == FL_KV_BF16 &&
+      (static_cast<int64_t>(cache->num_pages) + 1) * (static_cast<int64_t>(cache->Hkv) * cache->page_size / 8) > 0x7fffffff)
+    return FL_ERR_UNSUPPORTED;
   if (!std::isfinite(d.scale)) return FL_ERR_INVALID_ARG;
   if (d.mask_kind < FL_MASK_NONE || d.mask_kind > FL_MASK_DOCUMENT) return FL_ERR_INVALID_ARG;
   if (d.mask_kind > FL_MASK_SLIDING_WINDOW) return FL_ERR_UNSUPPORTED;
@@ -449,10 +454,8 @@ fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, con
     const uint64_t qd[4] = {D, G, Hkv, static_cast<uint64_t>(p.T)};
     const int64_t qs[3] = {p.q_h, p.q_h * p.G, p.q_t};
     const uint32_t qb[3] = {static_cast<uint32_t>(G), 1u, static_cast<uint32_t>(p.RT)};
-    // the pool as groups of 8 rows: 64 channels, rows, halves of a row, groups (that fit 31
-    // bits in any memory of less than 2 TB)
+    // the pool as groups of 8 rows: 64 channels, rows, halves of a row, groups
     const uint64_t groups = static_cast<uint64_t>(cache->num_pages) * Hkv * (page / 8);
-    if (groups + Hkv * (page / 8) > 0x7fffffffu) return FL_ERR_UNSUPPORTED;
     const uint64_t kd[4] = {64u, 8u, D / 64, groups};
     const int64_t ks[3] = {cache->d, 64, 8 * static_cast<int64_t>(cache->d)};
     const uint32_t kb[3] = {8u, static_cast<uint32_t>(D / 64),

@@ -146,8 +146,8 @@ cudaError_t launch_rope_d(RopeParams& p, int sm_count, cudaStream_t s) {
 // the rest x, in half turns at most 1/4 either way, goes through
 //   sin(pi x) = x S(x^2),  cos(pi x) = C(x^2)
 // (fit_poly.py turn: within 9e-8, two channels an instruction).  A thread takes
-// four neighbouring pairs at several positions.  131072 positions of 64 pairs: 14 us
-// (4.7 TB/s of writes; with sincospif 18), 4096 of 32 pairs 4.7 (the launch).
+// four neighbouring pairs at several positions.  131072 positions of 64 pairs: 12 us
+// (5.4 TB/s of writes; with sincospif 18), 4096 of 32 pairs 4.1 (the launch).
 constexpr int kTabThreads = 256;
 constexpr int kTabRowsMax = 8;  // positions of a thread
 

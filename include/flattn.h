@@ -380,7 +380,8 @@ FL_API size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, cons
  *                 calls that may overlap need one each
  * desc: B, Hq, Hkv, Lq (all rows of the call, at most 2^30), d == dv (the cache's
  * Hkv and d), Lk = max_pages * page_size, Hq / Hkv at most 128, mask NONE, CAUSAL
- * or SLIDING_WINDOW, any score_mod, k_strides and v_strides zero.
+ * or SLIDING_WINDOW, any score_mod, k_strides and v_strides zero; a bf16 pool of fewer
+ * than 2^34 rows (pages * Hkv * page_size).
  * Left as they are: rows from seq_offsets[B] on.  A visible key whose page is
  * outside the pool is left out and the call reports FL_ERR_DEVICE_BOUNDS through
  * fl_sync_status.  Rows that see no key get out = 0 and lse = -inf (with CAUSAL and

@@ -225,3 +225,13 @@ def test_rope_refuses_tables_that_want_a_gradient():
     for cos, sin in ((t, t.detach()), (t.detach(), t)):
         with pytest.raises(ValueError, match="gradient"):
             rope(x, x, cos, sin)
+
+
+def test_prefill_refuses_a_bf16_pool_past_its_row_count(L):
+    """Groups of 8 rows of the pool and one page fit 31 bits, or the call is refused."""
+    big, fits = 2 ** 34 // (2 * 16), 2 ** 34 // (2 * 16) - 2
+    for fmt, pages, want in ((0, big, UNS), (0, 2 ** 31 - 1, UNS)):
+        assert prefill(L, cache(format=fmt, num_pages=pages), prefill_desc()) == want
+    if not torch.cuda.is_available():
+        for fmt, pages in ((0, fits), (1, big)):
+            assert prefill(L, cache(format=fmt, num_pages=pages), prefill_desc()) == _lib.FL_ERR_CUDA
