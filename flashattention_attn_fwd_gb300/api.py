@@ -56,6 +56,13 @@ def _like(stream, t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t) if stream is None else _empty_on(stream, t.shape, t.dtype, t.device)
 
 
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous at a 16-byte address.  Autograd hands over slices of larger
+    gradients (of a concatenation, say), contiguous at any element."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _need(t: torch.Tensor, name: str, ndim: int, dtype=torch.bfloat16):
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.dim() == ndim:
         return
@@ -341,7 +348,7 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, out, lse = ctx.saved_tensors
-        dq, dk, dv = attn_bwd(q, k, v, out, dout.contiguous(), lse, **ctx.kw)
+        dq, dk, dv = attn_bwd(q, k, v, out, _aligned(dout), lse, **ctx.kw)
         return dq, dk, dv, None
 
 
@@ -362,7 +369,7 @@ class _DiffAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         lam, causal, scale = ctx.args
-        grads = diffattn_bwd(*ctx.saved_tensors, dout.contiguous(), lam, causal=causal, scale=scale)
+        grads = diffattn_bwd(*ctx.saved_tensors, _aligned(dout), lam, causal=causal, scale=scale)
         return (*grads, None, None, None)
 
 

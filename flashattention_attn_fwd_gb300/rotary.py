@@ -8,7 +8,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from .api import _empty_on, _need, _raw_stream, _stream_ptr
+from .api import _aligned, _empty_on, _need, _raw_stream, _stream_ptr
 from ._lib import ROPE_SCALINGS
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -117,10 +117,11 @@ def rope_bwd(dq_out, dk_out, rope_cos, rope_sin, *, positions=None, rope_interle
 
 
 def _dense(t):
-    """A gradient with strides that the kernel takes (an expanded one has zeros)."""
+    """A gradient with strides and an address that the kernel takes (an expanded one
+    has zero strides, a slice of a larger one may start anywhere)."""
     if t is None or (t.stride(3) == 1 and all(s > 0 and s % 8 == 0 for s in t.stride()[:3]) and t.data_ptr() % 16 == 0):
         return t
-    return t.contiguous()
+    return _aligned(t)
 
 
 class _Rope(torch.autograd.Function):
