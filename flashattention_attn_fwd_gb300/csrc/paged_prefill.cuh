@@ -602,7 +602,11 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
       constexpr uint32_t IDESC_O = ptx::idesc_bf16_f32(128, D, true) & kTypes;
       const uint32_t ring = ptx::smem_u32(smem + L::OFF_RING);
       const uint32_t qa = ptx::smem_u32(smem + L::OFF_Q);
-      auto wait = [&](uint64_t* bar, uint32_t parity, int where) { return pf_wait(bar, parity & 1u, ctl, where); };
+      // One answer for the warp: lanes that part where a wait gives up would not meet again
+      // at the next elect.sync.
+      auto wait = [&](uint64_t* bar, uint32_t parity, int where) {
+        return __all_sync(0xffffffffu, pf_wait(bar, parity & 1u, ctl, where)) != 0;
+      };
       auto full = [&](uint32_t ev, int where) { return wait(&sh.kv_full[ev % NS], ev / NS, where); };
       auto free_place = [&](uint32_t ev) {
         if (lane == 0) ptx::mbar_arrive(&sh.kv_empty[ev % NS]);
@@ -672,8 +676,8 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
               const bool v_ok = ptx::mbar_test_wait(v_bar, v_ph), k_ok = ptx::mbar_test_wait(k_bar, k_ph);
               const bool o_ok = ptx::mbar_test_wait(&sh.o_empty[s], ((oc >> s) + 1u) & 1u);
               const bool p_ok = ptx::mbar_test_wait(&sh.p_lo[s], (pc >> s) & 1u);
-              if (!(v_ok & (k_ok | !more) & (o_ok | (i > 0)) & p_ok)) {
-                go = pf_wait(v_bar, v_ph, ctl, 16) && (!more || pf_wait(k_bar, k_ph, ctl, 11)) &&
+              if (!__all_sync(0xffffffffu, v_ok & (k_ok | !more) & (o_ok | (i > 0)) & p_ok)) {
+                go = wait(v_bar, v_ph, 16) && (!more || wait(k_bar, k_ph, 11)) &&
                      (i > 0 || wait(&sh.o_empty[s], (oc >> s) + 1u, 13)) && wait(&sh.p_lo[s], pc >> s, 14);
                 if (!go) break;
               }
