@@ -63,6 +63,7 @@ EXPORTS = (
 )
 
 KV_FORMATS = {"bf16": 0, "e2m1": 1}
+ROPE_ZERO_Q, ROPE_ZERO_K = 0x10, 0x20
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 

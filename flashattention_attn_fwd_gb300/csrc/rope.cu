@@ -44,11 +44,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   if (token >= static_cast<int64_t>(p.B) * p.L) return;
   const int b = static_cast<int>(token / p.L), l = static_cast<int>(token % p.L);
   const int pos = p.positions ? __ldg(p.positions + b * p.pos_b + l) : l;
+  const int sub = lane / LPR, c8 = lane % LPR, c0 = 8 * c8;
   if (pos < 0 || pos >= p.table_rows) {
     if (lane == 0 && part == 0) atomicOr(p.status, 2u);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const RopeRows& t = p.t[k];
+      if (!t.zero) continue;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(t.y) + b * t.y_b + l * t.y_l + c0;
+      for (int r = part * RPS + sub; r < t.heads; r += p.splits * RPS)
+        *reinterpret_cast<uint4*>(dst + r * t.y_h) = make_uint4(0u, 0u, 0u, 0u);
+    }
     return;
   }
-  const int sub = lane / LPR, c8 = lane % LPR, c0 = 8 * c8;
   const bool turn = c0 < p.rope_dim;
   const int half = p.rope_dim >> 1;
   const bool second = !PAIRS && c0 >= half;

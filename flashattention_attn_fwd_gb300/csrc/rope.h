@@ -15,6 +15,7 @@ struct RopeRows {
   void* y;
   int64_t x_b, x_h, x_l, y_b, y_h, y_l;  // strides, elements
   int heads;
+  int zero;  // rows without a position in the tables become zeros
 };
 
 struct RopeParams {

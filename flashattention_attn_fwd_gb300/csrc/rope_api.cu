@@ -33,7 +33,8 @@ fl_status rope_call(const char* what, const void* q, const void* k, void* q_out,
   const fl_rope_desc& d = *desc;
   if (d.B < 1 || d.L < 1 || d.Hq < 1 || d.Hk < 0 || (d.Hk > 0) != (k != nullptr)) return FL_ERR_INVALID_ARG;
   if (!d.rope_cos || !d.rope_sin || d.rope_positions < 1 || d.rope_dim < 1 || d.rope_dim > d.d) return FL_ERR_INVALID_ARG;
-  if (d.rope_interleaved != 0 && d.rope_interleaved != 1) return FL_ERR_INVALID_ARG;
+  const int32_t interleaved = d.rope_interleaved & ~(FL_ROPE_ZERO_Q | FL_ROPE_ZERO_K);
+  if (interleaved != 0 && interleaved != 1) return FL_ERR_INVALID_ARG;
   if (d.positions ? d.positions_stride < 0 : d.L > d.rope_positions) return FL_ERR_INVALID_ARG;
   if (d.d != 32 && d.d != 64 && d.d != 128) return FL_ERR_UNSUPPORTED;
   if (d.rope_dim % 16) return FL_ERR_UNSUPPORTED;
@@ -51,6 +52,8 @@ fl_status rope_call(const char* what, const void* q, const void* k, void* q_out,
   fl_status st = rows(p.t[0], q, q_out, d.Hq, d.q_strides, d.q_out_strides);
   if (st == FL_OK && k) st = rows(p.t[1], k, k_out, d.Hk, d.k_strides, d.k_out_strides);
   if (st != FL_OK) return st;
+  p.t[0].zero = (d.rope_interleaved & FL_ROPE_ZERO_Q) != 0;
+  p.t[1].zero = (d.rope_interleaved & FL_ROPE_ZERO_K) != 0;
   int sm_count = 0;
   st = fl::device_info(&sm_count, &p.status);
   if (st != FL_OK) return st;
@@ -62,7 +65,7 @@ fl_status rope_call(const char* what, const void* q, const void* k, void* q_out,
   p.L = d.L;
   p.table_rows = d.rope_positions;
   p.rope_dim = d.rope_dim;
-  p.interleaved = d.rope_interleaved;
+  p.interleaved = interleaved;
   p.sign = sign;
   return fl::launch_result(what, fl::launch_rope(d.d, p, sm_count, static_cast<cudaStream_t>(d.stream)));
 }

@@ -9,7 +9,7 @@ from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .api import _aligned, _empty_on, _need, _raw_stream, _stream_ptr
-from ._lib import ROPE_SCALINGS
+from ._lib import ROPE_SCALINGS, ROPE_ZERO_K, ROPE_ZERO_Q
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
@@ -59,7 +59,10 @@ def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, 
     device = q.device
     qos = kos = ks = _NONE
     Hk = kp = kop = 0
+    # rows without a position in the tables: left in tensors that are given, zeros in others
+    layout = 1 if rope_interleaved else 0
     if q_out is None:
+        layout |= ROPE_ZERO_Q
         q_out = _empty_on(stream, shape, _BF16, device)
     else:
         qos = _rows(q_out, names[2], shape, index)
@@ -71,6 +74,7 @@ def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, 
             raise ValueError(f"{names[1]} must be [{B}, heads, {L}, {d}], got {list(kshape)}")
         ks = _rows(k, names[1], kshape, index)
         if k_out is None:
+            layout |= ROPE_ZERO_K
             k_out = _empty_on(stream, kshape, _BF16, device)
         else:
             kos = _rows(k_out, names[3], kshape, index)
@@ -88,7 +92,7 @@ def _rotate(call, names, q, k, rope_cos, rope_sin, positions, rope_interleaved, 
             raise ValueError("positions must have contiguous rows")
         pos = positions.data_ptr()
         pos_stride = steps[0] if n == 2 and B > 1 else 0
-    desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rows, 2 * half, 1 if rope_interleaved else 0, rope_cos.data_ptr(),
+    desc = _lib.ROPE_PACK(B, L, Hq, Hk, d, rows, 2 * half, layout, rope_cos.data_ptr(),
                           rope_sin.data_ptr(), pos, pos_stride, *qs, *ks, *qos, *kos,
                           _raw_stream(index) if stream is None else _stream_ptr(stream))
     L_ = _lib.lib()
@@ -103,7 +107,9 @@ def rope_fwd(q, k, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool
     """fl_rope_fwd: rotate q [B, Hq, L, d] and k [B, Hk, L, d] (or None), bf16
     with any strides that are multiples of 8, by positions (int32 [B, L] or [L];
     None: row l has position l); rope_cos, rope_sin fp32 [positions, rope_dim /
-    2].  Returns (q_out, k_out), contiguous when not given."""
+    2].  Returns (q_out, k_out), contiguous when not given.  Rows whose position is
+    outside the tables are reported by sync_status; given outputs keep what they
+    held there, others get zeros."""
     return _rotate("fl_rope_fwd", ("q", "k", "q_out", "k_out"), q, k, rope_cos, rope_sin, positions, rope_interleaved,
                    q_out, k_out, stream)
 
@@ -143,7 +149,8 @@ class _Rope(torch.autograd.Function):
 def rope(q, k, rope_cos, rope_sin, *, positions=None, rope_interleaved: bool = False):
     """Differentiable rotation of q and k (once; the tables have no gradient):
     rope_fwd in the forward, rope_bwd in the backward.  Returns contiguous (q, k)
-    as ``attention`` takes them."""
+    as ``attention`` takes them.  Rows whose position is outside the tables (reported
+    by sync_status) come out as zeros, and so do their gradients."""
     if rope_cos.requires_grad or rope_sin.requires_grad:
         raise ValueError("rope_cos and rope_sin have no gradient: detach them")
     return _Rope.apply(q, k, rope_cos, rope_sin, positions, rope_interleaved)

@@ -449,11 +449,17 @@ FL_API int32_t fl_kv_read_desc_size(void);
  * for each pair (x1, x2), cos and sin from row `position` of the tables; the rest
  * passes through.  Row l of batch entry b takes positions[b][l], or l.
  */
+/* Rows whose position is not in the tables: zeros in q_out (k_out), for outputs that
+   nothing was written to before. */
+#define FL_ROPE_ZERO_Q 0x10
+#define FL_ROPE_ZERO_K 0x20
+
 typedef struct fl_rope_desc {
   int32_t B, L, Hq, Hk, d;      /* Hk 0: no keys                               */
   int32_t rope_positions, rope_dim;
   int32_t rope_interleaved;     /* 0: channel c pairs with c + rope_dim / 2;
-                                   1: channel 2c with 2c + 1                   */
+                                   1: channel 2c with 2c + 1; FL_ROPE_ZERO_*
+                                   may be added                                */
   const float* rope_cos;        /* device fp32 [rope_positions, rope_dim / 2]  */
   const float* rope_sin;
   const int32_t* positions;     /* device int32, [b][l] at b * positions_stride
@@ -467,9 +473,9 @@ typedef struct fl_rope_desc {
 
 /*
  * q_out and k_out: the rotated q and k (in place is fine with the same strides).
- * A row whose position is not in the tables is left as it is, and the call
- * reports FL_ERR_DEVICE_BOUNDS through fl_sync_status (with positions NULL, L is
- * at most rope_positions).
+ * A row whose position is not in the tables is left as it is (or zeroed, with
+ * FL_ROPE_ZERO_Q and FL_ROPE_ZERO_K), and the call reports FL_ERR_DEVICE_BOUNDS
+ * through fl_sync_status (with positions NULL, L is at most rope_positions).
  */
 FL_API fl_status fl_rope_fwd(const void* q, const void* k, void* q_out, void* k_out, const fl_rope_desc* desc);
 
