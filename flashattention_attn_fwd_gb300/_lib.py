@@ -64,6 +64,7 @@ EXPORTS = (
 
 KV_FORMATS = {"bf16": 0, "e2m1": 1}
 ROPE_ZERO_Q, ROPE_ZERO_K = 0x10, 0x20
+FILL_OUT, FILL_LSE = 0x1, 0x2
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
@@ -83,7 +84,8 @@ class AttnDesc(ctypes.Structure):
         ("debug_flags", ctypes.c_uint32), ("debug_arg", ctypes.c_int32),
         ("wait_limit_ms", ctypes.c_uint32),
         ("sink", ctypes.c_int32),
-        ("reserved", ctypes.c_int32 * 6),
+        ("fill", ctypes.c_uint32),
+        ("reserved", ctypes.c_int32 * 5),
     ]
 
 
@@ -149,7 +151,7 @@ class RopeScaling(ctypes.Structure):
 
 # The structures as one packed bytes object (native alignment): a fraction of
 # the time of setting ctypes fields one by one.
-_ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i 6i")
+_ATTN = struct.Struct("@7i f 5i f 2P i 16q P I i I i I 5i")
 _APPEND = struct.Struct("@4i 3P q 2P 4i 4P 12q P")
 _READ = struct.Struct("@4i 3P q 4q P")
 _ROPE = struct.Struct("@8i 3P q 12q P")
@@ -175,11 +177,12 @@ SCALING_PACK = _packer(_SCALING)
 
 def desc_pack(B, Hq, Hkv, Lq, Lk, d, dv, *, scale=0.0, mask_kind=0, doc_causal=0, window=0, prefix=0, score_mod=0,
               softcap=0.0, slopes=0, doc_offsets=0, num_docs=0, q_strides=_ZERO4, k_strides=_ZERO4,
-              v_strides=_ZERO4, o_strides=_ZERO4, stream=0, debug_flags=0, debug_arg=-1, wait_limit_ms=0, sink=0):
+              v_strides=_ZERO4, o_strides=_ZERO4, stream=0, debug_flags=0, debug_arg=-1, wait_limit_ms=0, sink=0,
+              fill=0):
     """fl_attn_desc as bytes."""
     return ATTN_PACK(B, Hq, Hkv, Lq, Lk, d, dv, scale, mask_kind, doc_causal, window, prefix, score_mod, softcap,
                      slopes, doc_offsets, num_docs, *q_strides, *k_strides, *v_strides, *o_strides, stream,
-                     debug_flags, debug_arg, wait_limit_ms, sink, 0, 0, 0, 0, 0, 0)
+                     debug_flags, debug_arg, wait_limit_ms, sink, fill, 0, 0, 0, 0, 0)
 
 
 class FlattnError(RuntimeError):

@@ -149,6 +149,7 @@ struct PrefillParams {
   uint32_t* status;
   uint64_t timeout_ns;
   int dbg_skip_tile;           // < 0: off
+  uint32_t fill;               // FL_FILL_*: rows behind the last sequence
 };
 
 // One launch per format, head dim and score_mod; maps: q, k, v (bf16 cache only).

@@ -208,6 +208,7 @@ fl_status prefill_desc_check(const fl_kv_cache* cache, const fl_attn_desc* desc)
   if (d.score_mod < FL_SCORE_NONE || d.score_mod > FL_SCORE_SOFTCAP) return FL_ERR_INVALID_ARG;
   if (d.score_mod == FL_SCORE_ALIBI && !d.alibi_slopes) return FL_ERR_INVALID_ARG;
   if (d.score_mod == FL_SCORE_SOFTCAP && !(d.softcap > 0.f && std::isfinite(d.softcap))) return FL_ERR_INVALID_ARG;
+  if (d.fill & ~(FL_FILL_OUT | FL_FILL_LSE)) return FL_ERR_INVALID_ARG;
   for (int i = 0; i < 4; ++i)
     if (d.k_strides[i] || d.v_strides[i]) return FL_ERR_UNSUPPORTED;
   return FL_OK;
@@ -448,6 +449,7 @@ fl_status fl_attn_paged_prefill_fwd(const void* q, const fl_kv_cache* cache, con
   p.lpart = reinterpret_cast<float*>(ws + w.lpart);
   p.timeout_ns = d.wait_limit_ms ? static_cast<uint64_t>(d.wait_limit_ms) * 1000ull * 1000ull : kDefaultWaitNs;
   p.dbg_skip_tile = (d.debug_flags & FL_DEBUG_SKIP_KV_LOAD) ? d.debug_arg : -1;
+  p.fill = seq_offsets ? d.fill & (FL_FILL_OUT | (lse ? FL_FILL_LSE : 0u)) : 0u;
   CUtensorMap maps[3] = {};
   if (cache->format == FL_KV_BF16) {
     const uint64_t D = d.d, G = p.G, Hkv = d.Hkv, page = cache->page_size;

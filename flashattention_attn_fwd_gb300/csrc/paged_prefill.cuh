@@ -1229,12 +1229,31 @@ __global__ void __launch_bounds__(PfLayout<FMT, D>::THREADS, 1)
   }
 }
 
+// The rows behind the last sequence, spread over all threads of the grid: they belong to
+// no unit, and nothing else of the call writes them.
+template <int D>
+__device__ __forceinline__ void fill_rest(const PrefillParams& p) {
+  const int64_t last = min(max(__ldg(p.seq_offsets + p.B), 0), p.T);
+  const int64_t pieces = (p.T - last) * p.Hq * (D / 8);  // of 8 channels
+  const int64_t all = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pieces; i += all) {
+    const int64_t pair = i / (D / 8), row = last + pair / p.Hq, h = pair % p.Hq;
+    const int c = static_cast<int>(i % (D / 8)) * 8;
+    if (p.fill & FL_FILL_OUT)
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row * p.o_t + h * p.o_h + c) = make_uint4(0u, 0u, 0u, 0u);
+    if ((p.fill & FL_FILL_LSE) && c == 0) p.lse[row * p.Hq + h] = -CUDART_INF_F;
+  }
+}
+
 // Joins the partial results of the units that pieces share: 8 blocks of 32 rows
 // for every border between pieces; the first border inside of a unit does it.
 template <int D>
 __global__ void __launch_bounds__(128) paged_prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  // under the end of the first kernel, which began when all before it had ended
+  if (p.fill) fill_rest<D>(p);
   ptx::wait_prerequisites();
   const int border = 1 + blockIdx.x / 8, part = blockIdx.x % 8;
+  if (border >= p.grid) return;
   const int32_t* rec = p.rec + static_cast<int64_t>(border) * 8;
   if (!rec[0] || rec[4] != border - 1) return;
   const int s = part >> 2, r = (part & 3) * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
@@ -1313,8 +1332,9 @@ cudaError_t launch_prefill_score(const CUtensorMap* maps, const PrefillParams& p
   if (checked != cudaSuccess) return checked;
   kern<<<p.grid, L::THREADS, L::SMEM, s>>>(maps[0], maps[1], maps[2], p);
   const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.grid < 2) return e;
-  return launch_chained(paged_prefill_merge_kernel<D>, static_cast<unsigned>(p.grid - 1) * 8u, 128u, 0, s, p);
+  if (e != cudaSuccess || (p.grid < 2 && !p.fill)) return e;
+  const unsigned borders = p.grid < 2 ? 1u : static_cast<unsigned>(p.grid - 1);
+  return launch_chained(paged_prefill_merge_kernel<D>, borders * 8u, 128u, 0, s, p);
 }
 
 template <int FMT, int D>

@@ -10,7 +10,7 @@ import torch
 
 from . import _lib
 from .api import _empty_on, _need, _raw_stream, _stream_ptr, _zeros_on
-from ._lib import KV_FORMATS, MASKS, SCORE_MODS
+from ._lib import FILL_LSE, FILL_OUT, KV_FORMATS, MASKS, SCORE_MODS
 
 _SCALE_BLOCK = 16
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -323,8 +323,9 @@ def attn_paged_prefill_fwd(q, cache: PagedKVCache, kv_len, block_table, *, seq_o
     seq_offsets[b] to seq_offsets[b + 1] at the last positions of the first
     kv_len[b] cached tokens (seq_offsets None: one row per sequence); mask
     "causal", "none" or "window" (with ``window`` and ``sink``).  The workspace
-    is allocated with torch when not given.  Returns (out [T, Hq, d] bf16, lse
-    [T, Hq] fp32 or None)."""
+    is allocated with torch when not given.  Rows behind the last sequence (a batch
+    padded to a fixed T) keep what given outputs held; in others out is 0 and lse
+    -inf.  Returns (out [T, Hq, d] bf16, lse [T, Hq] fp32 or None)."""
     index = cache.index
     _current(index)
     B, max_pages, table_stride = _need_table(cache, kv_len, block_table)
@@ -341,9 +342,13 @@ def attn_paged_prefill_fwd(q, cache: PagedKVCache, kv_len, block_table, *, seq_o
         if alibi_slopes.shape[0] != Hq or not alibi_slopes.is_contiguous():
             raise ValueError("alibi_slopes must be contiguous [Hq]")
         slopes = alibi_slopes.data_ptr()
+    # rows behind the last sequence: left in tensors that are given, defined in others
+    fill = 0
     if out is None:
+        fill = FILL_OUT
         out = _empty_on(stream, shape, _BF16, cache.device)
     if lse is None and return_lse:
+        fill |= FILL_LSE
         lse = _empty_on(stream, shape[:2], _F32, cache.device)
     elif lse is not None:
         _check(lse, "lse", 2, _F32, index)
@@ -354,7 +359,8 @@ def attn_paged_prefill_fwd(q, cache: PagedKVCache, kv_len, block_table, *, seq_o
                          sink=sink or 0, score_mod=SCORE_MODS[score_mod], softcap=softcap or 0.0, slopes=slopes,
                          q_strides=(0, qs[1], qs[0], 1), o_strides=(0, os_[1], os_[0], 1),
                          stream=_raw_stream(index) if stream is None else _stream_ptr(stream),
-                         debug_flags=debug_flags, debug_arg=debug_arg, wait_limit_ms=wait_limit_ms)
+                         debug_flags=debug_flags, debug_arg=debug_arg, wait_limit_ms=wait_limit_ms,
+                         fill=fill if offsets else 0)
     L = _lib.lib()
     if workspace is None:
         n = int(L.fl_attn_paged_prefill_workspace_size(desc, cache._ref))

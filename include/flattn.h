@@ -86,6 +86,11 @@ typedef enum {
                                       small problems exercise the split and
                                       its merge; no effect with sinks */
 
+/* Rows of fl_attn_paged_prefill_fwd behind the last sequence (fl_attn_desc.fill): for
+   outputs that nothing was written to before. */
+#define FL_FILL_OUT 0x1u           /* out = 0                                  */
+#define FL_FILL_LSE 0x2u           /* lse = -inf                               */
+
 /*
  * Problem descriptor for fl_attn_fwd / fl_diffattn_fwd.
  *   q   [B, Hq,  Lq, d]     k [B, Hkv, Lk, d]     v [B, Hkv, Lk, dv]
@@ -116,7 +121,8 @@ typedef struct fl_attn_desc {
                                0 = default (2000 ms)                           */
   int32_t sink;             /* SLIDING_WINDOW: the first `sink` keys stay
                                visible to every later query; 0: none           */
-  int32_t reserved[6];
+  uint32_t fill;            /* FL_FILL_*: fl_attn_paged_prefill_fwd            */
+  int32_t reserved[5];
 } fl_attn_desc;
 
 /* Fill *desc with zeros and the defaults (mask NONE, score NONE, scale 1/sqrt(d)). */
@@ -382,8 +388,8 @@ FL_API size_t fl_attn_paged_decode_workspace_size(const fl_attn_desc* desc, cons
  * Hkv and d), Lk = max_pages * page_size, Hq / Hkv at most 128, mask NONE, CAUSAL
  * or SLIDING_WINDOW, any score_mod, k_strides and v_strides zero; a bf16 pool of fewer
  * than 2^34 rows (pages * Hkv * page_size).
- * Left as they are: rows from seq_offsets[B] on.  A visible key whose page is
- * outside the pool is left out and the call reports FL_ERR_DEVICE_BOUNDS through
+ * Left as they are: rows from seq_offsets[B] on (desc->fill: zeros, a log-sum-exp of
+ * -inf).  A visible key whose page is outside the pool is left out and the call reports FL_ERR_DEVICE_BOUNDS through
  * fl_sync_status.  Rows that see no key get out = 0 and lse = -inf (with CAUSAL and
  * SLIDING_WINDOW those at negative positions, kv_len[b] < n_b, among them).  The
  * work is cut by the lengths alone: a call's result is the same every time.
