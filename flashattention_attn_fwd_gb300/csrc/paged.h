@@ -1,5 +1,5 @@
-// Paged key/value cache: parameters shared by the host entry points, the
-// append kernel and the decode kernels (internal header).
+// Paged key/value cache: parameters shared by the host entry points and the
+// append, read, decode and chunk attention kernels (internal header).
 #pragma once
 
 #include <cuda.h>
@@ -161,7 +161,7 @@ FL_DECLARE_PREFILL(e2m1_d64)
 FL_DECLARE_PREFILL(e2m1_d128)
 #undef FL_DECLARE_PREFILL
 
-// ---- reading the cache back (kv_read.cu)
+// ---- reading the cache back (paged_read.cu)
 
 struct ReadParams {
   PagedCache c;

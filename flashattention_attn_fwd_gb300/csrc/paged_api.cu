@@ -1,5 +1,6 @@
 // C ABI of the paged key/value cache: argument checks, parameters and
-// launches of the append and of the decode attention.
+// launches of the append, the read, the decode attention and the attention of
+// chunks of new tokens.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

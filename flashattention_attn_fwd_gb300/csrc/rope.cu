@@ -148,9 +148,10 @@ cudaError_t launch_rope_d(RopeParams& p, int sm_count, cudaStream_t s) {
 }
 
 // Tables: cos and sin of position * angle step.  The angle is a 64-bit fraction
-// of a turn, so that position times step wraps where a turn ends and nothing is
-// lost at far positions (error 2^-64 turns times the position, with integer
-// sums where fp64's rate is low).  Its quarter turns pick the function and the sign;
+// of a turn, so that position times step wraps exactly where a turn ends, in
+// integers (fp64's rate is low).  What the step itself is off by grows with the
+// position: the host's fp64 gives it within about 2^-55 turns (352 units of 2^-64 at
+// worst over bases 1e4 and 5e5, 64 and 128 channels), 1e-10 of a turn at 2^22 positions.  Its quarter turns pick the function and the sign;
 // the rest x, in half turns at most 1/4 either way, goes through
 //   sin(pi x) = x S(x^2),  cos(pi x) = C(x^2)
 // (fit_poly.py turn: within 9e-8, two channels an instruction).  A thread takes

@@ -519,7 +519,8 @@ typedef struct fl_rope_scaling {
  * The tables that fl_rope_fwd and fl_kv_append read: rope_cos[p][i] = amplitude
  * cos(p inv_i), rope_sin the same, device fp32 [positions, rope_dim / 2], 16-byte
  * aligned; rope_dim a multiple of 16, at most 128.  inv_i in fp64, angles as
- * 64-bit fractions of a turn: at any position within a few roundings of fp32.
+ * 64-bit fractions of a turn: off by at most amplitude * (2.1e-7 + 2^-50 p), which
+ * is absolute (sines near zero have fewer digits).
  */
 FL_API fl_status fl_rope_tables(float* rope_cos, float* rope_sin, int32_t positions, int32_t rope_dim,
                                 const fl_rope_scaling* scaling, void* stream);
