@@ -39,9 +39,9 @@
 // the score), and P carries 2^7 so that weights down to 2^-31 of the largest
 // survive in fp16.  bf16: P is rounded to bf16, V's type.
 //
-// Measured: 2048 tokens over 32768, 32 heads over 8: bf16 d 128 680 us (1.57 PFLOP/s; 725
-// to 750 once the power cap has brought the clock down), d 64 505 (1.05), 4 bits d 128 774
-// (1.38), d 64 605 (0.88).  bf16 d 128 is bound by the feeding of the tensor core: a P V and
+// Measured: 2048 tokens over 32768, 32 heads over 8: bf16 d 128 672 us (1.59 PFLOP/s; 745
+// to 790 in a long run, once the power cap has brought the clock down), d 64 503 (1.06), 4 bits
+// d 128 764 (1.40), d 64 566 (0.94).  bf16 d 128 is bound by the feeding of the tensor core: a P V and
 // S pair takes 1034 cycles, one after another 1245, the waits for P between them.  The
 // others are bound by the softmax warps, two a scheduler: 2400 cycles a tile in which each
 // waits for S, loads it (300), looks for the maximum (450), writes P (1100).  A change of
